@@ -65,8 +65,10 @@ def bytes_per_step(w: I.Workload):
 
 
 # library sources behind each measured family: the projection and the mixing
-# kernels stand alone; the loss path is everything else in csrc/
-SOURCE_GROUPS = {"project": ("kd_project.cu",), "mix": ("kd_mix.cu",)}
+# kernels stand alone, and so do the token log-probabilities and the gradient
+# clipping (no counter captured); the loss path is everything else in csrc/
+SOURCE_GROUPS = {"project": ("kd_project.cu",), "mix": ("kd_mix.cu",),
+                 "logprob": ("kd_logprob.cu",), "clip": ("kd_clip.cu",)}
 
 
 def kernel_sources_hash(group: str = "loss") -> str:

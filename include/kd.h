@@ -81,6 +81,8 @@ typedef enum kd_status {
                                      * hold; nothing was computed (use
                                      * kd_project_teacher_logits + a
                                      * KD_TEACHER_LOGITS teacher instead) */
+#define KD_DEV_NONFINITE 0x20u /* kd_clip_grad_norm: the norm is infinite or NaN;
+                                * the gradients are passed on unscaled */
 
 typedef enum kd_dtype { KD_BF16 = 0, KD_FP32 = 1 } kd_dtype;
 
@@ -300,6 +302,105 @@ kd_status kd_mix_teacher_logits(const void* const* logits, int32_t k, const floa
                                 int64_t n_tokens, int64_t vocab, int32_t in_dtype,
                                 int32_t mode, void* out, int32_t out_dtype,
                                 uint32_t* dev_status, void* stream);
+
+/* Token log-probabilities.  For every token row n with logits z (given, or
+ * z = H W^T of hidden states and a head weight, which is never stored as a
+ * (tokens x vocab) matrix), a = z / temperature and p = softmax(a):
+ *   logprob[n]  = a[y] - logsumexp(a)          y = tokens[n]
+ *   entropy[n]  = - sum_v p_v log p_v
+ *   top alternatives: the K ids with the largest logits, best first (equal
+ *   logits: lowest id first; a NaN ranks above every number), and their
+ *   log-probabilities.
+ * With exp() of the latter as probabilities they are the cached teacher of
+ * KD_TEACHER_TOPK (probabilities not renormalised: orda-kernel README,
+ * "Teacher descriptors"; Full-Chunked-KL-Loss README, "Methods").
+ * A logit of -infinity is an id of probability 0.  A row in which every logit
+ * is -infinity has no distribution: logprob -infinity, entropy 0, the ids
+ * 0..K-1 with log-probability -infinity, and a zero gradient row.  A row with
+ * a NaN or a +infinity has logprob, entropy and log-probabilities NaN.
+ * Rows whose token is ignore_index are not computed, whatever their logits or
+ * hidden states hold: logprob 0, entropy 0, statistics 0, the ids 0..K-1 with
+ * log-probability -infinity (so such a row is a valid KD_TEACHER_TOPK row of
+ * mass 0), a zero gradient row and no share in d_w. */
+typedef struct kd_logprob_problem {
+  int64_t n_tokens;      /* N >= 0                                            */
+  int64_t vocab;         /* V >= 1                                            */
+  int64_t d_model;       /* D (KD_STUDENT_HIDDEN), multiple of 8 for bf16     */
+  int64_t ld_logits;     /* row pitch of logits in elements; 0 = vocab        */
+  int64_t ld_d_logits;   /* row pitch of d_logits in elements; 0 = vocab      */
+  int64_t ignore_index;  /* token value of rows that take no part             */
+  int32_t topk;          /* K alternatives, 0..1024, <= vocab                 */
+  int32_t dtype;         /* kd_dtype of logits / h / w and of the gradients   */
+  int32_t source;        /* kd_student_kind: hidden states or logits          */
+  float temperature;     /* > 0                                               */
+} kd_logprob_problem;
+
+/* Device pointers; NULL where the problem does not use one. */
+typedef struct kd_logprob_inputs {
+  const void* logits;    /* [N, V] rows of pitch ld_logits                    */
+  const void* h;         /* [N, D] hidden states (bf16: 16-byte aligned)      */
+  const void* w;         /* [V, D] head weight (bf16: 16-byte aligned)        */
+  const int64_t* tokens; /* [N] given tokens, or NULL: every row takes part   */
+                         /* and no logprob can be asked for                   */
+} kd_logprob_inputs;
+
+/* Floats per token in the statistics kd_logprob_fwd saves for
+ * kd_logprob_bwd: max z, log sum exp(a - max a), entropy, logsumexp(a). */
+#define KD_LOGPROB_STATS 4
+
+/* Bytes of device workspace of the two calls below on the current device.
+ * Either output pointer may be NULL. */
+kd_status kd_logprob_workspace_size(const kd_logprob_problem* problem, size_t* fwd_bytes,
+                                    size_t* bwd_bytes);
+
+/* Forward.  Any output may be NULL to skip it:
+ *   logprob, entropy  fp32 [N]         topk_idx int32 [N, K]
+ *   topk_logprob      fp32 [N, K]      stats    fp32 [N, KD_LOGPROB_STATS],
+ *                                               16-byte aligned
+ * A token that is neither ignore_index nor in [0, V) sets KD_DEV_BAD_LABEL in
+ * *dev_status (may be NULL) and gets logprob NaN; the row's other outputs are
+ * unaffected.  Sums are held in fp32. */
+kd_status kd_logprob_fwd(const kd_logprob_problem* problem, const kd_logprob_inputs* inputs,
+                         float* logprob, float* entropy, int32_t* topk_idx, float* topk_logprob,
+                         float* stats, uint32_t* dev_status, void* workspace, size_t ws_bytes,
+                         void* stream);
+
+/* Backward of logprob and entropy (the choice of alternatives has no
+ * gradient).  With upstream gradients d_logprob, d_entropy (fp32 [N]; NULL
+ * for zero) and the statistics of a kd_logprob_fwd on the same inputs,
+ *   d z_v = (1/T) (d_logprob (1[v = y] - p_v) - d_entropy p_v (log p_v + H))
+ * Writes (overwrites) the requested gradients in the problem's dtype:
+ *   d_logits [N, V] rows of pitch ld_d_logits (logits source; elements
+ *            between the rows are left as they are; it may be the logits
+ *            themselves when both pitches are equal)
+ *   d_h [N, D], d_w [V, D]    (hidden source)
+ * A bad token contributes no d_logprob term.  bf16 hidden problems round
+ * d z to bf16 (at most 2^-8 of each element) before the products with W and
+ * H, whose sums are fp32. */
+kd_status kd_logprob_bwd(const kd_logprob_problem* problem, const kd_logprob_inputs* inputs,
+                         const float* stats, const float* d_logprob, const float* d_entropy,
+                         void* d_h, void* d_w, void* d_logits, uint32_t* dev_status,
+                         void* workspace, size_t ws_bytes, void* stream);
+
+/* Global gradient norm over many tensors, and clipping: for example the
+ * gradients kd_bwd / kd_logprob_bwd wrote, before an optimiser takes them.
+ *   norm   = sqrt(sum over all tensors and elements of g^2)
+ *   out[i] = norm > max_norm ? g[i] max_norm / norm : g[i]
+ * grads / outs are host arrays of n_tensors device pointers, numel a host
+ * array of element counts (0 is allowed; its pointers may be NULL), all in
+ * `dtype`.  outs[i] may be grads[i] (in place: nothing is written when the
+ * norm is within bounds) but may not overlap any tensor otherwise (the same
+ * tensor listed twice is refused); outs = NULL only computes the norm.  norm_out: device fp32 scalar or NULL.  Squares are
+ * summed in fp32 per thread and in fp64 beyond, in a fixed order; elements up
+ * to the largest finite value do not overflow the norm.  If the norm is
+ * infinite or NaN, KD_DEV_NONFINITE is set and the gradients are passed on
+ * unscaled (so that a training loop can skip the step).
+ * max_norm >= 0 and finite.  workspace: kd_clip_grad_norm_workspace_size()
+ * bytes, 256-byte aligned. */
+kd_status kd_clip_grad_norm_workspace_size(const int64_t* numel, int32_t n_tensors, size_t* bytes);
+kd_status kd_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numel,
+                            int32_t n_tensors, int32_t dtype, float max_norm, float* norm_out,
+                            uint32_t* dev_status, void* workspace, size_t ws_bytes, void* stream);
 
 /* Static description of a status code. */
 const char* kd_status_string(kd_status status);

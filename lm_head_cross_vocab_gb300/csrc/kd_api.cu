@@ -241,6 +241,9 @@ int choose_splits(int64_t m_tiles, int64_t n_tiles, int nsm) {
   return best;
 }
 
+}  // namespace
+
+namespace kd {
 // Backward chunk (R rows x C columns of G).  Cost model in bytes: every extra
 // vocabulary chunk re-reads and re-writes the fp32 dH accumulator, every extra
 // row chunk the fp32 dW accumulator, plus a fixed cost per chunk.  A chunk
@@ -275,6 +278,9 @@ void choose_chunk(const kd_problem* p, int64_t budget_elems, int64_t col_quant, 
   if (p->seq_chunk <= 0) R = std::min(R, round_up(cdiv(n, cdiv(n, R)), 128));
   if (p->vocab_chunk <= 0) C = std::min(C, round_up(cdiv(v, cdiv(v, C)), col_quant));
 }
+}  // namespace kd
+
+namespace {
 
 kd_status make_plan(const kd_problem* p, bool has_labels, Plan& P) {
   memset(&P, 0, sizeof(P));

@@ -21,6 +21,10 @@ void note_launch(int k = 1);
 // devices at the same time each see their own device's answer.
 int max_active_clusters(const void* kern, const cudaLaunchConfig_t& cfg);
 
+// Backward chunk of G, R rows x C vocabulary columns (kd_api.cu).
+void choose_chunk(const kd_problem* p, int64_t budget_elems, int64_t col_quant, int64_t cap_div,
+                  int64_t& R, int64_t& C);
+
 // ---------------------------------------------------------------- aux kernels
 // Count valid labels into *count (int32, zeroed by the caller) and flag bad ones.
 void launch_label_check(const int64_t* labels, int64_t n, int64_t vocab, int64_t ignore,

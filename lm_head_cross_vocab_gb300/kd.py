@@ -9,7 +9,8 @@ calls raise.
 Low-level names mirror the ABI one to one: ``kd_workspace_size``, ``kd_fwd``,
 ``kd_bwd``, ``kd_status_string``, ``kd_device_supported``, ``kd_abi_version``,
 ``kd_diag_gemm_bf16``.  ``forward`` / ``backward`` are conveniences that build
-the structs from keyword arguments and tensors.
+the structs from keyword arguments and tensors, and so are ``token_logprobs`` /
+``token_logprobs_backward`` (kd_logprob_*) and ``clip_grad_norm``.
 """
 from __future__ import annotations
 
@@ -28,6 +29,7 @@ KD_OK, KD_ERR_INVALID_ARG, KD_ERR_UNSUPPORTED, KD_ERR_WORKSPACE = 0, 1, 2, 3
 KD_ERR_BAD_LABEL, KD_ERR_BAD_TOPK, KD_ERR_TIMEOUT, KD_ERR_CUDA, KD_ERR_NO_DEVICE = 4, 5, 6, 7, 8
 KD_DEV_BAD_LABEL, KD_DEV_BAD_TOPK, KD_DEV_TIMEOUT, KD_DEV_BAD_MAP = 0x1, 0x2, 0x4, 0x8
 KD_DEV_MAP_UNSUPPORTED = 0x10
+KD_DEV_NONFINITE = 0x20
 KD_BF16, KD_FP32 = 0, 1
 KD_STUDENT_HIDDEN, KD_STUDENT_LOGITS = 0, 1
 KD_TEACHER_NONE, KD_TEACHER_TIED, KD_TEACHER_SEPARATE, KD_TEACHER_LOGITS, KD_TEACHER_TOPK = range(5)
@@ -72,6 +74,19 @@ class kd_inputs(ctypes.Structure):
                  "topk_p", "token_map")]
 
 
+class kd_logprob_problem(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("d_model", ctypes.c_int64),
+        ("ld_logits", ctypes.c_int64), ("ld_d_logits", ctypes.c_int64),
+        ("ignore_index", ctypes.c_int64), ("topk", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("source", ctypes.c_int32), ("temperature", ctypes.c_float),
+    ]
+
+
+class kd_logprob_inputs(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("logits", "h", "w", "tokens")]
+
+
 class KDError(RuntimeError):
     def __init__(self, status: int, where: str):
         super().__init__(f"{where}: {kd_status_string(status)} (status {status})")
@@ -114,11 +129,20 @@ def load_library(path: str = LIB_PATH):
                                           ctypes.c_int32, ctypes.c_int32, vp, ctypes.c_int32, vp,
                                           vp]
     lib.kd_bwd_grads.argtypes = [P, I, vp, vp, ctypes.c_float, vp, vp, vp, ctypes.c_size_t, vp]
+    L, LI, i32 = ctypes.POINTER(kd_logprob_problem), ctypes.POINTER(kd_logprob_inputs), ctypes.c_int32
+    lib.kd_logprob_workspace_size.argtypes = [L, sz, sz]
+    lib.kd_logprob_fwd.argtypes = [L, LI, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.kd_logprob_bwd.argtypes = [L, LI, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.kd_clip_grad_norm_workspace_size.argtypes = [vp, i32, sz]
+    lib.kd_clip_grad_norm.argtypes = [vp, vp, vp, i32, i32, ctypes.c_float, vp, vp, vp,
+                                      ctypes.c_size_t, vp]
     lib.kd_launch_count.restype = ctypes.c_uint64
     for f in ("kd_workspace_size", "kd_fwd", "kd_bwd", "kd_device_supported", "kd_abi_version",
               "kd_diag_gemm_bf16", "kd_set_profile_events", "kd_set_profile_launch_events",
               "kd_fwd_static_scratch", "kd_project_workspace_size", "kd_project_teacher_logits",
-              "kd_plan_info", "kd_mix_teacher_logits", "kd_bwd_grads"):
+              "kd_plan_info", "kd_mix_teacher_logits", "kd_bwd_grads",
+              "kd_logprob_workspace_size", "kd_logprob_fwd", "kd_logprob_bwd",
+              "kd_clip_grad_norm_workspace_size", "kd_clip_grad_norm"):
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -327,6 +351,8 @@ def check_status(dev_status: torch.Tensor, assume_valid: bool = False):
         raise KDError(KD_ERR_UNSUPPORTED, "token map too skewed for the fused projected teacher")
     if s & KD_DEV_BAD_MAP:
         raise KDError(KD_ERR_INVALID_ARG, "token map entry outside [-1, V_student)")
+    if s & KD_DEV_NONFINITE:
+        raise KDError(KD_ERR_INVALID_ARG, "the gradient norm is infinite or NaN")
     if not assume_valid:
         if s & KD_DEV_BAD_LABEL:
             raise KDError(KD_ERR_BAD_LABEL, "device")
@@ -497,3 +523,219 @@ def mix_teacher_logits(logits, weights=None, mode: str = "arithmetic", out_dtype
     if check and int(dev_status.item()) & KD_DEV_TIMEOUT:
         raise KDError(KD_ERR_TIMEOUT, "a bounded wait timed out")
     return out
+
+
+# ---------------------------------------------------------------- token log-probabilities
+
+KD_LOGPROB_STATS = 4
+KD_LOGPROB_MAX_TOPK = 1024
+SOURCES = {"hidden": KD_STUDENT_HIDDEN, "logits": KD_STUDENT_LOGITS}
+_TORCH_DTYPES = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+@dataclasses.dataclass(frozen=True)
+class LogprobProblem:
+    """Keyword form of ``kd_logprob_problem`` (row pitches come from the tensors)."""
+
+    n_tokens: int
+    vocab: int
+    d_model: int = 0
+    topk: int = 0
+    dtype: str = "bf16"
+    source: str = "logits"
+    temperature: float = 1.0
+    ignore_index: int = -100
+
+    def to_c(self, ld_logits: int = 0, ld_d_logits: int = 0) -> kd_logprob_problem:
+        return kd_logprob_problem(self.n_tokens, self.vocab, self.d_model, ld_logits, ld_d_logits,
+                                  self.ignore_index, self.topk, DTYPES[self.dtype],
+                                  SOURCES[self.source], self.temperature)
+
+
+def kd_logprob_workspace_size(problem: kd_logprob_problem):
+    f, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    st = load_library().kd_logprob_workspace_size(ctypes.byref(problem), ctypes.byref(f),
+                                                  ctypes.byref(b))
+    if st != KD_OK:
+        raise KDError(st, "kd_logprob_workspace_size")
+    return int(f.value), int(b.value)
+
+
+def _rows_pitch(name: str, t: torch.Tensor, shape, dtype, device) -> int:
+    """Row pitch of a [N, V] matrix whose rows are contiguous (0 when it is dense)."""
+    _same(name, t, shape, dtype, device)
+    if t.is_contiguous():
+        return 0
+    if t.stride(1) != 1 or t.stride(0) < shape[1]:
+        raise ValueError(f"{name}: rows must be contiguous and may not overlap")
+    return t.stride(0)
+
+
+def _same(name: str, t: torch.Tensor, shape, dtype, device):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on {device}, "
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+
+
+def _dense(name: str, t: Optional[torch.Tensor], shape, dtype, device):
+    if t is None:
+        return None
+    _same(name, t, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _logprob_inputs(problem: LogprobProblem, tensors: dict):
+    """(kd_logprob_inputs, device, row pitch of the logits) of checked tensors."""
+    dtype = _TORCH_DTYPES[problem.dtype]
+    main = tensors.get("logits" if problem.source == "logits" else "h")
+    if main is None or not main.is_cuda:
+        raise ValueError("logits, or h and w, must be given as CUDA tensors")
+    dev, ld = main.device, 0
+    ins = kd_logprob_inputs()
+    if problem.source == "logits":
+        ld = _rows_pitch("logits", main, (problem.n_tokens, problem.vocab), dtype, dev)
+        ins.logits = main.data_ptr()
+    else:
+        if tensors.get("w") is None:
+            raise ValueError("a hidden source needs the head weight w")
+        ins.h = _dense("h", main, (problem.n_tokens, problem.d_model), dtype, dev)
+        ins.w = _dense("w", tensors["w"], (problem.vocab, problem.d_model), dtype, dev)
+    ins.tokens = _dense("tokens", tensors.get("tokens"), (problem.n_tokens,), torch.int64, dev)
+    return ins, dev, ld
+
+
+def token_logprobs(problem: LogprobProblem, tensors: dict, workspace: Optional[Workspace] = None,
+                   check: bool = True, out: Optional[dict] = None, save_stats: bool = True):
+    """Run kd_logprob_fwd; returns dict(logprob, entropy, topk_idx, topk_logprob,
+    stats, dev_status).
+
+    ``tensors``: ``logits`` [N, V] (rows contiguous, any row pitch), or ``h``
+    [N, D] and ``w`` [V, D]; ``tokens`` int64 [N], or None, with which every
+    row takes part and ``logprob`` is None.  ``topk_idx`` / ``topk_logprob``
+    are None with topk = 0, ``stats`` with save_stats=False (no backward).
+    ``out``: a dict this function returned for the same problem, to be written
+    again.  ``exp(topk_logprob)`` and ``topk_idx`` are a cached top-K teacher of
+    ``Problem(teacher="topk")``."""
+    ins, dev, ld = _logprob_inputs(problem, tensors)
+    n, k, f32 = problem.n_tokens, problem.topk, torch.float32
+    if out is None:
+        out = {
+            "logprob": (torch.empty(n, device=dev, dtype=f32) if ins.tokens is not None else None),
+            "entropy": torch.empty(n, device=dev, dtype=f32),
+            "topk_idx": torch.empty(n, k, device=dev, dtype=torch.int32) if k else None,
+            "topk_logprob": torch.empty(n, k, device=dev, dtype=f32) if k else None,
+            "stats": (torch.empty(n, KD_LOGPROB_STATS, device=dev, dtype=f32)
+                      if save_stats else None),
+            "dev_status": torch.zeros((), device=dev, dtype=torch.int32),
+        }
+    ptrs = [_dense(name, out.get(name), shape, dt, dev) for name, shape, dt in (
+        ("logprob", (n,), f32), ("entropy", (n,), f32), ("topk_idx", (n, k), torch.int32),
+        ("topk_logprob", (n, k), f32), ("stats", (n, KD_LOGPROB_STATS), f32))]
+    cp = problem.to_c(ld)
+    with torch.cuda.device(dev):
+        fb, _ = kd_logprob_workspace_size(cp)
+        wptr, wbytes = (workspace or Workspace()).get(fb, dev) if fb else (None, 0)
+        st = load_library().kd_logprob_fwd(ctypes.byref(cp), ctypes.byref(ins), *ptrs,
+                                           out["dev_status"].data_ptr(), wptr, wbytes,
+                                           _stream(dev))
+    if st != KD_OK:
+        raise KDError(st, "kd_logprob_fwd")
+    if check:
+        check_status(out["dev_status"])
+    return out
+
+
+def token_logprobs_backward(problem: LogprobProblem, tensors: dict, stats: torch.Tensor, *,
+                            d_logprob: Optional[torch.Tensor] = None,
+                            d_entropy: Optional[torch.Tensor] = None, want=("h", "w", "logits"),
+                            workspace: Optional[Workspace] = None, check: bool = True,
+                            out: Optional[dict] = None):
+    """Run kd_logprob_bwd; returns dict of the requested gradients (+ dev_status).
+
+    ``stats`` is token_logprobs' on the same inputs; d_logprob and d_entropy
+    are fp32 [N] (None: zero).  ``out`` may bring the gradients' own buffers,
+    for example d_logits over the logits themselves."""
+    ins, dev, ld = _logprob_inputs(problem, tensors)
+    n, v, d, f32 = problem.n_tokens, problem.vocab, problem.d_model, torch.float32
+    dtype = _TORCH_DTYPES[problem.dtype]
+    if out is None:
+        out = {"dev_status": torch.zeros((), device=dev, dtype=torch.int32)}
+        for name in ("h", "w") if problem.source == "hidden" else ("logits",):
+            if name in want:
+                out["d_" + name] = torch.empty(tensors[name].shape, device=dev, dtype=dtype)
+    ldg, pz = 0, None
+    if out.get("d_logits") is not None:
+        ldg = _rows_pitch("d_logits", out["d_logits"], (n, v), dtype, dev)
+        pz = out["d_logits"].data_ptr()
+    cp = problem.to_c(ld, ldg)
+    with torch.cuda.device(dev):
+        _, bb = kd_logprob_workspace_size(cp)
+        wptr, wbytes = (workspace or Workspace()).get(bb, dev) if bb else (None, 0)
+        st = load_library().kd_logprob_bwd(
+            ctypes.byref(cp), ctypes.byref(ins),
+            _dense("stats", stats, (n, KD_LOGPROB_STATS), f32, dev),
+            _dense("d_logprob", d_logprob, (n,), f32, dev),
+            _dense("d_entropy", d_entropy, (n,), f32, dev),
+            _dense("d_h", out.get("d_h"), (n, d), dtype, dev),
+            _dense("d_w", out.get("d_w"), (v, d), dtype, dev), pz,
+            out["dev_status"].data_ptr(), wptr, wbytes, _stream(dev))
+    if st != KD_OK:
+        raise KDError(st, "kd_logprob_bwd")
+    if check:
+        check_status(out["dev_status"])
+    return out
+
+
+# ---------------------------------------------------------------- gradient clipping
+
+class GradList:
+    """The tensors of kd_clip_grad_norm, checked once for many calls: contiguous
+    CUDA tensors of one dtype and device.  ``out``: tensors of the same shapes
+    for the clipped gradients; None clips in place."""
+
+    def __init__(self, grads, out=None):
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        if not self.grads or len(self.out) != len(self.grads):
+            raise ValueError("one or more gradients, and one out for each")
+        g0 = self.grads[0]
+        names = {dt: name for name, dt in _TORCH_DTYPES.items()}
+        if g0.dtype not in names or not g0.is_cuda:
+            raise ValueError("gradients are CUDA tensors in bf16 or fp32")
+        for g, o in zip(self.grads, self.out):
+            _dense("gradient", g, g.shape, g0.dtype, g0.device)
+            _dense("out", o, g.shape, g0.dtype, g0.device)
+        self.device, self.dtype, n = g0.device, DTYPES[names[g0.dtype]], len(self.grads)
+        self._grads = (ctypes.c_void_p * n)(*[g.data_ptr() for g in self.grads])
+        self._outs = (ctypes.c_void_p * n)(*[o.data_ptr() for o in self.out])
+        self._numel = (ctypes.c_int64 * n)(*[g.numel() for g in self.grads])
+        nbytes = ctypes.c_size_t(0)
+        st = load_library().kd_clip_grad_norm_workspace_size(self._numel, n, ctypes.byref(nbytes))
+        if st != KD_OK:
+            raise KDError(st, "kd_clip_grad_norm_workspace_size")
+        self._bytes = nbytes.value
+
+
+def clip_grad_norm(grads, max_norm: float, *, out=None, workspace: Optional[Workspace] = None,
+                   check: bool = True):
+    """Run kd_clip_grad_norm; returns dict(norm, grads, dev_status).
+
+    ``grads``: a GradList, or the tensors themselves (``out`` as for GradList).
+    The norm is a device scalar; check=True raises when it is infinite or NaN
+    (the gradients are then passed on unscaled)."""
+    gl = grads if isinstance(grads, GradList) else GradList(grads, out)
+    dev = gl.device
+    norm = torch.empty((), device=dev, dtype=torch.float32)
+    status = torch.zeros((), device=dev, dtype=torch.int32)
+    with torch.cuda.device(dev):
+        wptr, wbytes = (workspace or Workspace()).get(gl._bytes, dev)
+        st = load_library().kd_clip_grad_norm(gl._grads, gl._outs, gl._numel, len(gl.grads),
+                                              gl.dtype, float(max_norm), norm.data_ptr(),
+                                              status.data_ptr(), wptr, wbytes, _stream(dev))
+    if st != KD_OK:
+        raise KDError(st, "kd_clip_grad_norm")
+    if check:
+        check_status(status)
+    return {"norm": norm, "grads": gl.out, "dev_status": status}

@@ -1,0 +1,470 @@
+"""Token log-probabilities on the GPU (kd_logprob_*) against the fp64 oracle.
+
+Tolerances, in units of u = 2^-24 (half a step of fp32 near 1), derived from
+the sums the kernels form; none is fitted to a run.  With x = (z - max z) / T:
+  * each exponential has a relative error of at most (4 |x| + 8) u (rounding of
+    z - max z, of the scale, of the product, 2 ulp of ex2); weighted with p the
+    |x| average to at most log V + 1 (the entropy bound), and a sum of V terms
+    over at least 256 accumulators has at most V/256 + 24 further roundings:
+    S, and with it log S, is off by e_S = (V/256 + 32 + 4 (log V + 1)) u.
+  * log p = x - log S: e_S + (2 |x| + 2 |log p| + 4) u.
+  * entropy = log S - t/S: e_S plus e_S relative on t/S <= log V + 1:
+    e_S (log V + 3).
+  * dz = p (c0 + c1 log p): p is off by (4 |x| + 16) u + e_S relative, the
+    bracket by (e_H |g_H| + 8 u (|g_l| + |g_H| (|log p| + H + log V)));
+    plus half a step of the gradient's own type (u for fp32, 2^-8 for bf16),
+    and the smallest fp32 / bf16 normal number (results below are flushed).
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from lm_head_cross_vocab_gb300 import kd
+from oracle import token_oracle as O
+from oracle.kd_oracle import as_f64
+
+pytestmark = pytest.mark.gpu
+
+DT = {"fp32": torch.float32, "bf16": torch.bfloat16}
+HALF = {"fp32": 2.0 ** -24, "bf16": 2.0 ** -8}
+U = 2.0 ** -24
+TINY = 2.0 ** -126
+IGN = -100
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    kd.load_library()
+    assert kd.kd_device_supported(0), "tests need an sm_103 GPU"
+
+
+def _logits(n, v, dtype, seed, std=3.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(n, v, generator=g) * std).to(DT[dtype])
+
+
+def _tokens(n, v, seed, ignore=0.2):
+    g = torch.Generator().manual_seed(seed + 1)
+    y = torch.randint(0, v, (n,), generator=g)
+    y[torch.rand(n, generator=g) < ignore] = IGN
+    return y
+
+
+def _e_s(v):
+    return (v / 256 + 32 + 4 * (math.log(v) + 1)) * U
+
+
+def _spread(z, t):
+    """|z - max z| / T of every finite logit, 0 elsewhere."""
+    z = as_f64(z)
+    with np.errstate(invalid="ignore"):
+        x = np.abs(z - z.max(axis=1, keepdims=True)) / t
+    return np.where(np.isfinite(x), x, 0.0)
+
+
+def _close(got, ref, tol, what):
+    got, ref = np.asarray(got, dtype=np.float64), np.asarray(ref, dtype=np.float64)
+    assert got.shape == ref.shape
+    with np.errstate(over="ignore"):  # beyond fp32: its infinity
+        ref = np.where(np.isinf(ref.astype(np.float32)), np.sign(ref) * math.inf, ref)
+    fin = np.isfinite(ref)
+    assert (np.isnan(got) == np.isnan(ref)).all(), what
+    odd = ~fin & ~np.isnan(ref)
+    assert (got[odd] == ref[odd]).all(), what
+    tol = np.broadcast_to(tol, ref.shape)
+    bad = np.abs(got - ref)[fin] > tol[fin]
+    assert not bad.any(), (what, np.abs(got - ref)[fin][bad].max(), tol[fin][bad].min())
+
+
+def _check_forward(out, z, y, t, k, has_tokens=True):
+    """z: the exact logits [N, V] (any dtype, CPU)."""
+    ref = O.forward(z, None if not has_tokens else y.tolist(), temperature=t, topk=k,
+                    ignore_index=IGN)
+    n, v = z.shape
+    es, x = _e_s(v), _spread(z, t)
+    if has_tokens:
+        yy = y.clamp(0, v - 1).numpy()
+        tol = es + (2 * x[np.arange(n), yy] + 2 * np.nan_to_num(np.abs(ref["logprob"]), posinf=0)
+                    + 4) * U
+        _close(out["logprob"].cpu(), ref["logprob"], tol, "logprob")
+    _close(out["entropy"].cpu(), ref["entropy"], es * (math.log(v) + 3), "entropy")
+    if k:
+        assert (out["topk_idx"].cpu().numpy() == ref["topk_idx"]).all()
+        xt = np.take_along_axis(x, ref["topk_idx"], axis=1)
+        lp = np.nan_to_num(np.abs(ref["topk_logprob"]), posinf=0)
+        _close(out["topk_logprob"].cpu(), ref["topk_logprob"], es + (2 * xt + 2 * lp + 4) * U,
+               "topk_logprob")
+    return ref
+
+
+def _grad_tol(z, y, gl, gh, t, dtype):
+    """(elementwise tolerance, reference) of d_logits."""
+    ref = O.grad_logits(z, None if y is None else y.tolist(),
+                        None if gl is None else gl.tolist(), None if gh is None else gh.tolist(),
+                        temperature=t, ignore_index=IGN)
+    n, v = z.shape
+    zz = as_f64(z)
+    zero = np.zeros(n)
+    a_l = np.abs(zero if gl is None else gl.double().numpy())[:, None]
+    a_h = np.abs(zero if gh is None else gh.double().numpy())[:, None]
+    es, x = _e_s(v), _spread(z, t)
+    with np.errstate(invalid="ignore", divide="ignore"):
+        a = zz / t
+        lp = a - a.max(axis=1, keepdims=True)
+        lp = lp - np.log(np.exp(lp).sum(axis=1, keepdims=True))
+        p = np.nan_to_num(np.exp(lp))
+        lp = np.where(p > 0, np.abs(lp), 0.0)
+    lv = math.log(v) + 1
+    bracket = a_l + a_h * (lp + lv)
+    tol = p * (((4 * x + 16) * U + es) * bracket + a_h * es * (lv + 2) + 8 * U * bracket) / t
+    return tol + HALF[dtype] * (np.abs(ref) + tol) + 4 * U * a_l / t + TINY, ref
+
+
+def _run(z, y, t, k, dtype, **kw):
+    n, v = z.shape
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, topk=k, dtype=dtype, temperature=t)
+    tens = {"logits": z.cuda(), "tokens": None if y is None else y.cuda()}
+    return p, tens, kd.token_logprobs(p, tens, **kw)
+
+
+# sizes around the vectors, warps and blocks of the kernels; K from none to all
+SHAPES = [(1, 1, 1), (3, 1, 0), (5, 7, 7), (4, 31, 5), (2, 256, 256), (7, 257, 20), (3, 1000, 1000),
+          (2, 2047, 1024), (33, 4099, 3), (1, 5000, 100), (6, 32003, 64), (2, 40961, 1024),
+          (1, 151936, 20), (1, 151937, 1000), (300, 1024, 8), (700, 9000, 1), (2, 600011, 30)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,v,k", SHAPES)
+def test_logits_forward_and_backward(n, v, k, dtype):
+    t = (1.0, 0.7, 2.0)[(n + v) % 3]
+    z, y = _logits(n, v, dtype, n + v), _tokens(n, v, n + v)
+    p, tens, out = _run(z, y, t, k, dtype)
+    if n * v <= 4_000_000:
+        _check_forward(out, z, y, t, k)
+    g = torch.Generator().manual_seed(v)
+    gl, gh = torch.randn(n, generator=g), torch.randn(n, generator=g) * 0.3
+    r = kd.token_logprobs_backward(p, tens, out["stats"], d_logprob=gl.cuda(), d_entropy=gh.cuda())
+    if n * v <= 4_000_000:
+        tol, ref = _grad_tol(z, y, gl, gh, t, dtype)
+        _close(r["d_logits"].float().cpu(), ref, tol, "d_logits")
+        assert (r["d_logits"][(y == IGN).cuda()] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_without_tokens_and_single_upstreams(dtype):
+    z, y = _logits(9, 3001, dtype, 3), _tokens(9, 3001, 3)
+    p, tens, out = _run(z, None, 1.0, 6, dtype)
+    assert out["logprob"] is None
+    _check_forward(out, z, y, 1.0, 6, has_tokens=False)
+    gh = torch.linspace(-1, 1, 9)
+    r = kd.token_logprobs_backward(p, tens, out["stats"], d_entropy=gh.cuda())
+    tol, ref = _grad_tol(z, None, None, gh, 1.0, dtype)
+    _close(r["d_logits"].float().cpu(), ref, tol, "entropy alone")
+    p, tens, out = _run(z, y, 1.0, 0, dtype)
+    r = kd.token_logprobs_backward(p, tens, out["stats"], d_logprob=gh.cuda())
+    tol, ref = _grad_tol(z, y, gh, None, 1.0, dtype)
+    _close(r["d_logits"].float().cpu(), ref, tol, "logprob alone")
+    r = kd.token_logprobs_backward(p, tens, out["stats"])
+    assert (r["d_logits"] == 0).all()
+
+
+def _special_rows(v, dtype):
+    """Rows where a selection or a running maximum goes wrong."""
+    inf, lo = math.inf, torch.finfo(DT[dtype]).min
+    up = torch.linspace(-20, 20, v)
+    rows = [torch.zeros(v), up, up.flip(0), torch.full((v,), lo), torch.full((v,), -inf),
+            torch.full((v,), 5.0), -up.abs(), torch.where(torch.arange(v) % 2 == 0, up, -up)]
+    few = torch.full((v,), -inf)
+    few[v // 2], few[v - 1], few[0] = 1.0, 3.0, -2.0
+    rows.append(few)
+    few = torch.full((v,), lo)
+    few[v // 3] = 2.0
+    rows.append(few)
+    neg = torch.zeros(v)
+    neg[::3] = -0.0
+    rows.append(neg)
+    big = torch.randn(v, generator=torch.Generator().manual_seed(1)) * 1e4
+    rows += [big, big * 1e30, torch.cat([torch.full((v - 1,), lo), torch.full((1,), -lo)])]
+    nan = up.clone()
+    nan[v // 4] = math.nan
+    pinf = up.clone()
+    pinf[v // 5] = inf
+    one = torch.full((v,), -inf)
+    one[v // 7] = math.nan
+    rows += [nan, pinf, one, torch.full((v,), math.nan)]
+    return torch.stack(rows).to(DT[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("v,k", [(64, 64), (1000, 5), (1000, 257), (9001, 1024), (9000, 20)])
+@pytest.mark.parametrize("t", [1.0, 0.5])
+def test_special_rows(v, k, dtype, t):
+    z = _special_rows(v, dtype)
+    n = len(z)
+    y = torch.arange(n) * 37 % v
+    p, tens, out = _run(z, y, t, k, dtype)
+    _check_forward(out, z, y, t, k)
+    fine = [r for r in range(n) if not (torch.isnan(z[r]).any() or (z[r] == math.inf).any())]
+    gl, gh = torch.linspace(-1, 1, n), torch.linspace(0.3, -0.4, n)
+    r = kd.token_logprobs_backward(p, tens, out["stats"], d_logprob=gl.cuda(), d_entropy=gh.cuda())
+    tol, ref = _grad_tol(z[fine], y[fine], gl[fine], gh[fine], t, dtype)
+    _close(r["d_logits"][fine].float().cpu(), ref, tol, "d_logits")
+    # the same rows ignored: exact zeros, whatever they hold
+    y[:] = IGN
+    p, tens, out = _run(z, y, t, k, dtype)
+    assert (out["logprob"] == 0).all() and (out["entropy"] == 0).all()
+    assert (out["topk_idx"].cpu() == torch.arange(k).expand(n, k)).all()
+    assert (out["topk_logprob"] == -math.inf).all()
+    r = kd.token_logprobs_backward(p, tens, out["stats"], d_logprob=gl.cuda() * math.nan,
+                                   d_entropy=gh.cuda())
+    assert (r["d_logits"] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("v,pitch,shift", [(1000, 1000, 1), (1000, 1003, 0), (1001, 1016, 3),
+                                           (4096, 4104, 8), (32003, 32100, 5)])
+def test_pitches_and_unaligned_rows(v, pitch, shift, dtype):
+    n = 5
+    store = _logits(1, n * pitch + shift, dtype, v).reshape(-1).cuda()
+    z = store[shift:shift + n * pitch].view(n, pitch)[:, :v]
+    y = _tokens(n, v, v)
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, topk=9, dtype=dtype)
+    tens = {"logits": z, "tokens": y.cuda()}
+    out = kd.token_logprobs(p, tens)
+    _check_forward(out, z.cpu(), y, 1.0, 9)
+    gl = torch.linspace(-1, 1, n)
+    grad = torch.full_like(store, 7.0)
+    dz = grad[shift:shift + n * pitch].view(n, pitch)[:, :v]
+    kd.token_logprobs_backward(p, tens, out["stats"], d_logprob=gl.cuda(),
+                               out={"d_logits": dz, "dev_status": out["dev_status"]})
+    tol, ref = _grad_tol(z.cpu(), y, gl, None, 1.0, dtype)
+    _close(dz.float().cpu(), ref, tol, "d_logits")
+    between = torch.ones_like(grad, dtype=torch.bool)
+    between[shift:shift + n * pitch].view(n, pitch)[:, :v] = False
+    assert (grad[between] == 7.0).all()
+    # into the logits' own memory, and into a dense tensor
+    dense = kd.token_logprobs_backward(p, tens, out["stats"], d_logprob=gl.cuda())["d_logits"]
+    assert torch.equal(dense, dz)
+    kd.token_logprobs_backward(p, tens, out["stats"], d_logprob=gl.cuda(),
+                               out={"d_logits": z, "dev_status": out["dev_status"]})
+    assert torch.equal(z, dz)
+
+
+def test_bad_tokens_are_reported():
+    z, y = _logits(4, 100, "fp32", 1), torch.tensor([3, 100, -1, 99])
+    with pytest.raises(kd.KDError) as e:
+        _run(z, y, 1.0, 2, "fp32")
+    assert e.value.status == kd.KD_ERR_BAD_LABEL
+    p, tens, out = _run(z, y, 1.0, 2, "fp32", check=False)
+    _check_forward(out, z, y, 1.0, 2)
+    assert int(out["dev_status"].item()) == kd.KD_DEV_BAD_LABEL
+    gl = torch.ones(4)
+    r = kd.token_logprobs_backward(p, tens, out["stats"], d_logprob=gl.cuda(), check=False)
+    tol, ref = _grad_tol(z, y, gl, None, 1.0, "fp32")
+    _close(r["d_logits"].cpu(), ref, tol, "d_logits")
+    assert int(r["dev_status"].item()) == kd.KD_DEV_BAD_LABEL
+
+
+def test_no_tokens_no_rows():
+    for kw in (dict(source="logits"), dict(source="hidden", d_model=64)):
+        p = kd.LogprobProblem(n_tokens=0, vocab=300, topk=3, **kw)
+        bf = torch.bfloat16
+        tens = {"logits": torch.empty(0, 300, dtype=bf, device="cuda"),
+                "h": torch.empty(0, 64, dtype=bf, device="cuda"),
+                "w": torch.ones(300, 64, dtype=bf, device="cuda"),
+                "tokens": torch.empty(0, dtype=torch.int64, device="cuda")}
+        out = kd.token_logprobs(p, tens)
+        assert out["topk_idx"].shape == (0, 3)
+        r = kd.token_logprobs_backward(p, tens, out["stats"])
+        if kw["source"] == "hidden":
+            assert (r["d_w"] == 0).all()
+
+
+# ------------------------------------------------------------------ hidden states
+
+def _hidden(n, v, d, dtype, seed, grid=True):
+    """On the grid every logit is an exact sum (products of multiples of 2^-4
+    and 2^-10, fewer than 2^24 units in all), so the logits are known exactly."""
+    g = torch.Generator().manual_seed(seed)
+    h, w = torch.randn(n, d, generator=g), torch.randn(v, d, generator=g) * 0.05
+    if grid:
+        h = (h * 16).round().clamp(-64, 64) / 16
+        w = (w * 1024).round().clamp(-255, 255) / 1024
+    return h.to(DT[dtype]), w.to(DT[dtype])
+
+
+def _exact(h, w):
+    return h.double() @ w.double().t()
+
+
+HIDDEN = [(1, 1, 8, 1), (1, 700, 64, 7), (5, 33, 8, 33), (3, 257, 72, 20), (70, 1000, 136, 5),
+          (130, 2049, 64, 100), (257, 5003, 200, 33), (300, 513, 520, 0), (17, 6000, 1032, 1024),
+          (1, 9001, 4096, 300), (1000, 3001, 256, 1)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,v,d,k", HIDDEN)
+def test_hidden_forward(n, v, d, k, dtype):
+    t = (1.0, 0.7)[v % 2]
+    h, w = _hidden(n, v, d, dtype, n + v)
+    y = _tokens(n, v, n + v)
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, d_model=d, topk=k, dtype=dtype, source="hidden",
+                          temperature=t)
+    tens = {"h": h.cuda(), "w": w.cuda(), "tokens": y.cuda()}
+    out = kd.token_logprobs(p, tens)
+    _check_forward(out, _exact(h, w), y, t, k)
+    # the same logits, materialised in fp32 (exact), give the same alternatives
+    q = kd.LogprobProblem(n_tokens=n, vocab=v, topk=k, dtype="fp32", temperature=t)
+    ref = kd.token_logprobs(q, {"logits": _exact(h, w).float().cuda(), "tokens": y.cuda()})
+    if k:
+        assert torch.equal(out["topk_idx"], ref["topk_idx"])
+    es = _e_s(v)
+    assert torch.allclose(out["entropy"], ref["entropy"], rtol=0, atol=2 * es * (math.log(v) + 3))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,v,d", [(1, 700, 64), (3, 257, 72), (130, 2049, 64), (257, 5003, 200),
+                                   (300, 513, 520), (600, 700, 136)])
+def test_hidden_backward(n, v, d, dtype):
+    """d_h = G W and d_w = G^T H: |error| is at most the product of the matrices
+    of absolute values with G's own error (its tolerance: half a step of its
+    type, which is bf16 for bf16 problems), K roundings of the fp32 sum, and
+    half a step of the result."""
+    t = (1.0, 0.7)[v % 2]
+    h, w = _hidden(n, v, d, dtype, n + v)
+    y = _tokens(n, v, n + v)
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, d_model=d, dtype=dtype, source="hidden",
+                          temperature=t)
+    bad = h.clone()
+    bad[y == IGN] = math.nan  # rows that take no part may hold anything
+    tens = {"h": bad.cuda(), "w": w.cuda(), "tokens": y.cuda()}
+    out = kd.token_logprobs(p, tens)
+    z = _exact(h, w)
+    _check_forward(out, z, y, t, 0)
+    g = torch.Generator().manual_seed(v)
+    gl, gh = torch.randn(n, generator=g), torch.randn(n, generator=g) * 0.3
+    r = kd.token_logprobs_backward(p, tens, out["stats"], d_logprob=gl.cuda(), d_entropy=gh.cuda())
+    g_tol, g_ref = _grad_tol(z, y, gl, gh, t, dtype)
+    hh, ww = as_f64(h), as_f64(w)
+    for name, a, at, b in (("d_h", g_ref, g_tol, ww), ("d_w", g_ref.T, g_tol.T, hh)):
+        ref = a @ b
+        mass = (np.abs(a) + at) @ np.abs(b)
+        # twice u: the tensor cores may cut a sum off instead of rounding it
+        tol = at @ np.abs(b) + 2 * U * a.shape[1] * mass
+        tol = tol + HALF[dtype] * (np.abs(ref) + tol) + TINY
+        _close(r[name].float().cpu(), ref, tol, name)
+    assert (r["d_h"][(y == IGN).cuda()] == 0).all()
+    one = kd.token_logprobs_backward(p, tens, out["stats"], d_logprob=gl.cuda(),
+                                     d_entropy=gh.cuda(), want=("w",))
+    assert "d_h" not in one and torch.equal(one["d_w"], r["d_w"])
+
+
+def test_gradients_by_differences():
+    """The fp32 backward against central differences of the fp64 definition."""
+    n, v, d = 3, 40, 8
+    h, w = _hidden(n, v, d, "fp32", 11, grid=False)
+    y = torch.tensor([5, IGN, 39])
+    gl, gh = torch.tensor([0.7, 0.2, -1.1]), torch.tensor([-0.4, 0.3, 0.6])
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, d_model=d, dtype="fp32", source="hidden",
+                          temperature=0.8)
+    tens = {"h": h.cuda(), "w": w.cuda(), "tokens": y.cuda()}
+    out = kd.token_logprobs(p, tens)
+    r = kd.token_logprobs_backward(p, tens, out["stats"], d_logprob=gl.cuda(), d_entropy=gh.cuda())
+
+    def f(hh, ww):
+        o = O.forward(hh @ ww.T, y.tolist(), temperature=0.8, ignore_index=IGN)
+        return float(gl.double().numpy() @ o["logprob"] + gh.double().numpy() @ o["entropy"])
+
+    hh, ww = as_f64(h), as_f64(w)
+    for name, x in (("d_h", hh), ("d_w", ww)):
+        num = np.zeros_like(x)
+        for i in np.ndindex(x.shape):
+            old = x[i]
+            x[i] = old + 1e-4
+            up = f(hh, ww)
+            x[i] = old - 1e-4
+            num[i] = (up - f(hh, ww)) / 2e-4
+            x[i] = old
+        # truncation 1e-8 |f'''| and fp32 sums: both well below 1e-5 here
+        assert np.abs(r[name].cpu().double().numpy() - num).max() <= 1e-5
+
+
+# ------------------------------------------------------------------ use
+
+def test_streams_and_graphs():
+    """On a side stream, and captured twice with a workspace of its own each;
+    replays follow the inputs."""
+    n, v, d = 40, 3000, 128
+    h, w = (x.cuda() for x in _hidden(n, v, d, "bf16", 5))
+    y = _tokens(n, v, 5).cuda()
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, d_model=d, topk=12, source="hidden")
+    tens = {"h": h, "w": w, "tokens": y}
+    gl = torch.linspace(-1, 1, n, device="cuda")
+
+    def call(ws, o, g):
+        o = kd.token_logprobs(p, tens, workspace=ws, check=False, out=o)
+        return o, kd.token_logprobs_backward(p, tens, o["stats"], d_logprob=gl, workspace=ws,
+                                             check=False, out=g)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        o1, g1 = call(kd.Workspace(), None, None)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        ws, o, g = kd.Workspace(), None, None
+        with torch.cuda.stream(s):
+            o, g = call(ws, o, g)
+        torch.cuda.synchronize()
+        cg = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(cg, stream=s):
+            call(ws, o, g)
+        graphs.append((cg, o, g))
+    h.copy_(h.flip(0))
+    y.copy_(y.flip(0))
+    o2, g2 = call(kd.Workspace(), None, None)
+    for cg, o, g in graphs:
+        cg.replay()
+        torch.cuda.synchronize()
+        for key in ("logprob", "entropy", "topk_idx", "topk_logprob", "stats"):
+            assert torch.equal(o[key], o2[key]), key
+        assert torch.equal(g["d_h"], g2["d_h"]) and torch.equal(g["d_w"], g2["d_w"])
+    assert torch.equal(o2["logprob"], o1["logprob"].flip(0))
+
+
+def test_cache_teacher_then_distil_then_clip():
+    """The run of calls a distillation program makes: a teacher's hidden states
+    to a top-K cache, the cache to the sparse loss and its gradients, and the
+    gradients clipped."""
+    from oracle import kd_oracle as KO
+    n, v, d, k = 96, 1500, 64, 16
+    ht, wt = _hidden(n, v, 128, "bf16", 1)
+    hs, ws = _hidden(n, v, d, "bf16", 2, grid=False)
+    y = _tokens(n, v, 1)
+    cache = kd.token_logprobs(
+        kd.LogprobProblem(n_tokens=n, vocab=v, d_model=128, topk=k, source="hidden"),
+        {"h": ht.cuda(), "w": wt.cuda(), "tokens": y.cuda()}, save_stats=False)
+    assert cache["stats"] is None
+    t = {"h_s": hs.cuda(), "w_s": ws.cuda(), "labels": y.cuda(), "topk_idx": cache["topk_idx"],
+         "topk_p": cache["topk_logprob"].exp()}
+    prob = kd.Problem(n_tokens=n, vocab=v, d_student=d, topk=k, teacher="topk", w_student_ce=0.0)
+    fwd = kd.forward(prob, t)
+    g = kd.backward(prob, t, fwd["stats"], want=("h_s", "w_s"))
+    r = kd.clip_grad_norm([g["d_h_s"], g["d_w_s"]], 0.01)
+    ref = O.forward(_exact(ht, wt), y.tolist(), topk=k, ignore_index=IGN)
+    kw = dict(topk_idx=ref["topk_idx"], topk_p=np.exp(ref["topk_logprob"]), w_student_ce=0.0,
+              ignore_index=IGN)
+    zs = KO.project(hs, ws)
+    loss = KO.forward(zs, None, y.numpy(), **kw)["loss"]
+    assert abs(fwd["loss"].item() - loss) <= 2e-3 * abs(loss)
+    gs, _ = KO.grad_logits(zs, None, y.numpy(), **kw)
+    dh, dw = KO.hidden_grads(hs, ws, gs)
+    norm, out = O.clip([dh, dw], 0.01)
+    assert norm > 0.01 and abs(r["norm"].item() - norm) <= 1e-2 * norm
+    for got, want in zip(r["grads"], out):
+        err = np.linalg.norm(as_f64(got) - want) / np.linalg.norm(want)
+        assert err <= 2e-2  # 1e-2 of the gradients (the loss's own bound), 1e-2 of the norm

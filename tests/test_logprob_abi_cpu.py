@@ -1,0 +1,167 @@
+"""Host-side rules of kd_logprob_* and kd_clip_grad_norm: struct layout, refused
+arguments, workspace sizes.  No kernel is launched on this machine, and the GPU
+is never reached by a refused call."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE = 1 << 20  # a pointer that is never followed
+
+
+@pytest.fixture(scope="module")
+def kd():
+    from lm_head_cross_vocab_gb300 import build, kd as K
+    build.build()
+    K.load_library()
+    return K
+
+
+@pytest.mark.parametrize("name", ["kd_logprob_problem", "kd_logprob_inputs"])
+def test_struct_layout_matches_c(kd, tmp_path, name):
+    struct = getattr(kd, name)
+    fields = [f for f, _ in struct._fields_]
+    prog = ["#include <stdio.h>", "#include <stddef.h>", '#include "kd.h"', "int main(void){",
+            f'printf("%zu\\n", sizeof({name}));']
+    prog += [f'printf("%zu\\n", offsetof({name}, {f}));' for f in fields] + ["return 0;}"]
+    c, exe = tmp_path / "probe.c", tmp_path / "probe"
+    c.write_text("\n".join(prog))
+    subprocess.run(["gcc", "-std=c99", "-I", os.path.join(ROOT, "include"), str(c), "-o",
+                    str(exe)], check=True)
+    vals = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True,
+                                           check=True).stdout.split()]
+    assert vals[0] == ctypes.sizeof(struct)
+    assert vals[1:] == [getattr(struct, f).offset for f in fields]
+
+
+def _prob(kd, ld=0, ldg=0, **kw):
+    base = dict(n_tokens=8, vocab=100, d_model=64, topk=4, dtype="bf16", source="logits")
+    base.update(kw)
+    return kd.LogprobProblem(**base).to_c(ld, ldg)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(n_tokens=-1), dict(n_tokens=1 << 31), dict(vocab=0), dict(vocab=(1 << 30) + 1),
+    dict(temperature=0.0), dict(temperature=-1.0), dict(temperature=float("nan")),
+    dict(temperature=float("inf")), dict(temperature=1e-45), dict(topk=-1), dict(topk=101),
+    dict(topk=1025, vocab=5000), dict(ld=99), dict(ldg=99), dict(source="hidden", d_model=0),
+])
+def test_bad_problems_are_refused(kd, bad):
+    p = _prob(kd, **bad)
+    f, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    st = kd.load_library().kd_logprob_workspace_size(ctypes.byref(p), ctypes.byref(f),
+                                                     ctypes.byref(b))
+    assert st == kd.KD_ERR_INVALID_ARG
+
+
+def test_unknown_types_and_null_problem(kd):
+    lib = kd.load_library()
+    assert lib.kd_logprob_workspace_size(None, None, None) == kd.KD_ERR_INVALID_ARG
+    for field in ("dtype", "source"):
+        p = _prob(kd)
+        setattr(p, field, 7)
+        assert lib.kd_logprob_workspace_size(ctypes.byref(p), None, None) == kd.KD_ERR_INVALID_ARG
+    # a bf16 head is read by TMA: rows of a multiple of 16 bytes
+    p = _prob(kd, source="hidden", d_model=60)
+    assert lib.kd_logprob_workspace_size(ctypes.byref(p), None, None) == kd.KD_ERR_UNSUPPORTED
+    p = _prob(kd, source="hidden", d_model=60, dtype="fp32")
+    assert lib.kd_logprob_workspace_size(ctypes.byref(p), None, None) == kd.KD_OK
+
+
+def _fwd(kd, p, ins, **out):
+    o = {k: out.get(k) for k in ("logprob", "entropy", "topk_idx", "topk_logprob", "stats")}
+    return kd.load_library().kd_logprob_fwd(ctypes.byref(p), ctypes.byref(ins), *o.values(), None,
+                                            out.get("ws"), out.get("bytes", 0), None)
+
+
+def test_forward_argument_rules(kd):
+    logits = kd.kd_logprob_inputs(logits=FAKE, tokens=FAKE)
+    assert _fwd(kd, _prob(kd), kd.kd_logprob_inputs(), entropy=FAKE) == kd.KD_ERR_INVALID_ARG
+    assert _fwd(kd, _prob(kd), kd.kd_logprob_inputs(logits=FAKE), logprob=FAKE) \
+        == kd.KD_ERR_INVALID_ARG  # a log-probability of which token
+    assert _fwd(kd, _prob(kd), logits, stats=FAKE + 4) == kd.KD_ERR_INVALID_ARG
+    hidden = _prob(kd, source="hidden")
+    assert _fwd(kd, hidden, logits, entropy=FAKE) == kd.KD_ERR_INVALID_ARG
+    odd = kd.kd_logprob_inputs(h=FAKE + 8, w=FAKE)
+    assert _fwd(kd, hidden, odd, entropy=FAKE) == kd.KD_ERR_UNSUPPORTED
+    ok = kd.kd_logprob_inputs(h=FAKE, w=FAKE)
+    assert _fwd(kd, hidden, ok, entropy=FAKE) == kd.KD_ERR_WORKSPACE
+    f, _ = kd.kd_logprob_workspace_size(hidden)
+    assert _fwd(kd, hidden, ok, entropy=FAKE, ws=FAKE + 16, bytes=f) == kd.KD_ERR_WORKSPACE
+    assert _fwd(kd, hidden, ok, entropy=FAKE, ws=FAKE, bytes=f - 1) == kd.KD_ERR_WORKSPACE
+
+
+def test_backward_argument_rules(kd):
+    lib = kd.load_library()
+
+    def bwd(p, ins, stats=FAKE, dlp=None, dh=None, dw=None, dz=None, ws=None, nbytes=0):
+        return lib.kd_logprob_bwd(ctypes.byref(p), ctypes.byref(ins), stats, dlp, None, dh, dw,
+                                  dz, None, ws, nbytes, None)
+
+    logits = kd.kd_logprob_inputs(logits=FAKE)
+    hidden = kd.kd_logprob_inputs(h=FAKE, w=FAKE, tokens=FAKE)
+    assert bwd(_prob(kd), logits, dh=FAKE) == kd.KD_ERR_INVALID_ARG
+    assert bwd(_prob(kd), logits, stats=None, dz=FAKE) == kd.KD_ERR_INVALID_ARG
+    assert bwd(_prob(kd), logits, dlp=FAKE, dz=FAKE) == kd.KD_ERR_INVALID_ARG  # no tokens
+    assert bwd(_prob(kd, source="hidden"), hidden, dz=FAKE) == kd.KD_ERR_INVALID_ARG
+    assert bwd(_prob(kd, source="hidden"), hidden, dw=FAKE) == kd.KD_ERR_WORKSPACE
+
+
+def test_no_scratch_buffer_spans_tokens_by_vocab(kd):
+    """Large hidden problems: neither pass holds the logits, nor half of them in bf16."""
+    for n, v, d in ((4096, 32000, 2048), (32768, 151936, 4096)):
+        f, b = kd.kd_logprob_workspace_size(_prob(kd, n_tokens=n, vocab=v, d_model=d, topk=100,
+                                                  source="hidden"))
+        assert f < n * v * 2
+        assert b - 4 * (n + v) * d - 2 * n * d < n * v * 2
+
+
+def _clip(kd, grads, outs, numel, n=None, dtype=None, max_norm=1.0, ws=FAKE, nbytes=1 << 20):
+    arr = (ctypes.c_void_p * max(1, len(grads)))(*grads)
+    oarr = None if outs is None else (ctypes.c_void_p * max(1, len(outs)))(*outs)
+    cnt = (ctypes.c_int64 * max(1, len(numel)))(*numel)
+    return kd.load_library().kd_clip_grad_norm(
+        arr, oarr, cnt, len(numel) if n is None else n, kd.KD_BF16 if dtype is None else dtype,
+        ctypes.c_float(max_norm), None, None, ws, nbytes, None)
+
+
+def test_clip_argument_rules(kd):
+    import torch
+    a, b = FAKE, 2 * FAKE
+    bad = [dict(n=-1), dict(dtype=5), dict(max_norm=-1.0), dict(max_norm=float("nan")),
+           dict(max_norm=float("inf"))]
+    for kw in bad:
+        assert _clip(kd, [a, b], [a, b], [10, 10], **kw) == kd.KD_ERR_INVALID_ARG, kw
+    refused = [
+        ([a, None], [a, b], [10, 10]), ([a, b], [a, None], [10, 10]), ([a, b], [a, b], [10, -1]),
+        ([a + 1, b], [a + 1, b], [10, 10]),            # odd address of a bf16 tensor
+        ([a, a], [a, a], [10, 10]),                     # the same tensor twice
+        ([a, b], [a, a + 18], [10, 10]),                # an out inside another tensor
+        ([a, b], [a + 2, b], [10, 10]),                 # an out that overlaps its own gradient
+        ([a, b], [4 * FAKE, 4 * FAKE + 19], [10, 10]),  # two outs one element apart
+    ]
+    for g, o, cnt in refused:
+        assert _clip(kd, g, o, cnt) == kd.KD_ERR_INVALID_ARG, (g, o, cnt)
+    for kw in (dict(ws=None), dict(ws=FAKE + 8), dict(nbytes=0)):
+        assert _clip(kd, [a], [a], [10], **kw) == kd.KD_ERR_WORKSPACE, kw
+    if torch.cuda.is_available():
+        return  # well-formed calls would launch
+    for g, o, cnt in (([a, b], [a, b], [10, 10]), ([a, b], None, [10, 10]),
+                      ([a, a], None, [10, 10]), ([None, b], [None, b], [0, 10]),
+                      ([a, b], [a + 20, b + 20], [10, 10])):
+        assert _clip(kd, g, o, cnt) == kd.KD_ERR_NO_DEVICE, (g, o, cnt)
+
+
+def test_binding_refuses_wrong_tensors(kd):
+    import torch
+    p = kd.LogprobProblem(n_tokens=2, vocab=8)
+    with pytest.raises(ValueError):
+        kd.token_logprobs(p, {"logits": torch.zeros(2, 8, dtype=torch.bfloat16)})
+    with pytest.raises(ValueError):
+        kd.token_logprobs(p, {})
+    with pytest.raises(ValueError):
+        kd.GradList([])
+    with pytest.raises(ValueError):
+        kd.GradList([torch.zeros(3)])
