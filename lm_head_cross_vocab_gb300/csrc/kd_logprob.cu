@@ -8,6 +8,7 @@
 //   log S = ln s,  entropy = ln s - ln2 t / s,  log p_v = (z_v - m) / T - ln s.
 // Nothing is taken as a difference of two large log-sum-exps, so rows of very
 // large or very negative logits keep their absolute accuracy.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -18,6 +19,8 @@
 #include <cstring>
 
 #include "kd_internal.h"
+
+namespace cg = cooperative_groups;
 
 namespace kd {
 namespace {
@@ -62,7 +65,6 @@ __device__ __forceinline__ uint64_t cand_word(uint32_t key, uint32_t id) {
 struct LpState {
   float m, s, t;
 };
-__device__ __forceinline__ LpState lp_empty() { return {neg_inf(), 0.f, 0.f}; }
 // 2^((z - m) k) and its exponent, for z <= m (NaN kept)
 __device__ __forceinline__ float lp_x(float z, float m, float k) {
   return max_nan((z - m) * k, kXMin);
@@ -81,13 +83,6 @@ __device__ __forceinline__ void lp_merge(LpState& a, LpState b, float k) {
   lp_raise(b, m, k);
   a.s += b.s;
   a.t += b.t;
-}
-__device__ __forceinline__ void lp_add(LpState& a, float z, float k) {
-  if (z > a.m) lp_raise(a, z, k);
-  if (z == neg_inf()) return;
-  const float x = lp_x(z, a.m, k), e = ex2(x);
-  a.s += e;
-  a.t = fmaf(e, x, a.t);
 }
 __device__ __forceinline__ LpState lp_shfl_xor(const LpState& a, int o) {
   return {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
@@ -153,20 +148,176 @@ __device__ __forceinline__ void lp_store_ignored(const LpArgs& a, int64_t r) {
   }
 }
 
-// ------------------------------------------------------------------ selection
-struct SelectShared {
-  uint64_t cand[kMaxTopk];
-  uint32_t hist[256];
-  uint32_t prefix, want, count;
-  uint32_t warp_ties[32];
+// ------------------------------------------------------------------ rows
+// One block of NT threads takes a row, or, when there are too few rows to fill
+// the device, a cluster of blocks takes it in slices that are joined through
+// distributed shared memory.  A slice is read once in 16-byte vectors, four in
+// flight per thread beside the four being folded into (offset, s, t); the
+// offset trails the running maximum by up to 2^8, so that most vectors need no
+// rescale.  What the K best cost on top: each thread keeps the maximum of every
+// slot (a run of its vectors, at most kSlots of them); the K-th largest of the
+// slot maxima bounds the K-th largest logit from below, so only the vectors of
+// the few slots above it are read again (from L2), and what lies above the
+// bound in them, little more than K ids, is sorted.
+constexpr int kSlots = 8;
+constexpr int kUnroll = 4;
+constexpr float kRaise = 8.f;  // exponent the offset may trail by
+
+struct Words {
+  uint32_t w[4];
+};
+__device__ __forceinline__ Words load16(const void* p) {
+  Words v;
+  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3])
+               : "l"(p));
+  return v;
+}
+// A vector of the row: elements, and -inf in each.
+template <class T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  static constexpr uint32_t kNone = 0xff800000u;
+  static __device__ __forceinline__ void get(const Words& v, float* f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v.w[i]);
+  }
+  static __device__ __forceinline__ float top(const Words& v) {
+    return max_nan(max_nan(__uint_as_float(v.w[0]), __uint_as_float(v.w[1])),
+                   max_nan(__uint_as_float(v.w[2]), __uint_as_float(v.w[3])));
+  }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static constexpr uint32_t kNone = kNegInfX2;
+  static __device__ __forceinline__ void get(const Words& v, float* f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16lo(v.w[i]);
+      f[2 * i + 1] = bf16hi(v.w[i]);
+    }
+  }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  static __device__ __forceinline__ float top(const Words& v) {
+    const uint32_t m = max2(max2(v.w[0], v.w[1]), max2(v.w[2], v.w[3]));
+    return max_nan(bf16lo(m), bf16hi(m));
+  }
 };
 
-// The K best of a row by radix selection on the order keys: eight bits a
-// sweep, then one sweep that collects what lies above the K-th key and the
-// lowest ids among those equal to it.  Exact for any row.
+// The part of a row one block takes: `nvec` vectors from the 16-byte boundary
+// `head` elements into the row (those of all blocks of the cluster together
+// cover the row's vectors); block 0 takes the `loose` elements before and
+// behind the vectors as well.
 template <class T>
-__device__ void select_exact(const T* z, int64_t v, int k, SelectShared& sh) {
+struct Slice {
+  const T* z;
+  int64_t v0;           // first vector
+  int nvec, rounds;     // vectors; per thread
+  int head, loose;
+  int64_t tail0;        // first element behind the vectors
+  int64_t base;         // element index of vector 0 of the slice
+
+  __device__ __forceinline__ Slice(const T* row, int64_t vocab, int rank, int blocks, int nt) {
+    constexpr int N = Vec<T>::N;
+    z = row;
+    const int off = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+    head = off ? N - off : 0;
+    if (head > vocab) head = (int)vocab;
+    const int64_t all = (vocab - head) / N;
+    v0 = all * rank / blocks;
+    nvec = (int)(all * (rank + 1) / blocks - v0);
+    rounds = (nvec + nt - 1) / nt;
+    tail0 = head + all * N;
+    loose = rank == 0 ? head + (int)(vocab - tail0) : 0;
+    base = head + v0 * N;
+  }
+  __device__ __forceinline__ Words vec(int i) const { return load16(z + base + (int64_t)i * Vec<T>::N); }
+  __device__ __forceinline__ int64_t loose_at(int i) const { return i < head ? i : tail0 + (i - head); }
+  // elements of the slice, in the order of their ids, for the exact selection
+  __device__ __forceinline__ int64_t size() const { return (int64_t)nvec * Vec<T>::N + loose; }
+  __device__ __forceinline__ int64_t at(int64_t i) const {
+    if (loose == 0) return base + i;
+    if (i < head) return i;
+    i -= head;
+    const int64_t body = (int64_t)nvec * Vec<T>::N;
+    return i < body ? base + i : tail0 + (i - body);
+  }
+};
+
+// Four vectors into the running sums.
+template <class T>
+struct Fold {
+  float off, off_up, k;  // exponent offset; raised when a logit passes off_up
+  float top;             // true maximum
+  float2 s, t;
+
+  __device__ __forceinline__ void init(float k_) {
+    k = k_;
+    off = off_up = top = neg_inf();
+    s = t = make_float2(0.f, 0.f);
+  }
+  __device__ __forceinline__ void raise(float m) {
+    const float x = lp_x(off, m, k), f = ex2(x);
+    const float2 ff = make_float2(f, f);
+    t = mul2(ff, fma2(s, make_float2(x, x), t));
+    s = mul2(ff, s);
+    off = m;
+    off_up = m + kRaise / k;
+  }
+  // the vector's maximum (m) tested first
+  __device__ __forceinline__ void add(const Words& v) {
+    constexpr int N = Vec<T>::N;
+    float z[N];
+    Vec<T>::get(v, z);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      float2 x = sub2(make_float2(z[i], z[i + 1]), make_float2(off, off));
+      x = mul2(x, make_float2(k, k));
+      x.x = max_nan(x.x, kXMin);
+      x.y = max_nan(x.y, kXMin);
+      const float2 e = make_float2(ex2(x.x), ex2(x.y));
+      s = add2(s, e);
+      t = fma2(e, x, t);
+    }
+  }
+  __device__ __forceinline__ void add_one(float z) {
+    if (z == neg_inf()) return;
+    if (z > top) top = z;
+    if (z > off_up) raise(z);
+    const float x = lp_x(z, off, k), e = ex2(x);
+    s.x += e;
+    t.x = fmaf(e, x, t.x);
+  }
+  // sums relative to the true maximum
+  __device__ __forceinline__ LpState state() const {
+    LpState a{off, s.x + s.y, t.x + t.y};
+    lp_raise(a, top, k);
+    return a;
+  }
+};
+
+// Shared memory of the selection; cand has `cap` places.
+struct SelectShared {
+  uint32_t hist[256];
+  uint32_t prefix, want, count, pairs;
+  uint32_t warp_sum[2][32];
+};
+
+// The K best of a slice by radix selection on the order keys: eight bits a
+// sweep, then one sweep that collects what lies above the K-th key and the
+// lowest ids among those equal to it.  Exact for any row; taken where too many
+// ids lie at or above the bound (long runs of equal logits).
+template <class T>
+__device__ void select_exact(const Slice<T>& sl, int k, SelectShared& sh, uint64_t* cand) {
   const int tid = threadIdx.x, nt = blockDim.x;
+  const int64_t v = sl.size();
   if (tid == 0) {
     sh.prefix = 0;
     sh.want = (uint32_t)k;
@@ -178,7 +329,7 @@ __device__ void select_exact(const T* z, int64_t v, int k, SelectShared& sh) {
     __syncthreads();
     const uint32_t prefix = sh.prefix;
     for (int64_t i = tid; i < v; i += nt) {
-      const uint32_t key = order_key(to_f(z[i]));
+      const uint32_t key = order_key(to_f(sl.z[sl.at(i)]));
       if ((key & mask) == prefix) atomicAdd(&sh.hist[(key >> shift) & 255u], 1u);
     }
     __syncthreads();
@@ -195,21 +346,21 @@ __device__ void select_exact(const T* z, int64_t v, int k, SelectShared& sh) {
   uint32_t seen = 0;
   for (int64_t base = 0; base < v; base += nt) {
     const int64_t i = base + tid;
-    const uint32_t key = i < v ? order_key(to_f(z[i])) : 0u;
-    if (i < v && key > kth) sh.cand[atomicAdd(&sh.count, 1u)] = cand_word(key, (uint32_t)i);
+    const int64_t id = i < v ? sl.at(i) : 0;
+    const uint32_t key = i < v ? order_key(to_f(sl.z[id])) : 0u;
+    if (i < v && key > kth) cand[atomicAdd(&sh.count, 1u)] = cand_word(key, (uint32_t)id);
     const bool tie = i < v && key == kth;
     if (__syncthreads_or(tie && seen < ties)) {
       const uint32_t b = __ballot_sync(0xffffffffu, tie);
-      if ((tid & 31) == 0) sh.warp_ties[tid >> 5] = __popc(b);
+      if ((tid & 31) == 0) sh.warp_sum[0][tid >> 5] = __popc(b);
       __syncthreads();
       uint32_t before = seen, total = 0;
       for (int w = 0; w < nt / 32; ++w) {
-        if (w < (tid >> 5)) before += sh.warp_ties[w];
-        total += sh.warp_ties[w];
+        if (w < (tid >> 5)) before += sh.warp_sum[0][w];
+        total += sh.warp_sum[0][w];
       }
       before += __popc(b & ((1u << (tid & 31)) - 1u));
-      if (tie && before < ties)
-        sh.cand[atomicAdd(&sh.count, 1u)] = cand_word(key, (uint32_t)i);
+      if (tie && before < ties) cand[atomicAdd(&sh.count, 1u)] = cand_word(key, (uint32_t)id);
       seen += total;
       __syncthreads();
     }
@@ -217,62 +368,288 @@ __device__ void select_exact(const T* z, int64_t v, int k, SelectShared& sh) {
   __syncthreads();
 }
 
-// Writes the K candidates in order: each one's place is the number of larger
-// words.
-__device__ void write_top(const LpArgs& a, int64_t r, const uint64_t* cand, const LpRow& row) {
-  for (int j = threadIdx.x; j < a.topk; j += blockDim.x) {
-    const uint64_t w = cand[j];
-    int place = 0;
-    for (int i = 0; i < a.topk; ++i) place += cand[i] > w;
-    if (a.topk_idx) a.topk_idx[r * a.topk + place] = (int32_t)~(uint32_t)w;
-    if (a.topk_lp)
-      a.topk_lp[r * a.topk + place] = lp_of(key_value((uint32_t)(w >> 32)), row, a.inv_t);
+// Largest 16-bit key that at least k of the block's slot maxima reach (0 when
+// there are fewer): by halving, one block-wide count a step.
+template <int NT>
+__device__ __forceinline__ uint32_t bound_key(const uint32_t* key, int n, int k,
+                                              SelectShared& sh) {
+  uint32_t lo = 0;
+  int flip = 0;
+  for (uint32_t bit = 0x8000u; bit; bit >>= 1, flip ^= 1) {
+    const uint32_t test = lo | bit;
+    uint32_t c = 0;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i)
+      if (i < n) c += (key[i] >> 16) >= test;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if ((threadIdx.x & 31) == 0) sh.warp_sum[flip][threadIdx.x >> 5] = c;
+    __syncthreads();
+    c = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) c += sh.warp_sum[flip][w];
+    if (c >= (uint32_t)k) lo = test;
   }
+  return lo;
 }
 
-// ------------------------------------------------------------------ forward
-constexpr int kRowThreads = 256;
-
-// One block per row.
-template <class T>
-__global__ void __launch_bounds__(kRowThreads) k_logprob_rows(LpArgs a) {
-  __shared__ SelectShared sh;
-  __shared__ LpState warp_state[kRowThreads / 32];
-  const int64_t r = blockIdx.x;
-  const T* z = static_cast<const T*>(a.z) + r * a.ld;
-  const int64_t y = a.tokens ? a.tokens[r] : -1;
-  if (a.tokens && y == a.ignore) {
-    lp_store_ignored(a, r);
+// Descending sort of cand[0, n) (n <= cap, a power of two): each word's place
+// is the number of larger ones when there are few, a bitonic sort otherwise
+// (at 512 threads and 1400 words 18 us by counting, 3 us by exchanges).
+template <int NT>
+__device__ void sort_words(uint64_t* cand, int n) {
+  if (n <= NT) {
+    const uint64_t w = (int)threadIdx.x < n ? cand[threadIdx.x] : 0;
+    int place = 0;
+    for (int i = 0; i < n; ++i) place += cand[i] > w;
+    __syncthreads();
+    if ((int)threadIdx.x < n) cand[place] = w;
+    __syncthreads();
     return;
   }
-  LpState st = lp_empty();
-  for (int64_t i = threadIdx.x; i < a.vocab; i += kRowThreads) lp_add(st, to_f(z[i]), a.k2);
+  int m = NT;
+  while (m < n) m <<= 1;
+  for (int i = n + threadIdx.x; i < m; i += NT) cand[i] = 0;
+  __syncthreads();
+  for (int size = 2; size <= m; size <<= 1)
+    for (int step = size >> 1; step > 0; step >>= 1) {
+      for (int i = threadIdx.x; i < m / 2; i += NT) {
+        const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
+        const uint64_t a = cand[lo], b = cand[hi];
+        if ((a < b) == ((lo & size) == 0)) {
+          cand[lo] = b;
+          cand[hi] = a;
+        }
+      }
+      __syncthreads();
+    }
+}
+
+// Dynamic shared memory: cand[cap] (u64), slot keys [kSlots][NT] (u32), list of
+// slots above the bound [kSlots * NT] (u16).
+__host__ __device__ constexpr int row_cap(int k) { return k <= 128 ? 1024 : 4096; }
+template <int NT>
+__host__ __device__ constexpr int row_smem(int k) {
+  return k == 0 ? 0 : row_cap(k) * 8 + kSlots * NT * 4 + kSlots * NT * 2;
+}
+
+template <class T, int NT, bool TOPK>
+__global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
+  extern __shared__ __align__(16) uint8_t dyn[];
+  __shared__ SelectShared sh;
+  __shared__ LpState warp_state[NT / 32];
+  __shared__ LpState block_state;
+  __shared__ int block_count;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int64_t r = blockIdx.x / blocks;
+  const int64_t y = a.tokens ? a.tokens[r] : -1;
+  if (a.tokens && y == a.ignore) {  // the whole cluster
+    if (rank == 0) lp_store_ignored(a, r);
+    return;
+  }
+  const int tid = threadIdx.x;
+  const Slice<T> sl(static_cast<const T*>(a.z) + r * a.ld, a.vocab, rank, blocks, NT);
+  const bool in = y >= 0 && y < a.vocab;
+  const float zy = (tid == 0 && rank == 0 && in) ? to_f(sl.z[y]) : 0.f;
+
+  // ---- one sweep
+  const int per_slot = max(1, (sl.rounds + kSlots - 1) / kSlots);
+  uint32_t key[kSlots];
+  uint32_t* slot_key = reinterpret_cast<uint32_t*>(dyn + row_cap(a.topk) * 8);
+  int slots = 0, left = per_slot;
+  float slot_top = neg_inf();
+  Fold<T> f;
+  f.init(a.k2);
+  if (tid < sl.loose) f.add_one(to_f(sl.z[sl.loose_at(tid)]));
+  Words none;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) none.w[i] = Vec<T>::kNone;
+  Words cur[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) cur[u] = tid + u * NT < sl.nvec ? sl.vec(tid + u * NT) : none;
+  for (int j = 0; j < sl.rounds; j += kUnroll) {
+    Words nxt[kUnroll];
+    const int i0 = tid + (j + kUnroll) * NT;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) nxt[u] = i0 + u * NT < sl.nvec ? sl.vec(i0 + u * NT) : none;
+    float m[kUnroll], mm = neg_inf();
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      m[u] = Vec<T>::top(cur[u]);
+      mm = max_nan(mm, m[u]);
+    }
+    if (mm != neg_inf()) {
+      f.top = fmaxf(f.top, mm);
+      if (mm > f.off_up) f.raise(mm);
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) f.add(cur[u]);
+    }
+    if (TOPK) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        if (j + u < sl.rounds) {
+          slot_top = max_nan(slot_top, m[u]);
+          if (--left == 0) {
+            slot_key[slots++ * NT + tid] = order_key(slot_top);
+            slot_top = neg_inf();
+            left = per_slot;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) cur[u] = nxt[u];
+  }
+  if (TOPK && left != per_slot) slot_key[slots++ * NT + tid] = order_key(slot_top);
+
+  // ---- the row's statistics
+  LpState st = f.state();
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) lp_merge(st, lp_shfl_xor(st, o), a.k2);
-  if ((threadIdx.x & 31) == 0) warp_state[threadIdx.x >> 5] = st;
+  if ((tid & 31) == 0) warp_state[tid >> 5] = st;
+  if (TOPK && tid == 0) sh.count = sh.pairs = 0;
   __syncthreads();
   st = warp_state[0];
-  for (int w = 1; w < kRowThreads / 32; ++w) lp_merge(st, warp_state[w], a.k2);
+#pragma unroll
+  for (int w = 1; w < NT / 32; ++w) lp_merge(st, warp_state[w], a.k2);
+
+  // ---- the slice's best
+  uint64_t* cand = reinterpret_cast<uint64_t*>(dyn);
+  int have = 0;
+  if (TOPK) {
+    const int cap = row_cap(a.topk);
+    const int want = (int)min((int64_t)a.topk, sl.size());
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+      key[i] = i < slots ? slot_key[i * NT + tid] : 0u;
+      best = max(best, key[i]);
+    }
+    // few alternatives: the threads' maxima bound them closely enough
+    const bool fine = want > NT / 4;
+    const uint32_t bound =
+        fine ? bound_key<NT>(key, slots, want, sh) : bound_key<NT>(&best, 1, want, sh);
+    uint16_t* list = reinterpret_cast<uint16_t*>(slot_key + kSlots * NT);
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i)
+      if (i < slots && (key[i] >> 16) >= bound)
+        list[atomicAdd(&sh.pairs, 1u)] = (uint16_t)(i * NT + tid);
+    auto offer = [&](float z, int64_t id) {
+      const uint32_t q = order_key(z);
+      if ((q >> 16) < bound) return;
+      const uint32_t at = atomicAdd(&sh.count, 1u);
+      if (at < (uint32_t)cap) cand[at] = cand_word(q, (uint32_t)id);
+    };
+    if (tid < sl.loose) offer(to_f(sl.z[sl.loose_at(tid)]), sl.loose_at(tid));
+    __syncthreads();
+    const int items = (int)sh.pairs * per_slot;
+    for (int i = tid; i < items; i += NT) {
+      const int pair = list[i / per_slot];
+      const int v = (pair / NT * per_slot + i % per_slot) * NT + pair % NT;
+      if (v >= sl.nvec) continue;
+      const Words w = sl.vec(v);
+      if ((order_key(Vec<T>::top(w)) >> 16) < bound) continue;
+      float z[Vec<T>::N];
+      Vec<T>::get(w, z);
+#pragma unroll
+      for (int e = 0; e < Vec<T>::N; ++e) offer(z[e], sl.base + (int64_t)v * Vec<T>::N + e);
+    }
+    __syncthreads();
+    have = (int)sh.count;
+    if (have > cap) {
+      __syncthreads();
+      select_exact(sl, want, sh, cand);
+      have = want;
+    }
+    sort_words<NT>(cand, have);
+    have = want;
+  }
+
+  // ---- join the slices
+  if (blocks > 1) {
+    if (tid == 0) {
+      block_state = st;
+      block_count = have;
+    }
+    cluster.sync();
+    st = *cluster.map_shared_rank(&block_state, 0);
+    for (int b = 1; b < blocks; ++b) lp_merge(st, *cluster.map_shared_rank(&block_state, b), a.k2);
+  }
   const LpRow row = lp_finish(st);
-  if (threadIdx.x == 0) {
-    const bool in = y >= 0 && y < a.vocab;
+  if (tid == 0 && rank == 0) {
     if (a.tokens && !in) set_status(a.status, KD_DEV_BAD_LABEL);
-    lp_store(a, r, row, y, in ? to_f(z[y]) : 0.f);
+    lp_store(a, r, row, y, zy);
   }
-  if (a.topk) {
-    select_exact(z, a.vocab, a.topk, sh);
-    write_top(a, r, sh.cand, row);
+  if (TOPK) {
+    for (int j = tid; j < have; j += NT) {
+      const uint64_t w = cand[j];
+      int place = j;  // larger words here, and in the other slices' sorted lists
+      for (int b = 0; b < blocks && place < a.topk; ++b) {
+        if (b == rank) continue;
+        const uint64_t* other = cluster.map_shared_rank(cand, b);
+        int lo = 0, hi = *cluster.map_shared_rank(&block_count, b);
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (other[mid] > w) lo = mid + 1;
+          else hi = mid;
+        }
+        place += lo;
+      }
+      if (place >= a.topk) continue;
+      if (a.topk_idx) a.topk_idx[r * a.topk + place] = (int32_t)~(uint32_t)w;
+      if (a.topk_lp)
+        a.topk_lp[r * a.topk + place] = lp_of(key_value((uint32_t)(w >> 32)), row, a.inv_t);
+    }
   }
+  if (blocks > 1) cluster.sync();  // no block leaves while another reads its lists
+}
+
+// Blocks of a cluster for each row: enough of them to give every SM work, as
+// long as a slice keeps 16 KiB.
+int row_blocks(int64_t n, int64_t row_bytes, int nsm) {
+  int c = 1;
+  while (c < 8 && n * c * 2 <= 2 * nsm && row_bytes / (2 * c) >= 16384) c *= 2;
+  return c;
+}
+
+template <class T, int NT, bool TOPK>
+int launch_rows_nt(const LpArgs& a, int blocks, cudaStream_t s) {
+  auto kern = k_logprob_rows<T, NT, TOPK>;
+  const int smem = row_smem<NT>(a.topk);
+  if (smem > 40000 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           smem) != cudaSuccess)
+    return 1;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)blocks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(a.n * blocks));
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = blocks > 1 ? 1 : 0;
+  note_launch();
+  return (int)cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 template <class T>
-void launch_rows(const LpArgs& a, cudaStream_t s) {
-  if (a.n <= 0) return;
-  note_launch();
-  k_logprob_rows<T><<<(unsigned)a.n, kRowThreads, 0, s>>>(a);
+int launch_rows(const LpArgs& a, int nsm, cudaStream_t s) {
+  if (a.n <= 0) return 0;
+  const int64_t bytes = a.vocab * (int64_t)sizeof(T);
+  const int blocks = row_blocks(a.n, bytes, nsm);
+  // short rows: more, smaller blocks on an SM
+  if (bytes < 32768 && blocks == 1)
+    return a.topk ? launch_rows_nt<T, 128, true>(a, 1, s) : launch_rows_nt<T, 128, false>(a, 1, s);
+  return a.topk ? launch_rows_nt<T, 512, true>(a, blocks, s)
+                : launch_rows_nt<T, 512, false>(a, blocks, s);
 }
 
 // ------------------------------------------------------------------ backward
+constexpr int kRowThreads = 256;
+
 struct LpGradArgs {
   const void* z;          // [n, cols] rows of pitch ld: columns col0 .. of the vocabulary
   int64_t n, cols, ld, col0, vocab;
@@ -325,27 +702,141 @@ __device__ __forceinline__ float lp_grad(float z, const LpGradRow& g, float k) {
   return ex2(x) * fmaf(g.c1, x, g.c0);
 }
 
-template <class T, class O>
-__global__ void __launch_bounds__(kRowThreads) k_logprob_grad(LpGradArgs a) {
+// dz of fp32 logit chunks (hidden sources), one block per row.
+template <class O>
+__global__ void __launch_bounds__(kRowThreads) k_logprob_grad_chunk(LpGradArgs a) {
   const int64_t r = blockIdx.x;
-  const T* z = static_cast<const T*>(a.z) + r * a.ld;
+  const float* z = static_cast<const float*>(a.z) + r * a.ld;
   O* out = static_cast<O*>(a.g) + r * a.ldg;
   const LpGradRow g = lp_grad_row(a, r);
   for (int64_t i = threadIdx.x; i < a.cols; i += kRowThreads) {
     float v = 0.f;
     if (g.live) {
-      v = lp_grad(to_f(z[i]), g, a.k2);
+      v = lp_grad(z[i], g, a.k2);
       if (a.col0 + i == g.y) v += g.cy;
     }
     from_f(v, out[i]);
   }
 }
 
-template <class T, class O>
-void launch_grad(const LpGradArgs& a, cudaStream_t s) {
-  if (a.n <= 0) return;
+// dz of materialised logits: a block takes kSegVecs vectors of a row, each
+// thread four 16-byte loads at a time, and stores what it loaded in place (so
+// d_logits may be the logits).  Bound by HBM: one read and one write of every
+// element.  Rows whose two sides differ in their offset from a 16-byte boundary
+// go element by element.
+constexpr int kSegVecs = 2048;
+
+template <class T>
+__device__ __forceinline__ void store_vec(T* p, const float* v);
+template <>
+__device__ __forceinline__ void store_vec(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+template <>
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float* v) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                            pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+
+template <class T>
+__global__ void __launch_bounds__(kRowThreads) k_logprob_grad(LpGradArgs a, int segs) {
+  constexpr int N = Vec<T>::N;
+  const int64_t r = blockIdx.x / segs;
+  const int seg = (int)(blockIdx.x % segs), tid = threadIdx.x;
+  const T* z = static_cast<const T*>(a.z) + r * a.ld;
+  T* out = static_cast<T*>(a.g) + r * a.ldg;
+  const LpGradRow g = lp_grad_row(a, r);
+  auto one = [&](int64_t i) {
+    float v = 0.f;
+    if (g.live) {
+      v = lp_grad(to_f(z[i]), g, a.k2);
+      if (i == g.y) v += g.cy;
+    }
+    from_f(v, out[i]);
+  };
+  const int zo = (int)(reinterpret_cast<uintptr_t>(z) & 15);
+  if (zo != (int)(reinterpret_cast<uintptr_t>(out) & 15)) {
+    const int64_t e0 = (int64_t)seg * kSegVecs * N, e1 = min(a.cols, e0 + (int64_t)kSegVecs * N);
+    for (int64_t i = e0 + tid; i < e1; i += kRowThreads) one(i);
+    return;
+  }
+  const int64_t head = min(a.cols, (int64_t)(zo ? N - zo / (int)sizeof(T) : 0));
+  const int64_t all = (a.cols - head) / N, tail0 = head + all * N;
+  if (seg == 0) {
+    const int loose = (int)(head + a.cols - tail0);
+    if (tid < loose) one(tid < head ? tid : tail0 + (tid - head));
+  }
+  const int64_t v0 = (int64_t)seg * kSegVecs;
+  const int n = (int)min((int64_t)kSegVecs, all - v0);  // may be < 0: no vector here
+  z += head + v0 * N;
+  out += head + v0 * N;
+  const int64_t y = g.y < 0 ? -1 : g.y - (head + v0 * N);
+  const float2 m2 = make_float2(g.m, g.m), k2 = make_float2(a.k2, a.k2);
+  const float2 off2 = make_float2(g.off, g.off);
+  const float2 c0 = make_float2(g.c0, g.c0), c1 = make_float2(g.c1, g.c1);
+  for (int i0 = tid; i0 < n; i0 += kUnroll * kRowThreads) {
+    uint4 w[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kRowThreads;
+      if (g.live && i < n) w[u] = *reinterpret_cast<const uint4*>(z + (int64_t)i * N);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kRowThreads;
+      if (i >= n) break;
+      float v[N];
+      if (g.live) {
+        Words q;
+        q.w[0] = w[u].x, q.w[1] = w[u].y, q.w[2] = w[u].z, q.w[3] = w[u].w;
+        Vec<T>::get(q, v);
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+          float2 x = mul2(sub2(make_float2(v[e], v[e + 1]), m2), k2);
+          x = sub2(x, off2);
+          x.x = max_nan(x.x, kXMin);
+          x.y = max_nan(x.y, kXMin);
+          x = mul2(make_float2(ex2(x.x), ex2(x.y)), fma2(c1, x, c0));
+          v[e] = x.x;
+          v[e + 1] = x.y;
+        }
+        if ((uint64_t)(y - (int64_t)i * N) < (uint64_t)N) {
+#pragma unroll
+          for (int e = 0; e < N; ++e)
+            if (y - (int64_t)i * N == e) v[e] += g.cy;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = 0.f;
+      }
+      store_vec<T>(out + (int64_t)i * N, v);
+    }
+  }
+}
+
+template <class O>
+void launch_grad_chunk(const LpGradArgs& a, cudaStream_t s) {
   note_launch();
-  k_logprob_grad<T, O><<<(unsigned)a.n, kRowThreads, 0, s>>>(a);
+  k_logprob_grad_chunk<O><<<(unsigned)a.n, kRowThreads, 0, s>>>(a);
+}
+template <class T>
+void launch_grad(const LpGradArgs& a, cudaStream_t s) {
+  const int64_t per = (int64_t)kSegVecs * Vec<T>::N;
+  const int64_t segs = (a.cols + per - 1) / per;
+  // rows in as many launches as the grid's 2^31 - 1 blocks ask for
+  const int64_t most = INT32_MAX / segs;
+  for (int64_t r0 = 0; r0 < a.n; r0 += most) {
+    LpGradArgs b = a;
+    b.n = std::min(most, a.n - r0);
+    b.z = static_cast<const T*>(a.z) + r0 * a.ld;
+    b.g = static_cast<T*>(a.g) + r0 * a.ldg;
+    if (a.tokens) b.tokens = a.tokens + r0;
+    b.stats = a.stats + r0 * KD_LOGPROB_STATS;
+    if (a.d_lp) b.d_lp = a.d_lp + r0;
+    if (a.d_ent) b.d_ent = a.d_ent + r0;
+    note_launch();
+    k_logprob_grad<T><<<(unsigned)(b.n * segs), kRowThreads, 0, s>>>(b, (int)segs);
+  }
 }
 
 // Copy of the hidden states with the rows of ignored tokens zeroed: their
@@ -366,7 +857,6 @@ __global__ void __launch_bounds__(kRowThreads) k_mask_rows(const T* __restrict__
 // ------------------------------------------------------------------ plan
 constexpr size_t kAlign = 256;
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
@@ -539,8 +1029,8 @@ extern "C" kd_status kd_logprob_fwd(const kd_logprob_problem* p, const kd_logpro
     rows_from(0, P.n);
     a.z = in->logits;
     a.ld = P.ld;
-    if (P.bf16) launch_rows<__nv_bfloat16>(a, s);
-    else launch_rows<float>(a, s);
+    if (P.bf16 ? launch_rows<__nv_bfloat16>(a, P.nsm, s) : launch_rows<float>(a, P.nsm, s))
+      return KD_ERR_CUDA;
   } else {
     float* z = at<float>(workspace, P.f_z);
     a.z = z;
@@ -549,7 +1039,7 @@ extern "C" kd_status kd_logprob_fwd(const kd_logprob_problem* p, const kd_logpro
       const int64_t rows = std::min(P.fr, P.n - r0);
       if (lp_logits(P, in, r0, rows, 0, P.v, z, P.v, dev_status, s)) return KD_ERR_CUDA;
       rows_from(r0, rows);
-      launch_rows<float>(a, s);
+      if (launch_rows<float>(a, P.nsm, s)) return KD_ERR_CUDA;
     }
   }
   return cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA;
@@ -586,6 +1076,7 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
   a.status = dev_status;
   if (!P.hidden) {
     if (!d_logits) return KD_OK;
+    if (d_logits == in->logits && P.ld != P.ldg) return KD_ERR_INVALID_ARG;
     a.z = in->logits;
     a.n = P.n;
     a.cols = P.v;
@@ -596,8 +1087,8 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
     a.d_ent = d_entropy;
     a.g = d_logits;
     a.ldg = P.ldg;
-    if (P.bf16) launch_grad<__nv_bfloat16, __nv_bfloat16>(a, s);
-    else launch_grad<float, float>(a, s);
+    if (P.bf16) launch_grad<__nv_bfloat16>(a, s);
+    else launch_grad<float>(a, s);
     return cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA;
   }
   if (!d_h && !d_w) return KD_OK;
@@ -633,7 +1124,7 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
       a.d_ent = d_entropy ? d_entropy + r0 : nullptr;
       a.g = g;
       if (!P.bf16) {
-        launch_grad<float, float>(a, s);
+        launch_grad_chunk<float>(a, s);
         const float* gf = static_cast<const float*>(g);
         if (d_h)
           launch_simt_gemm(gf, C, 1, static_cast<const float*>(in->w) + c0 * D, D, 1,
@@ -643,7 +1134,7 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
                            static_cast<float*>(d_w) + c0 * D, D, cc, D, rc, ri > 0, s);
         continue;
       }
-      launch_grad<float, __nv_bfloat16>(a, s);
+      launch_grad_chunk<__nv_bfloat16>(a, s);
       auto product = [&](const __nv_bfloat16* b, int64_t m, int64_t kk, bool a_mn, float* acc,
                          __nv_bfloat16* out, int64_t i, int64_t parts) {
         TcGemmArgs t;
