@@ -159,7 +159,9 @@ __device__ __forceinline__ void lp_store_ignored(const LpArgs& a, int64_t r) {
 // slot maxima bounds the K-th largest logit from below, so only the vectors of
 // the few slots above it are read again (from L2), and what lies above the
 // bound in them, little more than K ids, is sorted.
-constexpr int kSlots = 8;
+constexpr int kSlots = 32;
+constexpr int kPairs = 4096;   // slots above the bound the list holds
+constexpr int kMaxCap = 4096;  // candidates a block sorts at most
 constexpr int kUnroll = 4;
 constexpr float kRaise = 8.f;  // exponent the offset may trail by
 
@@ -303,11 +305,18 @@ struct Fold {
   }
 };
 
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Shared memory of the selection; cand has `cap` places.
 struct SelectShared {
   uint32_t hist[256];
-  uint32_t prefix, want, count, pairs;
-  uint32_t warp_sum[2][32];
+  uint32_t prefix, want, count, owners, pairs, bound;
+  uint32_t warp_sum[2][32];  // alternately, so that one barrier a step is enough
 };
 
 // The K best of a slice by radix selection on the order keys: eight bits a
@@ -315,7 +324,7 @@ struct SelectShared {
 // lowest ids among those equal to it.  Exact for any row; taken where too many
 // ids lie at or above the bound (long runs of equal logits).
 template <class T>
-__device__ void select_exact(const Slice<T>& sl, int k, SelectShared& sh, uint64_t* cand) {
+__device__ __noinline__ void select_exact(const Slice<T>& sl, int k, SelectShared& sh, uint64_t* cand) {
   const int tid = threadIdx.x, nt = blockDim.x;
   const int64_t v = sl.size();
   if (tid == 0) {
@@ -368,19 +377,48 @@ __device__ void select_exact(const Slice<T>& sl, int k, SelectShared& sh, uint64
   __syncthreads();
 }
 
-// Largest 16-bit key that at least k of the block's slot maxima reach (0 when
-// there are fewer): by halving, one block-wide count a step.
+// Largest 16-bit key that at least k of the threads' keys reach, k <= NT: one
+// warp, two bits a step below the highest bit in which the keys differ, so that
+// the other blocks of the SM keep the issue slots.
 template <int NT>
-__device__ __forceinline__ uint32_t bound_key(const uint32_t* key, int n, int k,
-                                              SelectShared& sh) {
+__device__ __forceinline__ void bound_key(const uint16_t* keys, int k, uint32_t* out) {
+  constexpr int P = NT / 32;
+  uint32_t key[P], lo = 0xffffu, hi = 0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    key[i] = keys[i * 32 + threadIdx.x];
+    lo = min(lo, key[i]);
+    hi = max(hi, key[i]);
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  int shift = (32 - __clz(lo ^ hi) + 1) & ~1;  // even; bits below it may differ
+  lo = lo >> shift << shift;
+#pragma unroll 1
+  while ((shift -= 2) >= 0) {
+    uint32_t c[3] = {0, 0, 0};
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) c[q] += key[i] >= (lo | ((uint32_t)(q + 1) << shift));
+      c[q] = __reduce_add_sync(0xffffffffu, c[q]);
+    }
+    lo |= (uint32_t)((c[0] >= (uint32_t)k) + (c[1] >= (uint32_t)k) + (c[2] >= (uint32_t)k))
+          << shift;
+  }
+  if (threadIdx.x == 0) *out = lo;
+}
+// Over all slots of all threads: one block-wide count a step.
+template <int NT>
+__device__ __forceinline__ uint32_t bound_key_slots(const uint16_t* keys, int slots, int k, SelectShared& sh) {
   uint32_t lo = 0;
   int flip = 0;
+#pragma unroll 1
   for (uint32_t bit = 0x8000u; bit; bit >>= 1, flip ^= 1) {
     const uint32_t test = lo | bit;
     uint32_t c = 0;
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i)
-      if (i < n) c += (key[i] >> 16) >= test;
+#pragma unroll 8
+    for (int i = 0; i < slots; ++i) c += keys[i * NT + threadIdx.x] >= test;
     c = __reduce_add_sync(0xffffffffu, c);
     if ((threadIdx.x & 31) == 0) sh.warp_sum[flip][threadIdx.x >> 5] = c;
     __syncthreads();
@@ -392,44 +430,168 @@ __device__ __forceinline__ uint32_t bound_key(const uint32_t* key, int n, int k,
   return lo;
 }
 
-// Descending sort of cand[0, n) (n <= cap, a power of two): each word's place
-// is the number of larger ones when there are few, a bitonic sort otherwise
-// (at 512 threads and 1400 words 18 us by counting, 3 us by exchanges).
+// One step of a bitonic sort, descending where `down`: of two words the one
+// that belongs at the lower index.
+__device__ __forceinline__ void exchange(uint64_t& a, uint64_t& b, bool down) {
+  if ((a < b) == down) {
+    const uint64_t t = a;
+    a = b;
+    b = t;
+  }
+}
+// Descending bitonic sort of NT * E words, zeros behind the first n.  Thread t
+// holds words t E .. t E + E - 1, so steps below E stay in its registers, steps
+// below 32 E in its warp, and only the few above go through shared memory.
+template <int NT, int E>
+__device__ __forceinline__ void sort_bitonic(uint64_t* cand, int n) {
+  const int t0 = threadIdx.x * E;
+  uint64_t w[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) w[i] = t0 + i < n ? cand[t0 + i] : 0;
+#pragma unroll 1
+  for (int size = 2; size <= NT * E; size <<= 1) {
+#pragma unroll 1
+    for (int step = size >> 1; step >= E; step >>= 1) {
+      const bool low = (t0 & step) == 0;         // this thread's words are the lower ones
+      const bool keep_max = ((t0 & size) == 0) == low;
+      if (step < 32 * E) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const uint64_t o = __shfl_xor_sync(0xffffffffu, w[i], step / E);
+          w[i] = keep_max ? max(w[i], o) : min(w[i], o);
+        }
+      } else {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < E; ++i) cand[i * NT + threadIdx.x] = w[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const uint64_t o = cand[i * NT + (threadIdx.x ^ (step / E))];
+          w[i] = keep_max ? max(w[i], o) : min(w[i], o);
+        }
+      }
+    }
+#pragma unroll
+    for (int step = E / 2; step > 0; step >>= 1) {
+      if (step > size >> 1) continue;
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if ((i & step) == 0) exchange(w[i], w[i + step], ((t0 + i) & size) == 0);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < E; ++i) cand[t0 + i] = w[i];
+  __syncthreads();
+}
+// Descending sort of cand[0, n), n <= cap: few words go to the place that the
+// number of larger ones gives, more through a bitonic sort.
 template <int NT>
-__device__ void sort_words(uint64_t* cand, int n) {
+__device__ __forceinline__ void sort_words(uint64_t* cand, int n) {
   if (n <= NT) {
     const uint64_t w = (int)threadIdx.x < n ? cand[threadIdx.x] : 0;
     int place = 0;
-    for (int i = 0; i < n; ++i) place += cand[i] > w;
+    if ((int)(threadIdx.x & ~31u) < n) {
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) place += cand[i] > w;
+    }
     __syncthreads();
     if ((int)threadIdx.x < n) cand[place] = w;
     __syncthreads();
-    return;
+  } else if (n <= 4 * NT) {
+    sort_bitonic<NT, 4>(cand, n);
+  } else if (n <= 8 * NT) {
+    sort_bitonic<NT, 8>(cand, n);
+  } else if (n <= 16 * NT) {
+    sort_bitonic<NT, 16>(cand, n);
+  } else if constexpr (kMaxCap > 16 * NT) {
+    sort_bitonic<NT, kMaxCap / NT>(cand, n);
   }
-  int m = NT;
-  while (m < n) m <<= 1;
-  for (int i = n + threadIdx.x; i < m; i += NT) cand[i] = 0;
-  __syncthreads();
-  for (int size = 2; size <= m; size <<= 1)
-    for (int step = size >> 1; step > 0; step >>= 1) {
-      for (int i = threadIdx.x; i < m / 2; i += NT) {
-        const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
-        const uint64_t a = cand[lo], b = cand[hi];
-        if ((a < b) == ((lo & size) == 0)) {
-          cand[lo] = b;
-          cand[hi] = a;
-        }
-      }
-      __syncthreads();
-    }
 }
 
-// Dynamic shared memory: cand[cap] (u64), slot keys [kSlots][NT] (u32), list of
-// slots above the bound [kSlots * NT] (u16).
-__host__ __device__ constexpr int row_cap(int k) { return k <= 128 ? 1024 : 4096; }
+// Dynamic shared memory: cand[cap] (u64), the upper halves of the slot keys
+// [kSlots][NT] and of the threads' own maxima [NT] (u16), and the list of slots
+// above the bound [kPairs] (u16); in clusters, all blocks' lists [blocks][k] (u64).
+__host__ __device__ constexpr int row_cap(int k) { return k <= 128 ? 1024 : kMaxCap; }
 template <int NT>
-__host__ __device__ constexpr int row_smem(int k) {
-  return k == 0 ? 0 : row_cap(k) * 8 + kSlots * NT * 4 + kSlots * NT * 2;
+__host__ __device__ constexpr int row_smem(int k, int blocks) {
+  return k == 0 ? 0
+                : row_cap(k) * 8 + (kSlots + 1) * NT * 2 + kPairs * 2 +
+                      (blocks > 1 ? blocks * k * 8 : 0);
+}
+
+// The slice's best `want` ids into cand, in order.  best: this thread's key.
+template <class T, int NT>
+__device__ __noinline__ void select_top(const Slice<T>& sl, int want, int cap, int slots, int per_slot,
+                           uint32_t best, SelectShared& sh, uint64_t* cand) {
+  const int tid = threadIdx.x;
+  uint16_t* slot_key = reinterpret_cast<uint16_t*>(cand + cap);
+  uint16_t* own_key = slot_key + kSlots * NT;
+  uint16_t* list = own_key + NT;
+  uint32_t bound;
+  // few alternatives: the threads' own maxima bound them closely enough (k of
+  // NT leave about -NT log(1 - k/NT) ids above the bound)
+  if (want <= NT / 2) {
+    own_key[tid] = (uint16_t)(best >> 16);
+    __syncthreads();
+    if (tid < 32) bound_key<NT>(own_key, want, &sh.bound);
+    __syncthreads();
+    bound = sh.bound;
+  } else {
+    bound = bound_key_slots<NT>(slot_key, slots, want, sh);
+  }
+  // threads above the bound, then their slots above it, spread over the block
+  if ((best >> 16) >= bound) own_key[atomicAdd(&sh.owners, 1u)] = (uint16_t)tid;
+  __syncthreads();
+  const int checks = (int)sh.owners * slots;
+  for (int i = tid; i < checks; i += NT) {
+    const int at = i % slots * NT + own_key[i / slots];
+    if (slot_key[at] >= bound) {
+      const uint32_t p = atomicAdd(&sh.pairs, 1u);
+      if (p < (uint32_t)kPairs) list[p] = (uint16_t)at;
+    }
+  }
+  auto offer = [&](float z, int64_t id) {
+    const uint32_t q = order_key(z);
+    if ((q >> 16) < bound) return;
+    const uint32_t at = atomicAdd(&sh.count, 1u);
+    if (at < (uint32_t)cap) cand[at] = cand_word(q, (uint32_t)id);
+  };
+  if (tid < sl.loose) offer(to_f(sl.z[sl.loose_at(tid)]), sl.loose_at(tid));
+  __syncthreads();
+  const int pairs = (int)sh.pairs;
+  const int items = pairs <= kPairs ? pairs * per_slot : 0;
+  for (int i0 = tid; i0 < items; i0 += kUnroll * NT) {
+    Words w[kUnroll];
+    int at[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * NT;
+      at[u] = INT32_MAX;
+      if (i < items) {
+        const int pair = list[i / per_slot];
+        at[u] = (pair / NT * per_slot + i % per_slot) * NT + pair % NT;
+      }
+      if (at[u] < sl.nvec) w[u] = sl.vec(at[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (at[u] >= sl.nvec || (order_key(Vec<T>::top(w[u])) >> 16) < bound) continue;
+      float z[Vec<T>::N];
+      Vec<T>::get(w[u], z);
+#pragma unroll
+      for (int e = 0; e < Vec<T>::N; ++e) offer(z[e], sl.base + (int64_t)at[u] * Vec<T>::N + e);
+    }
+  }
+  __syncthreads();
+  int have = (int)sh.count;
+  if (have > cap || pairs > kPairs) {
+    __syncthreads();
+    select_exact(sl, want, sh, cand);
+    have = want;
+  }
+  sort_words<NT>(cand, have);
 }
 
 template <class T, int NT, bool TOPK>
@@ -438,35 +600,43 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
   __shared__ SelectShared sh;
   __shared__ LpState warp_state[NT / 32];
   __shared__ LpState block_state;
-  __shared__ int block_count;
+  __shared__ int block_count, counts[8];
   cg::cluster_group cluster = cg::this_cluster();
   const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int tid = threadIdx.x;
+  const int cap = row_cap(a.topk);
+  uint64_t* cand = reinterpret_cast<uint64_t*>(dyn);
+  uint16_t* slot_key = reinterpret_cast<uint16_t*>(cand + cap);
+  Words none, cur[kUnroll];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) none.w[i] = Vec<T>::kNone;
   const int64_t r = blockIdx.x / blocks;
-  const int64_t y = a.tokens ? a.tokens[r] : -1;
-  if (a.tokens && y == a.ignore) {  // the whole cluster
+  const Slice<T> sl(static_cast<const T*>(a.z) + r * a.ld, a.vocab, rank, blocks, NT);
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) cur[u] = tid + u * NT < sl.nvec ? sl.vec(tid + u * NT) : none;
+  const int64_t label = a.tokens ? a.tokens[r] : -1;
+  if (a.tokens && label == a.ignore) {  // the whole cluster
     if (rank == 0) lp_store_ignored(a, r);
     return;
   }
-  const int tid = threadIdx.x;
-  const Slice<T> sl(static_cast<const T*>(a.z) + r * a.ld, a.vocab, rank, blocks, NT);
-  const bool in = y >= 0 && y < a.vocab;
-  const float zy = (tid == 0 && rank == 0 && in) ? to_f(sl.z[y]) : 0.f;
+  const bool in = label >= 0 && label < a.vocab;
+  const float zy = (tid == 0 && rank == 0 && in) ? to_f(sl.z[label]) : 0.f;
 
   // ---- one sweep
   const int per_slot = max(1, (sl.rounds + kSlots - 1) / kSlots);
-  uint32_t key[kSlots];
-  uint32_t* slot_key = reinterpret_cast<uint32_t*>(dyn + row_cap(a.topk) * 8);
   int slots = 0, left = per_slot;
   float slot_top = neg_inf();
+  uint32_t best = 0;  // key of the thread's maximum
+  auto close_slot = [&]() {
+    const uint32_t q = order_key(slot_top);
+    slot_key[slots++ * NT + tid] = (uint16_t)(q >> 16);
+    best = max(best, q);
+    slot_top = neg_inf();
+    left = per_slot;
+  };
   Fold<T> f;
   f.init(a.k2);
   if (tid < sl.loose) f.add_one(to_f(sl.z[sl.loose_at(tid)]));
-  Words none;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) none.w[i] = Vec<T>::kNone;
-  Words cur[kUnroll];
-#pragma unroll
-  for (int u = 0; u < kUnroll; ++u) cur[u] = tid + u * NT < sl.nvec ? sl.vec(tid + u * NT) : none;
   for (int j = 0; j < sl.rounds; j += kUnroll) {
     Words nxt[kUnroll];
     const int i0 = tid + (j + kUnroll) * NT;
@@ -489,133 +659,107 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
       for (int u = 0; u < kUnroll; ++u) {
         if (j + u < sl.rounds) {
           slot_top = max_nan(slot_top, m[u]);
-          if (--left == 0) {
-            slot_key[slots++ * NT + tid] = order_key(slot_top);
-            slot_top = neg_inf();
-            left = per_slot;
-          }
+          if (--left == 0) close_slot();
         }
       }
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) cur[u] = nxt[u];
   }
-  if (TOPK && left != per_slot) slot_key[slots++ * NT + tid] = order_key(slot_top);
+  if (TOPK && left != per_slot) close_slot();
 
   // ---- the row's statistics
   LpState st = f.state();
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) lp_merge(st, lp_shfl_xor(st, o), a.k2);
   if ((tid & 31) == 0) warp_state[tid >> 5] = st;
-  if (TOPK && tid == 0) sh.count = sh.pairs = 0;
+  if (TOPK && tid == 0) sh.count = sh.owners = sh.pairs = 0;
   __syncthreads();
-  st = warp_state[0];
+  st = warp_state[tid & (NT / 32 - 1)];
 #pragma unroll
-  for (int w = 1; w < NT / 32; ++w) lp_merge(st, warp_state[w], a.k2);
+  for (int o = NT / 64; o > 0; o >>= 1) lp_merge(st, lp_shfl_xor(st, o), a.k2);
 
   // ---- the slice's best
-  uint64_t* cand = reinterpret_cast<uint64_t*>(dyn);
   int have = 0;
   if (TOPK) {
-    const int cap = row_cap(a.topk);
-    const int want = (int)min((int64_t)a.topk, sl.size());
-    uint32_t best = 0;
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i) {
-      key[i] = i < slots ? slot_key[i * NT + tid] : 0u;
-      best = max(best, key[i]);
-    }
-    // few alternatives: the threads' maxima bound them closely enough
-    const bool fine = want > NT / 4;
-    const uint32_t bound =
-        fine ? bound_key<NT>(key, slots, want, sh) : bound_key<NT>(&best, 1, want, sh);
-    uint16_t* list = reinterpret_cast<uint16_t*>(slot_key + kSlots * NT);
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i)
-      if (i < slots && (key[i] >> 16) >= bound)
-        list[atomicAdd(&sh.pairs, 1u)] = (uint16_t)(i * NT + tid);
-    auto offer = [&](float z, int64_t id) {
-      const uint32_t q = order_key(z);
-      if ((q >> 16) < bound) return;
-      const uint32_t at = atomicAdd(&sh.count, 1u);
-      if (at < (uint32_t)cap) cand[at] = cand_word(q, (uint32_t)id);
-    };
-    if (tid < sl.loose) offer(to_f(sl.z[sl.loose_at(tid)]), sl.loose_at(tid));
-    __syncthreads();
-    const int items = (int)sh.pairs * per_slot;
-    for (int i = tid; i < items; i += NT) {
-      const int pair = list[i / per_slot];
-      const int v = (pair / NT * per_slot + i % per_slot) * NT + pair % NT;
-      if (v >= sl.nvec) continue;
-      const Words w = sl.vec(v);
-      if ((order_key(Vec<T>::top(w)) >> 16) < bound) continue;
-      float z[Vec<T>::N];
-      Vec<T>::get(w, z);
-#pragma unroll
-      for (int e = 0; e < Vec<T>::N; ++e) offer(z[e], sl.base + (int64_t)v * Vec<T>::N + e);
-    }
-    __syncthreads();
-    have = (int)sh.count;
-    if (have > cap) {
-      __syncthreads();
-      select_exact(sl, want, sh, cand);
-      have = want;
-    }
-    sort_words<NT>(cand, have);
-    have = want;
+    have = (int)min((int64_t)a.topk, sl.size());
+    select_top<T, NT>(sl, have, cap, slots, per_slot, best, sh, cand);
   }
 
-  // ---- join the slices
+  // ---- join the slices: every block fetches all sums and lists
+  uint64_t* all = reinterpret_cast<uint64_t*>(slot_key + (kSlots + 1) * NT + kPairs);
   if (blocks > 1) {
     if (tid == 0) {
       block_state = st;
       block_count = have;
     }
     cluster.sync();
-    st = *cluster.map_shared_rank(&block_state, 0);
-    for (int b = 1; b < blocks; ++b) lp_merge(st, *cluster.map_shared_rank(&block_state, b), a.k2);
+    const int b = tid & 31;
+    st = b < blocks ? *cluster.map_shared_rank(&block_state, b) : LpState{neg_inf(), 0.f, 0.f};
+    if (tid < blocks) counts[tid] = *cluster.map_shared_rank(&block_count, tid);
+    if (TOPK)
+      for (int i = tid; i < blocks * a.topk; i += NT)
+        all[i] = cluster.map_shared_rank(cand, i / a.topk)[i % a.topk];
+    __syncwarp();
+    cluster_arrive();  // this block has read the others
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) lp_merge(st, lp_shfl_xor(st, o), a.k2);
+    st.m = __shfl_sync(0xffffffffu, st.m, 0);
+    st.s = __shfl_sync(0xffffffffu, st.s, 0);
+    st.t = __shfl_sync(0xffffffffu, st.t, 0);
   }
   const LpRow row = lp_finish(st);
   if (tid == 0 && rank == 0) {
     if (a.tokens && !in) set_status(a.status, KD_DEV_BAD_LABEL);
-    lp_store(a, r, row, y, zy);
+    lp_store(a, r, row, label, zy);
   }
   if (TOPK) {
-    for (int j = tid; j < have; j += NT) {
-      const uint64_t w = cand[j];
-      int place = j;  // larger words here, and in the other slices' sorted lists
-      for (int b = 0; b < blocks && place < a.topk; ++b) {
+    int* place = reinterpret_cast<int*>(slot_key);  // of each word (the keys are done with)
+    if (blocks > 1) {
+      // larger words here, and in the other slices' sorted lists: one thread
+      // for each word and slice
+      for (int j = tid; j < have; j += NT) place[j] = j;
+      __syncthreads();
+      for (int i = tid; i < have * blocks; i += NT) {
+        const int j = i / blocks, b = i % blocks;
         if (b == rank) continue;
-        const uint64_t* other = cluster.map_shared_rank(cand, b);
-        int lo = 0, hi = *cluster.map_shared_rank(&block_count, b);
+        const uint64_t w = cand[j];
+        const uint64_t* other = all + b * a.topk;
+        int lo = 0, hi = counts[b];
         while (lo < hi) {
           const int mid = (lo + hi) >> 1;
           if (other[mid] > w) lo = mid + 1;
           else hi = mid;
         }
-        place += lo;
+        if (lo) atomicAdd(&place[j], lo);
       }
-      if (place >= a.topk) continue;
-      if (a.topk_idx) a.topk_idx[r * a.topk + place] = (int32_t)~(uint32_t)w;
+      __syncthreads();
+    }
+    for (int j = tid; j < have; j += NT) {
+      const uint64_t w = cand[j];
+      const int p = blocks > 1 ? place[j] : j;
+      if (p >= a.topk) continue;
+      if (a.topk_idx) a.topk_idx[r * a.topk + p] = (int32_t)~(uint32_t)w;
       if (a.topk_lp)
-        a.topk_lp[r * a.topk + place] = lp_of(key_value((uint32_t)(w >> 32)), row, a.inv_t);
+        a.topk_lp[r * a.topk + p] = lp_of(key_value((uint32_t)(w >> 32)), row, a.inv_t);
     }
   }
-  if (blocks > 1) cluster.sync();  // no block leaves while another reads its lists
+  __syncwarp();
+  if (blocks > 1) cluster_wait();  // no block leaves while another reads its lists
 }
 
 // Blocks of a cluster for each row: enough of them to give every SM work, as
 // long as a slice keeps 16 KiB.
 int row_blocks(int64_t n, int64_t row_bytes, int nsm) {
   int c = 1;
-  while (c < 8 && n * c * 2 <= 2 * nsm && row_bytes / (2 * c) >= 16384) c *= 2;
+  while (c < 8 && n * c * 2 <= 4 * nsm && row_bytes / (2 * c) >= 16384) c *= 2;
   return c;
 }
 
 template <class T, int NT, bool TOPK>
 int launch_rows_nt(const LpArgs& a, int blocks, cudaStream_t s) {
   auto kern = k_logprob_rows<T, NT, TOPK>;
-  const int smem = row_smem<NT>(a.topk);
+  const int smem = row_smem<NT>(a.topk, blocks);
   if (smem > 40000 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            smem) != cudaSuccess)
     return 1;
@@ -641,10 +785,10 @@ int launch_rows(const LpArgs& a, int nsm, cudaStream_t s) {
   const int64_t bytes = a.vocab * (int64_t)sizeof(T);
   const int blocks = row_blocks(a.n, bytes, nsm);
   // short rows: more, smaller blocks on an SM
-  if (bytes < 32768 && blocks == 1)
+  if (blocks == 1 && bytes < (a.topk <= 64 ? 98304 : 32768))
     return a.topk ? launch_rows_nt<T, 128, true>(a, 1, s) : launch_rows_nt<T, 128, false>(a, 1, s);
-  return a.topk ? launch_rows_nt<T, 512, true>(a, blocks, s)
-                : launch_rows_nt<T, 512, false>(a, blocks, s);
+  return a.topk ? launch_rows_nt<T, 256, true>(a, blocks, s)
+                : launch_rows_nt<T, 256, false>(a, blocks, s);
 }
 
 // ------------------------------------------------------------------ backward
