@@ -216,6 +216,40 @@ struct TcGradArgs {
 };
 int launch_tc_grad(const TcGradArgs& a, int num_ctas, cudaStream_t s);
 
+// Token log-probabilities of hidden states (forward): z = H W^T tile by tile,
+// per-row sums and top-K candidates in the epilogue (kd_logprob.cu joins them).
+constexpr int kTokTopk = 128;   // alternatives the epilogue keeps at most
+constexpr int kTokCap = 256;    // candidates of a row and part before they are cut
+struct TcTokArgs {
+  const void *h, *w;
+  int64_t n, vocab, d;
+  const int64_t* tokens;   // may be NULL
+  int64_t ignore;
+  float k2;                // log2(e) / T
+  int topk;
+  int n_splits;            // parts: 2 per split
+  float4* sums;            // [parts][n]: max z, s, t, z[token] (0 in the parts without it)
+  uint64_t* cand;          // [parts][n][kTokCap]
+  int32_t* count;          // [parts][n]
+  uint32_t* status;
+};
+int launch_tc_tok(const TcTokArgs& a, int num_sms, cudaStream_t s);
+
+// Its backward: G = d z of rows [r0, r0 + rc) x columns [c0, c0 + cc) in bf16.
+struct TcTokGradArgs {
+  const void *h, *w;
+  int64_t n, vocab, d;
+  int64_t r0, rc, c0, cc;
+  __nv_bfloat16* g;        // [rc, ldg]
+  int64_t ldg;
+  float inv_t, k2;
+  const int64_t* tokens;
+  int64_t ignore;
+  const float *stats, *d_lp, *d_ent;
+  uint32_t* status;
+};
+int launch_tc_tok_grad(const TcTokGradArgs& a, int num_sms, cudaStream_t s);
+
 // Tensor-core GEMM: C[M, N] = sum_k A[M, K] B[N, K] (+ A1 B1 over K1); each
 // operand K-major ([M, K] / [N, K]) or, with its _mn flag, MN-major ([K, M] /
 // [K, N]); bf16 operands, ld = pitch of the stored layout in elements, fp32

@@ -19,96 +19,12 @@
 #include <cstring>
 
 #include "kd_internal.h"
+#include "kd_logprob.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace kd {
 namespace {
-
-constexpr int kMaxTopk = 1024;
-constexpr float kLn2 = 0.6931471805599453f;
-// Exponents below this give 2^x = 0 in fp32; x is held above it so that the
-// product 2^x x of an id of probability 0 (z = -inf among others) is 0.
-constexpr float kXMin = -160.f;
-
-// ------------------------------------------------------------------ elements
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void from_f(float v, float& o) { o = v; }
-__device__ __forceinline__ void from_f(float v, __nv_bfloat16& o) { o = __float2bfloat16(v); }
-
-// max that keeps a NaN
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
-// Order of logits as unsigned integers: larger logit, larger key; -0 = +0; a
-// NaN above every number.
-__device__ __forceinline__ uint32_t order_key(float z) {
-  if (z != z) return 0xffffffffu;
-  const uint32_t b = __float_as_uint(z + 0.f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-__device__ __forceinline__ float key_value(uint32_t key) {
-  if (key == 0xffffffffu) return __int_as_float(0x7fffffff);
-  return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
-}
-// Candidate: key above, complement of the id below, so that a larger word is
-// an earlier alternative (ties to the lowest id) and no two are equal.
-__device__ __forceinline__ uint64_t cand_word(uint32_t key, uint32_t id) {
-  return ((uint64_t)key << 32) | (uint32_t)~id;
-}
-
-// ------------------------------------------------------------------ statistics
-struct LpState {
-  float m, s, t;
-};
-// 2^((z - m) k) and its exponent, for z <= m (NaN kept)
-__device__ __forceinline__ float lp_x(float z, float m, float k) {
-  return max_nan((z - m) * k, kXMin);
-}
-// Rescale of s and t when the maximum moves from a.m up to m.
-__device__ __forceinline__ void lp_raise(LpState& a, float m, float k) {
-  if (a.m == m) return;
-  const float x = lp_x(a.m, m, k), f = ex2(x);
-  a.t = f * fmaf(a.s, x, a.t);
-  a.s = f * a.s;
-  a.m = m;
-}
-__device__ __forceinline__ void lp_merge(LpState& a, LpState b, float k) {
-  const float m = fmaxf(a.m, b.m);
-  lp_raise(a, m, k);
-  lp_raise(b, m, k);
-  a.s += b.s;
-  a.t += b.t;
-}
-__device__ __forceinline__ LpState lp_shfl_xor(const LpState& a, int o) {
-  return {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
-          __shfl_xor_sync(0xffffffffu, a.t, o)};
-}
-
-struct LpRow {
-  float m, log_s, ent;
-};
-// m = -inf: no id has any probability (log S is 0 then, or NaN beside a NaN)
-__device__ __forceinline__ LpRow lp_finish(const LpState& a) {
-  LpRow r;
-  r.m = a.m;
-  if (a.m == neg_inf() && !(a.s != a.s)) {
-    r.log_s = 0.f;
-    r.ent = 0.f;
-  } else {
-    r.log_s = logf(a.s);
-    const float h = r.log_s - kLn2 * (a.t / a.s);
-    r.ent = h < 0.f ? 0.f : h;
-  }
-  return r;
-}
-__device__ __forceinline__ float lp_of(float z, const LpRow& r, float inv_t) {
-  return r.m == neg_inf() && r.log_s == 0.f ? neg_inf() : fmaf(z - r.m, inv_t, -r.log_s);
-}
 
 struct LpArgs {
   const void* z;          // [n, vocab] rows of pitch ld
@@ -163,7 +79,6 @@ constexpr int kSlots = 32;
 constexpr int kPairs = 4096;   // slots above the bound the list holds
 constexpr int kMaxCap = 4096;  // candidates a block sorts at most
 constexpr int kUnroll = 4;
-constexpr float kRaise = 8.f;  // exponent the offset may trail by
 
 struct Words {
   uint32_t w[4];
@@ -250,58 +165,6 @@ struct Slice {
     i -= head;
     const int64_t body = (int64_t)nvec * Vec<T>::N;
     return i < body ? base + i : tail0 + (i - body);
-  }
-};
-
-// Four vectors into the running sums.
-template <class T>
-struct Fold {
-  float off, off_up, k;  // exponent offset; raised when a logit passes off_up
-  float top;             // true maximum
-  float2 s, t;
-
-  __device__ __forceinline__ void init(float k_) {
-    k = k_;
-    off = off_up = top = neg_inf();
-    s = t = make_float2(0.f, 0.f);
-  }
-  __device__ __forceinline__ void raise(float m) {
-    const float x = lp_x(off, m, k), f = ex2(x);
-    const float2 ff = make_float2(f, f);
-    t = mul2(ff, fma2(s, make_float2(x, x), t));
-    s = mul2(ff, s);
-    off = m;
-    off_up = m + kRaise / k;
-  }
-  // the vector's maximum (m) tested first
-  __device__ __forceinline__ void add(const Words& v) {
-    constexpr int N = Vec<T>::N;
-    float z[N];
-    Vec<T>::get(v, z);
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      float2 x = sub2(make_float2(z[i], z[i + 1]), make_float2(off, off));
-      x = mul2(x, make_float2(k, k));
-      x.x = max_nan(x.x, kXMin);
-      x.y = max_nan(x.y, kXMin);
-      const float2 e = make_float2(ex2(x.x), ex2(x.y));
-      s = add2(s, e);
-      t = fma2(e, x, t);
-    }
-  }
-  __device__ __forceinline__ void add_one(float z) {
-    if (z == neg_inf()) return;
-    if (z > top) top = z;
-    if (z > off_up) raise(z);
-    const float x = lp_x(z, off, k), e = ex2(x);
-    s.x += e;
-    t.x = fmaf(e, x, t.x);
-  }
-  // sums relative to the true maximum
-  __device__ __forceinline__ LpState state() const {
-    LpState a{off, s.x + s.y, t.x + t.y};
-    lp_raise(a, top, k);
-    return a;
   }
 };
 
@@ -487,7 +350,7 @@ __device__ __forceinline__ void sort_bitonic(uint64_t* cand, int n) {
 }
 // Descending sort of cand[0, n), n <= cap: few words go to the place that the
 // number of larger ones gives, more through a bitonic sort.
-template <int NT>
+template <int NT, int CAP>
 __device__ __forceinline__ void sort_words(uint64_t* cand, int n) {
   if (n <= NT) {
     const uint64_t w = (int)threadIdx.x < n ? cand[threadIdx.x] : 0;
@@ -503,10 +366,10 @@ __device__ __forceinline__ void sort_words(uint64_t* cand, int n) {
     sort_bitonic<NT, 4>(cand, n);
   } else if (n <= 8 * NT) {
     sort_bitonic<NT, 8>(cand, n);
-  } else if (n <= 16 * NT) {
-    sort_bitonic<NT, 16>(cand, n);
-  } else if constexpr (kMaxCap > 16 * NT) {
-    sort_bitonic<NT, kMaxCap / NT>(cand, n);
+  } else if (CAP > 8 * NT && n <= 16 * NT) {
+    if constexpr (CAP > 8 * NT) sort_bitonic<NT, 16>(cand, n);
+  } else if constexpr (CAP > 16 * NT) {
+    sort_bitonic<NT, CAP / NT>(cand, n);
   }
 }
 
@@ -591,7 +454,7 @@ __device__ __noinline__ void select_top(const Slice<T>& sl, int want, int cap, i
     select_exact(sl, want, sh, cand);
     have = want;
   }
-  sort_words<NT>(cand, have);
+  sort_words<NT, kMaxCap>(cand, have);
 }
 
 template <class T, int NT, bool TOPK>
@@ -634,7 +497,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
     slot_top = neg_inf();
     left = per_slot;
   };
-  Fold<T> f;
+  LpFold f;
   f.init(a.k2);
   if (tid < sl.loose) f.add_one(to_f(sl.z[sl.loose_at(tid)]));
   for (int j = 0; j < sl.rounds; j += kUnroll) {
@@ -649,10 +512,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
       mm = max_nan(mm, m[u]);
     }
     if (mm != neg_inf()) {
-      f.top = fmaxf(f.top, mm);
-      if (mm > f.off_up) f.raise(mm);
+      f.expect(mm);
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) f.add(cur[u]);
+      for (int u = 0; u < kUnroll; ++u) {
+        float z[Vec<T>::N];
+        Vec<T>::get(cur[u], z);
+#pragma unroll
+        for (int e = 0; e < Vec<T>::N; e += 2) f.add_pair(z[e], z[e + 1]);
+      }
     }
     if (TOPK) {
 #pragma unroll
@@ -748,6 +615,141 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
   if (blocks > 1) cluster_wait();  // no block leaves while another reads its lists
 }
 
+// ------------------------------------------------------------------ joining parts
+// Hidden sources: the records of the tensor-core epilogue, one per part (half a
+// tile of a vocabulary split) and row.
+struct LpJoin {
+  LpArgs a;
+  const float4* sums;      // [parts][n]
+  const uint64_t* cand;    // [parts][n][kTokCap]
+  const int32_t* count;    // [parts][n]
+  int parts;
+};
+
+// One warp: the joined sums of row r and the logit of its token.
+__device__ __forceinline__ LpState join_sums(const LpJoin& j, int64_t r, float& zy) {
+  LpState st{neg_inf(), 0.f, 0.f};
+  zy = 0.f;
+  for (int p = threadIdx.x & 31; p < j.parts; p += 32) {
+    const float4 q = j.sums[(int64_t)p * j.a.n + r];
+    lp_merge(st, LpState{q.x, q.y, q.z}, j.a.k2);
+    zy += q.w;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    lp_merge(st, lp_shfl_xor(st, o), j.a.k2);
+    zy += __shfl_xor_sync(0xffffffffu, zy, o);
+  }
+  return st;
+}
+
+__device__ __forceinline__ void join_store(const LpJoin& j, int64_t r, int64_t y,
+                                           const LpRow& row, float zy) {
+  if (j.a.tokens && !(y >= 0 && y < j.a.vocab)) set_status(j.a.status, KD_DEV_BAD_LABEL);
+  lp_store(j.a, r, row, y, zy);
+}
+
+// Without alternatives: a warp per row.
+__global__ void __launch_bounds__(256) k_logprob_join(LpJoin j) {
+  const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (r >= j.a.n) return;
+  const int64_t y = j.a.tokens ? j.a.tokens[r] : -1;
+  const bool off = j.a.tokens && y == j.a.ignore;
+  float zy = 0.f;
+  LpState st{neg_inf(), 0.f, 0.f};
+  if (!off) st = join_sums(j, r, zy);  // (the parts of an ignored row are not written)
+  if (threadIdx.x & 31) return;
+  if (off) {
+    LpArgs a = j.a;
+    if (a.logprob) a.logprob[r] = 0.f;
+    if (a.entropy) a.entropy[r] = 0.f;
+    if (a.stats) reinterpret_cast<float4*>(a.stats)[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+  } else {
+    join_store(j, r, y, lp_finish(st), zy);
+  }
+}
+
+// With alternatives: a block per row.  The K-th largest of the threads' best
+// candidates bounds the K-th best from below; what lies above it is sorted.
+constexpr int kJoinThreads = 256;
+
+__global__ void __launch_bounds__(kJoinThreads) k_logprob_join_top(LpJoin j) {
+  __shared__ uint64_t cand[kMaxCap / 2];
+  __shared__ uint16_t own_key[kJoinThreads];
+  __shared__ SelectShared sh;
+  __shared__ LpRow row;
+  __shared__ uint64_t last;
+  const LpArgs& a = j.a;
+  const int64_t r = blockIdx.x;
+  const int tid = threadIdx.x, k = a.topk;
+  const int64_t y = a.tokens ? a.tokens[r] : -1;
+  if (a.tokens && y == a.ignore) {
+    lp_store_ignored(a, r);
+    return;
+  }
+  // a warp a part, its lanes over the part's candidates
+  auto each = [&](auto&& f) {
+    for (int p = tid >> 5; p < j.parts; p += kJoinThreads / 32) {
+      const int64_t at = (int64_t)p * a.n + r;
+      const int n = j.count[at];
+      for (int i = tid & 31; i < n; i += 32) f(j.cand[at * kTokCap + i]);
+    }
+  };
+  uint64_t best = 0;
+  each([&](uint64_t w) { best = max(best, w); });
+  own_key[tid] = (uint16_t)(best >> 48);
+  if (tid == 0) sh.count = 0;
+  float zy;
+  if (tid < 32) {
+    const LpRow q = lp_finish(join_sums(j, r, zy));
+    if (tid == 0) {
+      row = q;
+      join_store(j, r, y, q, zy);
+    }
+  }
+  __syncthreads();
+  if (tid < 32) bound_key<kJoinThreads>(own_key, k, &sh.bound);
+  __syncthreads();
+  const uint32_t bound = sh.bound;
+  each([&](uint64_t w) {
+    if ((uint32_t)(w >> 48) < bound) return;
+    const uint32_t at = atomicAdd(&sh.count, 1u);
+    if (at < kMaxCap / 2) cand[at] = w;
+  });
+  __syncthreads();
+  const int have = (int)sh.count;
+  if (have <= kMaxCap / 2) {
+    sort_words<kJoinThreads, kMaxCap / 2>(cand, have);
+  } else {
+    // many equal logits: one after the other
+    if (tid == 0) last = ~(uint64_t)0;
+    for (int i = 0; i < k; ++i) {
+      __syncthreads();
+      const uint64_t l = last;
+      uint64_t w = 0;
+      each([&](uint64_t q) {
+        if (q < l) w = max(w, q);
+      });
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) w = max(w, __shfl_xor_sync(0xffffffffu, w, o));
+      __shared__ uint64_t warp_best[kJoinThreads / 32];
+      if ((tid & 31) == 0) warp_best[tid >> 5] = w;
+      __syncthreads();
+      if (tid == 0) {
+        for (int q = 1; q < kJoinThreads / 32; ++q) w = max(w, warp_best[q]);
+        cand[i] = last = w;
+      }
+    }
+    __syncthreads();
+  }
+  for (int i = tid; i < k; i += kJoinThreads) {
+    const uint64_t w = cand[i];
+    if (a.topk_idx) a.topk_idx[r * k + i] = (int32_t)~(uint32_t)w;
+    if (a.topk_lp) a.topk_lp[r * k + i] = lp_of(key_value((uint32_t)(w >> 32)), row, a.inv_t);
+  }
+}
+
+// ------------------------------------------------------------------ launches
 // Blocks of a cluster for each row: enough of them to give every SM work, as
 // long as a slice keeps 16 KiB.
 int row_blocks(int64_t n, int64_t row_bytes, int nsm) {
@@ -794,64 +796,10 @@ int launch_rows(const LpArgs& a, int nsm, cudaStream_t s) {
 // ------------------------------------------------------------------ backward
 constexpr int kRowThreads = 256;
 
-struct LpGradArgs {
-  const void* z;          // [n, cols] rows of pitch ld: columns col0 .. of the vocabulary
-  int64_t n, cols, ld, col0, vocab;
-  float inv_t, k2;
-  const int64_t* tokens;
-  int64_t ignore;
-  const float *stats, *d_lp, *d_ent;
-  void* g;                // [n, cols] rows of pitch ldg
-  int64_t ldg;
-  uint32_t* status;
-};
-
-// dz_v = p (c0 + c1 x) + [v = y] cy with x = log2 p:
-//   c0 = -(g_l + g_H H) / T, c1 = -g_H ln2 / T, cy = g_l / T
-struct LpGradRow {
-  float m, off;          // x = (z - m) k - off, off = log2 S
-  float c0, c1, cy;
-  int64_t y;
-  bool live;             // false: a zero row
-};
-__device__ __forceinline__ LpGradRow lp_grad_row(const LpGradArgs& a, int64_t r) {
-  LpGradRow g;
-  const int64_t y = a.tokens ? a.tokens[r] : -1;
-  g.live = !(a.tokens && y == a.ignore);
-  g.y = -1;
-  g.m = g.off = g.c0 = g.c1 = g.cy = 0.f;
-  if (!g.live) return g;
-  const float4 st = reinterpret_cast<const float4*>(a.stats)[r];
-  float gl = a.d_lp ? a.d_lp[r] : 0.f;
-  const float gh = a.d_ent ? a.d_ent[r] : 0.f;
-  const bool in = y >= 0 && y < a.vocab;
-  if (!in) {
-    if (a.tokens) set_status(a.status, KD_DEV_BAD_LABEL);
-    gl = 0.f;
-  }
-  if (st.x == neg_inf() && st.y == 0.f) {
-    g.live = false;
-    return g;
-  }
-  g.y = in ? y : -1;
-  g.m = st.x;
-  g.off = st.y * kL2E;
-  g.c0 = -(gl + gh * st.z) * a.inv_t;
-  g.c1 = -gh * kLn2 * a.inv_t;
-  g.cy = gl * a.inv_t;
-  return g;
-}
-__device__ __forceinline__ float lp_grad(float z, const LpGradRow& g, float k) {
-  const float x = max_nan(fmaf(z - g.m, k, -g.off), kXMin);
-  return ex2(x) * fmaf(g.c1, x, g.c0);
-}
-
-// dz of fp32 logit chunks (hidden sources), one block per row.
-template <class O>
+// dz of an fp32 logit chunk in its place (fp32 hidden sources), a block per row.
 __global__ void __launch_bounds__(kRowThreads) k_logprob_grad_chunk(LpGradArgs a) {
   const int64_t r = blockIdx.x;
-  const float* z = static_cast<const float*>(a.z) + r * a.ld;
-  O* out = static_cast<O*>(a.g) + r * a.ldg;
+  float* z = static_cast<float*>(a.g) + r * a.ldg;
   const LpGradRow g = lp_grad_row(a, r);
   for (int64_t i = threadIdx.x; i < a.cols; i += kRowThreads) {
     float v = 0.f;
@@ -859,7 +807,7 @@ __global__ void __launch_bounds__(kRowThreads) k_logprob_grad_chunk(LpGradArgs a
       v = lp_grad(z[i], g, a.k2);
       if (a.col0 + i == g.y) v += g.cy;
     }
-    from_f(v, out[i]);
+    z[i] = v;
   }
 }
 
@@ -915,9 +863,6 @@ __global__ void __launch_bounds__(kRowThreads) k_logprob_grad(LpGradArgs a, int 
   z += head + v0 * N;
   out += head + v0 * N;
   const int64_t y = g.y < 0 ? -1 : g.y - (head + v0 * N);
-  const float2 m2 = make_float2(g.m, g.m), k2 = make_float2(a.k2, a.k2);
-  const float2 off2 = make_float2(g.off, g.off);
-  const float2 c0 = make_float2(g.c0, g.c0), c1 = make_float2(g.c1, g.c1);
   for (int i0 = tid; i0 < n; i0 += kUnroll * kRowThreads) {
     uint4 w[kUnroll];
 #pragma unroll
@@ -935,15 +880,7 @@ __global__ void __launch_bounds__(kRowThreads) k_logprob_grad(LpGradArgs a, int 
         q.w[0] = w[u].x, q.w[1] = w[u].y, q.w[2] = w[u].z, q.w[3] = w[u].w;
         Vec<T>::get(q, v);
 #pragma unroll
-        for (int e = 0; e < N; e += 2) {
-          float2 x = mul2(sub2(make_float2(v[e], v[e + 1]), m2), k2);
-          x = sub2(x, off2);
-          x.x = max_nan(x.x, kXMin);
-          x.y = max_nan(x.y, kXMin);
-          x = mul2(make_float2(ex2(x.x), ex2(x.y)), fma2(c1, x, c0));
-          v[e] = x.x;
-          v[e + 1] = x.y;
-        }
+        for (int e = 0; e < N; e += 2) lp_grad_pair(v[e], v[e + 1], g, a.k2);
         if ((uint64_t)(y - (int64_t)i * N) < (uint64_t)N) {
 #pragma unroll
           for (int e = 0; e < N; ++e)
@@ -958,10 +895,9 @@ __global__ void __launch_bounds__(kRowThreads) k_logprob_grad(LpGradArgs a, int 
   }
 }
 
-template <class O>
 void launch_grad_chunk(const LpGradArgs& a, cudaStream_t s) {
   note_launch();
-  k_logprob_grad_chunk<O><<<(unsigned)a.n, kRowThreads, 0, s>>>(a);
+  k_logprob_grad_chunk<<<(unsigned)a.n, kRowThreads, 0, s>>>(a);
 }
 template <class T>
 void launch_grad(const LpGradArgs& a, cudaStream_t s) {
@@ -1009,10 +945,12 @@ struct LpPlan {
   int64_t n, v, d, ld, ldg;
   int nsm;
   float inv_t, k2;
-  int64_t fr;               // forward: rows of a logit chunk
+  bool fused;               // forward: sums and alternatives in the tensor-core epilogue
+  int splits;               // its vocabulary splits
+  int64_t fr;               // forward: rows a launch takes
   int64_t R, C;             // backward: chunk of G
-  size_t f_z, f_bytes;
-  size_t b_h, b_z, b_g, b_dh, b_dw, b_bytes;
+  size_t f_z, f_sums, f_count, f_cand, f_bytes;
+  size_t b_h, b_g, b_dh, b_dw, b_bytes;
 };
 
 size_t take(size_t& off, size_t bytes) {
@@ -1023,6 +961,27 @@ size_t take(size_t& off, size_t bytes) {
 template <class T>
 T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
+}
+
+// Rows of one fused launch: bounds the candidates' workspace.
+constexpr int64_t kFusedRows = 16384;
+
+// Vocabulary splits of the fused forward: the smallest makespan, in tiles, of
+// m_tiles * s items on `workers` CTAs (pairs).  An item costs more than its
+// tiles: its record, and with alternatives the first tiles, of which nearly
+// every logit becomes a candidate.
+int tok_splits(int64_t m_tiles, int64_t n_tiles, int workers, bool topk) {
+  int best = 1;
+  double best_cost = 1e300;
+  for (int64_t s = 1; s <= std::min<int64_t>(n_tiles, 128); ++s) {
+    const int64_t waves = cdiv(m_tiles * s, workers);
+    const double cost = (double)waves * ((double)cdiv(n_tiles, s) + (topk ? 1.0 : 0.02));
+    if (cost < best_cost - 1e-9) {
+      best_cost = cost;
+      best = (int)s;
+    }
+  }
+  return best;
 }
 
 kd_status lp_plan(const kd_logprob_problem* p, LpPlan& P) {
@@ -1053,10 +1012,24 @@ kd_status lp_plan(const kd_logprob_problem* p, LpPlan& P) {
   if (!P.bf16 && (P.v > (int64_t)65535 * 64 || P.d > (int64_t)65535 * 64))
     return KD_ERR_UNSUPPORTED;
   const int64_t n = std::max<int64_t>(P.n, 1);
-  // forward: fp32 logits of fr rows, at most 128 MiB (or one block of rows)
-  P.fr = std::min(n, std::max<int64_t>(256, ((int64_t)32 << 20) / P.v / 256 * 256));
   size_t off = 0;
-  P.f_z = take(off, (size_t)P.fr * P.v * 4);
+  P.fused = P.bf16 && p->topk <= kTokTopk;
+  if (P.fused) {
+    const bool pair = tc_use_pairs();
+    P.fr = std::min<int64_t>(n, kFusedRows);
+    P.splits = tok_splits(cdiv(P.fr, tc_tile_rows(pair)), cdiv(P.v, 256),
+                          pair ? std::max(1, P.nsm / 2) : P.nsm, p->topk > 0);
+    const size_t recs = (size_t)2 * P.splits * P.fr;
+    P.f_sums = take(off, recs * sizeof(float4));
+    if (p->topk > 0) {
+      P.f_count = take(off, recs * 4);
+      P.f_cand = take(off, recs * kTokCap * 8);
+    }
+  } else {
+    // fp32 logits of fr rows, at most 128 MiB (or one block of rows)
+    P.fr = std::min(n, std::max<int64_t>(256, ((int64_t)32 << 20) / P.v / 256 * 256));
+    P.f_z = take(off, (size_t)P.fr * P.v * 4);
+  }
   P.f_bytes = off;
   // backward
   kd_problem q;
@@ -1070,8 +1043,7 @@ kd_status lp_plan(const kd_logprob_problem* p, LpPlan& P) {
   off = 0;
   const size_t esz = P.bf16 ? 2 : 4;
   P.b_h = take(off, (size_t)n * P.d * esz);
-  P.b_z = take(off, (size_t)P.R * P.C * 4);
-  P.b_g = P.bf16 ? take(off, (size_t)P.R * P.C * 2) : P.b_z;  // fp32: G in place of z
+  P.b_g = take(off, (size_t)P.R * P.C * esz);  // fp32: z, then G in its place
   if (P.bf16 && cdiv(P.v, P.C) > 1) P.b_dh = take(off, (size_t)n * P.d * 4);
   if (P.bf16 && cdiv(n, P.R) > 1) P.b_dw = take(off, (size_t)P.v * P.d * 4);
   P.b_bytes = off;
@@ -1175,6 +1147,31 @@ extern "C" kd_status kd_logprob_fwd(const kd_logprob_problem* p, const kd_logpro
     a.ld = P.ld;
     if (P.bf16 ? launch_rows<__nv_bfloat16>(a, P.nsm, s) : launch_rows<float>(a, P.nsm, s))
       return KD_ERR_CUDA;
+  } else if (P.fused) {
+    for (int64_t r0 = 0; r0 < P.n; r0 += P.fr) {
+      rows_from(r0, std::min(P.fr, P.n - r0));
+      TcTokArgs t;
+      memset(&t, 0, sizeof(t));
+      t.h = static_cast<const __nv_bfloat16*>(in->h) + r0 * P.d;
+      t.w = in->w;
+      t.n = a.n;
+      t.vocab = P.v;
+      t.d = P.d;
+      t.tokens = a.tokens;
+      t.ignore = a.ignore;
+      t.k2 = P.k2;
+      t.topk = k;
+      t.n_splits = P.splits;
+      t.sums = at<float4>(workspace, P.f_sums);
+      t.cand = at<uint64_t>(workspace, P.f_cand);
+      t.count = at<int32_t>(workspace, P.f_count);
+      t.status = dev_status;
+      if (launch_tc_tok(t, P.nsm, s)) return KD_ERR_CUDA;
+      const LpJoin j{a, t.sums, t.cand, t.count, 2 * P.splits};
+      note_launch();
+      if (k) k_logprob_join_top<<<(unsigned)a.n, kJoinThreads, 0, s>>>(j);
+      else k_logprob_join<<<(unsigned)cdiv(a.n, 8), 256, 0, s>>>(j);
+    }
   } else {
     float* z = at<float>(workspace, P.f_z);
     a.z = z;
@@ -1238,8 +1235,8 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
   if (!d_h && !d_w) return KD_OK;
   const int64_t n = P.n, v = P.v, D = P.d, R = P.R, C = P.C;
   const int64_t nr = cdiv(n, R), nc = cdiv(v, C);
-  float* z = at<float>(workspace, P.b_z);
   void* g = at<char>(workspace, P.b_g);
+  float* z = static_cast<float*>(g);
   void* hm = at<char>(workspace, P.b_h);
   if (d_w) {
     note_launch();
@@ -1256,8 +1253,32 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
     const int64_t r0 = ri * R, rc = std::min(R, n - r0);
     for (int64_t ci = 0; ci < nc; ++ci) {
       const int64_t c0 = ci * C, cc = std::min(C, v - c0);
-      if (lp_logits(P, in, r0, rc, c0, cc, z, C, dev_status, s)) return KD_ERR_CUDA;
-      a.z = z;
+      if (P.bf16) {
+        TcTokGradArgs t;
+        memset(&t, 0, sizeof(t));
+        t.h = in->h;
+        t.w = in->w;
+        t.n = n;
+        t.vocab = v;
+        t.d = D;
+        t.r0 = r0;
+        t.rc = rc;
+        t.c0 = c0;
+        t.cc = cc;
+        t.g = static_cast<__nv_bfloat16*>(g);
+        t.ldg = C;
+        t.inv_t = P.inv_t;
+        t.k2 = P.k2;
+        t.tokens = in->tokens;
+        t.ignore = p->ignore_index;
+        t.stats = stats;
+        t.d_lp = d_logprob;
+        t.d_ent = d_entropy;
+        t.status = dev_status;
+        if (launch_tc_tok_grad(t, P.nsm, s)) return KD_ERR_CUDA;
+      } else if (lp_logits(P, in, r0, rc, c0, cc, z, C, dev_status, s)) {
+        return KD_ERR_CUDA;
+      }
       a.n = rc;
       a.cols = cc;
       a.col0 = c0;
@@ -1268,7 +1289,7 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
       a.d_ent = d_entropy ? d_entropy + r0 : nullptr;
       a.g = g;
       if (!P.bf16) {
-        launch_grad_chunk<float>(a, s);
+        launch_grad_chunk(a, s);
         const float* gf = static_cast<const float*>(g);
         if (d_h)
           launch_simt_gemm(gf, C, 1, static_cast<const float*>(in->w) + c0 * D, D, 1,
@@ -1278,7 +1299,6 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
                            static_cast<float*>(d_w) + c0 * D, D, cc, D, rc, ri > 0, s);
         continue;
       }
-      launch_grad_chunk<__nv_bfloat16>(a, s);
       auto product = [&](const __nv_bfloat16* b, int64_t m, int64_t kk, bool a_mn, float* acc,
                          __nv_bfloat16* out, int64_t i, int64_t parts) {
         TcGemmArgs t;

@@ -1,6 +1,6 @@
 // Tensor-core (tcgen05 / TMA / TMEM) kernels for sm_103a.
 //
-// One persistent, warp-specialised kernel skeleton serves three jobs:
+// One persistent, warp-specialised kernel skeleton serves these jobs:
 //   EPI_FWD   fused logits tile(s) -> online-softmax CE / KL state per row
 //             (student tile z_s = H_s W_s^T and teacher tile z_t = H_t W_t^T
 //             for the same 128 rows x BN vocabulary columns; either side may
@@ -11,6 +11,10 @@
 //             dW = G^T H read it as stored)
 //             (Full-Chunked-KL-Loss README, "Full Chunked KL": the backward
 //             recomputes each chunk and applies M softmax(z) - p)
+//   EPI_TOK / EPI_TOP  logits tile -> running sums of the token
+//             log-probabilities per row (and, EPI_TOP, the row's top-K
+//             candidates) -> a partial record per (row, vocabulary split, half)
+//   EPI_TOKG  recomputed logits tile -> their gradient G (bf16), as EPI_GRAD
 //   EPI_GEMM  plain C = A B^T with an fp32 / bf16 / accumulate epilogue
 //             (dH and dW from the G chunks); each operand K-major or MN-major
 //
@@ -44,6 +48,7 @@
 #include <mutex>
 
 #include "kd_internal.h"
+#include "kd_logprob.cuh"
 
 namespace kd {
 
@@ -54,7 +59,7 @@ constexpr int BK = 64;              // k elements per stage (one 128-byte swizzl
 constexpr int kThreads = 320;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // 1 s per wait
 
-enum Epi { EPI_FWD = 0, EPI_GRAD = 1, EPI_GEMM = 2 };
+enum Epi { EPI_FWD = 0, EPI_GRAD = 1, EPI_GEMM = 2, EPI_TOK = 3, EPI_TOP = 4, EPI_TOKG = 5 };
 
 // ------------------------------------------------------------------ PTX
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -299,6 +304,8 @@ struct TcParams {  // (128-byte aligned by its tensor maps)
   TcFwdArgs fwd;
   TcGradArgs grad;
   TcGemmArgs gemm;
+  TcTokArgs tok;
+  TcTokGradArgs tokg;
 };
 
 template <int BN, bool PAIR>
@@ -463,6 +470,154 @@ struct FwdEpi {
     const TcFwdArgs& a = P.fwd;
     if (!row_ok) return;
     st.store(a.partials + ((int64_t)(split * 2 + half) * a.n + row) * kRec);
+  }
+};
+
+// The best k of one row's candidates stay (the whole warp works on the row of
+// one lane): the largest value that at least k of the keys reach is narrowed
+// down two bits a step, until few enough candidates lie at or above it.  The
+// order, ascending ids, is kept; equal keys beyond the k-th go by id.  Returns
+// the number kept, and in *bound the value that a later candidate has to pass:
+// k earlier ones reach it.
+__device__ __noinline__ int cut_candidates(uint64_t* cand, int n, int k, float* bound) {
+  constexpr int P = kTokCap / 32;
+  const int lane = threadIdx.x & 31;
+  uint64_t w[P];
+  uint32_t lo = 0xffffffffu, hi = 0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    w[i] = i * 32 + lane < n ? cand[i * 32 + lane] : 0;  // no real key is 0
+    const uint32_t key = (uint32_t)(w[i] >> 32);
+    if (key) lo = min(lo, key);
+    hi = max(hi, key);
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  int shift = (32 - __clz(lo ^ hi) + 1) & ~1;  // even; bits below it may differ
+  lo = shift >= 32 ? 0u : lo >> shift << shift;
+  int above = n;                                // candidates at or above lo
+  while (above > k + 16 && (shift -= 2) >= 0) {
+    uint32_t c[3] = {0, 0, 0};
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      const uint32_t test = lo | ((uint32_t)(q + 1) << shift);
+#pragma unroll
+      for (int i = 0; i < P; ++i) c[q] += (uint32_t)(w[i] >> 32) >= test;
+      c[q] = __reduce_add_sync(0xffffffffu, c[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      if (c[q] >= (uint32_t)k) above = (int)c[q];
+    lo |= (uint32_t)((c[0] >= (uint32_t)k) + (c[1] >= (uint32_t)k) + (c[2] >= (uint32_t)k))
+          << shift;
+  }
+  int ties = n;  // candidates equal to lo that stay
+  if (above > k + 16) {
+    uint32_t more = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) more += (uint32_t)(w[i] >> 32) > lo;
+    ties = k - (int)__reduce_add_sync(0xffffffffu, more);
+  }
+  int kept = 0, seen = 0;
+  __syncwarp();  // every lane has read the row
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const uint32_t key = (uint32_t)(w[i] >> 32);
+    const bool tie = key == lo && w[i] != 0;
+    const uint32_t tb = __ballot_sync(0xffffffffu, tie);
+    const uint32_t below = (1u << lane) - 1u;
+    const bool keep = key > lo || (tie && seen + __popc(tb & below) < ties);
+    const uint32_t kb = __ballot_sync(0xffffffffu, keep);
+    if (keep) cand[kept + __popc(kb & below)] = w[i];
+    kept += __popc(kb);
+    seen += __popc(tb);
+  }
+  __syncwarp();
+  *bound = key_value(lo);
+  return kept;
+}
+
+// Token log-probabilities: the sums of one (row, half) over the item's tiles,
+// and its candidates.  Rows of ignored tokens and rows behind the last are
+// computed along and not stored.
+template <int BN, bool TOP>
+struct TokEpi {
+  LpFold f;
+  float zy, bound;
+  int64_t row, y;
+  bool row_ok;
+  int count;
+  uint64_t* cand;
+
+  __device__ __forceinline__ void begin(const TcParams& P, int64_t row_, int split, int half) {
+    const TcTokArgs& a = P.tok;
+    f.init(a.k2);
+    row = row_;
+    row_ok = row < a.n;
+    y = (row_ok && a.tokens) ? a.tokens[row] : -1;
+    if (a.tokens && y == a.ignore) row_ok = false;
+    zy = 0.f;
+    if (TOP) {
+      bound = __int_as_float(0x7fffffff);  // NaN: every logit passes
+      count = 0;
+      cand = a.cand + ((int64_t)(split * 2 + half) * a.n + (row_ok ? row : 0)) * kTokCap;
+    }
+  }
+  // 32 columns; called by the whole warp
+  __device__ __forceinline__ void chunk(const TcParams& P, float* v, int64_t col0) {
+    const TcTokArgs& a = P.tok;
+    const int nv = valid_cols(a.vocab - col0, 32);
+    if (nv <= 0) return;
+    if (nv < 32) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j >= nv) v[j] = neg_inf();
+    }
+    if (row_ok) {
+      float m = max_nan(v[0], v[1]);
+#pragma unroll
+      for (int j = 2; j < 32; j += 2) m = max_nan(m, max_nan(v[j], v[j + 1]));
+      if (m != neg_inf()) {
+        f.expect(m);
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) f.add_pair(v[j], v[j + 1]);
+      }
+      if (y >= col0 && y < col0 + nv) zy = pick32(v, (int)(y - col0));
+      if (TOP && !(m <= bound)) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (!(v[j] <= bound) && j < nv)
+            cand[count++] = cand_word(order_key(v[j]), (uint32_t)(col0 + j));
+      }
+    }
+    if (TOP) cut(P, kTokCap - 32);
+  }
+  // Cut the rows of this warp that hold more than `most` candidates.
+  __device__ __forceinline__ void cut(const TcParams& P, int most) {
+    uint32_t todo = __ballot_sync(0xffffffffu, row_ok && count > most);
+    while (todo) {
+      const int l = __ffs(todo) - 1;
+      todo &= todo - 1;
+      __syncwarp();  // lane l's stores before the others' reads
+      uint64_t* c = reinterpret_cast<uint64_t*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(cand), l));
+      const int n = __shfl_sync(0xffffffffu, count, l);
+      float b;
+      const int kept = cut_candidates(c, n, P.tok.topk, &b);
+      if ((threadIdx.x & 31) == l) {
+        count = kept;
+        bound = b;
+      }
+    }
+  }
+  __device__ __forceinline__ void end(const TcParams& P, int split, int half) {
+    const TcTokArgs& a = P.tok;
+    if (TOP) cut(P, a.topk + 16);
+    if (!row_ok) return;
+    const int64_t at = (int64_t)(split * 2 + half) * a.n + row;
+    const LpState st = f.state();
+    a.sums[at] = make_float4(st.m, st.s, st.t, zy);
+    if (TOP) a.count[at] = count;
   }
 };
 
@@ -659,6 +814,20 @@ __device__ __forceinline__ void grad32_any(int gv, int pw, float* vs, const floa
   }
 }
 
+__device__ __forceinline__ LpGradArgs tok_grad_args(const TcTokGradArgs& a) {
+  LpGradArgs g;
+  g.vocab = a.vocab;
+  g.inv_t = a.inv_t;
+  g.k2 = a.k2;
+  g.tokens = a.tokens;
+  g.ignore = a.ignore;
+  g.stats = a.stats;
+  g.d_lp = a.d_lp;
+  g.d_ent = a.d_ent;
+  g.status = a.status;
+  return g;
+}
+
 // ------------------------------------------------------------------ kernel
 template <int EPI, int BN, bool HAS_T, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcParams P) {
@@ -680,7 +849,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
   S.acc_empty = bars + 16 * C::STAGES + 16;   // [2]
   S.drain = bars + 16 * C::STAGES + 32;       // [1]
   S.abort_flag = abort_flag;
-  S.status = EPI == EPI_FWD ? P.fwd.status : EPI == EPI_GRAD ? P.grad.status : P.gemm.status;
+  S.status = EPI == EPI_FWD    ? P.fwd.status
+             : EPI == EPI_GRAD ? P.grad.status
+             : EPI == EPI_GEMM ? P.gemm.status
+             : EPI == EPI_TOKG ? P.tokg.status
+                               : P.tok.status;
   S.cluster_acquire = false;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -856,12 +1029,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
       int m_tile, split, t0, t1;
       item_range(P, item, m_tile, split, t0, t1);
       const int64_t tile_row = (int64_t)m_tile * C::ROWS + r_in_pair;
-      FwdEpi<BN> fe;
-      if (EPI == EPI_FWD) fe.begin(P, tile_row, t0, half);
-      // gradient epilogue: the row's constants, loaded while the MMAs run
-      GradRow gr;
       int64_t g_row = 0, g_y = -1;
       bool g_ok = false;
+      FwdEpi<BN> fe;
+      if (EPI == EPI_FWD) fe.begin(P, tile_row, t0, half);
+      TokEpi<BN, EPI == EPI_TOP> te;
+      if constexpr (EPI == EPI_TOK || EPI == EPI_TOP) te.begin(P, tile_row, split, half);
+      LpGradRow tg;
+      if constexpr (EPI == EPI_TOKG) {
+        g_row = tile_row;
+        g_ok = g_row < P.tokg.rc;
+        if (g_ok) tg = lp_grad_row(tok_grad_args(P.tokg), P.tokg.r0 + g_row);
+      }
+      // gradient epilogue: the row's constants, loaded while the MMAs run
+      GradRow gr;
       if constexpr (EPI == EPI_GRAD) {
         const TcGradArgs& a = P.grad;
         g_row = a.r0 + tile_row;
@@ -978,6 +1159,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
               if (want_gt) store_bf16x32(a.gt + (row - a.r0) * a.ldg + lc0, vt, nv, a.ldg);
             }
           }
+        } else if constexpr (EPI == EPI_TOK || EPI == EPI_TOP) {
+#pragma unroll 1
+          for (int cc = 0; cc < BN / 2; cc += 32) {
+            const int col_in_tile = half * (BN / 2) + cc;
+            float v[32];
+            __syncwarp();
+            tmem_ld16(tbase + col_in_tile, v);
+            tmem_ld16(tbase + col_in_tile + 16, v + 16);
+            tmem_ld_wait();
+            te.chunk(P, v, (int64_t)t * BN + col_in_tile);
+          }
+        } else if constexpr (EPI == EPI_TOKG) {
+          const TcTokGradArgs& a = P.tokg;
+#pragma unroll 1
+          for (int cc = 0; cc < BN / 2; cc += 32) {
+            const int col_in_tile = half * (BN / 2) + cc;
+            const int64_t lc0 = (int64_t)t * BN + col_in_tile;  // column within the chunk
+            float v[32];
+            __syncwarp();
+            tmem_ld16(tbase + col_in_tile, v);
+            tmem_ld16(tbase + col_in_tile + 16, v + 16);
+            tmem_ld_wait();
+            const int nv = valid_cols(a.cc - lc0, 32);
+            if (g_ok && nv > 0) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) lp_grad_pair(v[j], v[j + 1], tg, a.k2);
+              const int64_t jy = tg.y - (a.c0 + lc0);
+              if (tg.y >= 0 && jy >= 0 && jy < 32) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = fmaf(j == (int)jy ? 1.f : 0.f, tg.cy, v[j]);
+              }
+              store_bf16x32(a.g + g_row * a.ldg + lc0, v, nv, a.ldg, tg.live);
+            }
+          }
         } else {  // EPI_GEMM
           const TcGemmArgs& a = P.gemm;
           const int64_t row = tile_row;
@@ -1058,6 +1273,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
         }
       }
       if (EPI == EPI_FWD && ok) fe.end(P, split, half);
+      if constexpr (EPI == EPI_TOK || EPI == EPI_TOP) {
+        if (ok) te.end(P, split, half);
+      }
     }
   }
   tc_fence_before();
@@ -1283,6 +1501,49 @@ int launch_tc_grad(const TcGradArgs& a, int num_sms, cudaStream_t s) {
                  : launch<EPI_GRAD, 128, false, false>(P, num_sms, s);
   return has_t ? launch<EPI_GRAD, 256, true, false>(P, num_sms, s)
                : launch<EPI_GRAD, 256, false, false>(P, num_sms, s);
+}
+
+// One GEMM side, H rows [r0, r0 + rows) against W rows [c0, c0 + cols).
+static bool setup_tok(TcParams& P, const void* h, const void* w, int64_t n, int64_t vocab,
+                      int64_t d, bool pair, int64_t r0, int64_t rows, int64_t c0, int64_t cols) {
+  TcFwdArgs f;
+  memset(&f, 0, sizeof(f));
+  f.h_s = h;
+  f.w_s = w;
+  f.n = n;
+  f.vocab = vocab;
+  f.d_s = d;
+  f.s_gemm = 1;
+  return setup_segments(P, f, 256, pair ? 128 : 256, tc_tile_rows(pair), r0, rows, c0, cols);
+}
+
+int launch_tc_tok(const TcTokArgs& a, int num_sms, cudaStream_t s) {
+  TcParams P;
+  memset(&P, 0, sizeof(P));
+  const bool pair = tc_use_pairs();
+  if (!setup_tok(P, a.h, a.w, a.n, a.vocab, a.d, pair, 0, a.n, 0, a.vocab)) return fail_map();
+  P.n_splits = a.n_splits;
+  P.items = P.m_tiles * P.n_splits;
+  P.m_band = band_tiles(P, tc_tile_rows(pair));
+  P.tok = a;
+  if (a.topk)
+    return pair ? launch<EPI_TOP, 256, false, true>(P, num_sms, s)
+                : launch<EPI_TOP, 256, false, false>(P, num_sms, s);
+  return pair ? launch<EPI_TOK, 256, false, true>(P, num_sms, s)
+              : launch<EPI_TOK, 256, false, false>(P, num_sms, s);
+}
+
+int launch_tc_tok_grad(const TcTokGradArgs& a, int num_sms, cudaStream_t s) {
+  TcParams P;
+  memset(&P, 0, sizeof(P));
+  const bool pair = tc_use_pairs();
+  if (!setup_tok(P, a.h, a.w, a.n, a.vocab, a.d, pair, a.r0, a.rc, a.c0, a.cc)) return fail_map();
+  P.n_splits = P.n_tiles;  // one tile per item
+  P.items = P.m_tiles * P.n_tiles;
+  P.m_band = band_tiles(P, tc_tile_rows(pair));
+  P.tokg = a;
+  return pair ? launch<EPI_TOKG, 256, false, true>(P, num_sms, s)
+              : launch<EPI_TOKG, 256, false, false>(P, num_sms, s);
 }
 
 int launch_tc_gemm(const TcGemmArgs& a, int num_sms, cudaStream_t s) {
