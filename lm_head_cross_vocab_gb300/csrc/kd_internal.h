@@ -223,14 +223,16 @@ constexpr int kTokCap = 256;    // candidates of a row and part before they are 
 struct TcTokArgs {
   const void *h, *w;
   int64_t n, vocab, d;
+  int64_t h_rows;          // rows of h (>= n; those behind n are computed along)
   const int64_t* tokens;   // may be NULL
   int64_t ignore;
   float k2;                // log2(e) / T
   int topk;
   int n_splits;            // parts: 2 per split
   float4* sums;            // [parts][n]: max z, s, t, z[token] (0 in the parts without it)
-  uint64_t* cand;          // [parts][n][kTokCap]
+  uint64_t* cand;          // [parts][n][kTokCap]: logit << 32 | complement of the id
   int32_t* count;          // [parts][n]
+  float* pub;              // [parts][n] values the parts publish, NaN before
   uint32_t* status;
 };
 int launch_tc_tok(const TcTokArgs& a, int num_sms, cudaStream_t s);

@@ -618,6 +618,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
 // ------------------------------------------------------------------ joining parts
 // Hidden sources: the records of the tensor-core epilogue, one per part (half a
 // tile of a vocabulary split) and row.
+constexpr int kMaxSplits = 128;
+
 struct LpJoin {
   LpArgs a;
   const float4* sums;      // [parts][n]
@@ -630,10 +632,17 @@ struct LpJoin {
 __device__ __forceinline__ LpState join_sums(const LpJoin& j, int64_t r, float& zy) {
   LpState st{neg_inf(), 0.f, 0.f};
   zy = 0.f;
-  for (int p = threadIdx.x & 31; p < j.parts; p += 32) {
-    const float4 q = j.sums[(int64_t)p * j.a.n + r];
-    lp_merge(st, LpState{q.x, q.y, q.z}, j.a.k2);
-    zy += q.w;
+  for (int p0 = threadIdx.x & 31; p0 < j.parts; p0 += 8 * 32) {
+    float4 q[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      q[u] = p0 + 32 * u < j.parts ? j.sums[(int64_t)(p0 + 32 * u) * j.a.n + r]
+                                   : make_float4(neg_inf(), 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      lp_merge(st, LpState{q[u].x, q[u].y, q[u].z}, j.a.k2);
+      zy += q[u].w;
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -679,6 +688,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_logprob_join_top(LpJoin j) {
   __shared__ SelectShared sh;
   __shared__ LpRow row;
   __shared__ uint64_t last;
+  __shared__ int first[2 * kMaxSplits + 1];
   const LpArgs& a = j.a;
   const int64_t r = blockIdx.x;
   const int tid = threadIdx.x, k = a.topk;
@@ -687,26 +697,72 @@ __global__ void __launch_bounds__(kJoinThreads) k_logprob_join_top(LpJoin j) {
     lp_store_ignored(a, r);
     return;
   }
-  // a warp a part, its lanes over the part's candidates
+  // candidates of all parts, numbered through: part p's from first[p] on
+  if (tid < 32) {
+    int c[2 * kMaxSplits / 32], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 2 * kMaxSplits / 32; ++i)
+      c[i] = 32 * i + tid < j.parts ? j.count[(int64_t)(32 * i + tid) * a.n + r] : 0;
+#pragma unroll
+    for (int i = 0; i < 2 * kMaxSplits / 32; ++i) {
+      int up = c[i];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int q = __shfl_up_sync(0xffffffffu, up, o);
+        if (tid >= o) up += q;
+      }
+      if (32 * i + tid < j.parts) first[32 * i + tid] = sum + up - c[i];
+      sum += __shfl_sync(0xffffffffu, up, 31);
+    }
+    if (tid == 0) {
+      first[j.parts] = sum;
+      sh.count = 0;
+    }
+  } else if (tid < 64) {
+    float zy;
+    const LpRow q = lp_finish(join_sums(j, r, zy));
+    if (tid == 32) {
+      row = q;
+      join_store(j, r, y, q, zy);
+    }
+  }
+  __syncthreads();
+  const int total = first[j.parts];
+  auto word = [&](int i) -> uint64_t {
+    int lo = 0, hi = j.parts;  // first[lo] <= i < first[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first[mid] <= i) lo = mid;
+      else hi = mid;
+    }
+    const uint64_t w = j.cand[((int64_t)lo * a.n + r) * kTokCap + (i - first[lo])];
+    return cand_word(order_key(__uint_as_float((uint32_t)(w >> 32))), ~(uint32_t)w);
+  };
+  constexpr int kHeld = 4;  // words a thread holds; those behind are read again
+  uint64_t held[kHeld];
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) {
+    const int i = tid + u * kJoinThreads;
+    held[u] = i < total ? word(i) : 0;
+  }
   auto each = [&](auto&& f) {
-    for (int p = tid >> 5; p < j.parts; p += kJoinThreads / 32) {
-      const int64_t at = (int64_t)p * a.n + r;
-      const int n = j.count[at];
-      for (int i = tid & 31; i < n; i += 32) f(j.cand[at * kTokCap + i]);
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u)
+      if (held[u]) f(held[u]);
+#pragma unroll 1
+    for (int i0 = tid + kHeld * kJoinThreads; i0 < total; i0 += kHeld * kJoinThreads) {
+      uint64_t w[kHeld];
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u)
+        w[u] = i0 + u * kJoinThreads < total ? word(i0 + u * kJoinThreads) : 0;
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u)
+        if (w[u]) f(w[u]);
     }
   };
   uint64_t best = 0;
   each([&](uint64_t w) { best = max(best, w); });
   own_key[tid] = (uint16_t)(best >> 48);
-  if (tid == 0) sh.count = 0;
-  float zy;
-  if (tid < 32) {
-    const LpRow q = lp_finish(join_sums(j, r, zy));
-    if (tid == 0) {
-      row = q;
-      join_store(j, r, y, q, zy);
-    }
-  }
   __syncthreads();
   if (tid < 32) bound_key<kJoinThreads>(own_key, k, &sh.bound);
   __syncthreads();
@@ -934,9 +990,18 @@ __global__ void __launch_bounds__(kRowThreads) k_mask_rows(const T* __restrict__
   }
 }
 
+// rows >= n behind the first n: zeros
+__global__ void __launch_bounds__(kRowThreads) k_pad_rows(const uint4* __restrict__ h, int64_t n,
+                                                          int64_t vecs, uint4* __restrict__ out) {
+  const int64_t r = blockIdx.x;
+  for (int64_t i = threadIdx.x; i < vecs; i += kRowThreads)
+    out[r * vecs + i] = r < n ? h[r * vecs + i] : make_uint4(0, 0, 0, 0);
+}
+
 // ------------------------------------------------------------------ plan
 constexpr size_t kAlign = 256;
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
@@ -949,7 +1014,7 @@ struct LpPlan {
   int splits;               // its vocabulary splits
   int64_t fr;               // forward: rows a launch takes
   int64_t R, C;             // backward: chunk of G
-  size_t f_z, f_sums, f_count, f_cand, f_bytes;
+  size_t f_z, f_h, f_sums, f_count, f_pub, f_cand, f_bytes;
   size_t b_h, b_g, b_dh, b_dw, b_bytes;
 };
 
@@ -964,18 +1029,23 @@ T* at(void* ws, size_t off) {
 }
 
 // Rows of one fused launch: bounds the candidates' workspace.
-constexpr int64_t kFusedRows = 16384;
+constexpr int64_t kFusedRows = 8192;
+// Fewer rows than kFewRows are copied into kPadRows, zeros behind them: with
+// one row every SM fetches the same few lines of H at the same time, which
+// halves the rate at which W arrives (one row of D 4096 against 151936 columns:
+// 320 us as it is, 199 us from 16 rows on, whatever they hold).
+constexpr int64_t kFewRows = 16, kPadRows = 64;
 
 // Vocabulary splits of the fused forward: the smallest makespan, in tiles, of
 // m_tiles * s items on `workers` CTAs (pairs).  An item costs more than its
-// tiles: its record, and with alternatives the first tiles, of which nearly
-// every logit becomes a candidate.
+// tiles: its record, and with alternatives the first tile, of which nearly every
+// logit is listed, and the parts' candidates in the join.
 int tok_splits(int64_t m_tiles, int64_t n_tiles, int workers, bool topk) {
   int best = 1;
   double best_cost = 1e300;
-  for (int64_t s = 1; s <= std::min<int64_t>(n_tiles, 128); ++s) {
-    const int64_t waves = cdiv(m_tiles * s, workers);
-    const double cost = (double)waves * ((double)cdiv(n_tiles, s) + (topk ? 1.0 : 0.02));
+  for (int64_t s = 1; s <= std::min<int64_t>(n_tiles, kMaxSplits); ++s) {
+    const int64_t rounds = cdiv(m_tiles * s, workers);
+    const double cost = (double)rounds * ((double)cdiv(n_tiles, s) + (topk ? 1.0 : 0.02));
     if (cost < best_cost - 1e-9) {
       best_cost = cost;
       best = (int)s;
@@ -1019,10 +1089,12 @@ kd_status lp_plan(const kd_logprob_problem* p, LpPlan& P) {
     P.fr = std::min<int64_t>(n, kFusedRows);
     P.splits = tok_splits(cdiv(P.fr, tc_tile_rows(pair)), cdiv(P.v, 256),
                           pair ? std::max(1, P.nsm / 2) : P.nsm, p->topk > 0);
+    if (n < kFewRows) P.f_h = take(off, (size_t)kPadRows * P.d * 2);
     const size_t recs = (size_t)2 * P.splits * P.fr;
     P.f_sums = take(off, recs * sizeof(float4));
     if (p->topk > 0) {
       P.f_count = take(off, recs * 4);
+      P.f_pub = take(off, recs * 4);
       P.f_cand = take(off, recs * kTokCap * 8);
     }
   } else {
@@ -1038,8 +1110,15 @@ kd_status lp_plan(const kd_logprob_problem* p, LpPlan& P) {
   q.vocab = P.v;
   q.d_student = P.d;
   q.student = KD_STUDENT_HIDDEN;
-  if (P.bf16) choose_chunk(&q, (int64_t)64 << 20, 256, 4, P.R, P.C);
-  else choose_chunk(&q, (int64_t)8 << 20, 64, 8, P.R, P.C);
+  const int64_t quant = P.bf16 ? 256 : 64;
+  if (round_up(n, 128) * round_up(P.v, quant) <= (int64_t)8 << 20) {
+    P.R = round_up(n, 128);  // little enough to take whole
+    P.C = round_up(P.v, quant);
+  } else if (P.bf16) {
+    choose_chunk(&q, (int64_t)64 << 20, quant, 4, P.R, P.C);
+  } else {
+    choose_chunk(&q, (int64_t)8 << 20, quant, 8, P.R, P.C);
+  }
   off = 0;
   const size_t esz = P.bf16 ? 2 : 4;
   P.b_h = take(off, (size_t)n * P.d * esz);
@@ -1153,6 +1232,14 @@ extern "C" kd_status kd_logprob_fwd(const kd_logprob_problem* p, const kd_logpro
       TcTokArgs t;
       memset(&t, 0, sizeof(t));
       t.h = static_cast<const __nv_bfloat16*>(in->h) + r0 * P.d;
+      t.h_rows = a.n;
+      if (a.n < kFewRows && P.n < kFewRows) {
+        note_launch();
+        k_pad_rows<<<(unsigned)kPadRows, kRowThreads, 0, s>>>(
+            static_cast<const uint4*>(t.h), a.n, P.d / 8, at<uint4>(workspace, P.f_h));
+        t.h = at<char>(workspace, P.f_h);
+        t.h_rows = kPadRows;
+      }
       t.w = in->w;
       t.n = a.n;
       t.vocab = P.v;
@@ -1165,6 +1252,9 @@ extern "C" kd_status kd_logprob_fwd(const kd_logprob_problem* p, const kd_logpro
       t.sums = at<float4>(workspace, P.f_sums);
       t.cand = at<uint64_t>(workspace, P.f_cand);
       t.count = at<int32_t>(workspace, P.f_count);
+      t.pub = at<float>(workspace, P.f_pub);
+      if (k && cudaMemsetAsync(t.pub, 0xff, (size_t)2 * P.splits * a.n * 4, s) != cudaSuccess)
+        return KD_ERR_CUDA;
       t.status = dev_status;
       if (launch_tc_tok(t, P.nsm, s)) return KD_ERR_CUDA;
       const LpJoin j{a, t.sums, t.cand, t.count, 2 * P.splits};

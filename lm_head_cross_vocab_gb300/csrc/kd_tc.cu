@@ -46,6 +46,8 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
+#include <utility>
 
 #include "kd_internal.h"
 #include "kd_logprob.cuh"
@@ -135,6 +137,16 @@ __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) 
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
+               : "memory");
+}
+// Arrivals that order no memory: for a barrier that only guards TMEM (its reads
+// are complete after tcgen05.wait::ld).  A releasing arrival would first wait
+// for the thread's global stores, thousands of cycles behind the operands' copies.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
                : "memory");
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
@@ -298,6 +310,7 @@ struct TcParams {  // (128-byte aligned by its tensor maps)
   int a_mn[2], b_mn[2];  // 1: the operand is stored MN-major ([K, M] / [K, N])
   int m_tiles, n_tiles, n_splits, items;
   int m_band;         // row tiles per band of the item order (see item_range)
+  int split_first;    // 1: the splits of a row tile follow one another instead
   int acc_stride;     // TMEM columns per accumulator stage
   int acc_stages;     // 1 or 2 accumulator stages in the 512 allocated columns
   int logits_vec;     // materialised logits rows are 16-byte aligned
@@ -373,8 +386,13 @@ __device__ __forceinline__ void item_range(const TcParams& P, int item, int& m_t
   const int band = item / per_band, idx = item - band * per_band;
   const int m0 = band * P.m_band;
   const int mb = min(P.m_band, P.m_tiles - m0);  // row tiles in this band
-  m_tile = m0 + idx % mb;
-  split = idx / mb;
+  if (P.split_first) {
+    m_tile = m0 + idx / P.n_splits;
+    split = idx % P.n_splits;
+  } else {
+    m_tile = m0 + idx % mb;
+    split = idx / mb;
+  }
   t0 = (int)((int64_t)P.n_tiles * split / P.n_splits);
   t1 = (int)((int64_t)P.n_tiles * (split + 1) / P.n_splits);
 }
@@ -473,80 +491,209 @@ struct FwdEpi {
   }
 };
 
-// The best k of one row's candidates stay (the whole warp works on the row of
-// one lane): the largest value that at least k of the keys reach is narrowed
-// down two bits a step, until few enough candidates lie at or above it.  The
-// order, ascending ids, is kept; equal keys beyond the k-th go by id.  Returns
-// the number kept, and in *bound the value that a later candidate has to pass:
-// k earlier ones reach it.
-__device__ __noinline__ int cut_candidates(uint64_t* cand, int n, int k, float* bound) {
+// The best k candidates of each row in `rows` (one row a lane) stay; the whole
+// warp works on one row after the other, the next one's words under way.  The
+// largest value that at least k of a row's keys reach is narrowed down two bits
+// a step, until few enough candidates lie at or above it.  The order, ascending
+// ids, is kept; equal keys beyond the k-th go by id.  The lane of a row gets the
+// number kept, and in *bound a value that k of them reach: a later candidate
+// has to pass it.
+__device__ __noinline__ void cut_candidates(uint32_t rows, uint64_t* cand, int* count,
+                                            float* bound, int k) {
   constexpr int P = kTokCap / 32;
   const int lane = threadIdx.x & 31;
-  uint64_t w[P];
-  uint32_t lo = 0xffffffffu, hi = 0;
+  const unsigned long long mine = reinterpret_cast<unsigned long long>(cand);
+  uint64_t w[P], next[P];
+  int n = 0, l = 0;
+  auto fetch = [&](int row, uint64_t* v) {
+    const uint64_t* c = reinterpret_cast<const uint64_t*>(__shfl_sync(0xffffffffu, mine, row));
+    const int m = __shfl_sync(0xffffffffu, *count, row);
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    w[i] = i * 32 + lane < n ? cand[i * 32 + lane] : 0;  // no real key is 0
-    const uint32_t key = (uint32_t)(w[i] >> 32);
-    if (key) lo = min(lo, key);
-    hi = max(hi, key);
-  }
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  hi = __reduce_max_sync(0xffffffffu, hi);
-  int shift = (32 - __clz(lo ^ hi) + 1) & ~1;  // even; bits below it may differ
-  lo = shift >= 32 ? 0u : lo >> shift << shift;
-  int above = n;                                // candidates at or above lo
-  while (above > k + 16 && (shift -= 2) >= 0) {
-    uint32_t c[3] = {0, 0, 0};
+    for (int i = 0; i < P; ++i) v[i] = i * 32 + lane < m ? c[i * 32 + lane] : 0;
+    return m;
+  };
+  __syncwarp();  // the rows' stores before these loads
+  int l_next = __ffs(rows) - 1;
+  int n_next = fetch(l_next, next);
+  while (rows) {
+    rows &= rows - 1;
+    l = l_next;
+    n = n_next;
 #pragma unroll
-    for (int q = 0; q < 3; ++q) {
-      const uint32_t test = lo | ((uint32_t)(q + 1) << shift);
-#pragma unroll
-      for (int i = 0; i < P; ++i) c[q] += (uint32_t)(w[i] >> 32) >= test;
-      c[q] = __reduce_add_sync(0xffffffffu, c[q]);
+    for (int i = 0; i < P; ++i) w[i] = next[i];
+    if (rows) {
+      l_next = __ffs(rows) - 1;
+      n_next = fetch(l_next, next);
     }
+    uint32_t key[P], lo = 0xffffffffu, hi = 0;
 #pragma unroll
-    for (int q = 0; q < 3; ++q)
-      if (c[q] >= (uint32_t)k) above = (int)c[q];
-    lo |= (uint32_t)((c[0] >= (uint32_t)k) + (c[1] >= (uint32_t)k) + (c[2] >= (uint32_t)k))
-          << shift;
-  }
-  int ties = n;  // candidates equal to lo that stay
-  if (above > k + 16) {
-    uint32_t more = 0;
+    for (int i = 0; i < P; ++i) {
+      // no real key is 0
+      key[i] = i * 32 + lane < n ? order_key(__uint_as_float((uint32_t)(w[i] >> 32))) : 0;
+      if (key[i]) lo = min(lo, key[i]);
+      hi = max(hi, key[i]);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    int shift = (32 - __clz(lo ^ hi) + 1) & ~1;  // even; bits below it may differ
+    lo = shift >= 32 ? 0u : lo >> shift << shift;
+    int above = n;  // candidates at or above lo
+    while (above > k + 16 && (shift -= 2) >= 0) {
+      uint32_t c[3] = {0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < P; ++i) more += (uint32_t)(w[i] >> 32) > lo;
-    ties = k - (int)__reduce_add_sync(0xffffffffu, more);
-  }
-  int kept = 0, seen = 0;
-  __syncwarp();  // every lane has read the row
+      for (int q = 0; q < 3; ++q) {
+        const uint32_t test = lo | ((uint32_t)(q + 1) << shift);
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const uint32_t key = (uint32_t)(w[i] >> 32);
-    const bool tie = key == lo && w[i] != 0;
-    const uint32_t tb = __ballot_sync(0xffffffffu, tie);
-    const uint32_t below = (1u << lane) - 1u;
-    const bool keep = key > lo || (tie && seen + __popc(tb & below) < ties);
-    const uint32_t kb = __ballot_sync(0xffffffffu, keep);
-    if (keep) cand[kept + __popc(kb & below)] = w[i];
-    kept += __popc(kb);
-    seen += __popc(tb);
+        for (int i = 0; i < P; ++i) c[q] += key[i] >= test;
+        c[q] = __reduce_add_sync(0xffffffffu, c[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+        if (c[q] >= (uint32_t)k) above = (int)c[q];
+      lo |= (uint32_t)((c[0] >= (uint32_t)k) + (c[1] >= (uint32_t)k) + (c[2] >= (uint32_t)k))
+            << shift;
+    }
+    int ties = n;  // candidates equal to lo that stay
+    if (above > k + 16) {
+      uint32_t more = 0;
+#pragma unroll
+      for (int i = 0; i < P; ++i) more += key[i] > lo;
+      ties = k - (int)__reduce_add_sync(0xffffffffu, more);
+    }
+    uint64_t* c = reinterpret_cast<uint64_t*>(__shfl_sync(0xffffffffu, mine, l));
+    int kept = 0, seen = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const bool tie = key[i] == lo && key[i] != 0;
+      const uint32_t tb = __ballot_sync(0xffffffffu, tie);
+      const uint32_t below = (1u << lane) - 1u;
+      const bool keep = key[i] > lo || (tie && seen + __popc(tb & below) < ties);
+      const uint32_t kb = __ballot_sync(0xffffffffu, keep);
+      if (keep) c[kept + __popc(kb & below)] = w[i];
+      kept += __popc(kb);
+      seen += __popc(tb);
+    }
+    if (lane == l) {
+      *count = kept;
+      *bound = key_value(lo);
+    }
   }
   __syncwarp();
-  *bound = key_value(lo);
-  return kept;
 }
 
 // Token log-probabilities: the sums of one (row, half) over the item's tiles,
 // and its candidates.  Rows of ignored tokens and rows behind the last are
 // computed along and not stored.
+//
+// A logit becomes a candidate unless k logits of its row are known to be better:
+//   floor  every part keeps the kLead best of its columns' maxima by fours and
+//          publishes the least of them; where q parts, q kLead >= k, have
+//          published at least x, k logits of the row reach x, and what lies
+//          below x is out.  The parts run side by side, so this is close to the
+//          k-th best of all they have seen.
+//   bound  when a part's list is full all the same (rows of rising logits), it
+//          is cut to its own best k, and what does not pass the k-th is out.
+// What the others have published when a part reads it changes which candidates
+// are kept, never which come out on top.  A load takes long here, behind the
+// operands' copies (5 to 10 us where those are bound by HBM): the floor is read
+// in one batch, which a whole tile's work covers once there is one at all.
+constexpr int kLead = 8;
+constexpr int kRead = 32;  // published values read at most (fewer: a weaker floor, as true)
+
+__device__ __forceinline__ float ld_relaxed(const float* p) {
+  float v;
+  asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void st_relaxed(float* p, float v) {
+  asm volatile("st.relaxed.gpu.global.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
+}
+__device__ __forceinline__ void order2(float& a, float& b) {  // the larger one first
+  const float hi = fmaxf(a, b);
+  b = fminf(a, b);
+  a = hi;
+}
+// Descending order of a list that rises and then falls, or falls and then rises.
+__device__ __forceinline__ void order_bitonic8(float* v) {
+#pragma unroll
+  for (int step = 4; step > 0; step >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((i & step) == 0) order2(v[i], v[i + step]);
+}
+// The 8 largest of a descending list and 8 values in any order, descending.
+__device__ __forceinline__ void merge_lead(float* lead, float* v) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) order2(v[i + ((i >> 1) & 1)], v[i + 1 - ((i >> 1) & 1)]);
+#pragma unroll
+  for (int i = 0; i < 8; i += 4) {
+    const int d = (i >> 2) & 1;  // the upper four ascend
+#pragma unroll
+    for (int step = 2; step > 0; step >>= 1)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if ((q & step) == 0) order2(v[i + (d ? q + step : q)], v[i + (d ? q : q + step)]);
+  }
+  order_bitonic8(v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) lead[i] = fmaxf(lead[i], v[7 - i]);
+  order_bitonic8(lead);
+}
+// Descending order of 32 values: the 191 exchanges of an odd-even merge sort.
+struct Order32 {
+  static constexpr int N = 191;
+  int lo[N], hi[N];
+  constexpr Order32() : lo(), hi() {
+    int n = 0;
+    for (int p = 1; p < 32; p *= 2)
+      for (int k = p; k >= 1; k /= 2)
+        for (int i = k % p; i + k < 32; ++i)
+          if ((i - k % p) % (2 * k) < k && i / (2 * p) == (i + k) / (2 * p)) {
+            lo[n] = i;
+            hi[n++] = i + k;
+          }
+  }
+};
+template <size_t... I>
+__device__ __forceinline__ void order32(float* v, std::index_sequence<I...>) {
+  constexpr Order32 o;
+  (order2(v[o.lo[I]], v[o.hi[I]]), ...);
+}
+// One logit to the list at c if it is not below `limit` (or either is a NaN):
+// (value, complement of the id).  Predicated, so that the 32 of a chunk do not
+// branch.
+__device__ __forceinline__ void keep_candidate(uint64_t*& c, float v, float limit, uint32_t id) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.geu.f32 p, %1, %2;\n\t"
+      "@p st.global.v2.b32 [%0], {%3, %4};\n\t"
+      "@p add.s64 %0, %0, 8;\n\t}"
+      : "+l"(c)
+      : "f"(v), "f"(limit), "r"(~id), "r"(__float_as_uint(v))
+      : "memory");
+}
+// x = v if `take`, as an instruction of its own: a chain of selects over an
+// array would be made an indexed load, and the array put in local memory.
+__device__ __forceinline__ void take_if(float& x, float v, bool take) {
+  asm("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\t@p mov.f32 %0, %1;\n\t}"
+      : "+f"(x)
+      : "f"(v), "r"((int)take));
+}
+// The least float above x (x itself when it is infinite or a NaN)
+__device__ __forceinline__ float next_up(float x) {
+  if (!(fabsf(x) < __int_as_float(0x7f800000))) return x;
+  return key_value(order_key(x) + 1u);
+}
+
 template <int BN, bool TOP>
 struct TokEpi {
   LpFold f;
-  float zy, bound;
+  float zy;
+  float limit;  // what lies below it is out; NaN: nothing is
+  float lead[TOP ? kLead : 1];
   int64_t row, y;
   bool row_ok;
-  int count;
+  int count, part;
   uint64_t* cand;
 
   __device__ __forceinline__ void begin(const TcParams& P, int64_t row_, int split, int half) {
@@ -557,14 +704,22 @@ struct TokEpi {
     y = (row_ok && a.tokens) ? a.tokens[row] : -1;
     if (a.tokens && y == a.ignore) row_ok = false;
     zy = 0.f;
+    part = split * 2 + half;
     if (TOP) {
-      bound = __int_as_float(0x7fffffff);  // NaN: every logit passes
+      limit = __int_as_float(0x7fffffff);
       count = 0;
-      cand = a.cand + ((int64_t)(split * 2 + half) * a.n + (row_ok ? row : 0)) * kTokCap;
+#pragma unroll
+      for (int i = 0; i < kLead; ++i) lead[i] = neg_inf();
+      cand = a.cand + ((int64_t)part * a.n + (row_ok ? row : 0)) * kTokCap;
     }
   }
-  // 32 columns; called by the whole warp
-  __device__ __forceinline__ void chunk(const TcParams& P, float* v, int64_t col0) {
+  __device__ __forceinline__ void raise_limit(float x) {
+    if (!(x <= limit)) limit = x;  // (a NaN in either gives way)
+  }
+  // 32 columns (`more` follow in this item): the running sums and the part's best
+  // logits (SUMS), the candidates (LIST).  Called by the whole warp.
+  template <bool SUMS, bool LIST>
+  __device__ __forceinline__ void chunk(const TcParams& P, float* v, int64_t col0, bool more) {
     const TcTokArgs& a = P.tok;
     const int nv = valid_cols(a.vocab - col0, 32);
     if (nv <= 0) return;
@@ -573,53 +728,96 @@ struct TokEpi {
       for (int j = 0; j < 32; ++j)
         if (j >= nv) v[j] = neg_inf();
     }
+    bool hit = false;
     if (row_ok) {
-      float m = max_nan(v[0], v[1]);
+      float four[8], m;
 #pragma unroll
-      for (int j = 2; j < 32; j += 2) m = max_nan(m, max_nan(v[j], v[j + 1]));
-      if (m != neg_inf()) {
-        f.expect(m);
+      for (int i = 0; i < 8; ++i)
+        four[i] = max_nan(max_nan(v[4 * i], v[4 * i + 1]), max_nan(v[4 * i + 2], v[4 * i + 3]));
+      m = max_nan(max_nan(max_nan(four[0], four[1]), max_nan(four[2], four[3])),
+                  max_nan(max_nan(four[4], four[5]), max_nan(four[6], four[7])));
+      if (SUMS) {
+        if (m != neg_inf()) {
+          f.expect(m);
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) f.add_pair(v[j], v[j + 1]);
+          for (int j = 0; j < 32; j += 2) f.add_pair(v[j], v[j + 1]);
+        }
+        if (y >= col0 && y < col0 + nv) zy = pick32(v, (int)(y - col0));
+        if (TOP) merge_lead(lead, four);  // (a NaN does not enter)
       }
-      if (y >= col0 && y < col0 + nv) zy = pick32(v, (int)(y - col0));
-      if (TOP && !(m <= bound)) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (!(v[j] <= bound) && j < nv)
-            cand[count++] = cand_word(order_key(v[j]), (uint32_t)(col0 + j));
-      }
+      hit = LIST && !(m < limit);
     }
-    if (TOP) cut(P, kTokCap - 32);
-  }
-  // Cut the rows of this warp that hold more than `most` candidates.
-  __device__ __forceinline__ void cut(const TcParams& P, int most) {
-    uint32_t todo = __ballot_sync(0xffffffffu, row_ok && count > most);
-    while (todo) {
-      const int l = __ffs(todo) - 1;
-      todo &= todo - 1;
-      __syncwarp();  // lane l's stores before the others' reads
-      uint64_t* c = reinterpret_cast<uint64_t*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(cand), l));
-      const int n = __shfl_sync(0xffffffffu, count, l);
-      float b;
-      const int kept = cut_candidates(c, n, P.tok.topk, &b);
-      if ((threadIdx.x & 31) == l) {
-        count = kept;
-        bound = b;
+    if (!LIST) return;
+    if (__any_sync(0xffffffffu, hit)) {
+      if (hit) {
+        uint64_t* c = cand + count;
+        if (nv == 32) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) keep_candidate(c, v[j], limit, (uint32_t)(col0 + j));
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < nv; ++j)
+            keep_candidate(c, pick32(v, j), limit, (uint32_t)(col0 + j));
+        }
+        count = (int)(c - cand);
       }
+      if (more) cut(P);
     }
   }
-  __device__ __forceinline__ void end(const TcParams& P, int split, int half) {
+  // Cut the rows of this warp whose lists may overflow in the next 32 columns.
+  __device__ __forceinline__ void cut(const TcParams& P) {
+    const bool full = row_ok && count > kTokCap - 32;
+    const uint32_t rows = __ballot_sync(0xffffffffu, full);
+    if (!rows) return;
+    int n = count;
+    float b;
+    cut_candidates(rows, cand, &n, &b, P.tok.topk);
+    if (full) {
+      count = n;
+      raise_limit(next_up(b));
+    }
+  }
+  __device__ __forceinline__ bool wants_floor() const {
+    return __any_sync(0xffffffffu, row_ok && limit != limit);
+  }
+  __device__ __forceinline__ void publish(const TcParams& P) {
     const TcTokArgs& a = P.tok;
-    if (TOP) cut(P, a.topk + 16);
+    if (row_ok && lead[kLead - 1] > neg_inf())
+      st_relaxed(a.pub + (int64_t)part * a.n + row, lead[kLead - 1]);
+  }
+  // Published values of this row, spread evenly over the parts from this one on.
+  __device__ __forceinline__ void ask(const TcParams& P, float* v) const {
+    const TcTokArgs& a = P.tok;
+    const int parts = 2 * a.n_splits;
+    const float* pub = a.pub + (row_ok ? row : 0);
+#pragma unroll
+    for (int u = 0; u < kRead; ++u) {
+      int at = part + (parts <= kRead ? u : (int)((int64_t)u * parts / kRead));
+      if (at >= parts) at -= parts;
+      v[u] = u < parts ? ld_relaxed(pub + (int64_t)at * a.n) : neg_inf();
+    }
+  }
+  __device__ __forceinline__ void answer(const TcParams& P, float* v) {
+    const int q = (P.tok.topk + kLead - 1) / kLead;
+#pragma unroll
+    for (int u = 0; u < kRead; ++u) v[u] = fmaxf(v[u], neg_inf());  // NaN: not yet published
+    order32(v, std::make_index_sequence<Order32::N>());
+    float x = neg_inf();
+#pragma unroll
+    for (int u = 0; u < kTokTopk / kLead; ++u) take_if(x, v[u], u == q - 1);
+    if (x > neg_inf()) raise_limit(x);
+  }
+  __device__ __forceinline__ void end(const TcParams& P) {
+    const TcTokArgs& a = P.tok;
     if (!row_ok) return;
-    const int64_t at = (int64_t)(split * 2 + half) * a.n + row;
+    const int64_t at = (int64_t)part * a.n + row;
     const LpState st = f.state();
     a.sums[at] = make_float4(st.m, st.s, st.t, zy);
     if (TOP) a.count[at] = count;
   }
 };
+// Tiles of an item during which the floor is asked for again.
+__device__ __forceinline__ bool ask_at(int i) { return i > 0 && (i & (i - 1)) == 0; }
 
 // 32 consecutive values of one row as bf16 (16-byte stores when aligned);
 // zeros instead when !keep (a masked row), selected on the packed words.
@@ -1160,15 +1358,38 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
             }
           }
         } else if constexpr (EPI == EPI_TOK || EPI == EPI_TOP) {
+          auto tile = [&](auto sums, auto list) {
 #pragma unroll 1
-          for (int cc = 0; cc < BN / 2; cc += 32) {
-            const int col_in_tile = half * (BN / 2) + cc;
-            float v[32];
-            __syncwarp();
-            tmem_ld16(tbase + col_in_tile, v);
-            tmem_ld16(tbase + col_in_tile + 16, v + 16);
-            tmem_ld_wait();
-            te.chunk(P, v, (int64_t)t * BN + col_in_tile);
+            for (int cc = 0; cc < BN / 2; cc += 32) {
+              const int col_in_tile = half * (BN / 2) + cc;
+              float v[32];
+              __syncwarp();
+              tmem_ld16(tbase + col_in_tile, v);
+              tmem_ld16(tbase + col_in_tile + 16, v + 16);
+              tmem_ld_wait();
+              te.template chunk<decltype(sums)::value, decltype(list)::value>(
+                  P, v, (int64_t)t * BN + col_in_tile, t + 1 < t1 || cc + 32 < BN / 2);
+            }
+          };
+          if constexpr (EPI == EPI_TOK) {
+            tile(std::true_type{}, std::false_type{});
+          } else {
+            float told[kRead];
+            const bool ask = ask_at(t - t0);
+            if (ask) te.ask(P, told);
+            if (te.wants_floor()) {
+              // no floor yet: the sums first, and what they tell is published
+              // before anything is listed, in the hope of the other parts' values
+              tile(std::true_type{}, std::false_type{});
+              te.publish(P);
+              if (!ask) te.ask(P, told);
+              te.answer(P, told);
+              tile(std::false_type{}, std::true_type{});
+            } else {
+              tile(std::true_type{}, std::true_type{});
+              te.publish(P);
+              if (ask) te.answer(P, told);
+            }
           }
         } else if constexpr (EPI == EPI_TOKG) {
           const TcTokGradArgs& a = P.tokg;
@@ -1264,8 +1485,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (PAIR) mbar_arrive_cluster(mapa_shared(S.acc_empty + 8 * acc, 0));
-          else mbar_arrive(S.acc_empty + 8 * acc);
+          const uint32_t bar = S.acc_empty + 8 * acc;
+          if constexpr (EPI == EPI_FWD || EPI == EPI_GRAD) {
+            if (PAIR) mbar_arrive_cluster(mapa_shared(bar, 0));
+            else mbar_arrive(bar);
+          } else {
+            if (PAIR) mbar_arrive_cluster_relaxed(mapa_shared(bar, 0));
+            else mbar_arrive_relaxed(bar);
+          }
         }
         if (++acc == P.acc_stages) {
           acc = 0;
@@ -1274,7 +1501,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
       }
       if (EPI == EPI_FWD && ok) fe.end(P, split, half);
       if constexpr (EPI == EPI_TOK || EPI == EPI_TOP) {
-        if (ok) te.end(P, split, half);
+        if (ok) te.end(P);
       }
     }
   }
@@ -1521,10 +1748,15 @@ int launch_tc_tok(const TcTokArgs& a, int num_sms, cudaStream_t s) {
   TcParams P;
   memset(&P, 0, sizeof(P));
   const bool pair = tc_use_pairs();
-  if (!setup_tok(P, a.h, a.w, a.n, a.vocab, a.d, pair, 0, a.n, 0, a.vocab)) return fail_map();
+  if (!setup_tok(P, a.h, a.w, a.h_rows, a.vocab, a.d, pair, 0, a.n, 0, a.vocab)) return fail_map();
   P.n_splits = a.n_splits;
   P.items = P.m_tiles * P.n_splits;
   P.m_band = band_tiles(P, tc_tile_rows(pair));
+  // Row tiles first, so that concurrent items share W; the splits of a row tile
+  // first where otherwise too few parts of a row would run side by side to make
+  // a floor.
+  const int workers = pair ? num_sms / 2 : num_sms;
+  P.split_first = a.topk && 2 * workers < P.m_tiles * ((a.topk + kLead - 1) / kLead + 1);
   P.tok = a;
   if (a.topk)
     return pair ? launch<EPI_TOP, 256, false, true>(P, num_sms, s)

@@ -324,6 +324,33 @@ def test_hidden_forward(n, v, d, k, dtype):
     assert torch.allclose(out["entropy"], ref["entropy"], rtol=0, atol=2 * es * (math.log(v) + 3))
 
 
+@pytest.mark.parametrize("n,v", [(1, 40000), (5, 6000), (1100, 20000), (9000, 3000)])
+@pytest.mark.parametrize("k", [1, 20, 128])
+def test_hidden_alternatives_of_ordered_rows(n, v, k):
+    """Rows whose logits rise or fall with the id, have long runs of equal
+    values, or are all equal (a zero hidden state), between ordinary ones, over
+    several tiles of a part; against a stable sort of the exact logits."""
+    d = 64
+    h, w = _hidden(n, v, d, "bf16", v)
+    ids = torch.arange(v)
+    w[:, 0] = (ids // 256 / 8).to(w.dtype)       # exact: at most 8 bits each
+    w[:, 1] = (ids % 256 / 2048).to(w.dtype)
+    kind = torch.arange(n) % 6
+    h[kind > 0] = 0
+    h[kind == 1, :2] = 1.0
+    h[kind == 2, :2] = -1.0
+    h[kind == 3, 0] = 1.0
+    h[kind == 4, 1] = -2.0
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, d_model=d, topk=k, source="hidden")
+    out = kd.token_logprobs(p, {"h": h.cuda(), "w": w.cuda()})
+    z = (h.cuda().double() @ w.cuda().double().t()).float()  # exact
+    best, order = torch.sort(z, dim=1, descending=True, stable=True)
+    assert torch.equal(out["topk_idx"], order[:, :k].int())
+    lp = torch.log_softmax(z.double(), dim=1).gather(1, order[:, :k])
+    tol = _e_s(v) + (2 * (best[:, :1] - best[:, :k]).double() + 2 * lp.abs() + 4) * U
+    assert ((out["topk_logprob"].double() - lp).abs() <= tol).all()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("n,v,d", [(1, 700, 64), (3, 257, 72), (130, 2049, 64), (257, 5003, 200),
                                    (300, 513, 520), (600, 700, 136)])
