@@ -14,6 +14,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 #include <vector>
 
 #include "kd_internal.h"
@@ -24,21 +25,25 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kChunk = 16384;     // elements a block takes at a time
 constexpr int kMaxGrid = 608;     // partial sums a launch writes at most
-constexpr int kTable = 256;       // tensors a launch takes (its kernel parameters hold them)
+// tensors a launch takes: its kernel parameters hold them, and a short list costs
+// less to launch
+constexpr int kTable = 256, kShortTable = 64;
 
 struct ClipTensor {
   const void* g;
   void* out;
   int64_t n;
 };
+template <int MOST>
 struct ClipTable {
-  ClipTensor t[kTable];
-  uint32_t first[kTable + 1];  // first chunk of each tensor; [n]: number of chunks
+  ClipTensor t[MOST];
+  uint32_t first[MOST + 1];  // first chunk of each tensor; [n]: number of chunks
   int n;
 };
 
 // The tensor chunk c belongs to.
-__device__ __forceinline__ int clip_find(const ClipTable& tab, uint32_t c) {
+template <int MOST>
+__device__ __forceinline__ int clip_find(const ClipTable<MOST>& tab, uint32_t c) {
   int lo = 0, hi = tab.n;  // first[lo] <= c < first[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -64,51 +69,96 @@ __device__ double block_sum(double v) {
   return v;
 }
 
-// sum of (scale g)^2 over this thread's elements of a chunk
+// A 16-byte vector of the tensor's elements.
 template <class T>
-__device__ __forceinline__ float chunk_squares(const T* g, int n, float scale, bool& any) {
-  float s = 0.f;
-  bool a = false;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const float v = to_f(g[i]) * scale;
-    a |= v != 0.f;
-    s = fmaf(v, v, s);
+struct Vec {
+  static constexpr int N = 16 / (int)sizeof(T);
+};
+__device__ __forceinline__ void unpack(uint4 w, float* v, float) {
+  v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y);
+  v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
+}
+__device__ __forceinline__ void unpack(uint4 w, float* v, __nv_bfloat16) {
+  v[0] = bf16lo(w.x), v[1] = bf16hi(w.x), v[2] = bf16lo(w.y), v[3] = bf16hi(w.y);
+  v[4] = bf16lo(w.z), v[5] = bf16hi(w.z), v[6] = bf16lo(w.w), v[7] = bf16hi(w.w);
+}
+__device__ __forceinline__ uint4 pack(const float* v, float) {
+  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                    __float_as_uint(v[3]));
+}
+__device__ __forceinline__ uint4 pack(const float* v, __nv_bfloat16) {
+  return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                    pack_bf16(v[6], v[7]));
+}
+__device__ __forceinline__ bool aligned(const void* p) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+}
+constexpr int kUnroll = 4;  // vectors a thread has in flight
+
+// sum of (scale g)^2 over this thread's (at most 64) elements of a chunk
+template <class T>
+__device__ __forceinline__ float chunk_squares(const T* g, int n, float scale) {
+  constexpr int N = Vec<T>::N;
+  float s0 = 0.f, s1 = 0.f;
+  int i0 = 0;
+  if (aligned(g)) {
+    const int vecs = n / N;
+    i0 = vecs * N;
+    const uint4* p = reinterpret_cast<const uint4*>(g);
+    for (int j = threadIdx.x; j < vecs; j += kUnroll * kThreads) {
+      uint4 w[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        w[u] = j + u * kThreads < vecs ? p[j + u * kThreads] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        float v[N];
+        unpack(w[u], v, T());
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+          const float a = v[e] * scale, b = v[e + 1] * scale;
+          s0 = fmaf(a, a, s0);
+          s1 = fmaf(b, b, s1);
+        }
+      }
+    }
   }
-  any = a;
-  return s;
+  for (int i = i0 + threadIdx.x; i < n; i += kThreads) {
+    const float a = to_f(g[i]) * scale;
+    s0 = fmaf(a, a, s0);
+  }
+  return s0 + s1;
 }
 
-template <class T>
-__global__ void __launch_bounds__(kThreads) k_clip_norm(const __grid_constant__ ClipTable tab,
-                                                        double* partial) {
+// Bound by HBM: one read of everything.
+template <class T, int MOST>
+__global__ void __launch_bounds__(kThreads, 4)
+    k_clip_norm(const __grid_constant__ ClipTable<MOST> tab, double* partial) {
+  asm volatile("griddepcontrol.launch_dependents;");
   double sum = 0.0;
   for (uint32_t c = blockIdx.x; c < tab.first[tab.n]; c += gridDim.x) {
-    const ClipTensor& t = tab.t[clip_find(tab, c)];
-    const int64_t at = (int64_t)(c - tab.first[clip_find(tab, c)]) * kChunk;
-    const T* g = static_cast<const T*>(t.g) + at;
-    const int n = (int)min((int64_t)kChunk, t.n - at);
-    bool any;
-    float s = chunk_squares(g, n, 1.f, any);
-    double d = (double)s;
-    // squares outside fp32's range: once more, scaled by a power of two
-    if (!(s <= 3e38f)) {
-      bool unused;
-      d = (double)chunk_squares(g, n, 0x1p-72f, unused) * 0x1p144;
-    } else if (s < 1e-30f && any) {
-      bool unused;
-      d = (double)chunk_squares(g, n, 0x1p72f, unused) * 0x1p-144;
-    }
-    sum += d;
+    const int k = clip_find(tab, c);
+    const int64_t at = (int64_t)(c - tab.first[k]) * kChunk;
+    const T* g = static_cast<const T*>(tab.t[k].g) + at;
+    const int n = (int)min((int64_t)kChunk, tab.t[k].n - at);
+    const float s = chunk_squares(g, n, 1.f);
+    // squares at the ends of fp32's range: once more, scaled by a power of two
+    if (!(s <= 3e38f)) sum += (double)chunk_squares(g, n, 0x1p-72f) * 0x1p144;
+    else if (s < 1e-30f) sum += (double)chunk_squares(g, n, 0x1p72f) * 0x1p-144;
+    else sum += (double)s;
   }
   sum = block_sum(sum);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
-template <class T>
-__global__ void __launch_bounds__(kThreads) k_clip_scale(const __grid_constant__ ClipTable tab,
-                                                         const double* partial, int n_partial,
-                                                         float max_norm, float* norm_out,
-                                                         uint32_t* status) {
+// Launched to start while the norm kernel ends.  Takes the chunks backwards:
+// the last ones it read are still in L2.
+template <class T, int MOST>
+__global__ void __launch_bounds__(kThreads, 4)
+    k_clip_scale(const __grid_constant__ ClipTable<MOST> tab, const double* partial,
+                 int n_partial, float max_norm, float* norm_out, uint32_t* status) {
+  constexpr int N = Vec<T>::N;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   double sum = 0.0;
   for (int i = threadIdx.x; i < n_partial; i += kThreads) sum += partial[i];
   sum = block_sum(sum);
@@ -120,7 +170,9 @@ __global__ void __launch_bounds__(kThreads) k_clip_scale(const __grid_constant__
   }
   const bool clip = finite && norm > (double)max_norm;
   const float coef = clip ? (float)((double)max_norm / norm) : 1.f;
-  for (uint32_t c = blockIdx.x; c < tab.first[tab.n]; c += gridDim.x) {
+  const uint32_t chunks = tab.first[tab.n];
+  for (uint32_t b = blockIdx.x; b < chunks; b += gridDim.x) {
+    const uint32_t c = chunks - 1 - b;
     const int k = clip_find(tab, c);
     const ClipTensor& t = tab.t[k];
     if (!clip && t.out == t.g) continue;
@@ -128,7 +180,32 @@ __global__ void __launch_bounds__(kThreads) k_clip_scale(const __grid_constant__
     const T* g = static_cast<const T*>(t.g) + at;
     T* out = static_cast<T*>(t.out) + at;
     const int n = (int)min((int64_t)kChunk, t.n - at);
-    for (int i = threadIdx.x; i < n; i += kThreads) {
+    int i0 = 0;
+    if (aligned(g) && aligned(out)) {
+      const int vecs = n / N;
+      i0 = vecs * N;
+      const uint4* p = reinterpret_cast<const uint4*>(g);
+      uint4* o = reinterpret_cast<uint4*>(out);
+      for (int j = threadIdx.x; j < vecs; j += kUnroll * kThreads) {
+        uint4 w[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+          if (j + u * kThreads < vecs) w[u] = p[j + u * kThreads];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          if (j + u * kThreads >= vecs) break;
+          if (clip) {  // (not multiplied by 1: a NaN is passed on as it is)
+            float v[N];
+            unpack(w[u], v, T());
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[e] *= coef;
+            w[u] = pack(v, T());
+          }
+          __stcs(&o[j + u * kThreads], w[u]);
+        }
+      }
+    }
+    for (int i = i0 + threadIdx.x; i < n; i += kThreads) {
       T v = g[i];
       if (clip) from_f(to_f(v) * coef, v);
       out[i] = v;
@@ -174,12 +251,12 @@ bool clip_disjoint(const void* const* grads, void* const* outs, const int64_t* n
   return true;
 }
 
-template <class T>
-void clip_run(const void* const* grads, void* const* outs, const int64_t* numel, int32_t n,
+template <class T, int MOST>
+bool clip_run(const void* const* grads, void* const* outs, const int64_t* numel, int32_t n,
               float max_norm, float* norm_out, uint32_t* status, double* partial,
               cudaStream_t s) {
-  auto table = [&](int32_t t0, ClipTable& tab) {
-    tab.n = (int)std::min<int32_t>(kTable, n - t0);
+  auto table = [&](int32_t t0, ClipTable<MOST>& tab) {
+    tab.n = (int)std::min<int32_t>(MOST, n - t0);
     uint32_t c = 0;
     for (int i = 0; i < tab.n; ++i) {
       tab.t[i] = ClipTensor{grads[t0 + i], outs ? outs[t0 + i] : nullptr, numel[t0 + i]};
@@ -190,31 +267,46 @@ void clip_run(const void* const* grads, void* const* outs, const int64_t* numel,
     return c;
   };
   int used = 0;
-  ClipTable tab;
+  bool told = false;  // the norm has been written
+  ClipTable<MOST> tab;
   memset(&tab, 0, sizeof(tab));
-  for (int32_t t0 = 0; t0 < n; t0 += kTable) {
+  for (int32_t t0 = 0; t0 < n; t0 += MOST) {
     const uint32_t chunks = table(t0, tab);
     if (!chunks) continue;
     const int grid = (int)std::min<uint32_t>(chunks, kMaxGrid);
     note_launch();
-    k_clip_norm<T><<<grid, kThreads, 0, s>>>(tab, partial + used);
+    k_clip_norm<T, MOST><<<grid, kThreads, 0, s>>>(tab, partial + used);
     used += grid;
   }
-  bool told = false;  // the norm has been written
-  for (int32_t t0 = 0; t0 < n && outs; t0 += kTable) {
+  auto scale = [&](int grid, float* norm) {
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    // only right behind the norm kernel: a second scaling kernel (or one with
+    // no norm kernel before it) follows in stream order
+    cfg.numAttrs = used > 0 && !told ? 1 : 0;
+    note_launch();
+    return cudaLaunchKernelEx(&cfg, k_clip_scale<T, MOST>, tab, (const double*)partial, used, max_norm,
+                              norm, status) == cudaSuccess;
+  };
+  for (int32_t t0 = 0; t0 < n && outs; t0 += MOST) {
     const uint32_t chunks = table(t0, tab);
     if (!chunks) continue;
-    note_launch();
-    k_clip_scale<T><<<(int)std::min<uint32_t>(chunks, kMaxGrid), kThreads, 0, s>>>(
-        tab, partial, used, max_norm, told ? nullptr : norm_out, status);
+    if (!scale((int)std::min<uint32_t>(chunks, kMaxGrid), told ? nullptr : norm_out)) return false;
     told = true;
   }
   if (!told) {  // norm only, or nothing in the tensors
     tab.n = 0;
     tab.first[0] = 0;
-    note_launch();
-    k_clip_scale<T><<<1, kThreads, 0, s>>>(tab, partial, used, max_norm, norm_out, status);
+    if (!scale(1, norm_out)) return false;
   }
+  return true;
 }
 
 }  // namespace
@@ -257,10 +349,14 @@ extern "C" kd_status kd_clip_grad_norm(const void* const* grads, void* const* ou
   if (cudaGetDevice(&dev) != cudaSuccess || !kd_device_supported(dev)) return KD_ERR_NO_DEVICE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   double* partial = static_cast<double*>(workspace);
-  if (dtype == KD_BF16)
-    clip_run<__nv_bfloat16>(grads, outs, numel, n_tensors, max_norm, norm_out, dev_status,
-                            partial, s);
-  else
-    clip_run<float>(grads, outs, numel, n_tensors, max_norm, norm_out, dev_status, partial, s);
-  return cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA;
+  auto run = [&](auto few) {
+    constexpr int MOST = decltype(few)::value ? kShortTable : kTable;
+    return dtype == KD_BF16
+               ? clip_run<__nv_bfloat16, MOST>(grads, outs, numel, n_tensors, max_norm, norm_out,
+                                               dev_status, partial, s)
+               : clip_run<float, MOST>(grads, outs, numel, n_tensors, max_norm, norm_out,
+                                       dev_status, partial, s);
+  };
+  const bool ok = n_tensors <= kShortTable ? run(std::true_type{}) : run(std::false_type{});
+  return ok && cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA;
 }

@@ -561,6 +561,26 @@ def kd_logprob_workspace_size(problem: kd_logprob_problem):
     return int(f.value), int(b.value)
 
 
+class _on:
+    """``with _on(device) as stream``: the device current, its current stream's
+    handle (the device is left alone where it is current already)."""
+
+    __slots__ = ("device", "guard")
+
+    def __init__(self, device: torch.device):
+        self.device, self.guard = device, None
+
+    def __enter__(self) -> int:
+        if torch.cuda.current_device() != self.device.index:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
 def _rows_pitch(name: str, t: torch.Tensor, shape, dtype, device) -> int:
     """Row pitch of a [N, V] matrix whose rows are contiguous (0 when it is dense)."""
     _same(name, t, shape, dtype, device)
@@ -572,7 +592,7 @@ def _rows_pitch(name: str, t: torch.Tensor, shape, dtype, device) -> int:
 
 
 def _same(name: str, t: torch.Tensor, shape, dtype, device):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
+    if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on {device}, "
                          f"got {tuple(t.shape)} {t.dtype} on {t.device}")
 
@@ -630,16 +650,18 @@ def token_logprobs(problem: LogprobProblem, tensors: dict, workspace: Optional[W
                       if save_stats else None),
             "dev_status": torch.zeros((), device=dev, dtype=torch.int32),
         }
-    ptrs = [_dense(name, out.get(name), shape, dt, dev) for name, shape, dt in (
-        ("logprob", (n,), f32), ("entropy", (n,), f32), ("topk_idx", (n, k), torch.int32),
-        ("topk_logprob", (n, k), f32), ("stats", (n, KD_LOGPROB_STATS), f32))]
+    ptrs = (_dense("logprob", out.get("logprob"), (n,), f32, dev),
+            _dense("entropy", out.get("entropy"), (n,), f32, dev),
+            _dense("topk_idx", out.get("topk_idx"), (n, k), torch.int32, dev),
+            _dense("topk_logprob", out.get("topk_logprob"), (n, k), f32, dev),
+            _dense("stats", out.get("stats"), (n, KD_LOGPROB_STATS), f32, dev))
     cp = problem.to_c(ld)
-    with torch.cuda.device(dev):
-        fb, _ = kd_logprob_workspace_size(cp)
-        wptr, wbytes = (workspace or Workspace()).get(fb, dev) if fb else (None, 0)
+    with _on(dev) as stream:
+        wptr, wbytes = None, 0
+        if problem.source == "hidden":  # (rows of logits need no workspace)
+            wptr, wbytes = (workspace or Workspace()).get(kd_logprob_workspace_size(cp)[0], dev)
         st = load_library().kd_logprob_fwd(ctypes.byref(cp), ctypes.byref(ins), *ptrs,
-                                           out["dev_status"].data_ptr(), wptr, wbytes,
-                                           _stream(dev))
+                                           out["dev_status"].data_ptr(), wptr, wbytes, stream)
     if st != KD_OK:
         raise KDError(st, "kd_logprob_fwd")
     if check:
@@ -670,9 +692,10 @@ def token_logprobs_backward(problem: LogprobProblem, tensors: dict, stats: torch
         ldg = _rows_pitch("d_logits", out["d_logits"], (n, v), dtype, dev)
         pz = out["d_logits"].data_ptr()
     cp = problem.to_c(ld, ldg)
-    with torch.cuda.device(dev):
-        _, bb = kd_logprob_workspace_size(cp)
-        wptr, wbytes = (workspace or Workspace()).get(bb, dev) if bb else (None, 0)
+    with _on(dev) as stream:
+        wptr, wbytes = None, 0
+        if problem.source == "hidden":
+            wptr, wbytes = (workspace or Workspace()).get(kd_logprob_workspace_size(cp)[1], dev)
         st = load_library().kd_logprob_bwd(
             ctypes.byref(cp), ctypes.byref(ins),
             _dense("stats", stats, (n, KD_LOGPROB_STATS), f32, dev),
@@ -680,7 +703,7 @@ def token_logprobs_backward(problem: LogprobProblem, tensors: dict, stats: torch
             _dense("d_entropy", d_entropy, (n,), f32, dev),
             _dense("d_h", out.get("d_h"), (n, d), dtype, dev),
             _dense("d_w", out.get("d_w"), (v, d), dtype, dev), pz,
-            out["dev_status"].data_ptr(), wptr, wbytes, _stream(dev))
+            out["dev_status"].data_ptr(), wptr, wbytes, stream)
     if st != KD_OK:
         raise KDError(st, "kd_logprob_bwd")
     if check:
@@ -693,7 +716,8 @@ def token_logprobs_backward(problem: LogprobProblem, tensors: dict, stats: torch
 class GradList:
     """The tensors of kd_clip_grad_norm, checked once for many calls: contiguous
     CUDA tensors of one dtype and device.  ``out``: tensors of the same shapes
-    for the clipped gradients; None clips in place."""
+    for the clipped gradients; None clips in place.  ``dev_status`` collects the
+    status bits of its calls; the caller may zero it."""
 
     def __init__(self, grads, out=None):
         self.grads = list(grads)
@@ -716,6 +740,7 @@ class GradList:
         if st != KD_OK:
             raise KDError(st, "kd_clip_grad_norm_workspace_size")
         self._bytes = nbytes.value
+        self.dev_status = torch.zeros((), device=self.device, dtype=torch.int32)
 
 
 def clip_grad_norm(grads, max_norm: float, *, out=None, workspace: Optional[Workspace] = None,
@@ -728,14 +753,17 @@ def clip_grad_norm(grads, max_norm: float, *, out=None, workspace: Optional[Work
     gl = grads if isinstance(grads, GradList) else GradList(grads, out)
     dev = gl.device
     norm = torch.empty((), device=dev, dtype=torch.float32)
-    status = torch.zeros((), device=dev, dtype=torch.int32)
-    with torch.cuda.device(dev):
+    with _on(dev) as stream:
         wptr, wbytes = (workspace or Workspace()).get(gl._bytes, dev)
         st = load_library().kd_clip_grad_norm(gl._grads, gl._outs, gl._numel, len(gl.grads),
                                               gl.dtype, float(max_norm), norm.data_ptr(),
-                                              status.data_ptr(), wptr, wbytes, _stream(dev))
+                                              gl.dev_status.data_ptr(), wptr, wbytes, stream)
     if st != KD_OK:
         raise KDError(st, "kd_clip_grad_norm")
     if check:
-        check_status(status)
-    return {"norm": norm, "grads": gl.out, "dev_status": status}
+        try:
+            check_status(gl.dev_status)
+        except KDError:
+            gl.dev_status.zero_()  # told
+            raise
+    return {"norm": norm, "grads": gl.out, "dev_status": gl.dev_status}
