@@ -237,6 +237,13 @@ struct TcTokArgs {
 };
 int launch_tc_tok(const TcTokArgs& a, int num_sms, cudaStream_t s);
 
+// Launches in a chain overlap their tails: each may start when the one before it
+// is on its last items, with all earlier ones complete.  So a launch may use what
+// the last but one (or an earlier one) wrote, and write what the last but one
+// read, but not of the last.  TC_CHAIN_FIRST begins a chain behind whatever the
+// stream holds; whatever follows the last one waits for all of it.
+enum TcChain { TC_CHAIN_NONE = 0, TC_CHAIN_FIRST = 1, TC_CHAIN_NEXT = 2 };
+
 // Its backward: G = d z of rows [r0, r0 + rc) x columns [c0, c0 + cc) in bf16.
 struct TcTokGradArgs {
   const void *h, *w;
@@ -248,6 +255,7 @@ struct TcTokGradArgs {
   const int64_t* tokens;
   int64_t ignore;
   const float *stats, *d_lp, *d_ent;
+  int chain;               // TC_CHAIN_*
   uint32_t* status;
 };
 int launch_tc_tok_grad(const TcTokGradArgs& a, int num_sms, cudaStream_t s);
@@ -267,8 +275,13 @@ struct TcGemmArgs {
   int64_t ldc32;
   __nv_bfloat16* c16;      // bf16 output [M, ldc16]
   int64_t ldc16;
+  int k_splits;            // > 1: K0 in that many parts (K1 = 0, TC_OUT_F32), part i's sums
+                           // at c32 + i M ldc32
+  int chain;               // TC_CHAIN_*
   uint32_t* status;
 };
+// Parts of K that give every CTA (pair) a tile where the tiles are few: 1 or more.
+int tc_gemm_k_splits(int64_t M, int64_t N, int64_t K, int num_sms);
 int launch_tc_gemm(const TcGemmArgs& a, int num_ctas, cudaStream_t s);
 
 }  // namespace kd

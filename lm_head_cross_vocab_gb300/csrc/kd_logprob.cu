@@ -977,17 +977,30 @@ void launch_grad(const LpGradArgs& a, cudaStream_t s) {
 
 // Copy of the hidden states with the rows of ignored tokens zeroed: their
 // gradient rows are 0, but 0 times what a padded row holds need not be.
-template <class T>
-__global__ void __launch_bounds__(kRowThreads) k_mask_rows(const T* __restrict__ h, int64_t d,
+template <class V>
+__global__ void __launch_bounds__(kRowThreads) k_mask_rows(const V* __restrict__ h, int64_t d,
                                                            const int64_t* tokens, int64_t ignore,
-                                                           T* __restrict__ out) {
+                                                           V* __restrict__ out) {
   const int64_t r = blockIdx.x;
   const bool live = !(tokens && tokens[r] == ignore);
-  for (int64_t i = threadIdx.x; i < d; i += kRowThreads) {
-    T v;
-    from_f(0.f, v);
-    out[r * d + i] = live ? h[r * d + i] : v;
+  for (int64_t i = threadIdx.x; i < d; i += kRowThreads) out[r * d + i] = live ? h[r * d + i] : V();
+}
+// Sum of the parts of a product whose K was split, in their order.
+__global__ void __launch_bounds__(kRowThreads) k_sum_parts(const float4* __restrict__ part,
+                                                           int64_t vecs, int parts,
+                                                           const float4* __restrict__ add,
+                                                           float4* __restrict__ o32,
+                                                           uint2* __restrict__ o16) {
+  const int64_t i = blockIdx.x * (int64_t)kRowThreads + threadIdx.x;
+  if (i >= vecs) return;
+  float4 s = add ? add[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) {
+    const float4 v = part[p * vecs + i];
+    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
   }
+  if (o32) o32[i] = s;
+  if (o16) o16[i] = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
 }
 
 // rows >= n behind the first n: zeros
@@ -1015,7 +1028,9 @@ struct LpPlan {
   int64_t fr;               // forward: rows a launch takes
   int64_t R, C;             // backward: chunk of G
   size_t f_z, f_h, f_sums, f_count, f_pub, f_cand, f_bytes;
-  size_t b_h, b_g, b_dh, b_dw, b_bytes;
+  int bufs;                 // chunk buffers
+  int ks;                   // parts of K in dH = G W
+  size_t b_h, b_g, b_dh, b_dw, b_part, b_bytes;
 };
 
 size_t take(size_t& off, size_t bytes) {
@@ -1122,7 +1137,16 @@ kd_status lp_plan(const kd_logprob_problem* p, LpPlan& P) {
   off = 0;
   const size_t esz = P.bf16 ? 2 : 4;
   P.b_h = take(off, (size_t)n * P.d * esz);
-  P.b_g = take(off, (size_t)P.R * P.C * esz);  // fp32: z, then G in its place
+  // bf16: a chunk is made while the products read the last one and the tail of
+  // the one before it still runs
+  const int64_t chunks = cdiv(n, P.R) * cdiv(P.v, P.C);
+  P.bufs = P.bf16 ? (int)std::min<int64_t>(chunks, 3) : 1;
+  P.b_g = take(off, (size_t)P.bufs * P.R * P.C * esz);  // fp32: z, then G in its place
+  P.ks = 1;
+  if (P.bf16) {
+    P.ks = tc_gemm_k_splits(std::min(n, P.R), P.d, std::min(P.v, P.C), P.nsm);
+    if (P.ks > 1) P.b_part = take(off, (size_t)P.ks * std::min(n, P.R) * P.d * 4);
+  }
   if (P.bf16 && cdiv(P.v, P.C) > 1) P.b_dh = take(off, (size_t)n * P.d * 4);
   if (P.bf16 && cdiv(n, P.R) > 1) P.b_dw = take(off, (size_t)P.v * P.d * 4);
   P.b_bytes = off;
@@ -1326,102 +1350,154 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
   const int64_t n = P.n, v = P.v, D = P.d, R = P.R, C = P.C;
   const int64_t nr = cdiv(n, R), nc = cdiv(v, C);
   void* g = at<char>(workspace, P.b_g);
-  float* z = static_cast<float*>(g);
   void* hm = at<char>(workspace, P.b_h);
   if (d_w) {
     note_launch();
     if (P.bf16)
-      k_mask_rows<__nv_bfloat16><<<(unsigned)n, kRowThreads, 0, s>>>(
-          static_cast<const __nv_bfloat16*>(in->h), D, in->tokens, p->ignore_index,
-          static_cast<__nv_bfloat16*>(hm));
+      k_mask_rows<uint4><<<(unsigned)n, kRowThreads, 0, s>>>(
+          static_cast<const uint4*>(in->h), D / 8, in->tokens, p->ignore_index,
+          static_cast<uint4*>(hm));
     else
       k_mask_rows<float><<<(unsigned)n, kRowThreads, 0, s>>>(
           static_cast<const float*>(in->h), D, in->tokens, p->ignore_index,
           static_cast<float*>(hm));
   }
-  for (int64_t ri = 0; ri < nr; ++ri) {
-    const int64_t r0 = ri * R, rc = std::min(R, n - r0);
-    for (int64_t ci = 0; ci < nc; ++ci) {
-      const int64_t c0 = ci * C, cc = std::min(C, v - c0);
-      if (P.bf16) {
-        TcTokGradArgs t;
-        memset(&t, 0, sizeof(t));
-        t.h = in->h;
-        t.w = in->w;
-        t.n = n;
-        t.vocab = v;
-        t.d = D;
-        t.r0 = r0;
-        t.rc = rc;
-        t.c0 = c0;
-        t.cc = cc;
-        t.g = static_cast<__nv_bfloat16*>(g);
-        t.ldg = C;
-        t.inv_t = P.inv_t;
-        t.k2 = P.k2;
-        t.tokens = in->tokens;
-        t.ignore = p->ignore_index;
-        t.stats = stats;
-        t.d_lp = d_logprob;
-        t.d_ent = d_entropy;
-        t.status = dev_status;
-        if (launch_tc_tok_grad(t, P.nsm, s)) return KD_ERR_CUDA;
-      } else if (lp_logits(P, in, r0, rc, c0, cc, z, C, dev_status, s)) {
-        return KD_ERR_CUDA;
-      }
-      a.n = rc;
-      a.cols = cc;
-      a.col0 = c0;
-      a.ld = a.ldg = C;
-      a.tokens = in->tokens ? in->tokens + r0 : nullptr;
-      a.stats = stats + r0 * KD_LOGPROB_STATS;
-      a.d_lp = d_logprob ? d_logprob + r0 : nullptr;
-      a.d_ent = d_entropy ? d_entropy + r0 : nullptr;
-      a.g = g;
-      if (!P.bf16) {
+  if (!P.bf16) {
+    for (int64_t ri = 0; ri < nr; ++ri) {
+      const int64_t r0 = ri * R, rc = std::min(R, n - r0);
+      for (int64_t ci = 0; ci < nc; ++ci) {
+        const int64_t c0 = ci * C, cc = std::min(C, v - c0);
+        float* z = static_cast<float*>(g);
+        if (lp_logits(P, in, r0, rc, c0, cc, z, C, dev_status, s)) return KD_ERR_CUDA;
+        a.n = rc;
+        a.cols = cc;
+        a.col0 = c0;
+        a.ld = a.ldg = C;
+        a.tokens = in->tokens ? in->tokens + r0 : nullptr;
+        a.stats = stats + r0 * KD_LOGPROB_STATS;
+        a.d_lp = d_logprob ? d_logprob + r0 : nullptr;
+        a.d_ent = d_entropy ? d_entropy + r0 : nullptr;
+        a.g = g;
         launch_grad_chunk(a, s);
-        const float* gf = static_cast<const float*>(g);
         if (d_h)
-          launch_simt_gemm(gf, C, 1, static_cast<const float*>(in->w) + c0 * D, D, 1,
+          launch_simt_gemm(z, C, 1, static_cast<const float*>(in->w) + c0 * D, D, 1,
                            static_cast<float*>(d_h) + r0 * D, D, rc, D, cc, ci > 0, s);
         if (d_w)
-          launch_simt_gemm(gf, 1, C, static_cast<const float*>(hm) + r0 * D, D, 1,
+          launch_simt_gemm(z, 1, C, static_cast<const float*>(hm) + r0 * D, D, 1,
                            static_cast<float*>(d_w) + c0 * D, D, cc, D, rc, ri > 0, s);
-        continue;
       }
-      auto product = [&](const __nv_bfloat16* b, int64_t m, int64_t kk, bool a_mn, float* acc,
-                         __nv_bfloat16* out, int64_t i, int64_t parts) {
-        TcGemmArgs t;
-        memset(&t, 0, sizeof(t));
-        t.a0 = static_cast<const __nv_bfloat16*>(g);
-        t.lda0 = C;
-        t.a0_mn = a_mn;
-        t.b0 = b;
-        t.ldb0 = D;
-        t.b0_mn = 1;
-        t.M = m;
-        t.N = D;
-        t.K0 = kk;
-        t.mode = parts == 1      ? TC_OUT_BF16
-                 : i == 0        ? TC_OUT_F32
-                 : i + 1 < parts ? TC_OUT_F32_ACC
-                                 : TC_OUT_F32_ACC_BF16;
-        t.c32 = acc;
-        t.ldc32 = D;
-        t.c16 = out;
-        t.ldc16 = D;
-        t.status = dev_status;
-        return launch_tc_gemm(t, P.nsm, s);
-      };
-      if (d_h && product(static_cast<const __nv_bfloat16*>(in->w) + c0 * D, rc, cc, false,
-                         nc > 1 ? at<float>(workspace, P.b_dh) + r0 * D : nullptr,
-                         static_cast<__nv_bfloat16*>(d_h) + r0 * D, ci, nc))
-        return KD_ERR_CUDA;
-      if (d_w && product(static_cast<const __nv_bfloat16*>(hm) + r0 * D, cc, rc, true,
-                         nr > 1 ? at<float>(workspace, P.b_dw) + c0 * D : nullptr,
-                         static_cast<__nv_bfloat16*>(d_w) + c0 * D, ri, nr))
-        return KD_ERR_CUDA;
     }
+    return cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA;
   }
+  // Chunk i is made before the products of chunk i - 1 are launched, into the
+  // buffer after the one they read; with the launches chained, the next one
+  // fills the SMs that the partial last wave of the one before leaves idle.
+  struct Chunk {
+    int64_t ri, ci, r0, rc, c0, cc;
+    __nv_bfloat16* g;
+  };
+  const int64_t chunks = nr * nc;
+  auto chunk = [&](int64_t i) {
+    Chunk k;
+    k.ri = i / nc;
+    k.ci = i % nc;
+    k.r0 = k.ri * R;
+    k.rc = std::min(R, n - k.r0);
+    k.c0 = k.ci * C;
+    k.cc = std::min(C, v - k.c0);
+    k.g = static_cast<__nv_bfloat16*>(g) + (size_t)(i % P.bufs) * R * C;
+    return k;
+  };
+  // one launch between a chunk and its products, or none can be chained
+  const bool chained = chunks > 1 && P.ks == 1;
+  bool first = true;
+  auto link = [&]() {
+    const int c = !chained ? TC_CHAIN_NONE : first ? TC_CHAIN_FIRST : TC_CHAIN_NEXT;
+    first = false;
+    return c;
+  };
+  auto make = [&](const Chunk& k) {
+    TcTokGradArgs t;
+    memset(&t, 0, sizeof(t));
+    t.h = in->h;
+    t.w = in->w;
+    t.n = n;
+    t.vocab = v;
+    t.d = D;
+    t.r0 = k.r0;
+    t.rc = k.rc;
+    t.c0 = k.c0;
+    t.cc = k.cc;
+    t.g = k.g;
+    t.ldg = C;
+    t.inv_t = P.inv_t;
+    t.k2 = P.k2;
+    t.tokens = in->tokens;
+    t.ignore = p->ignore_index;
+    t.stats = stats;
+    t.d_lp = d_logprob;
+    t.d_ent = d_entropy;
+    t.chain = link();
+    t.status = dev_status;
+    return launch_tc_tok_grad(t, P.nsm, s);
+  };
+  // C[m, D] (+)= A B over chunk part i of `parts`
+  auto product = [&](const Chunk& k, const __nv_bfloat16* b, int64_t m, int64_t kk, bool a_mn,
+                     float* acc, __nv_bfloat16* out, int64_t i, int64_t parts) {
+    TcGemmArgs t;
+    memset(&t, 0, sizeof(t));
+    t.a0 = k.g;
+    t.lda0 = C;
+    t.a0_mn = a_mn;
+    t.b0 = b;
+    t.ldb0 = D;
+    t.b0_mn = 1;
+    t.M = m;
+    t.N = D;
+    t.K0 = kk;
+    t.status = dev_status;
+    t.ldc32 = D;
+    t.ldc16 = D;
+    t.chain = link();
+    const bool last = i + 1 == parts;
+    if (!a_mn && P.ks > 1) {  // dH over few rows: K in parts, then their sum
+      t.k_splits = P.ks;
+      t.mode = TC_OUT_F32;
+      t.c32 = at<float>(workspace, P.b_part);
+      if (launch_tc_gemm(t, P.nsm, s)) return 1;
+      const int64_t vecs = m * D / 4;
+      note_launch();
+      k_sum_parts<<<(unsigned)cdiv(vecs, kRowThreads), kRowThreads, 0, s>>>(
+          reinterpret_cast<const float4*>(t.c32), vecs, P.ks,
+          i > 0 ? reinterpret_cast<const float4*>(acc) : nullptr,
+          last ? nullptr : reinterpret_cast<float4*>(acc),
+          last ? reinterpret_cast<uint2*>(out) : nullptr);
+      return 0;
+    }
+    t.mode = parts == 1 ? TC_OUT_BF16
+             : i == 0   ? TC_OUT_F32
+             : !last    ? TC_OUT_F32_ACC
+                        : TC_OUT_F32_ACC_BF16;
+    t.c32 = acc;
+    t.c16 = out;
+    return launch_tc_gemm(t, P.nsm, s);
+  };
+  auto products = [&](const Chunk& k) {
+    if (d_h && product(k, static_cast<const __nv_bfloat16*>(in->w) + k.c0 * D, k.rc, k.cc, false,
+                       nc > 1 ? at<float>(workspace, P.b_dh) + k.r0 * D : nullptr,
+                       static_cast<__nv_bfloat16*>(d_h) + k.r0 * D, k.ci, nc))
+      return 1;
+    return d_w && product(k, static_cast<const __nv_bfloat16*>(hm) + k.r0 * D, k.cc, k.rc, true,
+                          nr > 1 ? at<float>(workspace, P.b_dw) + k.c0 * D : nullptr,
+                          static_cast<__nv_bfloat16*>(d_w) + k.c0 * D, k.ri, nr)
+               ? 1
+               : 0;
+  };
+  if (make(chunk(0))) return KD_ERR_CUDA;
+  for (int64_t i = 1; i < chunks; ++i)
+    if (make(chunk(i)) || products(chunk(i - 1))) return KD_ERR_CUDA;
+  // the last chunk's products follow it directly: not chained to it
+  first = true;
+  if (products(chunk(chunks - 1))) return KD_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA;
 }

@@ -311,6 +311,8 @@ struct TcParams {  // (128-byte aligned by its tensor maps)
   int m_tiles, n_tiles, n_splits, items;
   int m_band;         // row tiles per band of the item order (see item_range)
   int split_first;    // 1: the splits of a row tile follow one another instead
+  int k_splits;       // plain GEMM: parts of its K blocks, an item each (0: one)
+  int chain;          // TC_CHAIN_*
   int acc_stride;     // TMEM columns per accumulator stage
   int acc_stages;     // 1 or 2 accumulator stages in the 512 allocated columns
   int logits_vec;     // materialised logits rows are 16-byte aligned
@@ -395,6 +397,16 @@ __device__ __forceinline__ void item_range(const TcParams& P, int item, int& m_t
   }
   t0 = (int)((int64_t)P.n_tiles * split / P.n_splits);
   t1 = (int)((int64_t)P.n_tiles * (split + 1) / P.n_splits);
+}
+
+// The K blocks of an item of a plain GEMM whose K is split (the item is reduced
+// to its tile).
+__device__ __forceinline__ void k_range(const TcParams& P, int& item, int& part, int& kb0,
+                                        int& kb1) {
+  part = item % P.k_splits;
+  item /= P.k_splits;
+  kb0 = (int)((int64_t)P.kb[0] * part / P.k_splits);
+  kb1 = (int)((int64_t)P.kb[0] * (part + 1) / P.k_splits);
 }
 
 // v[j] for a runtime j in [0, 32) without dynamic register indexing
@@ -1099,11 +1111,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
     uint32_t phase = 0, issued = 0, par = 0;
     bool ok = true;
     for (int item = cid; ok && item < P.items; item += ncl) {
-      int m_tile, split, t0, t1;
-      item_range(P, item, m_tile, split, t0, t1);
+      int m_tile, split, t0, t1, kb0 = 0, kb1 = P.kb[0], part = 0, id = item;
+      if (EPI == EPI_GEMM && P.k_splits) k_range(P, id, part, kb0, kb1);
+      item_range(P, id, m_tile, split, t0, t1);
       for (int t = t0; ok && t < t1; ++t)
         for (int sg = 0; ok && sg < 2; ++sg)
-          for (int kb = 0; ok && kb < P.kb[sg]; ++kb) {
+          for (int kb = sg ? 0 : kb0; ok && kb < (sg ? P.kb[1] : kb1); ++kb) {
             if (!warp_wait(S, S.empty + 8 * stage, phase ^ 1)) {
               ok = false;
               break;
@@ -1157,8 +1170,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
     Sync Sc = S;
     Sc.cluster_acquire = PAIR;  // the peer's epilogue arrives on acc_empty remotely
     for (int item = cid; ok && item < P.items; item += ncl) {
-      int m_tile, split, t0, t1;
-      item_range(P, item, m_tile, split, t0, t1);
+      int m_tile, split, t0, t1, kb0 = 0, kb1 = P.kb[0], part = 0, id = item;
+      if (EPI == EPI_GEMM && P.k_splits) k_range(P, id, part, kb0, kb1);
+      item_range(P, id, m_tile, split, t0, t1);
       for (int t = t0; ok && t < t1; ++t) {
         if (!warp_wait(Sc, S.acc_empty + 8 * acc, acc_phase ^ 1)) {
           ok = false;
@@ -1172,7 +1186,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
           const uint32_t idesc = C::IDESC | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16);
           const uint32_t a_step = a_mn ? 128u : 2u;  // per K = 16, 16-byte units
           const uint32_t b_step = b_mn ? 128u : 2u;
-          for (int kb = 0; kb < P.kb[sg]; ++kb) {
+          const int first = sg ? 0 : kb0, last = sg ? P.kb[1] : kb1;
+          for (int kb = first; kb < last; ++kb) {
             if (!warp_wait(S, S.full + 8 * stage, phase)) {
               ok = false;
               break;
@@ -1184,7 +1199,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
               const uint64_t bd = b_mn ? smem_desc_mn(b_addr) : smem_desc(b_addr);
 #pragma unroll
               for (int k = 0; k < BK / 16; ++k) {
-                const uint32_t accum = (kb > 0 || k > 0 || P.seg_accum[sg]) ? 1u : 0u;
+                const uint32_t accum = (kb > first || k > 0 || P.seg_accum[sg]) ? 1u : 0u;
                 if (PAIR) mma_bf16_pair_e(d, ad + a_step * k, bd + b_step * k, idesc, accum);
                 else mma_bf16_e(d, ad + a_step * k, bd + b_step * k, idesc, accum);
               }
@@ -1224,8 +1239,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
     bool ok = true;
     const int r_in_pair = (int)rank * BM + r_in_tile;  // row within the (pair) tile
     for (int item = cid; ok && item < P.items; item += ncl) {
-      int m_tile, split, t0, t1;
-      item_range(P, item, m_tile, split, t0, t1);
+      int m_tile, split, t0, t1, kb0 = 0, kb1 = 0, part = 0, id = item;
+      if (EPI == EPI_GEMM && P.k_splits) k_range(P, id, part, kb0, kb1);
+      item_range(P, id, m_tile, split, t0, t1);
       const int64_t tile_row = (int64_t)m_tile * C::ROWS + r_in_pair;
       int64_t g_row = 0, g_y = -1;
       bool g_ok = false;
@@ -1430,7 +1446,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
             if (row < a.M && nv > 0) {
               const bool full = nv == 32;
               if (a.mode != TC_OUT_BF16) {
-                float* c = a.c32 + row * a.ldc32 + col0;
+                float* c = a.c32 + (part * a.M + row) * a.ldc32 + col0;
                 const bool vec = full && (a.ldc32 % 4) == 0;
                 if (a.mode != TC_OUT_F32) {
                   if (vec) {
@@ -1500,6 +1516,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
         }
       }
       if (EPI == EPI_FWD && ok) fe.end(P, split, half);
+      // A chained launch may overlap the tail of the one before it, and has to
+      // leave that one complete: behind its first item each CTA waits for it,
+      // and then lets the next launch in, which so finds all but this one done.
+      if ((EPI == EPI_GEMM || EPI == EPI_TOKG) && P.chain && warp == 2 && item == cid) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;");
+      }
       if constexpr (EPI == EPI_TOK || EPI == EPI_TOP) {
         if (ok) te.end(P);
       }
@@ -1579,7 +1602,9 @@ int launch(const TcParams& P, int num_sms, cudaStream_t s) {
   }
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
@@ -1594,6 +1619,7 @@ int launch(const TcParams& P, int num_sms, cudaStream_t s) {
   if (max_clusters <= 0) max_clusters = num_sms / 2;
   const int clusters = P.items < max_clusters ? P.items : max_clusters;
   cfg.gridDim = dim3(2 * clusters);
+  if (P.chain == TC_CHAIN_NEXT) cfg.numAttrs = 2;
   note_launch();
   e = cudaLaunchKernelEx(&cfg, kern, P);
   if (e != cudaSuccess) return (int)e;
@@ -1774,8 +1800,18 @@ int launch_tc_tok_grad(const TcTokGradArgs& a, int num_sms, cudaStream_t s) {
   P.items = P.m_tiles * P.n_tiles;
   P.m_band = band_tiles(P, tc_tile_rows(pair));
   P.tokg = a;
+  P.chain = pair ? a.chain : TC_CHAIN_NONE;
   return pair ? launch<EPI_TOKG, 256, false, true>(P, num_sms, s)
               : launch<EPI_TOKG, 256, false, false>(P, num_sms, s);
+}
+
+int tc_gemm_k_splits(int64_t M, int64_t N, int64_t K, int num_sms) {
+  const bool pair = tc_use_pairs();
+  const int64_t rows = tc_tile_rows(pair);
+  const int64_t tiles = ((M + rows - 1) / rows) * ((N + 255) / 256);
+  const int64_t workers = pair ? num_sms / 2 : num_sms;
+  const int64_t blocks = (K + BK - 1) / BK;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(workers / tiles, blocks / 8));
 }
 
 int launch_tc_gemm(const TcGemmArgs& a, int num_sms, cudaStream_t s) {
@@ -1809,9 +1845,11 @@ int launch_tc_gemm(const TcGemmArgs& a, int num_sms, cudaStream_t s) {
   P.m_tiles = (int)((a.M + tc_tile_rows(pair) - 1) / tc_tile_rows(pair));
   P.n_tiles = (int)((a.N + bn - 1) / bn);
   P.n_splits = P.n_tiles;
-  P.items = P.m_tiles * P.n_tiles;
+  P.k_splits = a.k_splits > 1 ? a.k_splits : 0;
+  P.items = P.m_tiles * P.n_tiles * (P.k_splits ? P.k_splits : 1);
   P.m_band = band_tiles(P, tc_tile_rows(pair));
   P.gemm = a;
+  P.chain = pair ? a.chain : TC_CHAIN_NONE;
   return pair ? launch<EPI_GEMM, 256, false, true>(P, num_sms, s)
               : launch<EPI_GEMM, 256, false, false>(P, num_sms, s);
 }

@@ -388,6 +388,44 @@ def test_hidden_backward(n, v, d, dtype):
     assert "d_h" not in one and torch.equal(one["d_w"], r["d_w"])
 
 
+@pytest.mark.parametrize("n,v,d", [(2100, 9000, 64), (700, 30000, 264), (5000, 5003, 136)])
+@pytest.mark.parametrize("want", [("h", "w"), ("h",), ("w",)])
+def test_hidden_backward_in_chunks(n, v, d, want):
+    """Problems whose gradient is made in several chunks of tokens and columns,
+    against the formula in fp64 (torch, on the same device), with the bound of
+    test_hidden_backward; three calls in a row give the same bits."""
+    h, w = (x.cuda() for x in _hidden(n, v, d, "bf16", n + v))
+    y = _tokens(n, v, n).cuda()
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, d_model=d, source="hidden")
+    tens = {"h": h, "w": w, "tokens": y}
+    out = kd.token_logprobs(p, tens)
+    g = torch.Generator().manual_seed(v)
+    gl, gh = (torch.randn(n, generator=g).cuda(), torch.randn(n, generator=g).cuda() * 0.3)
+    lp = torch.log_softmax(h.double() @ w.double().t(), dim=1)
+    pr, on = lp.exp(), (y != IGN)[:, None]
+    ent = -(pr * lp).sum(dim=1, keepdim=True)
+    a, b = gl.double()[:, None], gh.double()[:, None]
+    gz = -pr * (a + b * (lp + ent))
+    tol = pr * ((a.abs() + b.abs() * (lp.abs() + math.log(v) + 1)) * 200 * U
+                + b.abs() * _e_s(v) * (math.log(v) + 3))
+    gz[torch.arange(n), y.clamp(min=0)] += a[:, 0]
+    gz, tol = torch.where(on, gz, 0.0), torch.where(on, tol, 0.0)
+    tol = tol + 2.0 ** -8 * (gz.abs() + tol) + 4 * U * a.abs() * on
+    ws, kept = kd.Workspace(), []
+    for _ in range(3):
+        r = kd.token_logprobs_backward(p, tens, out["stats"], d_logprob=gl, d_entropy=gh,
+                                       want=want, workspace=ws)
+        kept.append(r)
+    for name, x, xt, m in (("d_h", gz, tol, w.double()), ("d_w", gz.t(), tol.t(), h.double())):
+        if name[2:] not in want:
+            continue
+        ref = x @ m
+        off = xt @ m.abs() + 2 * U * x.shape[1] * ((x.abs() + xt) @ m.abs())
+        off = off + 2.0 ** -8 * (ref.abs() + off) + TINY
+        assert ((kept[0][name].double() - ref).abs() <= off).all(), name
+        assert all(torch.equal(kept[0][name], r[name]) for r in kept[1:])
+
+
 def test_gradients_by_differences():
     """The fp32 backward against central differences of the fp64 definition."""
     n, v, d = 3, 40, 8
