@@ -244,6 +244,21 @@ int launch_tc_tok(const TcTokArgs& a, int num_sms, cudaStream_t s);
 // stream holds; whatever follows the last one waits for all of it.
 enum TcChain { TC_CHAIN_NONE = 0, TC_CHAIN_FIRST = 1, TC_CHAIN_NEXT = 2 };
 
+// Few source rows with an fp32 coefficient each, added to rows of a product:
+// out[o, :] += sum over the entries (q, c) of row o of c src[q, :].  Either one
+// entry a row, (one_q[o], one_c[o]) (one_q outside [0, src_rows): none), or up to
+// kTermRows, given as a count and the q of each (no entry if there are more), the
+// coefficient of q being one_c[q].
+constexpr int kTermRows = 4;
+struct TcTerms {
+  const __nv_bfloat16* src;  // rows of pitch ld_src; NULL: no terms
+  int64_t ld_src, src_rows;
+  const int64_t* one_q;      // NULL: lists
+  const int32_t* count;
+  const int32_t* list;       // [rows][kTermRows]
+  const float* one_c;
+};
+
 // Its backward: G = d z of rows [r0, r0 + rc) x columns [c0, c0 + cc) in bf16.
 struct TcTokGradArgs {
   const void *h, *w;
@@ -255,6 +270,7 @@ struct TcTokGradArgs {
   const int64_t* tokens;
   int64_t ignore;
   const float *stats, *d_lp, *d_ent;
+  float* rest;             // [n]: what rounding G to bf16 took from the token's element
   int chain;               // TC_CHAIN_*
   uint32_t* status;
 };
@@ -277,6 +293,7 @@ struct TcGemmArgs {
   int64_t ldc16;
   int k_splits;            // > 1: K0 in that many parts (K1 = 0, TC_OUT_F32), part i's sums
                            // at c32 + i M ldc32
+  TcTerms terms;           // added before the result is rounded to bf16
   int chain;               // TC_CHAIN_*
   uint32_t* status;
 };

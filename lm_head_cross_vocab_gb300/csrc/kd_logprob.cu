@@ -976,18 +976,28 @@ void launch_grad(const LpGradArgs& a, cudaStream_t s) {
 }
 
 // Copy of the hidden states with the rows of ignored tokens zeroed: their
-// gradient rows are 0, but 0 times what a padded row holds need not be.
+// gradient rows are 0, but 0 times what a padded row holds need not be.  With
+// `count`, also the tokens of each column: how many, and the first kTermRows
+// that are counted.
 template <class V>
 __global__ void __launch_bounds__(kRowThreads) k_mask_rows(const V* __restrict__ h, int64_t d,
                                                            const int64_t* tokens, int64_t ignore,
-                                                           V* __restrict__ out) {
+                                                           V* __restrict__ out, int64_t vocab,
+                                                           int32_t* count, int32_t* list) {
   const int64_t r = blockIdx.x;
-  const bool live = !(tokens && tokens[r] == ignore);
+  const int64_t y = tokens ? tokens[r] : -1;
+  const bool live = !(tokens && y == ignore);
+  if (count && threadIdx.x == 0 && live && y >= 0 && y < vocab) {
+    const int at = atomicAdd(&count[y], 1);
+    if (at < kTermRows) list[y * kTermRows + at] = (int32_t)r;
+  }
   for (int64_t i = threadIdx.x; i < d; i += kRowThreads) out[r * d + i] = live ? h[r * d + i] : V();
 }
-// Sum of the parts of a product whose K was split, in their order.
+// Sum of the parts of a product whose K was split, in their order, and of the
+// terms of its rows (of d floats).
 __global__ void __launch_bounds__(kRowThreads) k_sum_parts(const float4* __restrict__ part,
-                                                           int64_t vecs, int parts,
+                                                           int64_t vecs, int parts, int64_t d,
+                                                           const TcTerms terms,
                                                            const float4* __restrict__ add,
                                                            float4* __restrict__ o32,
                                                            uint2* __restrict__ o16) {
@@ -998,6 +1008,15 @@ __global__ void __launch_bounds__(kRowThreads) k_sum_parts(const float4* __restr
   for (int p = 0; p < parts; ++p) {
     const float4 v = part[p * vecs + i];
     s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+  }
+  if (terms.src) {
+    const int64_t row = 4 * i / d, col = 4 * i % d;
+    const TermRow t = term_row(terms, row);
+    if (t.n) {
+      const uint2 x = *reinterpret_cast<const uint2*>(t.src[0] + col);
+      s.x = fmaf(t.c[0], bf16lo(x.x), s.x), s.y = fmaf(t.c[0], bf16hi(x.x), s.y);
+      s.z = fmaf(t.c[0], bf16lo(x.y), s.z), s.w = fmaf(t.c[0], bf16hi(x.y), s.w);
+    }
   }
   if (o32) o32[i] = s;
   if (o16) o16[i] = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
@@ -1030,7 +1049,7 @@ struct LpPlan {
   size_t f_z, f_h, f_sums, f_count, f_pub, f_cand, f_bytes;
   int bufs;                 // chunk buffers
   int ks;                   // parts of K in dH = G W
-  size_t b_h, b_g, b_dh, b_dw, b_part, b_bytes;
+  size_t b_h, b_g, b_dh, b_dw, b_part, b_rest, b_count, b_list, b_bytes;
 };
 
 size_t take(size_t& off, size_t bytes) {
@@ -1146,6 +1165,9 @@ kd_status lp_plan(const kd_logprob_problem* p, LpPlan& P) {
   if (P.bf16) {
     P.ks = tc_gemm_k_splits(std::min(n, P.R), P.d, std::min(P.v, P.C), P.nsm);
     if (P.ks > 1) P.b_part = take(off, (size_t)P.ks * std::min(n, P.R) * P.d * 4);
+    P.b_rest = take(off, (size_t)n * 4);
+    P.b_count = take(off, (size_t)P.v * 4);
+    P.b_list = take(off, (size_t)P.v * kTermRows * 4);
   }
   if (P.bf16 && cdiv(P.v, P.C) > 1) P.b_dh = take(off, (size_t)n * P.d * 4);
   if (P.bf16 && cdiv(n, P.R) > 1) P.b_dw = take(off, (size_t)P.v * P.d * 4);
@@ -1351,16 +1373,27 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
   const int64_t nr = cdiv(n, R), nc = cdiv(v, C);
   void* g = at<char>(workspace, P.b_g);
   void* hm = at<char>(workspace, P.b_h);
+  // What rounding the tokens' elements of G to bf16 took from them (fp32) goes
+  // into both products at their end: into d_h[i] with W's row of token i, into
+  // d_w[v] with the hidden states of the tokens v where they are few (the sum
+  // of many averages the roundings out).  Rows without a token in range keep 0.
+  float* rest = P.bf16 ? at<float>(workspace, P.b_rest) : nullptr;
+  int32_t* count = P.bf16 ? at<int32_t>(workspace, P.b_count) : nullptr;
+  int32_t* list = P.bf16 ? at<int32_t>(workspace, P.b_list) : nullptr;
+  if (P.bf16 && in->tokens) {  // (count lies behind rest)
+    const size_t bytes = d_w ? P.b_count - P.b_rest + (size_t)v * 4 : (size_t)n * 4;
+    if (cudaMemsetAsync(rest, 0, bytes, s) != cudaSuccess) return KD_ERR_CUDA;
+  }
   if (d_w) {
     note_launch();
     if (P.bf16)
       k_mask_rows<uint4><<<(unsigned)n, kRowThreads, 0, s>>>(
           static_cast<const uint4*>(in->h), D / 8, in->tokens, p->ignore_index,
-          static_cast<uint4*>(hm));
+          static_cast<uint4*>(hm), v, in->tokens ? count : nullptr, list);
     else
       k_mask_rows<float><<<(unsigned)n, kRowThreads, 0, s>>>(
           static_cast<const float*>(in->h), D, in->tokens, p->ignore_index,
-          static_cast<float*>(hm));
+          static_cast<float*>(hm), v, nullptr, nullptr);
   }
   if (!P.bf16) {
     for (int64_t ri = 0; ri < nr; ++ri) {
@@ -1408,6 +1441,25 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
     k.g = static_cast<__nv_bfloat16*>(g) + (size_t)(i % P.bufs) * R * C;
     return k;
   };
+  auto terms = [&](const Chunk& k, bool of_w, bool last) {
+    TcTerms t;
+    memset(&t, 0, sizeof(t));
+    if (!in->tokens || !last) return t;
+    t.ld_src = D;
+    t.one_c = rest;
+    if (of_w) {
+      t.src = static_cast<const __nv_bfloat16*>(hm);
+      t.src_rows = n;
+      t.count = count + k.c0;
+      t.list = list + k.c0 * kTermRows;
+    } else {
+      t.src = static_cast<const __nv_bfloat16*>(in->w);
+      t.src_rows = v;
+      t.one_q = in->tokens + k.r0;
+      t.one_c = rest + k.r0;
+    }
+    return t;
+  };
   // one launch between a chunk and its products, or none can be chained
   const bool chained = chunks > 1 && P.ks == 1;
   bool first = true;
@@ -1437,6 +1489,7 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
     t.stats = stats;
     t.d_lp = d_logprob;
     t.d_ent = d_entropy;
+    t.rest = rest;
     t.chain = link();
     t.status = dev_status;
     return launch_tc_tok_grad(t, P.nsm, s);
@@ -1468,7 +1521,7 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
       const int64_t vecs = m * D / 4;
       note_launch();
       k_sum_parts<<<(unsigned)cdiv(vecs, kRowThreads), kRowThreads, 0, s>>>(
-          reinterpret_cast<const float4*>(t.c32), vecs, P.ks,
+          reinterpret_cast<const float4*>(t.c32), vecs, P.ks, D, terms(k, a_mn, last),
           i > 0 ? reinterpret_cast<const float4*>(acc) : nullptr,
           last ? nullptr : reinterpret_cast<float4*>(acc),
           last ? reinterpret_cast<uint2*>(out) : nullptr);
@@ -1478,6 +1531,7 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
              : i == 0   ? TC_OUT_F32
              : !last    ? TC_OUT_F32_ACC
                         : TC_OUT_F32_ACC_BF16;
+    t.terms = terms(k, a_mn, last);
     t.c32 = acc;
     t.c16 = out;
     return launch_tc_gemm(t, P.nsm, s);

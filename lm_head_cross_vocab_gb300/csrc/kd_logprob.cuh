@@ -15,6 +15,7 @@
 #include <stdint.h>
 
 #include "kd_common.cuh"
+#include "kd_internal.h"
 
 namespace kd {
 
@@ -214,6 +215,51 @@ __device__ __forceinline__ void lp_grad_pair(float& z0, float& z1, const LpGradR
 __device__ __forceinline__ float lp_grad(float z, const LpGradRow& g, float k) {
   const float x = max_nan(fmaf(z - g.m, k, -g.off), kXMin);
   return ex2(x) * fmaf(g.c1, x, g.c0);
+}
+
+// The terms of one row of a product (kd_internal.h).
+struct TermRow {
+  int n;
+  const __nv_bfloat16* src[kTermRows];
+  float c[kTermRows];
+};
+__device__ __forceinline__ TermRow term_row(const TcTerms& t, int64_t o) {
+  TermRow r;
+  r.n = 0;
+  int q[kTermRows];
+#pragma unroll
+  for (int i = 0; i < kTermRows; ++i) q[i] = INT32_MAX;
+  if (t.one_q) {
+    const int64_t y = t.one_q[o];
+    if (y >= 0 && y < t.src_rows) {
+      r.n = 1;
+      r.src[0] = t.src + y * t.ld_src;
+      r.c[0] = t.one_c[o];
+    }
+    return r;
+  }
+  const int n = t.count[o];
+  if (n < 1 || n > kTermRows) return r;
+  r.n = n;
+#pragma unroll
+  for (int i = 0; i < kTermRows; ++i)
+    if (i < n) q[i] = t.list[o * kTermRows + i];
+  // in ascending order, however they were listed
+#pragma unroll
+  for (int i = 0; i < kTermRows; ++i)
+#pragma unroll
+    for (int j = 0; j + 1 < kTermRows - i; ++j) {
+      const int a = min(q[j], q[j + 1]), b = max(q[j], q[j + 1]);
+      q[j] = a;
+      q[j + 1] = b;
+    }
+#pragma unroll
+  for (int i = 0; i < kTermRows; ++i)
+    if (i < n) {
+      r.src[i] = t.src + q[i] * t.ld_src;
+      r.c[i] = t.one_c[q[i]];
+    }
+  return r;
 }
 
 }  // namespace kd

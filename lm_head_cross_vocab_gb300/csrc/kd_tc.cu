@@ -1424,15 +1424,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
               for (int j = 0; j < 32; j += 2) lp_grad_pair(v[j], v[j + 1], tg, a.k2);
               const int64_t jy = tg.y - (a.c0 + lc0);
               if (tg.y >= 0 && jy >= 0 && jy < 32) {
+                // the token's element, nearly always by far the largest of the
+                // row: what rounding takes from it is added to the products
+                const float g = pick32(v, (int)jy) + tg.cy;
+                a.rest[a.r0 + g_row] = g - __bfloat162float(__float2bfloat16(g));
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = fmaf(j == (int)jy ? 1.f : 0.f, tg.cy, v[j]);
+                for (int j = 0; j < 32; ++j) take_if(v[j], g, j == (int)jy);
               }
               store_bf16x32(a.g + g_row * a.ldg + lc0, v, nv, a.ldg, tg.live);
             }
           }
-        } else {  // EPI_GEMM
+        } else {  // EPI_GEMM; HAS_T: with terms
           const TcGemmArgs& a = P.gemm;
           const int64_t row = tile_row;
+          TermRow terms;
+          if (HAS_T) {
+            terms.n = 0;
+            if (row < a.M) terms = term_row(a.terms, row);
+          }
 #pragma unroll 1
           for (int cc = 0; cc < BN / 2; cc += 32) {
             const int col_in_tile = half * (BN / 2) + cc;
@@ -1445,6 +1454,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
             const int nv = valid_cols(a.N - col0, 32);
             if (row < a.M && nv > 0) {
               const bool full = nv == 32;
+              if (HAS_T) {
+#pragma unroll
+                for (int i = 0; i < kTermRows; ++i) {
+                  if (i >= terms.n) break;
+                  float x[32];
+                  load_logits32(terms.src[i], col0, nv, true, x);
+#pragma unroll
+                  for (int j = 0; j < 32; ++j)
+                    if (j < nv) v[j] = fmaf(terms.c[i], x[j], v[j]);
+                }
+              }
               if (a.mode != TC_OUT_BF16) {
                 float* c = a.c32 + (part * a.M + row) * a.ldc32 + col0;
                 const bool vec = full && (a.ldc32 % 4) == 0;
@@ -1850,6 +1870,9 @@ int launch_tc_gemm(const TcGemmArgs& a, int num_sms, cudaStream_t s) {
   P.m_band = band_tiles(P, tc_tile_rows(pair));
   P.gemm = a;
   P.chain = pair ? a.chain : TC_CHAIN_NONE;
+  if (a.terms.src)
+    return pair ? launch<EPI_GEMM, 256, true, true>(P, num_sms, s)
+                : launch<EPI_GEMM, 256, true, false>(P, num_sms, s);
   return pair ? launch<EPI_GEMM, 256, false, true>(P, num_sms, s)
               : launch<EPI_GEMM, 256, false, false>(P, num_sms, s);
 }

@@ -426,6 +426,29 @@ def test_hidden_backward_in_chunks(n, v, d, want):
         assert all(torch.equal(kept[0][name], r[name]) for r in kept[1:])
 
 
+def test_ignore_index_that_is_an_id_and_repeated_tokens():
+    """Padding with an id of the vocabulary, and many tokens of one id: the
+    bound of test_hidden_backward, and rows that take no part exactly 0."""
+    n, v, d = 400, 900, 72
+    h, w = _hidden(n, v, d, "bf16", 3)
+    y = _tokens(n, v, 3, ignore=0.0)
+    y[::3], y[1::5] = 0, 7
+    y[50:53], y[60:64], y[70:75] = 11, 12, 13
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, d_model=d, source="hidden", ignore_index=0)
+    tens = {"h": h.cuda(), "w": w.cuda(), "tokens": y.cuda()}
+    out = kd.token_logprobs(p, tens)
+    gl = torch.linspace(-1, 1, n)
+    r = kd.token_logprobs_backward(p, tens, out["stats"], d_logprob=gl.cuda())
+    z, yy = _exact(h, w), torch.where(y == 0, IGN, y)
+    g_tol, g_ref = _grad_tol(z, yy, gl, None, 1.0, "bf16")
+    for name, a, at, b in (("d_h", g_ref, g_tol, as_f64(w)), ("d_w", g_ref.T, g_tol.T, as_f64(h))):
+        ref = a @ b
+        tol = at @ np.abs(b) + 2 * U * a.shape[1] * ((np.abs(a) + at) @ np.abs(b))
+        tol = tol + HALF["bf16"] * (np.abs(ref) + tol) + TINY
+        _close(r[name].float().cpu(), ref, tol, name)
+    assert (r["d_h"][(y == 0).cuda()] == 0).all()
+
+
 def test_gradients_by_differences():
     """The fp32 backward against central differences of the fp64 definition."""
     n, v, d = 3, 40, 8
