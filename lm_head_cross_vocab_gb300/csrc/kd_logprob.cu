@@ -703,6 +703,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_logprob_join_top(LpJoin j) {
 #pragma unroll
     for (int i = 0; i < 2 * kMaxSplits / 32; ++i)
       c[i] = 32 * i + tid < j.parts ? j.count[(int64_t)(32 * i + tid) * a.n + r] : 0;
+    // (a part that a timed-out wait ended has written nothing)
+#pragma unroll
+    for (int i = 0; i < 2 * kMaxSplits / 32; ++i) c[i] = max(0, min(c[i], kTokCap));
 #pragma unroll
     for (int i = 0; i < 2 * kMaxSplits / 32; ++i) {
       int up = c[i];
@@ -778,13 +781,13 @@ __global__ void __launch_bounds__(kJoinThreads) k_logprob_join_top(LpJoin j) {
     sort_words<kJoinThreads, kMaxCap / 2>(cand, have);
   } else {
     // many equal logits: one after the other
-    if (tid == 0) last = ~(uint64_t)0;
+    if (tid == 0) last = 0;
     for (int i = 0; i < k; ++i) {
       __syncthreads();
       const uint64_t l = last;
       uint64_t w = 0;
       each([&](uint64_t q) {
-        if (q < l) w = max(w, q);
+        if (i == 0 || q < l) w = max(w, q);
       });
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) w = max(w, __shfl_xor_sync(0xffffffffu, w, o));

@@ -223,6 +223,30 @@ def test_special_rows(v, k, dtype, t):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n", [1, 6, 400])
+@pytest.mark.parametrize("k", [1, 33, 700])
+def test_special_rows_of_a_large_vocabulary(n, k, dtype):
+    """The same kinds of rows split over the blocks of a cluster (few rows) and
+    in one block each, against a stable sort."""
+    v = 70001
+    kinds = _special_rows(v, dtype)[:14].cuda()  # (no NaN or +infinity)
+    z = kinds[torch.arange(n, device="cuda") % len(kinds) if n > 1 else [0]].contiguous()
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, topk=k, dtype=dtype)
+    out = kd.token_logprobs(p, {"logits": z})
+    order = torch.sort(z.double(), dim=1, descending=True, stable=True)[1]
+    assert torch.equal(out["topk_idx"], order[:, :k].int())
+    lp = torch.log_softmax(z.double(), dim=1).gather(1, order[:, :k])
+    dead = (z == -math.inf).all(dim=1)
+    lp[dead] = -math.inf
+    x = (z.double().amax(dim=1, keepdim=True) - z.double().gather(1, order[:, :k])).nan_to_num(0.0)
+    tol = _e_s(v) + (2 * x + 2 * lp.abs().nan_to_num(0.0, posinf=0.0) + 4) * U
+    got, fin = out["topk_logprob"].double(), torch.isfinite(lp.float())
+    assert torch.equal(torch.isfinite(got), fin)
+    assert ((got - lp).abs()[fin] <= tol[fin]).all()
+    assert (got[~fin] == -math.inf).all() and (out["entropy"][dead] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("v,pitch,shift", [(1000, 1000, 1), (1000, 1003, 0), (1001, 1016, 3),
                                            (4096, 4104, 8), (32003, 32100, 5)])
 def test_pitches_and_unaligned_rows(v, pitch, shift, dtype):
@@ -424,6 +448,79 @@ def test_hidden_backward_in_chunks(n, v, d, want):
         off = off + 2.0 ** -8 * (ref.abs() + off) + TINY
         assert ((kept[0][name].double() - ref).abs() <= off).all(), name
         assert all(torch.equal(kept[0][name], r[name]) for r in kept[1:])
+
+
+@pytest.mark.parametrize("v,k", [(300, 5), (30000, 128), (30000, 200)])
+def test_hidden_rows_that_are_not_finite(v, k):
+    """A hidden state with a NaN, and one that overflows the logits: that row is
+    NaN (its alternatives by id, a NaN above every number), the others are as
+    without it."""
+    n, d = 70, 64
+    h, w = _hidden(n, v, d, "bf16", 5)
+    y = _tokens(n, v, 5, ignore=0.0)
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, d_model=d, topk=k, source="hidden")
+    ref = kd.token_logprobs(p, {"h": h.cuda(), "w": w.cuda(), "tokens": y.cuda()})
+    bad = h.clone()
+    bad[3, 7], bad[40] = math.nan, math.inf
+    out = kd.token_logprobs(p, {"h": bad.cuda(), "w": w.cuda(), "tokens": y.cuda()})
+    fine = [r for r in range(n) if r not in (3, 40)]
+    for name in ("logprob", "entropy", "topk_idx", "topk_logprob"):
+        assert torch.equal(out[name][fine], ref[name][fine]), name
+    for r in (3, 40):
+        assert out["logprob"][r].isnan() and out["entropy"][r].isnan()
+        assert out["topk_logprob"][r].isnan().all()
+    assert out["topk_idx"][3].tolist() == list(range(k))
+
+
+def test_single_cta_tiles(monkeypatch):
+    """The CTA-pair tiles off (a debug override): the same alternatives, and
+    sums and gradients that differ by their order only."""
+    n, v, d, k = 300, 5003, 200, 20
+    h, w = _hidden(n, v, d, "bf16", 9)
+    y = _tokens(n, v, 9)
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, d_model=d, topk=k, source="hidden")
+    tens = {"h": h.cuda(), "w": w.cuda(), "tokens": y.cuda()}
+    gl = torch.linspace(-1, 1, n).cuda()
+    ref = kd.token_logprobs(p, tens)
+    grad = kd.token_logprobs_backward(p, tens, ref["stats"], d_logprob=gl)
+    monkeypatch.setenv("KD_TC_PAIR", "0")
+    out = kd.token_logprobs(p, tens)
+    _check_forward(out, _exact(h, w), y, 1.0, k)
+    assert torch.equal(out["topk_idx"], ref["topk_idx"])
+    one = kd.token_logprobs_backward(p, tens, ref["stats"], d_logprob=gl)
+    for name in ("d_h", "d_w"):
+        a, b = one[name].double(), grad[name].double()
+        # the sums differ by some u, so that a result may round the other way
+        assert ((a - b).abs() <= 2 * HALF["bf16"] * b.abs() + 1e-5 * b.abs().max()).all()
+
+
+def test_chunked_backward_in_a_graph():
+    """Several chunks captured into a graph and replayed on changed inputs."""
+    n, v, d = 2100, 9000, 64
+    h, w = (x.cuda() for x in _hidden(n, v, d, "bf16", 1))
+    y = _tokens(n, v, 1).cuda()
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, d_model=d, source="hidden")
+    tens, gl = {"h": h, "w": w, "tokens": y}, torch.linspace(-1, 1, n).cuda()
+    ws, s = kd.Workspace(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        o = kd.token_logprobs(p, tens, workspace=ws)
+        g = kd.token_logprobs_backward(p, tens, o["stats"], d_logprob=gl, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        kd.token_logprobs(p, tens, workspace=ws, check=False, out=o)
+        kd.token_logprobs_backward(p, tens, o["stats"], d_logprob=gl, workspace=ws, check=False,
+                                   out=g)
+    for _ in range(2):
+        h.copy_(h.roll(17, 0))
+        y.copy_(y.roll(5, 0))
+        graph.replay()
+        torch.cuda.synchronize()
+        o2 = kd.token_logprobs(p, tens)
+        g2 = kd.token_logprobs_backward(p, tens, o2["stats"], d_logprob=gl)
+        assert torch.equal(o["stats"], o2["stats"])
+        assert torch.equal(g["d_h"], g2["d_h"]) and torch.equal(g["d_w"], g2["d_w"])
 
 
 def test_ignore_index_that_is_an_id_and_repeated_tokens():
