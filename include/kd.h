@@ -374,9 +374,10 @@ kd_status kd_logprob_fwd(const kd_logprob_problem* problem, const kd_logprob_inp
  *            between the rows are left as they are; it may be the logits
  *            themselves when both pitches are equal)
  *   d_h [N, D], d_w [V, D]    (hidden source)
- * A bad token contributes no d_logprob term.  bf16 hidden problems round
- * d z to bf16 (at most 2^-8 of each element) before the products with W and
- * H, whose sums are fp32. */
+ * A bad token contributes no d_logprob term.  bf16 hidden problems round d z
+ * to bf16 (at most 2^-8 of each element) before the products with W and H,
+ * whose sums are fp32; what that takes from a row's element v = y goes into
+ * both products all the same (into d_w where at most four tokens are v). */
 kd_status kd_logprob_bwd(const kd_logprob_problem* problem, const kd_logprob_inputs* inputs,
                          const float* stats, const float* d_logprob, const float* d_entropy,
                          void* d_h, void* d_w, void* d_logits, uint32_t* dev_status,

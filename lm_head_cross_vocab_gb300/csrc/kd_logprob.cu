@@ -1161,8 +1161,9 @@ kd_status lp_plan(const kd_logprob_problem* p, LpPlan& P) {
   q.d_student = P.d;
   q.student = KD_STUDENT_HIDDEN;
   const int64_t quant = P.bf16 ? 256 : 64;
-  if (round_up(n, 128) * round_up(P.v, quant) <= (int64_t)8 << 20) {
-    P.R = round_up(n, 128);  // little enough to take whole
+  // few rows: less of G than there is of W, in one chunk
+  if (round_up(n, 128) * round_up(P.v, quant) <= (int64_t)(P.bf16 && n <= 256 ? 48 : 8) << 20) {
+    P.R = round_up(n, 128);
     P.C = round_up(P.v, quant);
   } else if (P.bf16) {
     choose_chunk(&q, (int64_t)64 << 20, quant, 4, P.R, P.C);
@@ -1476,11 +1477,11 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
     }
     return t;
   };
-  // one launch between a chunk and its products, or none can be chained
-  const bool chained = chunks > 1 && P.ks == 1;
+  // a chain ends where a launch needs the one right before it: between a chunk
+  // and its products when nothing is made between them, and at a sum of parts
   bool first = true;
   auto link = [&]() {
-    const int c = !chained ? TC_CHAIN_NONE : first ? TC_CHAIN_FIRST : TC_CHAIN_NEXT;
+    const int c = first ? TC_CHAIN_FIRST : TC_CHAIN_NEXT;
     first = false;
     return c;
   };
@@ -1529,19 +1530,11 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
     t.ldc16 = D;
     t.chain = link();
     const bool last = i + 1 == parts;
-    if (!a_mn && P.ks > 1) {  // dH over few rows: K in parts, then their sum
+    if (!a_mn && P.ks > 1) {  // dH over few rows: K in parts; sum_parts below
       t.k_splits = P.ks;
       t.mode = TC_OUT_F32;
       t.c32 = at<float>(workspace, P.b_part);
-      if (launch_tc_gemm(t, P.nsm, s)) return 1;
-      const int64_t vecs = m * D / 4;
-      note_launch();
-      k_sum_parts<<<(unsigned)cdiv(vecs, kRowThreads), kRowThreads, 0, s>>>(
-          reinterpret_cast<const float4*>(t.c32), vecs, P.ks, D, terms(k, a_mn, last),
-          i > 0 ? reinterpret_cast<const float4*>(acc) : nullptr,
-          last ? nullptr : reinterpret_cast<float4*>(acc),
-          last ? reinterpret_cast<uint2*>(out) : nullptr);
-      return 0;
+      return launch_tc_gemm(t, P.nsm, s);
     }
     t.mode = parts == 1 ? TC_OUT_BF16
              : i == 0   ? TC_OUT_F32
@@ -1552,21 +1545,34 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
     t.c16 = out;
     return launch_tc_gemm(t, P.nsm, s);
   };
+  auto sum_parts = [&](const Chunk& k, float* acc, __nv_bfloat16* out) {
+    const int64_t vecs = k.rc * D / 4;
+    const bool last = k.ci + 1 == nc;
+    note_launch();
+    k_sum_parts<<<(unsigned)cdiv(vecs, kRowThreads), kRowThreads, 0, s>>>(
+        at<float4>(workspace, P.b_part), vecs, P.ks, D, terms(k, false, last),
+        k.ci > 0 ? reinterpret_cast<const float4*>(acc) : nullptr,
+        last ? nullptr : reinterpret_cast<float4*>(acc),
+        last ? reinterpret_cast<uint2*>(out) : nullptr);
+  };
   auto products = [&](const Chunk& k) {
+    float* acc = nc > 1 ? at<float>(workspace, P.b_dh) + k.r0 * D : nullptr;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(d_h) + k.r0 * D;
     if (d_h && product(k, static_cast<const __nv_bfloat16*>(in->w) + k.c0 * D, k.rc, k.cc, false,
-                       nc > 1 ? at<float>(workspace, P.b_dh) + k.r0 * D : nullptr,
-                       static_cast<__nv_bfloat16*>(d_h) + k.r0 * D, k.ci, nc))
+                       acc, out, k.ci, nc))
       return 1;
-    return d_w && product(k, static_cast<const __nv_bfloat16*>(hm) + k.r0 * D, k.cc, k.rc, true,
-                          nr > 1 ? at<float>(workspace, P.b_dw) + k.c0 * D : nullptr,
-                          static_cast<__nv_bfloat16*>(d_w) + k.c0 * D, k.ri, nr)
-               ? 1
-               : 0;
+    if (d_w && product(k, static_cast<const __nv_bfloat16*>(hm) + k.r0 * D, k.cc, k.rc, true,
+                       nr > 1 ? at<float>(workspace, P.b_dw) + k.c0 * D : nullptr,
+                       static_cast<__nv_bfloat16*>(d_w) + k.c0 * D, k.ri, nr))
+      return 1;
+    if (d_h && P.ks > 1) sum_parts(k, acc, out);
+    return 0;
   };
   if (make(chunk(0))) return KD_ERR_CUDA;
-  for (int64_t i = 1; i < chunks; ++i)
+  for (int64_t i = 1; i < chunks; ++i) {
+    if (P.ks > 1) first = true;
     if (make(chunk(i)) || products(chunk(i - 1))) return KD_ERR_CUDA;
-  // the last chunk's products follow it directly: not chained to it
+  }
   first = true;
   if (products(chunk(chunks - 1))) return KD_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA;

@@ -716,8 +716,9 @@ def token_logprobs_backward(problem: LogprobProblem, tensors: dict, stats: torch
 class GradList:
     """The tensors of kd_clip_grad_norm, checked once for many calls: contiguous
     CUDA tensors of one dtype and device.  ``out``: tensors of the same shapes
-    for the clipped gradients; None clips in place.  ``dev_status`` collects the
-    status bits of its calls; the caller may zero it."""
+    for the clipped gradients; None clips in place.  It holds the tensors: build
+    another one where a program's gradients are new tensors.  ``dev_status``
+    collects the status bits of its calls; the caller may zero it."""
 
     def __init__(self, grads, out=None):
         self.grads = list(grads)
