@@ -653,3 +653,92 @@ def test_cache_teacher_then_distil_then_clip():
     for got, want in zip(r["grads"], out):
         err = np.linalg.norm(as_f64(got) - want) / np.linalg.norm(want)
         assert err <= 2e-2  # 1e-2 of the gradients (the loss's own bound), 1e-2 of the norm
+
+
+def test_offsets_beyond_32_bits():
+    """3.0e9 logits: the last rows, whose offsets pass 2^32 bytes and 2^31
+    elements, are as in a call of their own."""
+    n, v, tail = 20000, 151936, 40
+    z = torch.empty(n, v, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    z[-tail:] = (torch.randn(tail, v, generator=g, device="cuda") * 3).bfloat16()
+    z[:-tail] = 0
+    y = torch.randint(0, v, (n,), generator=g, device="cuda")
+    up = torch.linspace(-1, 1, n, device="cuda")
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, topk=3)
+    out = kd.token_logprobs(p, {"logits": z, "tokens": y})
+    q = kd.LogprobProblem(n_tokens=tail, vocab=v, topk=3)
+    last = {"logits": z[-tail:], "tokens": y[-tail:]}
+    ref = kd.token_logprobs(q, last)
+    assert torch.equal(out["topk_idx"][-tail:], ref["topk_idx"])
+    # (a row in one block or in eight: the sums differ by their order)
+    assert torch.allclose(out["stats"][-tail:], ref["stats"], rtol=2 * _e_s(v), atol=2 * _e_s(v))
+    assert torch.allclose(out["logprob"][:-tail], torch.full((1,), -math.log(v), device="cuda"))
+    assert out["topk_idx"][0].tolist() == [0, 1, 2]
+    dz = kd.token_logprobs_backward(p, {"logits": z, "tokens": y}, out["stats"], d_logprob=up,
+                                    out={"d_logits": z, "dev_status": out["dev_status"]})
+    assert torch.equal(dz["d_logits"][0, :5], dz["d_logits"][0, 1000:1005])
+    z2 = dz["d_logits"][-tail:].float().sum(dim=1)
+    # a row of the gradient sums to 0 but for the roundings of its elements
+    assert (z2.abs() <= 2.0 ** -7 * dz["d_logits"][-tail:].float().abs().sum(dim=1)).all()
+
+
+def test_hidden_gradient_without_tokens():
+    n, v, d = 150, 3001, 64
+    h, w = _hidden(n, v, d, "bf16", 21)
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, d_model=d, source="hidden")
+    tens = {"h": h.cuda(), "w": w.cuda()}
+    out = kd.token_logprobs(p, tens)
+    assert out["logprob"] is None
+    gh = torch.linspace(-1, 1, n)
+    r = kd.token_logprobs_backward(p, tens, out["stats"], d_entropy=gh.cuda())
+    g_tol, g_ref = _grad_tol(_exact(h, w), None, None, gh, 1.0, "bf16")
+    for name, a, at, b in (("d_h", g_ref, g_tol, as_f64(w)), ("d_w", g_ref.T, g_tol.T, as_f64(h))):
+        ref = a @ b
+        tol = at @ np.abs(b) + 2 * U * a.shape[1] * ((np.abs(a) + at) @ np.abs(b))
+        _close(r[name].float().cpu(), ref, tol + HALF["bf16"] * (np.abs(ref) + tol) + TINY, name)
+
+
+@pytest.mark.parametrize("source", ["logits", "hidden"])
+def test_outputs_can_be_left_out(source):
+    n, v, d, k = 20, 2000, 64, 9
+    h, w = _hidden(n, v, d, "bf16", 4)
+    tens = {"h": h.cuda(), "w": w.cuda(), "tokens": _tokens(n, v, 4).cuda(),
+            "logits": _logits(n, v, "bf16", 4).cuda()}
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, d_model=d, topk=k, source=source)
+    ref = kd.token_logprobs(p, tens)
+    for names in (("topk_idx",), ("topk_logprob",), ("logprob",), ("entropy", "stats"), ()):
+        out = {x: torch.empty_like(ref[x]) for x in names}
+        out["dev_status"] = torch.zeros((), dtype=torch.int32, device="cuda")
+        got = kd.token_logprobs(p, tens, out=out)
+        for x in names:
+            assert torch.equal(got[x], ref[x]) or (
+                x != "topk_idx" and torch.allclose(got[x], ref[x], rtol=0, atol=1e-5)), (names, x)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams with a workspace each, in flight together."""
+    n, v, d, k = 500, 20000, 256, 30
+    sides = []
+    for i in range(2):
+        h, w = (x.cuda() for x in _hidden(n, v, d, "bf16", 30 + i))
+        tens = {"h": h, "w": w, "tokens": _tokens(n, v, 30 + i).cuda()}
+        p = kd.LogprobProblem(n_tokens=n, vocab=v, d_model=d, topk=k, source="hidden")
+        up = torch.linspace(-1, 1, n, device="cuda")
+        ref = kd.token_logprobs(p, tens)
+        grad = kd.token_logprobs_backward(p, tens, ref["stats"], d_logprob=up)
+        sides.append((torch.cuda.Stream(), kd.Workspace(), p, tens, up, ref, grad))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for s, ws, p, tens, up, ref, grad in sides:
+            with torch.cuda.stream(s):
+                o = kd.token_logprobs(p, tens, workspace=ws, check=False)
+                g = kd.token_logprobs_backward(p, tens, o["stats"], d_logprob=up, workspace=ws,
+                                               check=False)
+                got.append((o, g, ref, grad))
+    torch.cuda.synchronize()
+    for o, g, ref, grad in got:
+        for x in ("logprob", "entropy", "topk_idx", "topk_logprob", "stats"):
+            assert torch.equal(o[x], ref[x]), x
+        assert torch.equal(g["d_h"], grad["d_h"]) and torch.equal(g["d_w"], grad["d_w"])
