@@ -186,7 +186,7 @@ __device__ __forceinline__ void cluster_wait() {
 // Shared memory of the selection; cand has `cap` places.
 struct SelectShared {
   uint32_t hist[256];
-  uint32_t prefix, want, count, owners, pairs, bound;
+  uint32_t prefix, want, count, pairs, bound;
   uint32_t warp_sum[2][32];  // alternately, so that one barrier a step is enough
 };
 
@@ -392,10 +392,28 @@ __host__ __device__ constexpr int row_smem(int k, int blocks) {
                       (blocks > 1 ? blocks * k * 8 : 0);
 }
 
-// The slice's best `want` ids into cand, in order.  best: this thread's key.
+// Places for each lane's n words behind *count: one scan and one atomic a warp.
+// All lanes take part.
+__device__ __forceinline__ uint32_t warp_places(uint32_t n, uint32_t* count) {
+  const int lane = threadIdx.x & 31;
+  uint32_t sum = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t below = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += below;
+  }
+  uint32_t at = 0;
+  if (lane == 31 && sum) at = atomicAdd(count, sum);
+  return __shfl_sync(0xffffffffu, at, 31) + sum - n;
+}
+
+// The slice's best `want` ids into cand, in order.  A slot is 1 << lg of a
+// thread's vectors; best: this thread's key.
 template <class T, int NT>
-__device__ __noinline__ void select_top(const Slice<T>& sl, int want, int cap, int slots, int per_slot,
+__device__ __noinline__ void select_top(const Slice<T>& sl, int want, int cap, int slots, int lg,
                            uint32_t best, SelectShared& sh, uint64_t* cand) {
+  constexpr int N = Vec<T>::N;
+  static_assert(kSlots <= 32 && kUnroll * N <= 32, "a bit each");
   const int tid = threadIdx.x;
   uint16_t* slot_key = reinterpret_cast<uint16_t*>(cand + cap);
   uint16_t* own_key = slot_key + kSlots * NT;
@@ -412,28 +430,30 @@ __device__ __noinline__ void select_top(const Slice<T>& sl, int want, int cap, i
   } else {
     bound = bound_key_slots<NT>(slot_key, slots, want, sh);
   }
-  // threads above the bound, then their slots above it, spread over the block
-  if ((best >> 16) >= bound) own_key[atomicAdd(&sh.owners, 1u)] = (uint16_t)tid;
-  __syncthreads();
-  const int checks = (int)sh.owners * slots;
-  for (int i = tid; i < checks; i += NT) {
-    const int at = i % slots * NT + own_key[i / slots];
-    if (slot_key[at] >= bound) {
-      const uint32_t p = atomicAdd(&sh.pairs, 1u);
-      if (p < (uint32_t)kPairs) list[p] = (uint16_t)at;
+  // the slots above the bound, of the threads above it
+  uint32_t bits = 0;
+  if ((best >> 16) >= bound) {
+#pragma unroll 8
+    for (int i = 0; i < slots; ++i) bits |= (uint32_t)(slot_key[i * NT + tid] >= bound) << i;
+  }
+  uint32_t p = warp_places(__popc(bits), &sh.pairs);
+  for (; bits; bits &= bits - 1, ++p)
+    if (p < (uint32_t)kPairs) list[p] = (uint16_t)((__ffs(bits) - 1) * NT + tid);
+  // not below the lowest value of that key; where the key is a NaN's or no
+  // value's, every logit is let through
+  const float low = key_value(bound << 16);
+  if (tid < sl.loose) {
+    const int64_t id = sl.loose_at(tid);
+    const float z = to_f(sl.z[id]);
+    if (!(z < low)) {
+      const uint32_t at = atomicAdd(&sh.count, 1u);
+      if (at < (uint32_t)cap) cand[at] = cand_word(order_key(z), (uint32_t)id);
     }
   }
-  auto offer = [&](float z, int64_t id) {
-    const uint32_t q = order_key(z);
-    if ((q >> 16) < bound) return;
-    const uint32_t at = atomicAdd(&sh.count, 1u);
-    if (at < (uint32_t)cap) cand[at] = cand_word(q, (uint32_t)id);
-  };
-  if (tid < sl.loose) offer(to_f(sl.z[sl.loose_at(tid)]), sl.loose_at(tid));
   __syncthreads();
   const int pairs = (int)sh.pairs;
-  const int items = pairs <= kPairs ? pairs * per_slot : 0;
-  for (int i0 = tid; i0 < items; i0 += kUnroll * NT) {
+  const int items = pairs <= kPairs ? pairs << lg : 0;
+  for (int i0 = tid; (i0 & ~31) < items; i0 += kUnroll * NT) {
     Words w[kUnroll];
     int at[kUnroll];
 #pragma unroll
@@ -441,18 +461,28 @@ __device__ __noinline__ void select_top(const Slice<T>& sl, int want, int cap, i
       const int i = i0 + u * NT;
       at[u] = INT32_MAX;
       if (i < items) {
-        const int pair = list[i / per_slot];
-        at[u] = (pair / NT * per_slot + i % per_slot) * NT + pair % NT;
+        const int pair = list[i >> lg];
+        at[u] = ((pair / NT << lg) + (i & ((1 << lg) - 1))) * NT + pair % NT;
       }
       if (at[u] < sl.nvec) w[u] = sl.vec(at[u]);
     }
+    uint32_t hits = 0;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if (at[u] >= sl.nvec || (order_key(Vec<T>::top(w[u])) >> 16) < bound) continue;
-      float z[Vec<T>::N];
+      if (at[u] >= sl.nvec) continue;
+      float z[N];
       Vec<T>::get(w[u], z);
 #pragma unroll
-      for (int e = 0; e < Vec<T>::N; ++e) offer(z[e], sl.base + (int64_t)at[u] * Vec<T>::N + e);
+      for (int e = 0; e < N; ++e)
+        if (!(z[e] < low)) hits |= 1u << (u * N + e);
+    }
+    uint32_t c = warp_places(__popc(hits), &sh.count);
+    for (; hits; hits &= hits - 1, ++c) {
+      if (c >= (uint32_t)cap) break;
+      const int bit = __ffs(hits) - 1, u = bit / N;
+      const int v = u < 2 ? (u == 0 ? at[0] : at[1]) : (u == 2 ? at[2] : at[3]);
+      const int64_t id = sl.base + (int64_t)v * N + bit % N;
+      cand[c] = cand_word(order_key(to_f(sl.z[id])), (uint32_t)id);
     }
   }
   __syncthreads();
@@ -494,16 +524,17 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
   const float zy = (tid == 0 && rank == 0 && in) ? to_f(sl.z[label]) : 0.f;
 
   // ---- one sweep
-  const int per_slot = max(1, (sl.rounds + kSlots - 1) / kSlots);
-  int slots = 0, left = per_slot;
+  int lg = 2, slots = 0, left = 0;  // a slot: 2^lg vectors
+  static_assert(kUnroll == 4, "a slot is a power of two of steps, or a vector");
+  // where the slots bound the alternatives a slot of a short row is one vector
+  if (a.topk > NT / 2 && sl.rounds <= kSlots) lg = 0;
+  else while (((sl.rounds - 1) >> lg) >= kSlots) ++lg;
   float slot_top = neg_inf();
   uint32_t best = 0;  // key of the thread's maximum
-  auto close_slot = [&]() {
-    const uint32_t q = order_key(slot_top);
+  auto close_slot = [&](float top) {
+    const uint32_t q = order_key(top);
     slot_key[slots++ * NT + tid] = (uint16_t)(q >> 16);
     best = max(best, q);
-    slot_top = neg_inf();
-    left = per_slot;
   };
   LpFold f;
   f.init(a.k2);
@@ -530,25 +561,30 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
       }
     }
     if (TOPK) {
+      if (lg == 0) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        if (j + u < sl.rounds) {
-          slot_top = max_nan(slot_top, m[u]);
-          if (--left == 0) close_slot();
+        for (int u = 0; u < kUnroll; ++u)
+          if (j + u < sl.rounds) close_slot(m[u]);
+      } else {
+        slot_top = max_nan(slot_top, mm);
+        if (((j + kUnroll) & ((1 << lg) - 1)) == 0) {
+          close_slot(slot_top);
+          slot_top = neg_inf();
+          left = j + kUnroll;
         }
       }
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) cur[u] = nxt[u];
   }
-  if (TOPK && left != per_slot) close_slot();
+  if (TOPK && lg != 0 && left < sl.rounds) close_slot(slot_top);
 
   // ---- the row's statistics
   LpState st = f.state();
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) lp_merge(st, lp_shfl_xor(st, o), a.k2);
   if ((tid & 31) == 0) warp_state[tid >> 5] = st;
-  if (TOPK && tid == 0) sh.count = sh.owners = sh.pairs = 0;
+  if (TOPK && tid == 0) sh.count = sh.pairs = 0;
   __syncthreads();
   st = warp_state[tid & (NT / 32 - 1)];
 #pragma unroll
@@ -558,7 +594,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
   int have = 0;
   if (TOPK) {
     have = (int)min((int64_t)a.topk, sl.size());
-    select_top<T, NT>(sl, have, cap, slots, per_slot, best, sh, cand);
+    select_top<T, NT>(sl, have, cap, slots, lg, best, sh, cand);
   }
 
   // ---- join the slices: every block fetches all sums and lists
