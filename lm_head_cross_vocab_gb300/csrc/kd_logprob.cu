@@ -98,6 +98,13 @@ __device__ __forceinline__ Words load16(const void* p) {
                : "l"(p));
   return v;
 }
+// 32 bytes (and a 32-byte boundary): one sector a lane.
+__device__ __forceinline__ void load32(const void* p, Words& a, Words& b) {
+  asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(a.w[0]), "=r"(a.w[1]), "=r"(a.w[2]), "=r"(a.w[3]), "=r"(b.w[0]),
+                 "=r"(b.w[1]), "=r"(b.w[2]), "=r"(b.w[3])
+               : "l"(p));
+}
 // A vector of the row: elements, and -inf in each.
 template <class T>
 struct Vec;
@@ -136,34 +143,39 @@ struct Vec<__nv_bfloat16> {
   }
 };
 
-// The part of a row one block takes: `nvec` vectors from the 16-byte boundary
-// `head` elements into the row (those of all blocks of the cluster together
-// cover the row's vectors); block 0 takes the `loose` elements before and
-// behind the vectors as well.
+// The part of a row one block takes: `nvec` vectors of 16 bytes, an even number,
+// from the 32-byte boundary `head` elements into the row (those of all blocks of
+// the cluster together cover the row's); block 0 takes the `loose` elements
+// before and behind them as well.  A thread takes 64 bytes, the least that HBM
+// gives, at a time: they are what it reads again.
 template <class T>
 struct Slice {
   const T* z;
-  int64_t v0;           // first vector
-  int nvec, rounds;     // vectors; per thread
+  int nvec, chunks, rounds;  // vectors; runs of four; vectors of a thread
   int head, loose;
-  int64_t tail0;        // first element behind the vectors
-  int64_t base;         // element index of vector 0 of the slice
+  int64_t tail0;             // first element behind the vectors
+  int64_t base;              // element index of vector 0 of the slice
 
   __device__ __forceinline__ Slice(const T* row, int64_t vocab, int rank, int blocks, int nt) {
     constexpr int N = Vec<T>::N;
     z = row;
-    const int off = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
-    head = off ? N - off : 0;
+    const int off = (int)((reinterpret_cast<uintptr_t>(row) & 31) / sizeof(T));
+    head = off ? 2 * N - off : 0;
     if (head > vocab) head = (int)vocab;
-    const int64_t all = (vocab - head) / N;
-    v0 = all * rank / blocks;
-    nvec = (int)(all * (rank + 1) / blocks - v0);
-    rounds = (nvec + nt - 1) / nt;
-    tail0 = head + all * N;
+    const int64_t all = (vocab - head) / (2 * N), v0 = all * rank / blocks;
+    nvec = 2 * (int)(all * (rank + 1) / blocks - v0);
+    chunks = (nvec + 3) / 4;
+    rounds = (chunks + nt - 1) / nt * 4;
+    tail0 = head + all * 2 * N;
     loose = rank == 0 ? head + (int)(vocab - tail0) : 0;
-    base = head + v0 * N;
+    base = head + v0 * 2 * N;
   }
-  __device__ __forceinline__ Words vec(int i) const { return load16(z + base + (int64_t)i * Vec<T>::N); }
+  __device__ __forceinline__ const T* at_vec(int i) const { return z + base + (int64_t)i * Vec<T>::N; }
+  __device__ __forceinline__ Words vec(int i) const { return load16(at_vec(i)); }
+  __device__ __forceinline__ void chunk(int c, Words* w) const {
+    if (4 * c < nvec) load32(at_vec(4 * c), w[0], w[1]);
+    if (4 * c + 2 < nvec) load32(at_vec(4 * c + 2), w[2], w[3]);
+  }
   __device__ __forceinline__ int64_t loose_at(int i) const { return i < head ? i : tail0 + (i - head); }
   // elements of the slice, in the order of their ids, for the exact selection
   __device__ __forceinline__ int64_t size() const { return (int64_t)nvec * Vec<T>::N + loose; }
@@ -421,7 +433,7 @@ __device__ __noinline__ void select_top(const Slice<T>& sl, int want, int cap, i
   uint32_t bound;
   // few alternatives: the threads' own maxima bound them closely enough (k of
   // NT leave about -NT log(1 - k/NT) ids above the bound)
-  if (want <= NT / 2) {
+  if (want <= min(NT, sl.chunks) / 2) {
     own_key[tid] = (uint16_t)(best >> 16);
     __syncthreads();
     if (tid < 32) bound_key<NT>(own_key, want, &sh.bound);
@@ -462,7 +474,8 @@ __device__ __noinline__ void select_top(const Slice<T>& sl, int want, int cap, i
       at[u] = INT32_MAX;
       if (i < items) {
         const int pair = list[i >> lg];
-        at[u] = ((pair / NT << lg) + (i & ((1 << lg) - 1))) * NT + pair % NT;
+        const int q = (pair / NT << lg) + (i & ((1 << lg) - 1));
+        at[u] = ((q / kUnroll) * NT + pair % NT) * kUnroll + q % kUnroll;
       }
       if (at[u] < sl.nvec) w[u] = sl.vec(at[u]);
     }
@@ -514,7 +527,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
   const int64_t r = blockIdx.x / blocks;
   const Slice<T> sl(static_cast<const T*>(a.z) + r * a.ld, a.vocab, rank, blocks, NT);
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) cur[u] = tid + u * NT < sl.nvec ? sl.vec(tid + u * NT) : none;
+  for (int u = 0; u < kUnroll; ++u) cur[u] = none;
+  sl.chunk(tid, cur);
   const int64_t label = a.tokens ? a.tokens[r] : -1;
   if (a.tokens && label == a.ignore) {  // the whole cluster
     if (rank == 0) lp_store_ignored(a, r);
@@ -527,7 +541,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
   int lg = 2, slots = 0, left = 0;  // a slot: 2^lg vectors
   static_assert(kUnroll == 4, "a slot is a power of two of steps, or a vector");
   // where the slots bound the alternatives a slot of a short row is one vector
-  if (a.topk > NT / 2 && sl.rounds <= kSlots) lg = 0;
+  if (a.topk > min(NT, sl.chunks) / 2 && sl.rounds <= kSlots) lg = 0;
   else while (((sl.rounds - 1) >> lg) >= kSlots) ++lg;
   float slot_top = neg_inf();
   uint32_t best = 0;  // key of the thread's maximum
@@ -541,9 +555,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
   if (tid < sl.loose) f.add_one(to_f(sl.z[sl.loose_at(tid)]));
   for (int j = 0; j < sl.rounds; j += kUnroll) {
     Words nxt[kUnroll];
-    const int i0 = tid + (j + kUnroll) * NT;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) nxt[u] = i0 + u * NT < sl.nvec ? sl.vec(i0 + u * NT) : none;
+    for (int u = 0; u < kUnroll; ++u) nxt[u] = none;
+    sl.chunk((j / kUnroll + 1) * NT + tid, nxt);
     float m[kUnroll], mm = neg_inf();
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -563,8 +577,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
     if (TOPK) {
       if (lg == 0) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-          if (j + u < sl.rounds) close_slot(m[u]);
+        for (int u = 0; u < kUnroll; ++u) close_slot(m[u]);
       } else {
         slot_top = max_nan(slot_top, mm);
         if (((j + kUnroll) & ((1 << lg) - 1)) == 0) {
