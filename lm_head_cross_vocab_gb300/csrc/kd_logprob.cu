@@ -86,6 +86,7 @@ __device__ __forceinline__ void lp_store_ignored(const LpArgs& a, int64_t r) {
 constexpr int kSlots = 32;
 constexpr int kPairs = 4096;   // slots above the bound the list holds
 constexpr int kMaxCap = 4096;  // candidates a block sorts at most
+constexpr int kFewK = 128, kFewCap = 1024;  // with up to kFewK alternatives
 constexpr int kUnroll = 4;
 
 struct Words {
@@ -156,14 +157,15 @@ struct Slice {
   int64_t tail0;             // first element behind the vectors
   int64_t base;              // element index of vector 0 of the slice
 
-  __device__ __forceinline__ Slice(const T* row, int64_t vocab, int rank, int blocks, int nt) {
+  // 1 << lb blocks
+  __device__ __forceinline__ Slice(const T* row, int64_t vocab, int rank, int lb, int nt) {
     constexpr int N = Vec<T>::N;
     z = row;
     const int off = (int)((reinterpret_cast<uintptr_t>(row) & 31) / sizeof(T));
     head = off ? 2 * N - off : 0;
     if (head > vocab) head = (int)vocab;
-    const int64_t all = (vocab - head) / (2 * N), v0 = all * rank / blocks;
-    nvec = 2 * (int)(all * (rank + 1) / blocks - v0);
+    const int64_t all = (vocab - head) / (2 * N), v0 = all * rank >> lb;
+    nvec = 2 * (int)((all * (rank + 1) >> lb) - v0);
     chunks = (nvec + 3) / 4;
     rounds = (chunks + nt - 1) / nt * 4;
     tail0 = head + all * 2 * N;
@@ -172,9 +174,18 @@ struct Slice {
   }
   __device__ __forceinline__ const T* at_vec(int i) const { return z + base + (int64_t)i * Vec<T>::N; }
   __device__ __forceinline__ Words vec(int i) const { return load16(at_vec(i)); }
-  __device__ __forceinline__ void chunk(int c, Words* w) const {
-    if (4 * c < nvec) load32(at_vec(4 * c), w[0], w[1]);
-    if (4 * c + 2 < nvec) load32(at_vec(4 * c + 2), w[2], w[3]);
+  // step j of thread t of nt; -inf behind the vectors
+  __device__ __forceinline__ void chunk(int j, int t, int nt, Words* w) const {
+    const int c = j * nt + t;
+    if (4 * (j + 1) * nt <= nvec) {
+      load32(at_vec(4 * c), w[0], w[1]);
+      load32(at_vec(4 * c + 2), w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i / 4].w[i % 4] = Vec<T>::kNone;
+      if (4 * c < nvec) load32(at_vec(4 * c), w[0], w[1]);
+      if (4 * c + 2 < nvec) load32(at_vec(4 * c + 2), w[2], w[3]);
+    }
   }
   __device__ __forceinline__ int64_t loose_at(int i) const { return i < head ? i : tail0 + (i - head); }
   // elements of the slice, in the order of their ids, for the exact selection
@@ -207,7 +218,7 @@ struct SelectShared {
 // lowest ids among those equal to it.  Exact for any row; taken where too many
 // ids lie at or above the bound (long runs of equal logits).
 template <class T>
-__device__ __noinline__ void select_exact(const Slice<T>& sl, int k, SelectShared& sh, uint64_t* cand) {
+__device__ __noinline__ void select_exact(Slice<T> sl, int k, SelectShared& sh, uint64_t* cand) {
   const int tid = threadIdx.x, nt = blockDim.x;
   const int64_t v = sl.size();
   if (tid == 0) {
@@ -368,6 +379,11 @@ __device__ __forceinline__ void sort_bitonic(uint64_t* cand, int n) {
   for (int i = 0; i < E; ++i) cand[t0 + i] = w[i];
   __syncthreads();
 }
+// The same out of line: more words than the sweep has registers to spare for.
+template <int NT, int E>
+__device__ __noinline__ void sort_many(uint64_t* cand, int n) {
+  sort_bitonic<NT, E>(cand, n);
+}
 // Descending sort of cand[0, n), n <= cap: few words go to the place that the
 // number of larger ones gives, more through a bitonic sort.
 template <int NT, int CAP>
@@ -385,18 +401,17 @@ __device__ __forceinline__ void sort_words(uint64_t* cand, int n) {
   } else if (n <= 4 * NT) {
     sort_bitonic<NT, 4>(cand, n);
   } else if (n <= 8 * NT) {
-    sort_bitonic<NT, 8>(cand, n);
-  } else if (CAP > 8 * NT && n <= 16 * NT) {
-    if constexpr (CAP > 8 * NT) sort_bitonic<NT, 16>(cand, n);
-  } else if constexpr (CAP > 16 * NT) {
-    sort_bitonic<NT, CAP / NT>(cand, n);
+    sort_many<NT, 8>(cand, n);
+  } else if constexpr (CAP > 8 * NT) {
+    static_assert(CAP <= 16 * NT, "");
+    sort_many<NT, 16>(cand, n);
   }
 }
 
 // Dynamic shared memory: cand[cap] (u64), the upper halves of the slot keys
 // [kSlots][NT] and of the threads' own maxima [NT] (u16), and the list of slots
 // above the bound [kPairs] (u16); in clusters, all blocks' lists [blocks][k] (u64).
-__host__ __device__ constexpr int row_cap(int k) { return k <= 128 ? 1024 : kMaxCap; }
+__host__ __device__ constexpr int row_cap(int k) { return k <= kFewK ? kFewCap : kMaxCap; }
 template <int NT>
 __host__ __device__ constexpr int row_smem(int k, int blocks) {
   return k == 0 ? 0
@@ -422,7 +437,7 @@ __device__ __forceinline__ uint32_t warp_places(uint32_t n, uint32_t* count) {
 // The slice's best `want` ids into cand, in order.  A slot is 1 << lg of a
 // thread's vectors; best: this thread's key.
 template <class T, int NT>
-__device__ __noinline__ void select_top(const Slice<T>& sl, int want, int cap, int slots, int lg,
+__device__ __forceinline__ void select_top(const Slice<T>& sl, int want, int cap, int slots, int lg,
                            uint32_t best, SelectShared& sh, uint64_t* cand) {
   constexpr int N = Vec<T>::N;
   static_assert(kSlots <= 32 && kUnroll * N <= 32, "a bit each");
@@ -430,30 +445,41 @@ __device__ __noinline__ void select_top(const Slice<T>& sl, int want, int cap, i
   uint16_t* slot_key = reinterpret_cast<uint16_t*>(cand + cap);
   uint16_t* own_key = slot_key + kSlots * NT;
   uint16_t* list = own_key + NT;
-  uint32_t bound;
+  uint32_t bound;  // upper half of an order key
   // few alternatives: the threads' own maxima bound them closely enough (k of
   // NT leave about -NT log(1 - k/NT) ids above the bound)
-  if (want <= min(NT, sl.chunks) / 2) {
+  const int own_bound = min(NT, sl.chunks) / 2;
+  if (want <= own_bound) {
     own_key[tid] = (uint16_t)(best >> 16);
     __syncthreads();
     if (tid < 32) bound_key<NT>(own_key, want, &sh.bound);
     __syncthreads();
     bound = sh.bound;
   } else {
+    // (a lowest denormal's upper half reads as that of -0, which is kept as +0)
+    for (int i = 0; i < slots; ++i) {
+      const uint32_t q = slot_key[i * NT + tid];
+      slot_key[i * NT + tid] =
+          q == 0x8000u ? 0x7fffu : (uint16_t)(order_key(__uint_as_float(q << 16)) >> 16);
+    }
     bound = bound_key_slots<NT>(slot_key, slots, want, sh);
   }
+  // not below the lowest value of that key; where the key is a NaN's or no
+  // value's, every logit is let through
+  const float low = key_value(bound << 16);
   // the slots above the bound, of the threads above it
   uint32_t bits = 0;
-  if ((best >> 16) >= bound) {
+  if (want > own_bound) {
 #pragma unroll 8
     for (int i = 0; i < slots; ++i) bits |= (uint32_t)(slot_key[i * NT + tid] >= bound) << i;
+  } else if ((best >> 16) >= bound) {
+#pragma unroll 8
+    for (int i = 0; i < slots; ++i)
+      bits |= (uint32_t)!(__uint_as_float((uint32_t)slot_key[i * NT + tid] << 16) < low) << i;
   }
   uint32_t p = warp_places(__popc(bits), &sh.pairs);
   for (; bits; bits &= bits - 1, ++p)
     if (p < (uint32_t)kPairs) list[p] = (uint16_t)((__ffs(bits) - 1) * NT + tid);
-  // not below the lowest value of that key; where the key is a NaN's or no
-  // value's, every logit is let through
-  const float low = key_value(bound << 16);
   if (tid < sl.loose) {
     const int64_t id = sl.loose_at(tid);
     const float z = to_f(sl.z[id]);
@@ -505,7 +531,8 @@ __device__ __noinline__ void select_top(const Slice<T>& sl, int want, int cap, i
     select_exact(sl, want, sh, cand);
     have = want;
   }
-  sort_words<NT, kMaxCap>(cand, have);
+  // (128 threads: at most kFewK alternatives)
+  sort_words<NT, NT == 128 ? kFewCap : kMaxCap>(cand, have);
 }
 
 template <class T, int NT, bool TOPK>
@@ -521,14 +548,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
   const int cap = row_cap(a.topk);
   uint64_t* cand = reinterpret_cast<uint64_t*>(dyn);
   uint16_t* slot_key = reinterpret_cast<uint16_t*>(cand + cap);
-  Words none, cur[kUnroll];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) none.w[i] = Vec<T>::kNone;
-  const int64_t r = blockIdx.x / blocks;
-  const Slice<T> sl(static_cast<const T*>(a.z) + r * a.ld, a.vocab, rank, blocks, NT);
-#pragma unroll
-  for (int u = 0; u < kUnroll; ++u) cur[u] = none;
-  sl.chunk(tid, cur);
+  Words even[kUnroll], odd[kUnroll];
+  const int lb = __ffs(blocks) - 1;
+  const int64_t r = blockIdx.x >> lb;
+  const Slice<T> sl(static_cast<const T*>(a.z) + r * a.ld, a.vocab, rank, lb, NT);
+  sl.chunk(0, tid, NT, even);
   const int64_t label = a.tokens ? a.tokens[r] : -1;
   if (a.tokens && label == a.ignore) {  // the whole cluster
     if (rank == 0) lp_store_ignored(a, r);
@@ -538,30 +562,26 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
   const float zy = (tid == 0 && rank == 0 && in) ? to_f(sl.z[label]) : 0.f;
 
   // ---- one sweep
-  int lg = 2, slots = 0, left = 0;  // a slot: 2^lg vectors
+  int lg = 2;  // a slot: 2^lg vectors
   static_assert(kUnroll == 4, "a slot is a power of two of steps, or a vector");
   // where the slots bound the alternatives a slot of a short row is one vector
   if (a.topk > min(NT, sl.chunks) / 2 && sl.rounds <= kSlots) lg = 0;
   else while (((sl.rounds - 1) >> lg) >= kSlots) ++lg;
-  float slot_top = neg_inf();
-  uint32_t best = 0;  // key of the thread's maximum
+  const int slots = ((sl.rounds - 1) >> lg) + 1;
+  uint16_t* slot = slot_key + tid;
+  float best = neg_inf(), slot_top = neg_inf();
   auto close_slot = [&](float top) {
-    const uint32_t q = order_key(top);
-    slot_key[slots++ * NT + tid] = (uint16_t)(q >> 16);
-    best = max(best, q);
+    *slot = (uint16_t)(__float_as_uint(top + 0.f) >> 16);
+    slot += NT;
   };
   LpFold f;
   f.init(a.k2);
   if (tid < sl.loose) f.add_one(to_f(sl.z[sl.loose_at(tid)]));
-  for (int j = 0; j < sl.rounds; j += kUnroll) {
-    Words nxt[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) nxt[u] = none;
-    sl.chunk((j / kUnroll + 1) * NT + tid, nxt);
+  auto step = [&](int j, const Words* w) {
     float m[kUnroll], mm = neg_inf();
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      m[u] = Vec<T>::top(cur[u]);
+      m[u] = Vec<T>::top(w[u]);
       mm = max_nan(mm, m[u]);
     }
     if (mm != neg_inf()) {
@@ -569,28 +589,34 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         float z[Vec<T>::N];
-        Vec<T>::get(cur[u], z);
+        Vec<T>::get(w[u], z);
 #pragma unroll
         for (int e = 0; e < Vec<T>::N; e += 2) f.add_pair(z[e], z[e + 1]);
       }
     }
     if (TOPK) {
+      best = max_nan(best, mm);
       if (lg == 0) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) close_slot(m[u]);
       } else {
         slot_top = max_nan(slot_top, mm);
-        if (((j + kUnroll) & ((1 << lg) - 1)) == 0) {
+        if ((((j + 1) * kUnroll) & ((1 << lg) - 1)) == 0) {
           close_slot(slot_top);
           slot_top = neg_inf();
-          left = j + kUnroll;
         }
       }
     }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) cur[u] = nxt[u];
+  };
+  const int steps = sl.rounds / kUnroll;
+  for (int j = 0; j < steps; j += 2) {
+    sl.chunk(j + 1, tid, NT, odd);
+    step(j, even);
+    if (j + 1 >= steps) break;
+    sl.chunk(j + 2, tid, NT, even);
+    step(j + 1, odd);
   }
-  if (TOPK && lg != 0 && left < sl.rounds) close_slot(slot_top);
+  if (TOPK && (sl.rounds & ((1 << lg) - 1))) close_slot(slot_top);
 
   // ---- the row's statistics
   LpState st = f.state();
@@ -599,16 +625,17 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
   if ((tid & 31) == 0) warp_state[tid >> 5] = st;
   if (TOPK && tid == 0) sh.count = sh.pairs = 0;
   __syncthreads();
-  st = warp_state[tid & (NT / 32 - 1)];
-#pragma unroll
-  for (int o = NT / 64; o > 0; o >>= 1) lp_merge(st, lp_shfl_xor(st, o), a.k2);
 
   // ---- the slice's best
   int have = 0;
   if (TOPK) {
     have = (int)min((int64_t)a.topk, sl.size());
-    select_top<T, NT>(sl, have, cap, slots, lg, best, sh, cand);
+    select_top<T, NT>(sl, have, cap, slots, lg, order_key(best), sh, cand);
   }
+
+  st = warp_state[tid & (NT / 32 - 1)];
+#pragma unroll
+  for (int o = NT / 64; o > 0; o >>= 1) lp_merge(st, lp_shfl_xor(st, o), a.k2);
 
   // ---- join the slices: every block fetches all sums and lists
   uint64_t* all = reinterpret_cast<uint64_t*>(slot_key + (kSlots + 1) * NT + kPairs);
@@ -908,7 +935,7 @@ int launch_rows(const LpArgs& a, int nsm, cudaStream_t s) {
   // short rows: more, smaller blocks on an SM (16384 x 32000 bf16: 169 us with
   // 128 threads a block, 195 us with 256; with 100 alternatives, for which 128
   // threads' maxima are no close bound, 474 us and 434 us)
-  if (blocks == 1 && bytes < (a.topk <= 64 ? 98304 : 32768))
+  if (blocks == 1 && a.topk <= kFewK && bytes < (a.topk <= 64 ? 98304 : 32768))
     return a.topk ? launch_rows_nt<T, 128, true>(a, 1, s) : launch_rows_nt<T, 128, false>(a, 1, s);
   return a.topk ? launch_rows_nt<T, 256, true>(a, blocks, s)
                 : launch_rows_nt<T, 256, false>(a, blocks, s);
