@@ -88,6 +88,7 @@ constexpr int kPairs = 4096;   // slots above the bound the list holds
 constexpr int kMaxCap = 4096;  // candidates a block sorts at most
 constexpr int kFewK = 128, kFewCap = 1024;  // with up to kFewK alternatives
 constexpr int kUnroll = 4;
+constexpr int kOwn = 256;      // maxima that bound few alternatives, one or two a thread
 
 struct Words {
   uint32_t w[4];
@@ -210,7 +211,7 @@ __device__ __forceinline__ void cluster_wait() {
 struct SelectShared {
   uint32_t hist[256];
   uint32_t prefix, want, count, pairs, bound;
-  uint32_t warp_sum[2][32];  // alternately, so that one barrier a step is enough
+  uint32_t warp_sum[2][32];
 };
 
 // The K best of a slice by radix selection on the order keys: eight bits a
@@ -271,12 +272,11 @@ __device__ __noinline__ void select_exact(Slice<T> sl, int k, SelectShared& sh, 
   __syncthreads();
 }
 
-// Largest 16-bit key that at least k of the threads' keys reach, k <= NT: one
+// Largest 16-bit key that at least k of 32 P keys reach, k <= 32 P: one
 // warp, two bits a step below the highest bit in which the keys differ, so that
 // the other blocks of the SM keep the issue slots.
-template <int NT>
+template <int P>
 __device__ __forceinline__ void bound_key(const uint16_t* keys, int k, uint32_t* out) {
-  constexpr int P = NT / 32;
   uint32_t key[P], lo = 0xffffu, hi = 0;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
@@ -302,24 +302,63 @@ __device__ __forceinline__ void bound_key(const uint16_t* keys, int k, uint32_t*
   }
   if (threadIdx.x == 0) *out = lo;
 }
-// Over all slots of all threads: one block-wide count a step.
+// The same over all slots of all threads: block-wide counts.
 template <int NT>
 __device__ __forceinline__ uint32_t bound_key_slots(const uint16_t* keys, int slots, int k, SelectShared& sh) {
-  uint32_t lo = 0;
-  int flip = 0;
-#pragma unroll 1
-  for (uint32_t bit = 0x8000u; bit; bit >>= 1, flip ^= 1) {
-    const uint32_t test = lo | bit;
-    uint32_t c = 0;
+  constexpr int W = NT / 32;
+  static_assert(2 * 3 * W <= 256, "counts of two steps");
+  const int warp = threadIdx.x >> 5;
+  const bool lane0 = (threadIdx.x & 31) == 0;
+  uint32_t lo = 0xffffu, hi = 0;
 #pragma unroll 8
-    for (int i = 0; i < slots; ++i) c += keys[i * NT + threadIdx.x] >= test;
-    c = __reduce_add_sync(0xffffffffu, c);
-    if ((threadIdx.x & 31) == 0) sh.warp_sum[flip][threadIdx.x >> 5] = c;
-    __syncthreads();
-    c = 0;
+  for (int i = 0; i < slots; ++i) {
+    lo = min(lo, (uint32_t)keys[i * NT + threadIdx.x]);
+    hi = max(hi, (uint32_t)keys[i * NT + threadIdx.x]);
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane0) {
+    sh.warp_sum[0][warp] = lo;
+    sh.warp_sum[1][warp] = hi;
+  }
+  __syncthreads();
 #pragma unroll
-    for (int w = 0; w < NT / 32; ++w) c += sh.warp_sum[flip][w];
-    if (c >= (uint32_t)k) lo = test;
+  for (int w = 0; w < W; ++w) {
+    lo = min(lo, sh.warp_sum[0][w]);
+    hi = max(hi, sh.warp_sum[1][w]);
+  }
+  int shift = (32 - __clz(lo ^ hi) + 1) & ~1;  // even; bits below it may differ
+  lo = lo >> shift << shift;
+  uint32_t* sum = sh.hist;
+#pragma unroll 1
+  while ((shift -= 2) >= 0) {
+    const uint32_t t = 1u << shift;
+    uint32_t c0 = 0, c1 = 0, c2 = 0;
+#pragma unroll 4
+    for (int i = 0; i < slots; ++i) {
+      const uint32_t q = keys[i * NT + threadIdx.x];
+      c0 += q >= (lo | t);
+      c1 += q >= (lo | 2 * t);
+      c2 += q >= (lo | 3 * t);
+    }
+    c0 = __reduce_add_sync(0xffffffffu, c0);
+    c1 = __reduce_add_sync(0xffffffffu, c1);
+    c2 = __reduce_add_sync(0xffffffffu, c2);
+    if (lane0) {
+      sum[warp] = c0;
+      sum[W + warp] = c1;
+      sum[2 * W + warp] = c2;
+    }
+    __syncthreads();
+    c0 = c1 = c2 = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      c0 += sum[w];
+      c1 += sum[W + w];
+      c2 += sum[2 * W + w];
+    }
+    lo |= (uint32_t)((c0 >= (uint32_t)k) + (c1 >= (uint32_t)k) + (c2 >= (uint32_t)k)) << shift;
+    sum = sh.hist + (sum == sh.hist ? 3 * W : 0);  // alternately: one barrier a step
   }
   return lo;
 }
@@ -389,14 +428,20 @@ __device__ __noinline__ void sort_many(uint64_t* cand, int n) {
 template <int NT, int CAP>
 __device__ __forceinline__ void sort_words(uint64_t* cand, int n) {
   if (n <= NT) {
-    const uint64_t w = (int)threadIdx.x < n ? cand[threadIdx.x] : 0;
+    // 1 << lg threads a word
+    constexpr int kBits = NT == 128 ? 7 : 8;
+    static_assert(NT == 1 << kBits, "");
+    const int lg = max(0, min(5, kBits - 32 + __clz(n - 1))), g = 1 << lg;
+    const int j = threadIdx.x >> lg, h = threadIdx.x & (g - 1);
+    const uint64_t w = j < n ? cand[j] : 0;
     int place = 0;
-    if ((int)(threadIdx.x & ~31u) < n) {
+    if ((int)(threadIdx.x & ~31u) >> lg < n) {
 #pragma unroll 8
-      for (int i = 0; i < n; ++i) place += cand[i] > w;
+      for (int i = h; i < n; i += g) place += cand[i] > w;
+      for (int o = 1; o < g; o <<= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
     }
     __syncthreads();
-    if ((int)threadIdx.x < n) cand[place] = w;
+    if (h == 0 && j < n) cand[place] = w;
     __syncthreads();
   } else if (n <= 4 * NT) {
     sort_bitonic<NT, 4>(cand, n);
@@ -409,13 +454,13 @@ __device__ __forceinline__ void sort_words(uint64_t* cand, int n) {
 }
 
 // Dynamic shared memory: cand[cap] (u64), the upper halves of the slot keys
-// [kSlots][NT] and of the threads' own maxima [NT] (u16), and the list of slots
+// [kSlots][NT] and of the threads' own maxima [kOwn] (u16), and the list of slots
 // above the bound [kPairs] (u16); in clusters, all blocks' lists [blocks][k] (u64).
 __host__ __device__ constexpr int row_cap(int k) { return k <= kFewK ? kFewCap : kMaxCap; }
 template <int NT>
 __host__ __device__ constexpr int row_smem(int k, int blocks) {
   return k == 0 ? 0
-                : row_cap(k) * 8 + (kSlots + 1) * NT * 2 + kPairs * 2 +
+                : row_cap(k) * 8 + (kSlots * NT + kOwn) * 2 + kPairs * 2 +
                       (blocks > 1 ? blocks * k * 8 : 0);
 }
 
@@ -434,45 +479,61 @@ __device__ __forceinline__ uint32_t warp_places(uint32_t n, uint32_t* count) {
   return __shfl_sync(0xffffffffu, at, 31) + sum - n;
 }
 
+// Own maxima of threads that have something.
+__device__ __forceinline__ int own_keys(int chunks) { return min(kOwn, chunks); }
+
 // The slice's best `want` ids into cand, in order.  A slot is 1 << lg of a
-// thread's vectors; best: this thread's key.
+// thread's vectors; own: this thread's maxima, of its even and odd steps if two.
 template <class T, int NT>
 __device__ __forceinline__ void select_top(const Slice<T>& sl, int want, int cap, int slots, int lg,
-                           uint32_t best, SelectShared& sh, uint64_t* cand) {
+                           const float (&own)[kOwn / NT], SelectShared& sh, uint64_t* cand) {
   constexpr int N = Vec<T>::N;
   static_assert(kSlots <= 32 && kUnroll * N <= 32, "a bit each");
   const int tid = threadIdx.x;
   uint16_t* slot_key = reinterpret_cast<uint16_t*>(cand + cap);
   uint16_t* own_key = slot_key + kSlots * NT;
-  uint16_t* list = own_key + NT;
+  uint16_t* list = own_key + kOwn;
   uint32_t bound;  // upper half of an order key
   // few alternatives: the threads' own maxima bound them closely enough (k of
-  // NT leave about -NT log(1 - k/NT) ids above the bound)
-  const int own_bound = min(NT, sl.chunks) / 2;
-  if (want <= own_bound) {
-    own_key[tid] = (uint16_t)(best >> 16);
-    __syncthreads();
-    if (tid < 32) bound_key<NT>(own_key, want, &sh.bound);
-    __syncthreads();
-    bound = sh.bound;
-  } else {
+  // n leave about -n log(1 - k/n) ids above the bound); more: those of their even
+  // and odd steps, or the slots
+  const bool few = want <= min(NT, sl.chunks) / 2, of_slots = !few && want > own_keys(sl.chunks) / 2;
+  uint32_t best = 0;
+#pragma unroll
+  for (int i = 0; i < kOwn / NT; ++i) {
+    const uint32_t q = order_key(own[i]) >> 16;
+    best = max(best, q);
+    own_key[i * NT + tid] = (uint16_t)q;
+  }
+  if (few) own_key[tid] = (uint16_t)best;
+  if (of_slots) {
     // (a lowest denormal's upper half reads as that of -0, which is kept as +0)
     for (int i = 0; i < slots; ++i) {
       const uint32_t q = slot_key[i * NT + tid];
       slot_key[i * NT + tid] =
           q == 0x8000u ? 0x7fffu : (uint16_t)(order_key(__uint_as_float(q << 16)) >> 16);
     }
+  }
+  __syncthreads();
+  if (of_slots) {
     bound = bound_key_slots<NT>(slot_key, slots, want, sh);
+  } else {
+    if (tid < 32) {
+      if (few) bound_key<NT / 32>(own_key, want, &sh.bound);
+      else bound_key<kOwn / 32>(own_key, want, &sh.bound);
+    }
+    __syncthreads();
+    bound = sh.bound;
   }
   // not below the lowest value of that key; where the key is a NaN's or no
   // value's, every logit is let through
   const float low = key_value(bound << 16);
   // the slots above the bound, of the threads above it
   uint32_t bits = 0;
-  if (want > own_bound) {
+  if (of_slots) {
 #pragma unroll 8
     for (int i = 0; i < slots; ++i) bits |= (uint32_t)(slot_key[i * NT + tid] >= bound) << i;
-  } else if ((best >> 16) >= bound) {
+  } else if (best >= bound) {
 #pragma unroll 8
     for (int i = 0; i < slots; ++i)
       bits |= (uint32_t)!(__uint_as_float((uint32_t)slot_key[i * NT + tid] << 16) < low) << i;
@@ -565,11 +626,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
   int lg = 2;  // a slot: 2^lg vectors
   static_assert(kUnroll == 4, "a slot is a power of two of steps, or a vector");
   // where the slots bound the alternatives a slot of a short row is one vector
-  if (a.topk > min(NT, sl.chunks) / 2 && sl.rounds <= kSlots) lg = 0;
+  if (a.topk > own_keys(sl.chunks) / 2 && sl.rounds <= kSlots) lg = 0;
   else while (((sl.rounds - 1) >> lg) >= kSlots) ++lg;
   const int slots = ((sl.rounds - 1) >> lg) + 1;
   uint16_t* slot = slot_key + tid;
-  float best = neg_inf(), slot_top = neg_inf();
+  float own[kOwn / NT], slot_top = neg_inf();
+#pragma unroll
+  for (int i = 0; i < kOwn / NT; ++i) own[i] = neg_inf();
   auto close_slot = [&](float top) {
     *slot = (uint16_t)(__float_as_uint(top + 0.f) >> 16);
     slot += NT;
@@ -577,7 +640,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
   LpFold f;
   f.init(a.k2);
   if (tid < sl.loose) f.add_one(to_f(sl.z[sl.loose_at(tid)]));
-  auto step = [&](int j, const Words* w) {
+  auto step = [&](int j, const Words* w, float& best) {
     float m[kUnroll], mm = neg_inf();
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -611,10 +674,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
   const int steps = sl.rounds / kUnroll;
   for (int j = 0; j < steps; j += 2) {
     sl.chunk(j + 1, tid, NT, odd);
-    step(j, even);
+    step(j, even, own[0]);
     if (j + 1 >= steps) break;
     sl.chunk(j + 2, tid, NT, even);
-    step(j + 1, odd);
+    step(j + 1, odd, own[kOwn / NT - 1]);
   }
   if (TOPK && (sl.rounds & ((1 << lg) - 1))) close_slot(slot_top);
 
@@ -624,13 +687,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
   for (int o = 16; o > 0; o >>= 1) lp_merge(st, lp_shfl_xor(st, o), a.k2);
   if ((tid & 31) == 0) warp_state[tid >> 5] = st;
   if (TOPK && tid == 0) sh.count = sh.pairs = 0;
-  __syncthreads();
 
   // ---- the slice's best
   int have = 0;
-  if (TOPK) {
+  if (!TOPK) {
+    __syncthreads();
+  } else {  // (with a barrier at its head)
     have = (int)min((int64_t)a.topk, sl.size());
-    select_top<T, NT>(sl, have, cap, slots, lg, order_key(best), sh, cand);
+    select_top<T, NT>(sl, have, cap, slots, lg, own, sh, cand);
   }
 
   st = warp_state[tid & (NT / 32 - 1)];
@@ -638,7 +702,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
   for (int o = NT / 64; o > 0; o >>= 1) lp_merge(st, lp_shfl_xor(st, o), a.k2);
 
   // ---- join the slices: every block fetches all sums and lists
-  uint64_t* all = reinterpret_cast<uint64_t*>(slot_key + (kSlots + 1) * NT + kPairs);
+  uint64_t* all = reinterpret_cast<uint64_t*>(slot_key + kSlots * NT + kOwn + kPairs);
   if (blocks > 1) {
     if (tid == 0) {
       block_state = st;
@@ -766,7 +830,7 @@ __global__ void __launch_bounds__(256) k_logprob_join(LpJoin j) {
 // candidates bounds the K-th best from below; what lies above it is sorted.
 // Bound by the latency of its few dependent loads: 8 us for one row, 29-50 us
 // for 2048 rows of about 1000 candidates.
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = kOwn;
 
 __global__ void __launch_bounds__(kJoinThreads) k_logprob_join_top(LpJoin j) {
   __shared__ uint64_t cand[kMaxCap / 2];
@@ -853,7 +917,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_logprob_join_top(LpJoin j) {
   each([&](uint64_t w) { best = max(best, w); });
   own_key[tid] = (uint16_t)(best >> 48);
   __syncthreads();
-  if (tid < 32) bound_key<kJoinThreads>(own_key, k, &sh.bound);
+  if (tid < 32) bound_key<kOwn / 32>(own_key, k, &sh.bound);
   __syncthreads();
   const uint32_t bound = sh.bound;
   each([&](uint64_t w) {
@@ -935,7 +999,7 @@ int launch_rows(const LpArgs& a, int nsm, cudaStream_t s) {
   // short rows: more, smaller blocks on an SM (16384 x 32000 bf16: 169 us with
   // 128 threads a block, 195 us with 256; with 100 alternatives, for which 128
   // threads' maxima are no close bound, 474 us and 434 us)
-  if (blocks == 1 && a.topk <= kFewK && bytes < (a.topk <= 64 ? 98304 : 32768))
+  if (blocks == 1 && a.topk <= kFewK && bytes < 163840)
     return a.topk ? launch_rows_nt<T, 128, true>(a, 1, s) : launch_rows_nt<T, 128, false>(a, 1, s);
   return a.topk ? launch_rows_nt<T, 256, true>(a, blocks, s)
                 : launch_rows_nt<T, 256, false>(a, blocks, s);
