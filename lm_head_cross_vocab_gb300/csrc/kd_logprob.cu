@@ -210,7 +210,7 @@ __device__ __forceinline__ void cluster_wait() {
 // Shared memory of the selection; cand has `cap` places.
 struct SelectShared {
   uint32_t hist[256];
-  uint32_t prefix, want, count, pairs, bound;
+  uint32_t prefix, want, count, bound;
   uint32_t warp_sum[2][32];
 };
 
@@ -418,15 +418,31 @@ __device__ __forceinline__ void sort_bitonic(uint64_t* cand, int n) {
   for (int i = 0; i < E; ++i) cand[t0 + i] = w[i];
   __syncthreads();
 }
-// The same out of line: more words than the sweep has registers to spare for.
-template <int NT, int E>
-__device__ __noinline__ void sort_many(uint64_t* cand, int n) {
-  sort_bitonic<NT, E>(cand, n);
-}
-// Descending sort of cand[0, n), n <= cap: few words go to the place that the
-// number of larger ones gives, more through a bitonic sort.
+// More than NT words, out of line: the sweep has no registers to spare for them.
+// Of more than 8 NT only the first 4 NT in order, the best of two halves (with 16
+// words a thread the kernel's registers do not suffice).
 template <int NT, int CAP>
-__device__ __forceinline__ void sort_words(uint64_t* cand, int n) {
+__device__ __noinline__ void sort_many(uint64_t* cand, int n) {
+  static_assert(CAP <= 16 * NT, "");
+  if (n <= 4 * NT) return sort_bitonic<NT, 4>(cand, n);
+  if constexpr (CAP > 8 * NT) {
+    static_assert(4 * NT >= kMaxTopk, "as many as are asked for");
+    if (n > 8 * NT) {
+      sort_bitonic<NT, 8>(cand + 8 * NT, n - 8 * NT);
+      sort_bitonic<NT, 8>(cand, 8 * NT);
+      for (int i = threadIdx.x; i < 4 * NT; i += NT) cand[4 * NT + i] = cand[8 * NT + i];
+      __syncthreads();
+      n = 8 * NT;
+    }
+  }
+  sort_bitonic<NT, 8>(cand, n);
+}
+// Words cand[0, n), n <= CAP, in descending order (of more than 8 NT the first
+// 4 NT): emit(place, word) for each,
+// which may write to cand[place] where in_place.  Few words go to the place that
+// the number of larger ones gives, more through a bitonic sort.
+template <int NT, int CAP, class F>
+__device__ __forceinline__ void sort_words(uint64_t* cand, int n, bool in_place, F&& emit) {
   if (n <= NT) {
     // 1 << lg threads a word
     constexpr int kBits = NT == 128 ? 7 : 8;
@@ -440,17 +456,15 @@ __device__ __forceinline__ void sort_words(uint64_t* cand, int n) {
       for (int i = h; i < n; i += g) place += cand[i] > w;
       for (int o = 1; o < g; o <<= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
     }
-    __syncthreads();
-    if (h == 0 && j < n) cand[place] = w;
-    __syncthreads();
-  } else if (n <= 4 * NT) {
-    sort_bitonic<NT, 4>(cand, n);
-  } else if (n <= 8 * NT) {
-    sort_many<NT, 8>(cand, n);
-  } else if constexpr (CAP > 8 * NT) {
-    static_assert(CAP <= 16 * NT, "");
-    sort_many<NT, 16>(cand, n);
+    if (in_place) __syncthreads();
+    if (h == 0 && j < n) emit(place, w);
+    if (in_place) __syncthreads();
+    return;
   }
+  sort_many<NT, CAP>(cand, n);
+  if (CAP > 8 * NT && n > 8 * NT) n = 4 * NT;
+  if (!in_place)
+    for (int i = threadIdx.x; i < n; i += NT) emit(i, cand[i]);
 }
 
 // Dynamic shared memory: cand[cap] (u64), the upper halves of the slot keys
@@ -464,9 +478,8 @@ __host__ __device__ constexpr int row_smem(int k, int blocks) {
                       (blocks > 1 ? blocks * k * 8 : 0);
 }
 
-// Places for each lane's n words behind *count: one scan and one atomic a warp.
-// All lanes take part.
-__device__ __forceinline__ uint32_t warp_places(uint32_t n, uint32_t* count) {
+// Words of the lanes before this one, and of all.
+__device__ __forceinline__ uint32_t lanes_before(uint32_t n, int& all) {
   const int lane = threadIdx.x & 31;
   uint32_t sum = n;
 #pragma unroll
@@ -474,19 +487,28 @@ __device__ __forceinline__ uint32_t warp_places(uint32_t n, uint32_t* count) {
     const uint32_t below = __shfl_up_sync(0xffffffffu, sum, o);
     if (lane >= o) sum += below;
   }
+  all = (int)__shfl_sync(0xffffffffu, sum, 31);
+  return sum - n;
+}
+// Places for them behind *count: one scan and one atomic a warp.
+__device__ __forceinline__ uint32_t warp_places(uint32_t n, uint32_t* count) {
+  int all;
+  const uint32_t before = lanes_before(n, all);
   uint32_t at = 0;
-  if (lane == 31 && sum) at = atomicAdd(count, sum);
-  return __shfl_sync(0xffffffffu, at, 31) + sum - n;
+  if ((threadIdx.x & 31) == 0 && all) at = atomicAdd(count, (uint32_t)all);
+  return __shfl_sync(0xffffffffu, at, 0) + before;
 }
 
 // Own maxima of threads that have something.
 __device__ __forceinline__ int own_keys(int chunks) { return min(kOwn, chunks); }
 
-// The slice's best `want` ids into cand, in order.  A slot is 1 << lg of a
+// The slice's best `want` ids, or some more, in order to emit (see sort_words).
+// One warp does `side` while another finds the bound.  A slot is 1 << lg of a
 // thread's vectors; own: this thread's maxima, of its even and odd steps if two.
-template <class T, int NT>
-__device__ __forceinline__ void select_top(const Slice<T>& sl, int want, int cap, int slots, int lg,
-                           const float (&own)[kOwn / NT], SelectShared& sh, uint64_t* cand) {
+template <class T, int NT, class Side, class Emit>
+__device__ __forceinline__ int select_top(const Slice<T>& sl, int want, int cap, int slots, int lg,
+                           const float (&own)[kOwn / NT], SelectShared& sh, uint64_t* cand,
+                           bool in_place, Side&& side, Emit&& emit) {
   constexpr int N = Vec<T>::N;
   static_assert(kSlots <= 32 && kUnroll * N <= 32, "a bit each");
   const int tid = threadIdx.x;
@@ -515,6 +537,7 @@ __device__ __forceinline__ void select_top(const Slice<T>& sl, int want, int cap
     }
   }
   __syncthreads();
+  if ((tid >> 5) == 1) side();
   if (of_slots) {
     bound = bound_key_slots<NT>(slot_key, slots, want, sh);
   } else {
@@ -538,9 +561,18 @@ __device__ __forceinline__ void select_top(const Slice<T>& sl, int want, int cap
     for (int i = 0; i < slots; ++i)
       bits |= (uint32_t)!(__uint_as_float((uint32_t)slot_key[i * NT + tid] << 16) < low) << i;
   }
-  uint32_t p = warp_places(__popc(bits), &sh.pairs);
+  // listed and read again by their own warp
+  constexpr int kWarpPairs = kPairs / (NT / 32);
+  uint16_t* mine = list + (tid >> 5) * kWarpPairs;
+  int pairs;
+  uint32_t p = lanes_before(__popc(bits), pairs);
   for (; bits; bits &= bits - 1, ++p)
-    if (p < (uint32_t)kPairs) list[p] = (uint16_t)((__ffs(bits) - 1) * NT + tid);
+    if (p < (uint32_t)kWarpPairs) mine[p] = (uint16_t)((__ffs(bits) - 1) * NT + tid);
+  __syncwarp();
+  if (pairs > kWarpPairs) {
+    if ((tid & 31) == 0) atomicAdd(&sh.count, (uint32_t)cap + 1);  // the exact selection
+    pairs = 0;
+  }
   if (tid < sl.loose) {
     const int64_t id = sl.loose_at(tid);
     const float z = to_f(sl.z[id]);
@@ -549,18 +581,16 @@ __device__ __forceinline__ void select_top(const Slice<T>& sl, int want, int cap
       if (at < (uint32_t)cap) cand[at] = cand_word(order_key(z), (uint32_t)id);
     }
   }
-  __syncthreads();
-  const int pairs = (int)sh.pairs;
-  const int items = pairs <= kPairs ? pairs << lg : 0;
-  for (int i0 = tid; (i0 & ~31) < items; i0 += kUnroll * NT) {
+  const int items = pairs << lg;
+  for (int i0 = tid & 31; (i0 & ~31) < items; i0 += kUnroll * 32) {
     Words w[kUnroll];
     int at[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * NT;
+      const int i = i0 + u * 32;
       at[u] = INT32_MAX;
       if (i < items) {
-        const int pair = list[i >> lg];
+        const int pair = mine[i >> lg];
         const int q = (pair / NT << lg) + (i & ((1 << lg) - 1));
         at[u] = ((q / kUnroll) * NT + pair % NT) * kUnroll + q % kUnroll;
       }
@@ -587,13 +617,14 @@ __device__ __forceinline__ void select_top(const Slice<T>& sl, int want, int cap
   }
   __syncthreads();
   int have = (int)sh.count;
-  if (have > cap || pairs > kPairs) {
+  if (have > cap) {
     __syncthreads();
     select_exact(sl, want, sh, cand);
     have = want;
   }
   // (128 threads: at most kFewK alternatives)
-  sort_words<NT, NT == 128 ? kFewCap : kMaxCap>(cand, have);
+  sort_words<NT, NT == 128 ? kFewCap : kMaxCap>(cand, have, in_place, emit);
+  return have;
 }
 
 template <class T, int NT, bool TOPK>
@@ -602,6 +633,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
   __shared__ SelectShared sh;
   __shared__ LpState warp_state[NT / 32];
   __shared__ LpState block_state;
+  __shared__ LpRow block_row;
   __shared__ int block_count, counts[8];
   cg::cluster_group cluster = cg::this_cluster();
   const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -620,7 +652,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
     return;
   }
   const bool in = label >= 0 && label < a.vocab;
-  const float zy = (tid == 0 && rank == 0 && in) ? to_f(sl.z[label]) : 0.f;
+  constexpr int kTeller = TOPK ? 32 : 0;  // the thread that writes the row's own values
+  const float zy = (tid == kTeller && rank == 0 && in) ? to_f(sl.z[label]) : 0.f;
 
   // ---- one sweep
   int lg = 2;  // a slot: 2^lg vectors
@@ -686,81 +719,96 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) lp_merge(st, lp_shfl_xor(st, o), a.k2);
   if ((tid & 31) == 0) warp_state[tid >> 5] = st;
-  if (TOPK && tid == 0) sh.count = sh.pairs = 0;
+  if (TOPK && tid == 0) sh.count = 0;
+  auto block_sums = [&]() {
+    st = warp_state[tid & (NT / 32 - 1)];
+#pragma unroll
+    for (int o = NT / 64; o > 0; o >>= 1) lp_merge(st, lp_shfl_xor(st, o), a.k2);
+  };
+  auto finish = [&]() {
+    const LpRow row = lp_finish(st);
+    if (tid == kTeller) {
+      if (a.tokens && !in) set_status(a.status, KD_DEV_BAD_LABEL);
+      lp_store(a, r, row, label, zy);
+    }
+    return row;
+  };
+  auto store_top = [&](int p, uint64_t w, const LpRow& row) {
+    if (a.topk_idx) a.topk_idx[r * a.topk + p] = (int32_t)~(uint32_t)w;
+    if (a.topk_lp) a.topk_lp[r * a.topk + p] = lp_of(key_value((uint32_t)(w >> 32)), row, a.inv_t);
+  };
 
   // ---- the slice's best
   int have = 0;
   if (!TOPK) {
     __syncthreads();
+    block_sums();
+    if (blocks == 1) finish();
   } else {  // (with a barrier at its head)
     have = (int)min((int64_t)a.topk, sl.size());
-    select_top<T, NT>(sl, have, cap, slots, lg, own, sh, cand);
+    auto side = [&]() {
+      block_sums();
+      if (blocks == 1) {
+        const LpRow row = finish();
+        if (tid == kTeller) block_row = row;
+      } else if (tid == kTeller) {
+        block_state = st;
+      }
+    };
+    auto emit = [&](int p, uint64_t w) {
+      if (blocks > 1) cand[p] = w;
+      else if (p < have) store_top(p, w, block_row);
+    };
+    select_top<T, NT>(sl, have, cap, slots, lg, own, sh, cand, blocks > 1, side, emit);
   }
-
-  st = warp_state[tid & (NT / 32 - 1)];
-#pragma unroll
-  for (int o = NT / 64; o > 0; o >>= 1) lp_merge(st, lp_shfl_xor(st, o), a.k2);
+  if (blocks == 1) return;
 
   // ---- join the slices: every block fetches all sums and lists
   uint64_t* all = reinterpret_cast<uint64_t*>(slot_key + kSlots * NT + kOwn + kPairs);
-  if (blocks > 1) {
-    if (tid == 0) {
-      block_state = st;
-      block_count = have;
-    }
-    cluster.sync();
-    const int b = tid & 31;
-    st = b < blocks ? *cluster.map_shared_rank(&block_state, b) : LpState{neg_inf(), 0.f, 0.f};
-    if (tid < blocks) counts[tid] = *cluster.map_shared_rank(&block_count, tid);
-    if (TOPK)
-      for (int i = tid; i < blocks * a.topk; i += NT)
-        all[i] = cluster.map_shared_rank(cand, i / a.topk)[i % a.topk];
-    __syncwarp();
-    cluster_arrive();  // this block has read the others
+  if (tid == 0) {
+    if (!TOPK) block_state = st;
+    block_count = have;
+  }
+  cluster.sync();
+  const int b = tid & 31;
+  st = b < blocks ? *cluster.map_shared_rank(&block_state, b) : LpState{neg_inf(), 0.f, 0.f};
+  if (tid < blocks) counts[tid] = *cluster.map_shared_rank(&block_count, tid);
+  if (TOPK)
+    for (int i = tid; i < blocks * a.topk; i += NT)
+      all[i] = cluster.map_shared_rank(cand, i / a.topk)[i % a.topk];
+  __syncwarp();
+  cluster_arrive();  // this block has read the others
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) lp_merge(st, lp_shfl_xor(st, o), a.k2);
-    st.m = __shfl_sync(0xffffffffu, st.m, 0);
-    st.s = __shfl_sync(0xffffffffu, st.s, 0);
-    st.t = __shfl_sync(0xffffffffu, st.t, 0);
-  }
-  const LpRow row = lp_finish(st);
-  if (tid == 0 && rank == 0) {
-    if (a.tokens && !in) set_status(a.status, KD_DEV_BAD_LABEL);
-    lp_store(a, r, row, label, zy);
-  }
+  for (int o = 4; o > 0; o >>= 1) lp_merge(st, lp_shfl_xor(st, o), a.k2);
+  st.m = __shfl_sync(0xffffffffu, st.m, 0);
+  st.s = __shfl_sync(0xffffffffu, st.s, 0);
+  st.t = __shfl_sync(0xffffffffu, st.t, 0);
+  const LpRow row = rank == 0 ? finish() : lp_finish(st);
   if (TOPK) {
     int* place = reinterpret_cast<int*>(slot_key);  // of each word (the keys are done with)
-    if (blocks > 1) {
-      // larger words here, and in the other slices' sorted lists: one thread
-      // for each word and slice
-      for (int j = tid; j < have; j += NT) place[j] = j;
-      __syncthreads();
-      for (int i = tid; i < have * blocks; i += NT) {
-        const int j = i / blocks, b = i % blocks;
-        if (b == rank) continue;
-        const uint64_t w = cand[j];
-        const uint64_t* other = all + b * a.topk;
-        int lo = 0, hi = counts[b];
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (other[mid] > w) lo = mid + 1;
-          else hi = mid;
-        }
-        if (lo) atomicAdd(&place[j], lo);
-      }
-      __syncthreads();
-    }
-    for (int j = tid; j < have; j += NT) {
+    // larger words here, and in the other slices' sorted lists: one thread
+    // for each word and slice
+    for (int j = tid; j < have; j += NT) place[j] = j;
+    __syncthreads();
+    for (int i = tid; i < have * blocks; i += NT) {
+      const int j = i >> lb, b = i & (blocks - 1);
+      if (b == rank) continue;
       const uint64_t w = cand[j];
-      const int p = blocks > 1 ? place[j] : j;
-      if (p >= a.topk) continue;
-      if (a.topk_idx) a.topk_idx[r * a.topk + p] = (int32_t)~(uint32_t)w;
-      if (a.topk_lp)
-        a.topk_lp[r * a.topk + p] = lp_of(key_value((uint32_t)(w >> 32)), row, a.inv_t);
+      const uint64_t* other = all + b * a.topk;
+      int lo = 0, hi = counts[b];
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (other[mid] > w) lo = mid + 1;
+        else hi = mid;
+      }
+      if (lo) atomicAdd(&place[j], lo);
     }
+    __syncthreads();
+    for (int j = tid; j < have; j += NT)
+      if (place[j] < a.topk) store_top(place[j], cand[j], row);
   }
   __syncwarp();
-  if (blocks > 1) cluster_wait();  // no block leaves while another reads its lists
+  cluster_wait();  // no block leaves while another reads its lists
 }
 
 // ------------------------------------------------------------------ joining parts
@@ -928,7 +976,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_logprob_join_top(LpJoin j) {
   __syncthreads();
   const int have = (int)sh.count;
   if (have <= kMaxCap / 2) {
-    sort_words<kJoinThreads, kMaxCap / 2>(cand, have);
+    sort_words<kJoinThreads, kMaxCap / 2>(cand, have, true, [&](int i, uint64_t w) { cand[i] = w; });
   } else {
     // many equal logits: one after the other
     if (tid == 0) last = 0;
