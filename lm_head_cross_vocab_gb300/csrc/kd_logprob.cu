@@ -418,7 +418,7 @@ __device__ __forceinline__ void sort_bitonic(uint64_t* cand, int n) {
   for (int i = 0; i < E; ++i) cand[t0 + i] = w[i];
   __syncthreads();
 }
-// More than NT words, out of line: the sweep has no registers to spare for them.
+// More than 2 NT words, out of line: the sweep has no registers to spare for them.
 // Of more than 8 NT only the first 4 NT in order, the best of two halves (with 16
 // words a thread the kernel's registers do not suffice).
 template <int NT, int CAP>
@@ -458,6 +458,22 @@ __device__ __forceinline__ void sort_words(uint64_t* cand, int n, bool in_place,
     }
     if (in_place) __syncthreads();
     if (h == 0 && j < n) emit(place, w);
+    if (in_place) __syncthreads();
+    return;
+  }
+  if (n <= 2 * NT) {  // two words a thread
+    const int j = threadIdx.x + NT;
+    const uint64_t w0 = cand[threadIdx.x], w1 = j < n ? cand[j] : ~0ull;
+    int p0 = 0, p1 = 0;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const uint64_t o = cand[i];
+      p0 += o > w0;
+      p1 += o > w1;
+    }
+    if (in_place) __syncthreads();
+    emit(p0, w0);
+    if (j < n) emit(p1, w1);
     if (in_place) __syncthreads();
     return;
   }
