@@ -154,14 +154,14 @@ template <class T>
 struct Slice {
   const T* z;
   int nvec, chunks, rounds;  // vectors; runs of four; vectors of a thread
-  int head, loose;
-  int64_t tail0;             // first element behind the vectors
-  int64_t base;              // element index of vector 0 of the slice
+  int head, loose, base;     // base: element index of vector 0 of the slice
+  int64_t vocab;
 
   // 1 << lb blocks
-  __device__ __forceinline__ Slice(const T* row, int64_t vocab, int rank, int lb, int nt) {
+  __device__ __forceinline__ Slice(const T* row, int64_t vocab_, int rank, int lb, int nt) {
     constexpr int N = Vec<T>::N;
     z = row;
+    vocab = vocab_;
     const int off = (int)((reinterpret_cast<uintptr_t>(row) & 31) / sizeof(T));
     head = off ? 2 * N - off : 0;
     if (head > vocab) head = (int)vocab;
@@ -169,9 +169,8 @@ struct Slice {
     nvec = 2 * (int)((all * (rank + 1) >> lb) - v0);
     chunks = (nvec + 3) / 4;
     rounds = (chunks + nt - 1) / nt * 4;
-    tail0 = head + all * 2 * N;
-    loose = rank == 0 ? head + (int)(vocab - tail0) : 0;
-    base = head + v0 * 2 * N;
+    loose = rank == 0 ? (int)(vocab - all * 2 * N) : 0;
+    base = head + (int)v0 * 2 * N;
   }
   __device__ __forceinline__ const T* at_vec(int i) const { return z + base + (int64_t)i * Vec<T>::N; }
   __device__ __forceinline__ Words vec(int i) const { return load16(at_vec(i)); }
@@ -188,15 +187,14 @@ struct Slice {
       if (4 * c + 2 < nvec) load32(at_vec(4 * c + 2), w[2], w[3]);
     }
   }
-  // asks L2 for the bytes of steps [j, j1) of nt threads
-  __device__ __forceinline__ void prefetch(int j, int j1, int nt) const {
-    const int from = 4 * j * nt, to = min(4 * j1 * nt, nvec);
-    if (from >= to) return;
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at_vec(from)),
-                 "r"((to - from) * 16)
-                 : "memory");
+  // asks L2 for the bytes of steps j and j + 1 of nt threads, if both are whole
+  __device__ __forceinline__ void prefetch(int j, int nt) const {
+    if (4 * (j + 2) * nt <= nvec)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at_vec(4 * j * nt)),
+                   "r"(2 * 4 * nt * 16)
+                   : "memory");
   }
-  __device__ __forceinline__ int64_t loose_at(int i) const { return i < head ? i : tail0 + (i - head); }
+  __device__ __forceinline__ int64_t loose_at(int i) const { return i < head ? i : vocab - loose + i; }
   // elements of the slice, in the order of their ids, for the exact selection
   __device__ __forceinline__ int64_t size() const { return (int64_t)nvec * Vec<T>::N + loose; }
   __device__ __forceinline__ int64_t at(int64_t i) const {
@@ -204,7 +202,7 @@ struct Slice {
     if (i < head) return i;
     i -= head;
     const int64_t body = (int64_t)nvec * Vec<T>::N;
-    return i < body ? base + i : tail0 + (i - body);
+    return i < body ? base + i : vocab - loose + head + (i - body);
   }
 };
 
@@ -526,52 +524,18 @@ __device__ __forceinline__ uint32_t warp_places(uint32_t n, uint32_t* count) {
 // Own maxima of threads that have something.
 __device__ __forceinline__ int own_keys(int chunks) { return min(kOwn, chunks); }
 
-// The slice's best `want` ids, or some more, in order to emit (see sort_words).
-// One warp does `side` while another finds the bound.  A slot is 1 << lg of a
-// thread's vectors; own: this thread's maxima, of its even and odd steps if two.
-template <class T, int NT, class Side, class Emit>
-__device__ __forceinline__ int select_top(const Slice<T>& sl, int want, int cap, int slots, int lg,
-                           const float (&own)[kOwn / NT], SelectShared& sh, uint64_t* cand,
-                           bool in_place, Side&& side, Emit&& emit) {
+// The ids of the slice whose order keys reach bound << 16, into cand; their number
+// (above cap: not all of them, and none is left out otherwise).  A slot is 1 << lg
+// of a thread's vectors, its key an order key where of_slots, else the upper half
+// of its largest logit; best: this thread's key.  Behind a barrier.
+template <class T, int NT>
+__device__ __forceinline__ int collect(const Slice<T>& sl, uint32_t bound, uint32_t best, bool of_slots,
+                                       int cap, int slots, int lg, SelectShared& sh, uint64_t* cand) {
   constexpr int N = Vec<T>::N;
   static_assert(kSlots <= 32 && kUnroll * N <= 32, "a bit each");
   const int tid = threadIdx.x;
-  uint16_t* slot_key = reinterpret_cast<uint16_t*>(cand + cap);
-  uint16_t* own_key = slot_key + kSlots * NT;
-  uint16_t* list = own_key + kOwn;
-  uint32_t bound;  // upper half of an order key
-  // few alternatives: the threads' own maxima bound them closely enough (k of
-  // n leave about -n log(1 - k/n) ids above the bound); more: those of their even
-  // and odd steps, or the slots
-  const bool few = want <= min(NT, sl.chunks) / 2, of_slots = !few && want > own_keys(sl.chunks) / 2;
-  uint32_t best = 0;
-#pragma unroll
-  for (int i = 0; i < kOwn / NT; ++i) {
-    const uint32_t q = order_key(own[i]) >> 16;
-    best = max(best, q);
-    own_key[i * NT + tid] = (uint16_t)q;
-  }
-  if (few) own_key[tid] = (uint16_t)best;
-  if (of_slots) {
-    // (a lowest denormal's upper half reads as that of -0, which is kept as +0)
-    for (int i = 0; i < slots; ++i) {
-      const uint32_t q = slot_key[i * NT + tid];
-      slot_key[i * NT + tid] =
-          q == 0x8000u ? 0x7fffu : (uint16_t)(order_key(__uint_as_float(q << 16)) >> 16);
-    }
-  }
-  __syncthreads();
-  if ((tid >> 5) == 1) side();
-  if (of_slots) {
-    bound = bound_key_slots<NT>(slot_key, slots, want, sh);
-  } else {
-    if (tid < 32) {
-      if (few) bound_key<NT / 32>(own_key, want, &sh.bound);
-      else bound_key<kOwn / 32>(own_key, want, &sh.bound);
-    }
-    __syncthreads();
-    bound = sh.bound;
-  }
+  const uint16_t* slot_key = reinterpret_cast<const uint16_t*>(cand + cap);
+  uint16_t* list = reinterpret_cast<uint16_t*>(cand + cap) + kSlots * NT + kOwn;
   // not below the lowest value of that key; where the key is a NaN's or no
   // value's, every logit is let through
   const float low = key_value(bound << 16);
@@ -640,7 +604,53 @@ __device__ __forceinline__ int select_top(const Slice<T>& sl, int want, int cap,
     }
   }
   __syncthreads();
-  int have = (int)sh.count;
+  return (int)sh.count;
+}
+
+// The slice's best `want` ids, or some more, in order to emit (see sort_words).
+// One warp does `side` while another finds the bound.  own: this
+// thread's maxima, of its even and odd steps if two.
+template <class T, int NT, class Side, class Emit>
+__device__ __forceinline__ int select_top(const Slice<T>& sl, int want, int cap, int slots, int lg,
+                           const float (&own)[kOwn / NT], SelectShared& sh, uint64_t* cand,
+                           bool in_place, Side&& side, Emit&& emit) {
+  const int tid = threadIdx.x;
+  uint16_t* slot_key = reinterpret_cast<uint16_t*>(cand + cap);
+  uint16_t* own_key = slot_key + kSlots * NT;
+  uint32_t bound;  // upper half of an order key
+  // few alternatives: the threads' own maxima bound them closely enough (k of
+  // n leave about -n log(1 - k/n) ids above the bound); more: those of their even
+  // and odd steps, or the slots
+  const bool few = want <= min(NT, sl.chunks) / 2, of_slots = !few && want > own_keys(sl.chunks) / 2;
+  uint32_t best = 0;
+#pragma unroll
+  for (int i = 0; i < kOwn / NT; ++i) {
+    const uint32_t q = order_key(own[i]) >> 16;
+    best = max(best, q);
+    own_key[i * NT + tid] = (uint16_t)q;
+  }
+  if (few) own_key[tid] = (uint16_t)best;
+  if (of_slots) {
+    // (a lowest denormal's upper half reads as that of -0, which is kept as +0)
+    for (int i = 0; i < slots; ++i) {
+      const uint32_t q = slot_key[i * NT + tid];
+      slot_key[i * NT + tid] =
+          q == 0x8000u ? 0x7fffu : (uint16_t)(order_key(__uint_as_float(q << 16)) >> 16);
+    }
+  }
+  __syncthreads();
+  if ((tid >> 5) == 1) side();
+  if (of_slots) {
+    bound = bound_key_slots<NT>(slot_key, slots, want, sh);
+  } else {
+    if (tid < 32) {
+      if (few) bound_key<NT / 32>(own_key, want, &sh.bound);
+      else bound_key<kOwn / 32>(own_key, want, &sh.bound);
+    }
+    __syncthreads();
+    bound = sh.bound;
+  }
+  int have = collect<T, NT>(sl, bound, best, of_slots, cap, slots, lg, sh, cand);
   if (have > cap) {
     __syncthreads();
     select_exact(sl, want, sh, cand);
@@ -651,7 +661,8 @@ __device__ __forceinline__ int select_top(const Slice<T>& sl, int want, int cap,
   return have;
 }
 
-template <class T, int NT, bool TOPK>
+// CL: a cluster of blocks a row, else one.
+template <class T, int NT, bool TOPK, bool CL>
 __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ SelectShared sh;
@@ -660,7 +671,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
   __shared__ LpRow block_row;
   __shared__ int block_count, counts[8];
   cg::cluster_group cluster = cg::this_cluster();
-  const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int blocks = CL ? (int)cluster.num_blocks() : 1, rank = CL ? (int)cluster.block_rank() : 0;
   const int tid = threadIdx.x;
   const int cap = row_cap(a.topk);
   uint64_t* cand = reinterpret_cast<uint64_t*>(dyn);
@@ -733,9 +744,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
   // them half on their way (8192 x 65536 with 20 alternatives 177 us, without it
   // 201 us; 4096 x 151936 220 and 225 us with 100).  Further ahead it only costs
   // (4 steps 227 us, 10 steps 255 us), as it does in rows of a few steps.
-  const bool ahead = tid == 0 && steps >= 8;
   for (int j = 0; j < steps; j += 2) {
-    if (ahead) sl.prefetch(j + 2, j + 4, NT);
+    if (tid == 0) sl.prefetch(j + 2, NT);
     sl.chunk(j + 1, tid, NT, odd);
     step(j, even, own[0]);
     if (j + 1 >= steps) break;
@@ -755,6 +765,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
 #pragma unroll
     for (int o = NT / 64; o > 0; o >>= 1) lp_merge(st, lp_shfl_xor(st, o), a.k2);
   };
+  auto join_states = [&]() {  // one a lane, of up to eight blocks
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) lp_merge(st, lp_shfl_xor(st, o), a.k2);
+    st.m = __shfl_sync(0xffffffffu, st.m, 0);
+    st.s = __shfl_sync(0xffffffffu, st.s, 0);
+    st.t = __shfl_sync(0xffffffffu, st.t, 0);
+  };
   auto finish = [&]() {
     const LpRow row = lp_finish(st);
     if (tid == kTeller) {
@@ -773,72 +790,135 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
   if (!TOPK) {
     __syncthreads();
     block_sums();
-    if (blocks == 1) finish();
+    if (!CL) finish();
   } else {  // (with a barrier at its head)
     have = (int)min((int64_t)a.topk, sl.size());
     auto side = [&]() {
       block_sums();
-      if (blocks == 1) {
+      if (!CL) {
         const LpRow row = finish();
         if (tid == kTeller) block_row = row;
       } else if (tid == kTeller) {
         block_state = st;
       }
     };
+    // few enough alternatives: the first block fetches and sorts what all blocks
+    // collect, with the bound of the whole row, from all blocks' maxima, each its
+    // share of little more than K ids
+    if constexpr (CL) if (a.topk <= blocks * NT / 2) {
+      static_assert(NT == kOwn, "a maximum a thread");
+      uint16_t* own_key = slot_key + kSlots * NT;
+      const uint32_t best = order_key(own[0]) >> 16;
+      own_key[tid] = (uint16_t)best;
+      __syncthreads();
+      uint32_t bound;
+      if (blocks * a.topk * 9 / 8 <= NT) {  // so few that each block's own bound will do
+        if (tid < 32) bound_key<NT / 32>(own_key, a.topk, &sh.bound);
+        if ((tid >> 5) == 1) side();
+        __syncthreads();
+        bound = sh.bound;
+      } else {
+        cluster_arrive();
+        if ((tid >> 5) == 1) side();
+        __syncwarp();
+        cluster_wait();
+        if (tid < blocks * (NT / 8))
+          reinterpret_cast<uint4*>(cand)[tid] = reinterpret_cast<const uint4*>(
+              cluster.map_shared_rank(own_key, tid / (NT / 8)))[tid % (NT / 8)];
+        __syncthreads();
+        bound = bound_key_slots<NT>(reinterpret_cast<const uint16_t*>(cand), blocks, a.topk, sh);
+      }
+      const int n = collect<T, NT>(sl, bound, best, false, cap, slots, lg, sh, cand);
+      if (tid == 0) block_count = n;
+      cluster.sync();
+      const int b = tid & 31;
+      const int c = b < blocks ? *cluster.map_shared_rank(&block_count, b) : 0;
+      int total;
+      const int first = (int)lanes_before((uint32_t)c, total);
+      if ((int)__reduce_max_sync(0xffffffffu, (uint32_t)c) <= cap && total <= cap) {
+        if (rank == 0) {
+          st = b < blocks ? *cluster.map_shared_rank(&block_state, b) : LpState{neg_inf(), 0.f, 0.f};
+          for (int i0 = tid & ~31; i0 < total; i0 += NT) {
+            const int i = i0 + b;
+            int q = 0, at = i;  // of block q, its word `at`
+            for (int o = 1; o < blocks; ++o) {
+              const int f = __shfl_sync(0xffffffffu, first, o);
+              if (i >= f) {
+                q = o;
+                at = i - f;
+              }
+            }
+            if (q > 0 && i < total) cand[i] = cluster.map_shared_rank(cand, q)[at];
+          }
+        }
+        __syncwarp();
+        cluster_arrive();
+        if (rank == 0) {
+          join_states();
+          const LpRow row = finish();
+          __syncthreads();
+          sort_words<NT, kMaxCap>(cand, total, false, [&](int p, uint64_t w) {
+            if (p < a.topk) store_top(p, w, row);
+          });
+        }
+        __syncwarp();
+        cluster_wait();  // no block leaves while the first reads its ids
+        return;
+      }
+      // long runs of equal logits: block by block
+      cluster.sync();
+      if (tid == 0) sh.count = 0;
+    }
     auto emit = [&](int p, uint64_t w) {
-      if (blocks > 1) cand[p] = w;
+      if (CL) cand[p] = w;
       else if (p < have) store_top(p, w, block_row);
     };
-    select_top<T, NT>(sl, have, cap, slots, lg, own, sh, cand, blocks > 1, side, emit);
+    select_top<T, NT>(sl, have, cap, slots, lg, own, sh, cand, CL, side, emit);
   }
-  if (blocks == 1) return;
-
-  // ---- join the slices: every block fetches all sums and lists
-  uint64_t* all = reinterpret_cast<uint64_t*>(slot_key + kSlots * NT + kOwn + kPairs);
-  if (tid == 0) {
-    if (!TOPK) block_state = st;
-    block_count = have;
-  }
-  cluster.sync();
-  const int b = tid & 31;
-  st = b < blocks ? *cluster.map_shared_rank(&block_state, b) : LpState{neg_inf(), 0.f, 0.f};
-  if (tid < blocks) counts[tid] = *cluster.map_shared_rank(&block_count, tid);
-  if (TOPK)
-    for (int i = tid; i < blocks * a.topk; i += NT)
-      all[i] = cluster.map_shared_rank(cand, i / a.topk)[i % a.topk];
-  __syncwarp();
-  cluster_arrive();  // this block has read the others
-#pragma unroll
-  for (int o = 4; o > 0; o >>= 1) lp_merge(st, lp_shfl_xor(st, o), a.k2);
-  st.m = __shfl_sync(0xffffffffu, st.m, 0);
-  st.s = __shfl_sync(0xffffffffu, st.s, 0);
-  st.t = __shfl_sync(0xffffffffu, st.t, 0);
-  const LpRow row = rank == 0 ? finish() : lp_finish(st);
-  if (TOPK) {
-    int* place = reinterpret_cast<int*>(slot_key);  // of each word (the keys are done with)
-    // larger words here, and in the other slices' sorted lists: one thread
-    // for each word and slice
-    for (int j = tid; j < have; j += NT) place[j] = j;
-    __syncthreads();
-    for (int i = tid; i < have * blocks; i += NT) {
-      const int j = i >> lb, b = i & (blocks - 1);
-      if (b == rank) continue;
-      const uint64_t w = cand[j];
-      const uint64_t* other = all + b * a.topk;
-      int lo = 0, hi = counts[b];
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (other[mid] > w) lo = mid + 1;
-        else hi = mid;
-      }
-      if (lo) atomicAdd(&place[j], lo);
+  if constexpr (CL) {
+    // ---- join the slices: every block fetches all sums and lists
+    uint64_t* all = reinterpret_cast<uint64_t*>(slot_key + kSlots * NT + kOwn + kPairs);
+    if (tid == 0) {
+      if (!TOPK) block_state = st;
+      block_count = have;
     }
-    __syncthreads();
-    for (int j = tid; j < have; j += NT)
-      if (place[j] < a.topk) store_top(place[j], cand[j], row);
+    cluster.sync();
+    const int b = tid & 31;
+    st = b < blocks ? *cluster.map_shared_rank(&block_state, b) : LpState{neg_inf(), 0.f, 0.f};
+    if (tid < blocks) counts[tid] = *cluster.map_shared_rank(&block_count, tid);
+    if (TOPK)
+      for (int i = tid; i < blocks * a.topk; i += NT)
+        all[i] = cluster.map_shared_rank(cand, i / a.topk)[i % a.topk];
+    __syncwarp();
+    cluster_arrive();  // this block has read the others
+    join_states();
+    const LpRow row = rank == 0 ? finish() : lp_finish(st);
+    if (TOPK) {
+      int* place = reinterpret_cast<int*>(slot_key);  // of each word (the keys are done with)
+      // larger words here, and in the other slices' sorted lists: one thread
+      // for each word and slice
+      for (int j = tid; j < have; j += NT) place[j] = j;
+      __syncthreads();
+      for (int i = tid; i < have * blocks; i += NT) {
+        const int j = i >> lb, b = i & (blocks - 1);
+        if (b == rank) continue;
+        const uint64_t w = cand[j];
+        const uint64_t* other = all + b * a.topk;
+        int lo = 0, hi = counts[b];
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (other[mid] > w) lo = mid + 1;
+          else hi = mid;
+        }
+        if (lo) atomicAdd(&place[j], lo);
+      }
+      __syncthreads();
+      for (int j = tid; j < have; j += NT)
+        if (place[j] < a.topk) store_top(place[j], cand[j], row);
+    }
+    __syncwarp();
+    cluster_wait();  // no block leaves while another reads its lists
   }
-  __syncwarp();
-  cluster_wait();  // no block leaves while another reads its lists
 }
 
 // ------------------------------------------------------------------ joining parts
@@ -1046,9 +1126,9 @@ int row_blocks(int64_t n, int64_t row_bytes, int nsm) {
   return c;
 }
 
-template <class T, int NT, bool TOPK>
+template <class T, int NT, bool TOPK, bool CL = false>
 int launch_rows_nt(const LpArgs& a, int blocks, cudaStream_t s) {
-  auto kern = k_logprob_rows<T, NT, TOPK>;
+  auto kern = k_logprob_rows<T, NT, TOPK, CL>;
   const int smem = row_smem<NT>(a.topk, blocks);
   if (smem > 40000 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            smem) != cudaSuccess)
@@ -1079,8 +1159,10 @@ int launch_rows(const LpArgs& a, int nsm, cudaStream_t s) {
   // threads' maxima are no close bound, 474 us and 434 us)
   if (blocks == 1 && a.topk <= kFewK && bytes < 163840)
     return a.topk ? launch_rows_nt<T, 128, true>(a, 1, s) : launch_rows_nt<T, 128, false>(a, 1, s);
-  return a.topk ? launch_rows_nt<T, 256, true>(a, blocks, s)
-                : launch_rows_nt<T, 256, false>(a, blocks, s);
+  if (blocks == 1)
+    return a.topk ? launch_rows_nt<T, 256, true>(a, 1, s) : launch_rows_nt<T, 256, false>(a, 1, s);
+  return a.topk ? launch_rows_nt<T, 256, true, true>(a, blocks, s)
+                : launch_rows_nt<T, 256, false, true>(a, blocks, s);
 }
 
 // ------------------------------------------------------------------ backward
