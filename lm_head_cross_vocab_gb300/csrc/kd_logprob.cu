@@ -443,6 +443,40 @@ __device__ __noinline__ void sort_many(uint64_t* cand, int n) {
   }
   sort_bitonic<NT, 8>(cand, n);
 }
+// How many of cand[i, end) are larger than w (i even).
+__device__ __forceinline__ int larger(const uint64_t* cand, int i, int end, uint64_t w) {
+  int n = 0;
+#pragma unroll 1
+  for (; i + 7 < end; i += 8) {
+    ulonglong2 o[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) o[u] = *reinterpret_cast<const ulonglong2*>(cand + i + 2 * u);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) n += (int)(o[u].x > w) + (int)(o[u].y > w);
+  }
+#pragma unroll 1
+  for (; i < end; ++i) n += cand[i] > w;
+  return n;
+}
+
+// emit(place, word) for each of the first n of cand[0, total), the place being the
+// number of larger ones: 1 << lg threads a word.
+template <int NT, class F>
+__device__ __forceinline__ void rank_words(const uint64_t* cand, int n, int total, F&& emit) {
+  constexpr int kBits = NT == 128 ? 7 : 8;
+  static_assert(NT == 1 << kBits, "");
+  const int lg = max(0, min(5, kBits - 32 + __clz(n - 1))), g = 1 << lg;
+  const int seg = (((total + g - 1) >> lg) + 1) & ~1, from = ((int)threadIdx.x & (g - 1)) * seg;
+  for (int j0 = 0; j0 < n; j0 += NT >> lg) {
+    const int j = j0 + ((int)threadIdx.x >> lg);
+    if (j - (((int)threadIdx.x & 31) >> lg) >= n) break;  // the whole warp
+    const uint64_t w = j < n ? cand[j] : ~0ull;
+    int place = larger(cand, from, min(total, from + seg), w);
+    for (int o = 1; o < g; o <<= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
+    if (from == 0 && j < n) emit(place, w);
+  }
+}
+
 // Words cand[0, n), n <= CAP, in descending order (of more than 8 NT the first
 // 4 NT): emit(place, word) for each,
 // which may write to cand[place] where in_place.  Few words go to the place that
@@ -450,33 +484,21 @@ __device__ __noinline__ void sort_many(uint64_t* cand, int n) {
 template <int NT, int CAP, class F>
 __device__ __forceinline__ void sort_words(uint64_t* cand, int n, bool in_place, F&& emit) {
   if (n <= NT) {
-    // 1 << lg threads a word
-    constexpr int kBits = NT == 128 ? 7 : 8;
-    static_assert(NT == 1 << kBits, "");
-    const int lg = max(0, min(5, kBits - 32 + __clz(n - 1))), g = 1 << lg;
-    const int j = threadIdx.x >> lg, h = threadIdx.x & (g - 1);
-    const uint64_t w = j < n ? cand[j] : 0;
     int place = 0;
-    if ((int)(threadIdx.x & ~31u) >> lg < n) {
-#pragma unroll 8
-      for (int i = h; i < n; i += g) place += cand[i] > w;
-      for (int o = 1; o < g; o <<= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
-    }
+    uint64_t w = 0;
+    rank_words<NT>(cand, n, n, [&](int p, uint64_t o) {
+      place = p + 1;
+      w = o;
+    });
     if (in_place) __syncthreads();
-    if (h == 0 && j < n) emit(place, w);
+    if (place) emit(place - 1, w);
     if (in_place) __syncthreads();
     return;
   }
   if (n <= 2 * NT) {  // two words a thread
     const int j = threadIdx.x + NT;
     const uint64_t w0 = cand[threadIdx.x], w1 = j < n ? cand[j] : ~0ull;
-    int p0 = 0, p1 = 0;
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-      const uint64_t o = cand[i];
-      p0 += o > w0;
-      p1 += o > w1;
-    }
+    const int p0 = larger(cand, 0, n, w0), p1 = larger(cand, 0, n, w1);
     if (in_place) __syncthreads();
     emit(p0, w0);
     if (j < n) emit(p1, w1);
@@ -802,9 +824,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
         block_state = st;
       }
     };
-    // few enough alternatives: the first block fetches and sorts what all blocks
-    // collect, with the bound of the whole row, from all blocks' maxima, each its
-    // share of little more than K ids
+    // few enough alternatives: each block fetches what the others collect and finds
+    // the places of its own; under the bound of the whole row, from all blocks'
+    // maxima, a block collects its share of little more than K ids
     if constexpr (CL) if (a.topk <= blocks * NT / 2) {
       static_assert(NT == kOwn, "a maximum a thread");
       uint16_t* own_key = slot_key + kSlots * NT;
@@ -833,36 +855,34 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
       cluster.sync();
       const int b = tid & 31;
       const int c = b < blocks ? *cluster.map_shared_rank(&block_count, b) : 0;
-      int total;
-      const int first = (int)lanes_before((uint32_t)c, total);
+      int others;
+      const int first = (int)lanes_before(b == rank ? 0u : (uint32_t)c, others);
+      const int total = n + others;
       if ((int)__reduce_max_sync(0xffffffffu, (uint32_t)c) <= cap && total <= cap) {
-        if (rank == 0) {
-          st = b < blocks ? *cluster.map_shared_rank(&block_state, b) : LpState{neg_inf(), 0.f, 0.f};
-          for (int i0 = tid & ~31; i0 < total; i0 += NT) {
-            const int i = i0 + b;
-            int q = 0, at = i;  // of block q, its word `at`
-            for (int o = 1; o < blocks; ++o) {
-              const int f = __shfl_sync(0xffffffffu, first, o);
-              if (i >= f) {
-                q = o;
-                at = i - f;
-              }
+        // the others' words behind this block's
+        for (int i0 = tid & ~31; i0 < others; i0 += NT) {
+          const int i = i0 + b;
+          int q = 0, at = 0;  // block q's word `at`
+          for (int o = 0; o < blocks; ++o) {
+            const int f = __shfl_sync(0xffffffffu, first, o);
+            if (i >= f && o != rank) {
+              q = o;
+              at = i - f;
             }
-            if (q > 0 && i < total) cand[i] = cluster.map_shared_rank(cand, q)[at];
           }
+          if (i < others) cand[n + i] = cluster.map_shared_rank(cand, q)[at];
         }
+        st = b < blocks ? *cluster.map_shared_rank(&block_state, b) : LpState{neg_inf(), 0.f, 0.f};
         __syncwarp();
-        cluster_arrive();
-        if (rank == 0) {
-          join_states();
-          const LpRow row = finish();
-          __syncthreads();
-          sort_words<NT, kMaxCap>(cand, total, false, [&](int p, uint64_t w) {
-            if (p < a.topk) store_top(p, w, row);
-          });
-        }
+        cluster_arrive();  // this block has read the others
+        join_states();
+        const LpRow row = rank == 0 ? finish() : lp_finish(st);
+        __syncthreads();
+        rank_words<NT>(cand, n, total, [&](int p, uint64_t w) {
+          if (p < a.topk) store_top(p, w, row);
+        });
         __syncwarp();
-        cluster_wait();  // no block leaves while the first reads its ids
+        cluster_wait();  // no block leaves while another reads its ids
         return;
       }
       // long runs of equal logits: block by block
@@ -991,7 +1011,7 @@ __global__ void __launch_bounds__(256) k_logprob_join(LpJoin j) {
 constexpr int kJoinThreads = kOwn;
 
 __global__ void __launch_bounds__(kJoinThreads) k_logprob_join_top(LpJoin j) {
-  __shared__ uint64_t cand[kMaxCap / 2];
+  __shared__ __align__(16) uint64_t cand[kMaxCap / 2];
   __shared__ uint16_t own_key[kJoinThreads];
   __shared__ SelectShared sh;
   __shared__ LpRow row;
