@@ -246,6 +246,61 @@ def test_special_rows_of_a_large_vocabulary(n, k, dtype):
     assert (got[~fin] == -math.inf).all() and (out["entropy"][dead] == 0).all()
 
 
+def _hard_rows(v, dtype, seed):
+    """Rows whose best ids lie together, are many, few, or hard to tell apart."""
+    g = torch.Generator().manual_seed(seed)
+    rows = torch.randn(10, v, generator=g) * 3
+    rows[1] = torch.linspace(-8, 8, v)
+    rows[2] = torch.linspace(8, -8, v)
+    rows[3] = rows[3].round()                       # long runs of equal values
+    rows[4] = -1.5
+    rows[5] = -math.inf
+    rows[5, torch.randint(0, v, (9,), generator=g)] = torch.randn(9, generator=g)
+    for i in range(64):                             # 64 bytes in each 16384: one warp's
+        rows[6, i * 8192 % max(v - 32, 1):][:32] += 20
+    rows[7, -min(v, 1100):] += 30                   # the end of the row
+    rows[8] = -rows[8].abs()
+    rows[8, ::97] = 0.0                             # the two zeros are equal
+    rows[8, ::89] = -0.0
+    rows[9] = -rows[9].abs() - 1
+    rows[9, ::101] = -0.0
+    if dtype == "fp32":                             # just below them
+        rows[9, 1::101] = -1e-40
+        rows[9, 2::101] = -3e-39
+    return rows.to(DT[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,v", [(1, 16411), (3, 151937), (9, 65543), (45, 40001), (170, 33001),
+                                 (650, 9001), (650, 33001), (650, 151936), (1300, 1003)])
+def test_alternatives_of_hard_rows(n, v, dtype):
+    """The ids of one row to several blocks, and of blocks to one row, around the
+    numbers of alternatives at which the selection changes: exact, and the same
+    in every copy of a row; the statistics do not depend on the alternatives."""
+    base = _hard_rows(v, dtype, n + v)
+    order = torch.sort(base.float() + 0.0, dim=1, descending=True, stable=True).indices
+    pick = torch.arange(n) % 10 if n > 9 else torch.arange(10)
+    for start in range(0, len(pick), n):            # few rows: a few at a time
+        rows = pick[start:start + n]
+        z = base[rows]
+        y = order[rows, 0].contiguous()
+        ref = None
+        for k in (0, 1, 14, 28, 29, 57, 64, 65, 113, 114, 128, 129, 300, 1000):
+            if k > v:
+                continue
+            _, _, out = _run(z, y, 1.0, k, dtype)
+            if k:
+                assert (out["topk_idx"].cpu() == order[rows, :k]).all(), (k, rows.tolist()[:10])
+                fin = torch.isfinite(out["logprob"])
+                assert torch.equal(out["topk_logprob"][fin, 0], out["logprob"][fin]), k
+            if ref is None:
+                ref = out
+            _close(out["entropy"].cpu(), ref["entropy"].cpu().double().numpy(),
+                   2 * _e_s(v) * (math.log(v) + 3), ("entropy", k))
+            _close(out["logprob"].cpu(), ref["logprob"].cpu().double().numpy(),
+                   2 * _e_s(v) + 8 * U * 40, ("logprob", k))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("v,pitch,shift", [(1000, 1000, 1), (1000, 1003, 0), (1001, 1016, 3),
                                            (4096, 4104, 8), (32003, 32100, 5)])
