@@ -463,7 +463,7 @@ __device__ __forceinline__ int larger(const uint64_t* cand, int i, int end, uint
 // number of larger ones: 1 << lg threads a word.
 template <int NT, class F>
 __device__ __forceinline__ void rank_words(const uint64_t* cand, int n, int total, F&& emit) {
-  constexpr int kBits = NT == 128 ? 7 : 8;
+  constexpr int kBits = NT == 128 ? 7 : NT == 256 ? 8 : 10;
   static_assert(NT == 1 << kBits, "");
   const int lg = max(0, min(5, kBits - 32 + __clz(n - 1))), g = 1 << lg;
   const int seg = (((total + g - 1) >> lg) + 1) & ~1, from = ((int)threadIdx.x & (g - 1)) * seg;
@@ -505,10 +505,12 @@ __device__ __forceinline__ void sort_words(uint64_t* cand, int n, bool in_place,
     if (in_place) __syncthreads();
     return;
   }
-  sort_many<NT, CAP>(cand, n);
-  if (CAP > 8 * NT && n > 8 * NT) n = 4 * NT;
-  if (!in_place)
-    for (int i = threadIdx.x; i < n; i += NT) emit(i, cand[i]);
+  if constexpr (CAP > 2 * NT) {
+    sort_many<NT, CAP>(cand, n);
+    if (CAP > 8 * NT && n > 8 * NT) n = 4 * NT;
+    if (!in_place)
+      for (int i = threadIdx.x; i < n; i += NT) emit(i, cand[i]);
+  }
 }
 
 // Dynamic shared memory: cand[cap] (u64), the upper halves of the slot keys
@@ -956,23 +958,31 @@ struct LpJoin {
 
 // One warp: the joined sums of row r and the logit of its token.
 __device__ __forceinline__ LpState join_sums(const LpJoin& j, int64_t r, float& zy) {
+  constexpr int P = 2 * kMaxSplits / 32;
+  float4 q[P];
+#pragma unroll
+  for (int u = 0; u < P; ++u) {
+    const int p = 32 * u + ((int)threadIdx.x & 31);
+    q[u] = p < j.parts ? j.sums[(int64_t)p * j.a.n + r] : make_float4(neg_inf(), 0.f, 0.f, 0.f);
+  }
   LpState st{neg_inf(), 0.f, 0.f};
+#pragma unroll
+  for (int u = 0; u < P; ++u) st.m = fmaxf(st.m, q[u].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) st.m = fmaxf(st.m, __shfl_xor_sync(0xffffffffu, st.m, o));
   zy = 0.f;
-  for (int p0 = threadIdx.x & 31; p0 < j.parts; p0 += 8 * 32) {
-    float4 q[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
-      q[u] = p0 + 32 * u < j.parts ? j.sums[(int64_t)(p0 + 32 * u) * j.a.n + r]
-                                   : make_float4(neg_inf(), 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      lp_merge(st, LpState{q[u].x, q[u].y, q[u].z}, j.a.k2);
-      zy += q[u].w;
-    }
+  for (int u = 0; u < P; ++u) {
+    LpState a{q[u].x, q[u].y, q[u].z};
+    lp_raise(a, st.m, j.a.k2);
+    st.s += a.s;
+    st.t += a.t;
+    zy += q[u].w;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    lp_merge(st, lp_shfl_xor(st, o), j.a.k2);
+    st.s += __shfl_xor_sync(0xffffffffu, st.s, o);
+    st.t += __shfl_xor_sync(0xffffffffu, st.t, o);
     zy += __shfl_xor_sync(0xffffffffu, zy, o);
   }
   return st;
@@ -1004,96 +1014,75 @@ __global__ void __launch_bounds__(256) k_logprob_join(LpJoin j) {
   }
 }
 
-// With alternatives: a block per row.  The K-th largest of the threads' best
-// candidates bounds the K-th best from below; what lies above it is sorted.
-// Bound by the latency of its few dependent loads: 8 us for one row, 29-50 us
-// for 2048 rows of about 1000 candidates.
-constexpr int kJoinThreads = kOwn;
-
-__global__ void __launch_bounds__(kJoinThreads) k_logprob_join_top(LpJoin j) {
+// With alternatives: a block per row, the parts' lists dealt to its warps.  The
+// K-th largest of kOwn best candidates bounds the K-th best from below; what lies
+// above it is sorted.  Bound by the latency of its few dependent loads, two sweeps
+// over the lists: JOINTIME
+template <int NT>
+__global__ void __launch_bounds__(NT) k_logprob_join_top(LpJoin j) {
+  constexpr int W = NT / 32, kGroup = NT / kOwn, kAtOnce = 4;
+  static_assert(2 * kMaxSplits <= 32 * W, "a lane for each part of a warp");
   __shared__ __align__(16) uint64_t cand[kMaxCap / 2];
-  __shared__ uint16_t own_key[kJoinThreads];
+  __shared__ uint16_t own_key[kOwn];
   __shared__ SelectShared sh;
   __shared__ LpRow row;
   __shared__ uint64_t last;
-  __shared__ int first[2 * kMaxSplits + 1];
   const LpArgs& a = j.a;
   const int64_t r = blockIdx.x;
-  const int tid = threadIdx.x, k = a.topk;
+  const int tid = threadIdx.x, k = a.topk, warp = tid >> 5, lane = tid & 31;
   const int64_t y = a.tokens ? a.tokens[r] : -1;
   if (a.tokens && y == a.ignore) {
     lp_store_ignored(a, r);
     return;
   }
-  // candidates of all parts, numbered through: part p's from first[p] on
-  if (tid < 32) {
-    int c[2 * kMaxSplits / 32], sum = 0;
+  if (tid == 0) sh.count = 0;
+  // lane i: the candidates of this warp's part i, part warp + W i of the row
+  // (a part that a timed-out wait ended has written nothing)
+  const int parts = (j.parts - warp + W - 1) / W;
+  const int mine =
+      lane < parts ? max(0, min(j.count[(int64_t)(warp + W * lane) * a.n + r], kTokCap)) : 0;
+  auto word = [&](int part, int i) -> uint64_t {
+    const uint64_t w = j.cand[((int64_t)(warp + W * part) * a.n + r) * kTokCap + i];
+    return cand_word(order_key(__uint_as_float((uint32_t)(w >> 32))), ~(uint32_t)w);
+  };
+  auto each = [&](auto&& f) {
+#pragma unroll 1
+    for (int p = 0; p < parts; p += kAtOnce) {
+      uint64_t w[kAtOnce][2];
+      int n[kAtOnce], most = 0;
 #pragma unroll
-    for (int i = 0; i < 2 * kMaxSplits / 32; ++i)
-      c[i] = 32 * i + tid < j.parts ? j.count[(int64_t)(32 * i + tid) * a.n + r] : 0;
-    // (a part that a timed-out wait ended has written nothing)
+      for (int u = 0; u < kAtOnce; ++u) {
+        n[u] = __shfl_sync(0xffffffffu, mine, (p + u) & 31);
+        if (p + u >= parts) n[u] = 0;
+        most = max(most, n[u]);
 #pragma unroll
-    for (int i = 0; i < 2 * kMaxSplits / 32; ++i) c[i] = max(0, min(c[i], kTokCap));
-#pragma unroll
-    for (int i = 0; i < 2 * kMaxSplits / 32; ++i) {
-      int up = c[i];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int q = __shfl_up_sync(0xffffffffu, up, o);
-        if (tid >= o) up += q;
+        for (int i = 0; i < 2; ++i) w[u][i] = 32 * i + lane < n[u] ? word(p + u, 32 * i + lane) : 0;
       }
-      if (32 * i + tid < j.parts) first[32 * i + tid] = sum + up - c[i];
-      sum += __shfl_sync(0xffffffffu, up, 31);
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (w[u][i]) f(w[u][i]);
+      if (most <= 64) continue;
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll 2
+        for (int i = 64 + lane; i < n[u]; i += 32) f(word(p + u, i));
     }
-    if (tid == 0) {
-      first[j.parts] = sum;
-      sh.count = 0;
-    }
-  } else if (tid < 64) {
+  };
+  if (warp == W - 1) {
     float zy;
     const LpRow q = lp_finish(join_sums(j, r, zy));
-    if (tid == 32) {
+    if (lane == 0) {
       row = q;
       join_store(j, r, y, q, zy);
     }
   }
-  __syncthreads();
-  const int total = first[j.parts];
-  auto word = [&](int i) -> uint64_t {
-    int lo = 0, hi = j.parts;  // first[lo] <= i < first[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (first[mid] <= i) lo = mid;
-      else hi = mid;
-    }
-    const uint64_t w = j.cand[((int64_t)lo * a.n + r) * kTokCap + (i - first[lo])];
-    return cand_word(order_key(__uint_as_float((uint32_t)(w >> 32))), ~(uint32_t)w);
-  };
-  constexpr int kHeld = 4;  // words a thread holds; those behind are read again
-  uint64_t held[kHeld];
-#pragma unroll
-  for (int u = 0; u < kHeld; ++u) {
-    const int i = tid + u * kJoinThreads;
-    held[u] = i < total ? word(i) : 0;
-  }
-  auto each = [&](auto&& f) {
-#pragma unroll
-    for (int u = 0; u < kHeld; ++u)
-      if (held[u]) f(held[u]);
-#pragma unroll 1
-    for (int i0 = tid + kHeld * kJoinThreads; i0 < total; i0 += kHeld * kJoinThreads) {
-      uint64_t w[kHeld];
-#pragma unroll
-      for (int u = 0; u < kHeld; ++u)
-        w[u] = i0 + u * kJoinThreads < total ? word(i0 + u * kJoinThreads) : 0;
-#pragma unroll
-      for (int u = 0; u < kHeld; ++u)
-        if (w[u]) f(w[u]);
-    }
-  };
   uint64_t best = 0;
   each([&](uint64_t w) { best = max(best, w); });
-  own_key[tid] = (uint16_t)(best >> 48);
+#pragma unroll
+  for (int o = 1; o < kGroup; o <<= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+  if (tid % kGroup == 0) own_key[tid / kGroup] = (uint16_t)(best >> 48);
   __syncthreads();
   if (tid < 32) bound_key<kOwn / 32>(own_key, k, &sh.bound);
   __syncthreads();
@@ -1104,9 +1093,14 @@ __global__ void __launch_bounds__(kJoinThreads) k_logprob_join_top(LpJoin j) {
     if (at < kMaxCap / 2) cand[at] = w;
   });
   __syncthreads();
+  auto store = [&](int i, uint64_t w) {
+    if (i >= k) return;
+    if (a.topk_idx) a.topk_idx[r * k + i] = (int32_t)~(uint32_t)w;
+    if (a.topk_lp) a.topk_lp[r * k + i] = lp_of(key_value((uint32_t)(w >> 32)), row, a.inv_t);
+  };
   const int have = (int)sh.count;
   if (have <= kMaxCap / 2) {
-    sort_words<kJoinThreads, kMaxCap / 2>(cand, have, true, [&](int i, uint64_t w) { cand[i] = w; });
+    sort_words<NT, kMaxCap / 2>(cand, have, false, store);
   } else {
     // many equal logits: one after the other
     if (tid == 0) last = 0;
@@ -1119,20 +1113,16 @@ __global__ void __launch_bounds__(kJoinThreads) k_logprob_join_top(LpJoin j) {
       });
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) w = max(w, __shfl_xor_sync(0xffffffffu, w, o));
-      __shared__ uint64_t warp_best[kJoinThreads / 32];
+      __shared__ uint64_t warp_best[W];
       if ((tid & 31) == 0) warp_best[tid >> 5] = w;
       __syncthreads();
       if (tid == 0) {
-        for (int q = 1; q < kJoinThreads / 32; ++q) w = max(w, warp_best[q]);
+        for (int q = 1; q < W; ++q) w = max(w, warp_best[q]);
         cand[i] = last = w;
       }
     }
     __syncthreads();
-  }
-  for (int i = tid; i < k; i += kJoinThreads) {
-    const uint64_t w = cand[i];
-    if (a.topk_idx) a.topk_idx[r * k + i] = (int32_t)~(uint32_t)w;
-    if (a.topk_lp) a.topk_lp[r * k + i] = lp_of(key_value((uint32_t)(w >> 32)), row, a.inv_t);
+    for (int i = tid; i < k; i += NT) store(i, cand[i]);
   }
 }
 
@@ -1642,7 +1632,9 @@ extern "C" kd_status kd_logprob_fwd(const kd_logprob_problem* p, const kd_logpro
       if (launch_tc_tok(t, P.nsm, s)) return KD_ERR_CUDA;
       const LpJoin j{a, t.sums, t.cand, t.count, 2 * P.splits};
       note_launch();
-      if (k) k_logprob_join_top<<<(unsigned)a.n, kJoinThreads, 0, s>>>(j);
+      // (few rows: more of each row's lists at once)
+      if (k && a.n <= P.nsm) k_logprob_join_top<1024><<<(unsigned)a.n, 1024, 0, s>>>(j);
+      else if (k) k_logprob_join_top<256><<<(unsigned)a.n, 256, 0, s>>>(j);
       else k_logprob_join<<<(unsigned)cdiv(a.n, 8), 256, 0, s>>>(j);
     }
   } else {
