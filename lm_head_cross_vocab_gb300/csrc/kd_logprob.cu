@@ -997,6 +997,7 @@ __device__ __forceinline__ void join_store(const LpJoin& j, int64_t r, int64_t y
 // Without alternatives: a warp per row.
 __global__ void __launch_bounds__(256) k_logprob_join(LpJoin j) {
   const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (r >= j.a.n) return;
   const int64_t y = j.a.tokens ? j.a.tokens[r] : -1;
   const bool off = j.a.tokens && y == j.a.ignore;
@@ -1030,6 +1031,7 @@ __global__ void __launch_bounds__(NT) k_logprob_join_top(LpJoin j) {
   const LpArgs& a = j.a;
   const int64_t r = blockIdx.x;
   const int tid = threadIdx.x, k = a.topk, warp = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t y = a.tokens ? a.tokens[r] : -1;
   if (a.tokens && y == a.ignore) {
     lp_store_ignored(a, r);
@@ -1127,6 +1129,22 @@ __global__ void __launch_bounds__(NT) k_logprob_join_top(LpJoin j) {
 }
 
 // ------------------------------------------------------------------ launches
+// Right behind the kernel that writes the parts: on the device when that ends.
+int launch_join(void (*kern)(LpJoin), int64_t grid, int threads, const LpJoin& j, cudaStream_t s) {
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  note_launch();
+  return (int)cudaLaunchKernelEx(&cfg, kern, j);
+}
+
 // Blocks of a cluster for each row: enough of them to give every SM work, as
 // long as a slice keeps 16 KiB (one row of 151936 bf16 in one block 41 us, in
 // eight 4.5 us; where the rows fill the device the join would only cost).
@@ -1350,8 +1368,11 @@ __global__ void __launch_bounds__(kRowThreads) k_sum_parts(const float4* __restr
 
 // rows >= n behind the first n: zeros
 __global__ void __launch_bounds__(kRowThreads) k_pad_rows(const uint4* __restrict__ h, int64_t n,
-                                                          int64_t vecs, uint4* __restrict__ out) {
+                                                          int64_t vecs, uint4* __restrict__ out,
+                                                          uint32_t* __restrict__ ones, int64_t words) {
   const int64_t r = blockIdx.x;
+  for (int64_t i = r * kRowThreads + threadIdx.x; i < words; i += (int64_t)gridDim.x * kRowThreads)
+    ones[i] = ~0u;
   for (int64_t i = threadIdx.x; i < vecs; i += kRowThreads)
     out[r * vecs + i] = r < n ? h[r * vecs + i] : make_uint4(0, 0, 0, 0);
 }
@@ -1606,12 +1627,17 @@ extern "C" kd_status kd_logprob_fwd(const kd_logprob_problem* p, const kd_logpro
       memset(&t, 0, sizeof(t));
       t.h = static_cast<const __nv_bfloat16*>(in->h) + r0 * P.d;
       t.h_rows = a.n;
+      t.pub = at<float>(workspace, P.f_pub);
+      const int64_t pubs = k ? (int64_t)2 * P.splits * a.n : 0;  // all ones: nothing published
       if (a.n < kFewRows && P.n < kFewRows) {
         note_launch();
         k_pad_rows<<<(unsigned)kPadRows, kRowThreads, 0, s>>>(
-            static_cast<const uint4*>(t.h), a.n, P.d / 8, at<uint4>(workspace, P.f_h));
+            static_cast<const uint4*>(t.h), a.n, P.d / 8, at<uint4>(workspace, P.f_h),
+            reinterpret_cast<uint32_t*>(t.pub), pubs);
         t.h = at<char>(workspace, P.f_h);
         t.h_rows = kPadRows;
+      } else if (pubs && cudaMemsetAsync(t.pub, 0xff, (size_t)pubs * 4, s) != cudaSuccess) {
+        return KD_ERR_CUDA;
       }
       t.w = in->w;
       t.n = a.n;
@@ -1625,17 +1651,14 @@ extern "C" kd_status kd_logprob_fwd(const kd_logprob_problem* p, const kd_logpro
       t.sums = at<float4>(workspace, P.f_sums);
       t.cand = at<uint64_t>(workspace, P.f_cand);
       t.count = at<int32_t>(workspace, P.f_count);
-      t.pub = at<float>(workspace, P.f_pub);
-      if (k && cudaMemsetAsync(t.pub, 0xff, (size_t)2 * P.splits * a.n * 4, s) != cudaSuccess)
-        return KD_ERR_CUDA;
       t.status = dev_status;
       if (launch_tc_tok(t, P.nsm, s)) return KD_ERR_CUDA;
       const LpJoin j{a, t.sums, t.cand, t.count, 2 * P.splits};
-      note_launch();
       // (few rows: more of each row's lists at once)
-      if (k && a.n <= P.nsm) k_logprob_join_top<1024><<<(unsigned)a.n, 1024, 0, s>>>(j);
-      else if (k) k_logprob_join_top<256><<<(unsigned)a.n, 256, 0, s>>>(j);
-      else k_logprob_join<<<(unsigned)cdiv(a.n, 8), 256, 0, s>>>(j);
+      if (!k ? launch_join(k_logprob_join, cdiv(a.n, 8), 256, j, s)
+          : a.n <= P.nsm ? launch_join(k_logprob_join_top<1024>, a.n, 1024, j, s)
+                         : launch_join(k_logprob_join_top<256>, a.n, 256, j, s))
+        return KD_ERR_CUDA;
     }
   } else {
     float* z = at<float>(workspace, P.f_z);
