@@ -232,7 +232,8 @@ struct TcTokArgs {
   float4* sums;            // [parts][n]: max z, s, t, z[token] (0 in the parts without it)
   uint64_t* cand;          // [parts][n][kTokCap]: logit << 32 | complement of the id
   int32_t* count;          // [parts][n]
-  float* pub;              // [parts][n] values the parts publish, NaN before
+  float* pub;              // [parts] rows of pitch pub_ld: values the parts publish, NaN before
+  int64_t pub_ld;          // >= n
   uint32_t* status;
 };
 int launch_tc_tok(const TcTokArgs& a, int num_sms, cudaStream_t s);

@@ -67,22 +67,25 @@ __device__ __forceinline__ void lp_store_ignored(const LpArgs& a, int64_t r) {
 // ------------------------------------------------------------------ rows
 // One block of NT threads takes a row, or, when there are too few rows to fill
 // the device, a cluster of blocks takes it in slices that are joined through
-// distributed shared memory.  A slice is read once in 16-byte vectors, four in
-// flight per thread beside the four being folded into (offset, s, t); the
-// offset trails the running maximum by up to 2^8, so that most vectors need no
-// rescale.  What the K best cost on top: each thread keeps the maximum of every
-// slot (a run of its vectors, at most kSlots of them); the K-th largest of the
-// slot maxima bounds the K-th largest logit from below, so only the vectors of
-// the few slots above it are read again (from L2), and what lies above the
-// bound in them, little more than K ids, is sorted.
+// distributed shared memory.  A slice is read once, 64 contiguous bytes a thread
+// and step, the next step's in flight beside the one being folded into (offset, s,
+// t); the offset trails the running maximum by up to 2^8, so that most steps need
+// no rescale.  What the K best cost on top: each thread keeps the maximum of every
+// slot (a step, or a run of them, at most kSlots) and of all; the K-th largest of
+// the threads' maxima (of the slots' for many alternatives) bounds the K-th
+// largest logit from below, so only the 64 bytes of the few slots above it are
+// read again, and what lies above the bound in them, little more than K ids, is
+// put in order.
 //
-// Without alternatives bound by HBM: 4096 x 151936 bf16 185-190 us (6.5-6.7 TB/s),
-// fp32 343 us (7.2 TB/s), 16384 x 32000 bf16 168 us.  With them a block's
-// selection follows its sweep, and the four blocks of an SM do not quite cover
-// one another's: 241 us with 20, 278 us with 100 (4.5 TB/s); more bytes in
-// flight (prefetch of the next row into L2, a ring of asynchronous copies) only
-// made the rows in flight overflow L2.  Few rows: one row of 151936 4.5 us, with
-// 20 alternatives 9.7 us (8 blocks, latency).
+// Without alternatives bound by HBM: 4096 x 151936 bf16 177-180 us (6.9-7.0 TB/s),
+// fp32 333-340 us (7.4 TB/s), 16384 x 32000 bf16 155 us.  With them a block's
+// selection follows its sweep, about 16000 of its 62000 cycles with 100, and the
+// four blocks of an SM do not quite cover one another's: 200 us with 20, 219 us
+// with 100 (5.7 TB/s), 375 us in fp32.  Nothing of a row is in local memory (the
+// selection out of line, with what it needs spilled, 278 us: the sweeps push such
+// lines out of L1), and its steps are few instructions, which wait their turn
+// behind the other blocks' sweeps.  Few rows, bound by latency: one row of 151936
+// 4.4 us, with 20 alternatives 7.6 us, with 100 9.8 us (8 blocks).
 constexpr int kSlots = 32;
 constexpr int kPairs = 4096;   // slots above the bound the list holds
 constexpr int kMaxCap = 4096;  // candidates a block sorts at most
@@ -1018,7 +1021,8 @@ __global__ void __launch_bounds__(256) k_logprob_join(LpJoin j) {
 // With alternatives: a block per row, the parts' lists dealt to its warps.  The
 // K-th largest of kOwn best candidates bounds the K-th best from below; what lies
 // above it is sorted.  Bound by the latency of its few dependent loads, two sweeps
-// over the lists: JOINTIME
+// over the lists: 13 us for one row with cold caches (25 us where every thread
+// looked for its word's part).
 template <int NT>
 __global__ void __launch_bounds__(NT) k_logprob_join_top(LpJoin j) {
   constexpr int W = NT / 32, kGroup = NT / kOwn, kAtOnce = 4;
@@ -1146,8 +1150,9 @@ int launch_join(void (*kern)(LpJoin), int64_t grid, int threads, const LpJoin& j
 }
 
 // Blocks of a cluster for each row: enough of them to give every SM work, as
-// long as a slice keeps 16 KiB (one row of 151936 bf16 in one block 41 us, in
-// eight 4.5 us; where the rows fill the device the join would only cost).
+// long as a slice keeps 16 KiB and no SM gets more than four blocks (with up to
+// twice as many blocks 80 rows of 151936 bf16 with 20 alternatives took 24 us for
+// 18 us, 333 fp32 rows of 32003 25 us for 16 us).
 int row_blocks(int64_t n, int64_t row_bytes, int nsm) {
   int c = 1;
   while (c < 8 && n * c * 2 <= 4 * nsm && row_bytes / (2 * c) >= 16384) c *= 2;
@@ -1182,9 +1187,10 @@ int launch_rows(const LpArgs& a, int nsm, cudaStream_t s) {
   if (a.n <= 0) return 0;
   const int64_t bytes = a.vocab * (int64_t)sizeof(T);
   const int blocks = row_blocks(a.n, bytes, nsm);
-  // short rows: more, smaller blocks on an SM (16384 x 32000 bf16: 169 us with
-  // 128 threads a block, 195 us with 256; with 100 alternatives, for which 128
-  // threads' maxima are no close bound, 474 us and 434 us)
+  // short rows: more, smaller blocks on an SM (128 and 256 threads: 16384 x 32000
+  // bf16 157 us and 181 us, with 20 alternatives 229 us and 305 us, with 100 350 us
+  // and 386 us; 8192 x 65536 with 20 204 us and 225 us, 6000 x 98000 237 us and
+  // 231 us, 4096 x 151936 245 us and 226 us)
   if (blocks == 1 && a.topk <= kFewK && bytes < 163840)
     return a.topk ? launch_rows_nt<T, 128, true>(a, 1, s) : launch_rows_nt<T, 128, false>(a, 1, s);
   if (blocks == 1)
@@ -1416,6 +1422,10 @@ constexpr int64_t kFusedRows = 8192;
 // halves the rate at which W arrives (one row of D 4096 against 151936 columns:
 // 320 us as it is, 199 us from 16 rows on, whatever they hold).
 constexpr int64_t kFewRows = 16, kPadRows = 64;
+// Published values of the parts: a line each where there are few rows, so that
+// all parts' reads of one row do not meet in a few lines (one row of 151936 x 4096
+// with 20 alternatives 211 us, 222 us with the values of its 256 parts side by side).
+int64_t pub_pitch(int64_t n) { return std::max<int64_t>(n, 32); }
 
 // Vocabulary splits of the fused forward: the smallest makespan, in tiles, of
 // m_tiles * s items on `workers` CTAs (pairs).  An item costs more than its
@@ -1475,7 +1485,7 @@ kd_status lp_plan(const kd_logprob_problem* p, LpPlan& P) {
     P.f_sums = take(off, recs * sizeof(float4));
     if (p->topk > 0) {
       P.f_count = take(off, recs * 4);
-      P.f_pub = take(off, recs * 4);
+      P.f_pub = take(off, (size_t)2 * P.splits * pub_pitch(P.fr) * 4);
       P.f_cand = take(off, recs * kTokCap * 8);
     }
   } else {
@@ -1628,7 +1638,8 @@ extern "C" kd_status kd_logprob_fwd(const kd_logprob_problem* p, const kd_logpro
       t.h = static_cast<const __nv_bfloat16*>(in->h) + r0 * P.d;
       t.h_rows = a.n;
       t.pub = at<float>(workspace, P.f_pub);
-      const int64_t pubs = k ? (int64_t)2 * P.splits * a.n : 0;  // all ones: nothing published
+      t.pub_ld = pub_pitch(a.n);
+      const int64_t pubs = k ? 2 * P.splits * t.pub_ld : 0;  // all ones: nothing published
       if (a.n < kFewRows && P.n < kFewRows) {
         note_launch();
         k_pad_rows<<<(unsigned)kPadRows, kRowThreads, 0, s>>>(

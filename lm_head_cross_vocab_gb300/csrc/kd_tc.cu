@@ -609,10 +609,10 @@ __device__ __noinline__ void cut_candidates(uint32_t rows, uint64_t* cand, int* 
 // are kept, never which come out on top.  On GB300 (forward with the join), bound
 // by the tensor pipe: 2048 x 151936, D 4096 1223-1260 us without alternatives
 // (2.0-2.1 PFLOP/s), 1280 us with 20, 1323 us with 100; cutting every part's list
-// down to its own k instead took 1926 us.  One row, bound by HBM: 196 us without,
-// 238 us with 20.  A load takes long here, behind the
-// operands' copies (5 to 10 us where those are bound by HBM): the floor is read
-// in one batch, which a whole tile's work covers once there is one at all.
+// down to its own k instead took 1926 us.  One row, bound by HBM: 199 us without,
+// 211 us with 20.  A load takes long here, behind the operands' copies (5 to 10 us
+// where those are bound by HBM): the floor is read in one batch, which a whole
+// tile's work covers once there is one at all.
 constexpr int kLead = 8;
 constexpr int kRead = 32;  // published values read at most (fewer: a weaker floor, as true)
 
@@ -799,7 +799,7 @@ struct TokEpi {
   __device__ __forceinline__ void publish(const TcParams& P) {
     const TcTokArgs& a = P.tok;
     if (row_ok && lead[kLead - 1] > neg_inf())
-      st_relaxed(a.pub + (int64_t)part * a.n + row, lead[kLead - 1]);
+      st_relaxed(a.pub + (int64_t)part * a.pub_ld + row, lead[kLead - 1]);
   }
   // Published values of this row, spread evenly over the parts from this one on.
   __device__ __forceinline__ void ask(const TcParams& P, float* v) const {
@@ -810,7 +810,7 @@ struct TokEpi {
     for (int u = 0; u < kRead; ++u) {
       int at = part + (parts <= kRead ? u : (int)((int64_t)u * parts / kRead));
       if (at >= parts) at -= parts;
-      v[u] = u < parts ? ld_relaxed(pub + (int64_t)at * a.n) : neg_inf();
+      v[u] = u < parts ? ld_relaxed(pub + (int64_t)at * a.pub_ld) : neg_inf();
     }
   }
   __device__ __forceinline__ void answer(const TcParams& P, float* v) {
