@@ -1020,12 +1020,13 @@ __global__ void __launch_bounds__(256) k_logprob_join(LpJoin j) {
 
 // With alternatives: a block per row, the parts' lists dealt to its warps.  The
 // K-th largest of kOwn best candidates bounds the K-th best from below; what lies
-// above it is sorted.  Bound by the latency of its few dependent loads, two sweeps
-// over the lists: 13 us for one row with cold caches (25 us where every thread
-// looked for its word's part).
+// above it is sorted.  Bound by the latency of its few dependent loads: with cold
+// caches 11 us for one row (25 us where every thread searched all parts for its
+// word's), 29 us for 2048 rows with 20 alternatives, 52 us with 100 (64 us with 4
+// words held by a thread, 55 us with 12).
 template <int NT>
 __global__ void __launch_bounds__(NT) k_logprob_join_top(LpJoin j) {
-  constexpr int W = NT / 32, kGroup = NT / kOwn, kAtOnce = 4;
+  constexpr int W = NT / 32, kGroup = NT / kOwn, kHeld = 8;
   static_assert(2 * kMaxSplits <= 32 * W, "a lane for each part of a warp");
   __shared__ __align__(16) uint64_t cand[kMaxCap / 2];
   __shared__ uint16_t own_key[kOwn];
@@ -1047,33 +1048,37 @@ __global__ void __launch_bounds__(NT) k_logprob_join_top(LpJoin j) {
   const int parts = (j.parts - warp + W - 1) / W;
   const int mine =
       lane < parts ? max(0, min(j.count[(int64_t)(warp + W * lane) * a.n + r], kTokCap)) : 0;
-  auto word = [&](int part, int i) -> uint64_t {
-    const uint64_t w = j.cand[((int64_t)(warp + W * part) * a.n + r) * kTokCap + i];
+  int total;
+  const int first = (int)lanes_before((uint32_t)mine, total);
+  // word i of the warp's lists, one behind the other
+  auto word = [&](int i) -> uint64_t {
+    int part = 0, at = i;
+    for (int o = 1; o < parts; ++o) {
+      const int f = __shfl_sync(0xffffffffu, first, o);
+      if (i >= f) {
+        part = o;
+        at = i - f;
+      }
+    }
+    if (i >= total) return 0;
+    const uint64_t w = j.cand[((int64_t)(warp + W * part) * a.n + r) * kTokCap + at];
     return cand_word(order_key(__uint_as_float((uint32_t)(w >> 32))), ~(uint32_t)w);
   };
+  uint64_t held[kHeld];  // those behind are read again
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) held[u] = 32 * u < total ? word(32 * u + lane) : 0;
   auto each = [&](auto&& f) {
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u)
+      if (held[u]) f(held[u]);
 #pragma unroll 1
-    for (int p = 0; p < parts; p += kAtOnce) {
-      uint64_t w[kAtOnce][2];
-      int n[kAtOnce], most = 0;
+    for (int i = 32 * kHeld; i < total; i += 4 * 32) {
+      uint64_t w[4];
 #pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-        n[u] = __shfl_sync(0xffffffffu, mine, (p + u) & 31);
-        if (p + u >= parts) n[u] = 0;
-        most = max(most, n[u]);
+      for (int u = 0; u < 4; ++u) w[u] = word(i + 32 * u + lane);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) w[u][i] = 32 * i + lane < n[u] ? word(p + u, 32 * i + lane) : 0;
-      }
-#pragma unroll
-      for (int u = 0; u < kAtOnce; ++u)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (w[u][i]) f(w[u][i]);
-      if (most <= 64) continue;
-#pragma unroll
-      for (int u = 0; u < kAtOnce; ++u)
-#pragma unroll 2
-        for (int i = 64 + lane; i < n[u]; i += 32) f(word(p + u, i));
+      for (int u = 0; u < 4; ++u)
+        if (w[u]) f(w[u]);
     }
   };
   if (warp == W - 1) {
@@ -1665,9 +1670,9 @@ extern "C" kd_status kd_logprob_fwd(const kd_logprob_problem* p, const kd_logpro
       t.status = dev_status;
       if (launch_tc_tok(t, P.nsm, s)) return KD_ERR_CUDA;
       const LpJoin j{a, t.sums, t.cand, t.count, 2 * P.splits};
-      // (few rows: more of each row's lists at once)
+      // (few rows, or many lists: more of a row's lists at once)
       if (!k ? launch_join(k_logprob_join, cdiv(a.n, 8), 256, j, s)
-          : a.n <= P.nsm ? launch_join(k_logprob_join_top<1024>, a.n, 1024, j, s)
+          : a.n <= P.nsm || j.parts > 64 ? launch_join(k_logprob_join_top<1024>, a.n, 1024, j, s)
                          : launch_join(k_logprob_join_top<256>, a.n, 256, j, s))
         return KD_ERR_CUDA;
     }
