@@ -80,14 +80,15 @@ __device__ __forceinline__ void lp_store_ignored(const LpArgs& a, int64_t r) {
 // Without alternatives bound by HBM: 4096 x 151936 bf16 177-180 us (6.9-7.0 TB/s),
 // fp32 333-340 us (7.4 TB/s), 16384 x 32000 bf16 155 us.  With them a block's
 // selection follows its sweep, about 16000 of its 62000 cycles with 100, and the
-// four blocks of an SM do not quite cover one another's: 200 us with 20, 219 us
-// with 100 (5.7 TB/s), 375 us in fp32.  Nothing of a row is in local memory (the
+// four blocks of an SM do not quite cover one another's: 199-204 us with 20,
+// 219-222 us with 100 (5.6 TB/s), 375 us in fp32.  Nothing of a row is in local memory (the
 // selection out of line, with what it needs spilled, 278 us: the sweeps push such
 // lines out of L1), and its steps are few instructions, which wait their turn
 // behind the other blocks' sweeps.  Few rows, bound by latency: one row of 151936
-// 4.4 us, with 20 alternatives 7.6 us, with 100 9.8 us (8 blocks).
+// 4.2-4.8 us, with 20 alternatives 7.6-8.0 us, with 100 9.8-10.1 us (8 blocks).
 constexpr int kSlots = 32;
-constexpr int kPairs = 4096;   // slots above the bound the list holds
+// slots above the bound the lists of a block's warps hold
+constexpr int row_pairs(int nt) { return nt == 128 ? 1024 : 4096; }
 constexpr int kMaxCap = 4096;  // candidates a block sorts at most
 constexpr int kFewK = 128, kFewCap = 1024;  // with up to kFewK alternatives
 constexpr int kUnroll = 4;
@@ -518,12 +519,12 @@ __device__ __forceinline__ void sort_words(uint64_t* cand, int n, bool in_place,
 
 // Dynamic shared memory: cand[cap] (u64), the upper halves of the slot keys
 // [kSlots][NT] and of the threads' own maxima [kOwn] (u16), and the list of slots
-// above the bound [kPairs] (u16); in clusters, all blocks' lists [blocks][k] (u64).
+// above the bound [row_pairs] (u16); in clusters, all blocks' lists [blocks][k] (u64).
 __host__ __device__ constexpr int row_cap(int k) { return k <= kFewK ? kFewCap : kMaxCap; }
 template <int NT>
 __host__ __device__ constexpr int row_smem(int k, int blocks) {
   return k == 0 ? 0
-                : row_cap(k) * 8 + (kSlots * NT + kOwn) * 2 + kPairs * 2 +
+                : row_cap(k) * 8 + (kSlots * NT + kOwn) * 2 + row_pairs(NT) * 2 +
                       (blocks > 1 ? blocks * k * 8 : 0);
 }
 
@@ -577,7 +578,7 @@ __device__ __forceinline__ int collect(const Slice<T>& sl, uint32_t bound, uint3
       bits |= (uint32_t)!(__uint_as_float((uint32_t)slot_key[i * NT + tid] << 16) < low) << i;
   }
   // listed and read again by their own warp
-  constexpr int kWarpPairs = kPairs / (NT / 32);
+  constexpr int kWarpPairs = row_pairs(NT) / (NT / 32);
   uint16_t* mine = list + (tid >> 5) * kWarpPairs;
   int pairs;
   uint32_t p = lanes_before(__popc(bits), pairs);
@@ -902,7 +903,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprob_rows(LpArgs a) {
   }
   if constexpr (CL) {
     // ---- join the slices: every block fetches all sums and lists
-    uint64_t* all = reinterpret_cast<uint64_t*>(slot_key + kSlots * NT + kOwn + kPairs);
+    uint64_t* all = reinterpret_cast<uint64_t*>(slot_key + kSlots * NT + kOwn + row_pairs(NT));
     if (tid == 0) {
       if (!TOPK) block_state = st;
       block_count = have;
