@@ -243,7 +243,19 @@ int launch_tc_tok(const TcTokArgs& a, int num_sms, cudaStream_t s);
 // the last but one (or an earlier one) wrote, and write what the last but one
 // read, but not of the last.  TC_CHAIN_FIRST begins a chain behind whatever the
 // stream holds; whatever follows the last one waits for all of it.
+// What is complete need not be visible: programmatic launch promises that only
+// behind a launch's own wait, which here comes behind its first item.  So the
+// launches of a chain carry ascending numbers; number `at` stores `at` to *done
+// (release, gpu scope) once its wait has returned, and the next one acquires it
+// before anything else touches global memory (and orders its TMA loads behind
+// that): what the launches before `at` wrote happens before all that `at` + 1
+// does.  *done is 0 before the first of them.
 enum TcChain { TC_CHAIN_NONE = 0, TC_CHAIN_FIRST = 1, TC_CHAIN_NEXT = 2 };
+struct TcLink {
+  int chain;               // TC_CHAIN_*
+  uint32_t at;
+  uint32_t* done;
+};
 
 // Few source rows with an fp32 coefficient each, added to rows of a product:
 // out[o, :] += sum over the entries (q, c) of row o of c src[q, :].  Either one
@@ -272,7 +284,7 @@ struct TcTokGradArgs {
   int64_t ignore;
   const float *stats, *d_lp, *d_ent;
   float* rest;             // [n]: what rounding G to bf16 took from the token's element
-  int chain;               // TC_CHAIN_*
+  TcLink link;
   uint32_t* status;
 };
 int launch_tc_tok_grad(const TcTokGradArgs& a, int num_sms, cudaStream_t s);
@@ -295,7 +307,7 @@ struct TcGemmArgs {
   int k_splits;            // > 1: K0 in that many parts (K1 = 0, TC_OUT_F32), part i's sums
                            // at c32 + i M ldc32
   TcTerms terms;           // added before the result is rounded to bf16
-  int chain;               // TC_CHAIN_*
+  TcLink link;
   uint32_t* status;
 };
 // Parts of K that give every CTA (pair) a tile where the tiles are few: 1 or more.

@@ -1408,7 +1408,7 @@ struct LpPlan {
   size_t f_z, f_h, f_sums, f_count, f_pub, f_cand, f_bytes;
   int bufs;                 // chunk buffers
   int ks;                   // parts of K in dH = G W
-  size_t b_h, b_g, b_dh, b_dw, b_part, b_rest, b_count, b_list, b_bytes;
+  size_t b_h, b_g, b_dh, b_dw, b_part, b_done, b_rest, b_count, b_list, b_bytes;
 };
 
 size_t take(size_t& off, size_t bytes) {
@@ -1529,6 +1529,7 @@ kd_status lp_plan(const kd_logprob_problem* p, LpPlan& P) {
   if (P.bf16) {
     P.ks = tc_gemm_k_splits(std::min(n, P.R), P.d, std::min(P.v, P.C), P.nsm);
     if (P.ks > 1) P.b_part = take(off, (size_t)P.ks * std::min(n, P.R) * P.d * 4);
+    P.b_done = take(off, 4);
     P.b_rest = take(off, (size_t)n * 4);
     P.b_count = take(off, (size_t)P.v * 4);
     P.b_list = take(off, (size_t)P.v * kTermRows * 4);
@@ -1749,9 +1750,12 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
   float* rest = P.bf16 ? at<float>(workspace, P.b_rest) : nullptr;
   int32_t* count = P.bf16 ? at<int32_t>(workspace, P.b_count) : nullptr;
   int32_t* list = P.bf16 ? at<int32_t>(workspace, P.b_list) : nullptr;
-  if (P.bf16 && in->tokens) {  // (count lies behind rest)
-    const size_t bytes = d_w ? P.b_count - P.b_rest + (size_t)v * 4 : (size_t)n * 4;
-    if (cudaMemsetAsync(rest, 0, bytes, s) != cudaSuccess) return KD_ERR_CUDA;
+  uint32_t* done = P.bf16 ? at<uint32_t>(workspace, P.b_done) : nullptr;
+  if (P.bf16) {  // (rest lies behind the chain's word, count behind rest)
+    const size_t bytes = !in->tokens ? 4
+                         : d_w       ? P.b_count - P.b_done + (size_t)v * 4
+                                     : P.b_rest - P.b_done + (size_t)n * 4;
+    if (cudaMemsetAsync(done, 0, bytes, s) != cudaSuccess) return KD_ERR_CUDA;
   }
   if (d_w) {
     note_launch();
@@ -1832,10 +1836,11 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
   // a chain ends where a launch needs the one right before it: between a chunk
   // and its products when nothing is made between them, and at a sum of parts
   bool first = true;
+  uint32_t launches = 0;
   auto link = [&]() {
-    const int c = first ? TC_CHAIN_FIRST : TC_CHAIN_NEXT;
+    const TcLink l{first ? TC_CHAIN_FIRST : TC_CHAIN_NEXT, ++launches, done};
     first = false;
-    return c;
+    return l;
   };
   auto make = [&](const Chunk& k) {
     TcTokGradArgs t;
@@ -1859,7 +1864,7 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
     t.d_lp = d_logprob;
     t.d_ent = d_entropy;
     t.rest = rest;
-    t.chain = link();
+    t.link = link();
     t.status = dev_status;
     return launch_tc_tok_grad(t, P.nsm, s);
   };
@@ -1880,7 +1885,7 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
     t.status = dev_status;
     t.ldc32 = D;
     t.ldc16 = D;
-    t.chain = link();
+    t.link = link();
     const bool last = i + 1 == parts;
     if (!a_mn && P.ks > 1) {  // dH over few rows: K in parts; sum_parts below
       t.k_splits = P.ks;

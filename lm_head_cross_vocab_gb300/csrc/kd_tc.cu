@@ -139,9 +139,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
                : "memory");
 }
-// Arrivals that order no memory: for a barrier that only guards TMEM (its reads
-// are complete after tcgen05.wait::ld).  A releasing arrival would first wait
-// for the thread's global stores, thousands of cycles behind the operands' copies.
+// Arrivals that order no memory: for a barrier that only guards TMEM.  The warp's
+// reads are complete after tcgen05.wait::ld, and tcgen05.fence::before_thread_sync
+// orders them before the arrival, as ::after_thread_sync orders the next MMAs
+// behind the wait for it: the hand-over that the PTX manual gives for tensor
+// memory between threads, with a relaxed arrival.  A releasing one would first
+// wait for the thread's global stores, thousands of cycles behind the operands'
+// copies, which this barrier does not guard.
 __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -312,7 +316,7 @@ struct TcParams {  // (128-byte aligned by its tensor maps)
   int m_band;         // row tiles per band of the item order (see item_range)
   int split_first;    // 1: the splits of a row tile follow one another instead
   int k_splits;       // plain GEMM: parts of its K blocks, an item each (0: one)
-  int chain;          // TC_CHAIN_*
+  TcLink link;        // chain of launches
   int acc_stride;     // TMEM columns per accumulator stage
   int acc_stages;     // 1 or 2 accumulator stages in the 512 allocated columns
   int logits_vec;     // materialised logits rows are 16-byte aligned
@@ -1075,6 +1079,31 @@ __device__ __forceinline__ LpGradArgs tok_grad_args(const TcTokGradArgs& a) {
   return g;
 }
 
+// A chained launch at its start: what all launches before the last one did is
+// visible behind this (to the block, behind a barrier).  The word holds what is
+// asked for by the time a launch can start, so this is one load; the limit is for
+// a launch before it that gave up.
+__device__ __forceinline__ bool chain_enter(const TcLink& l, uint32_t* status) {
+  const uint64_t t0 = globaltimer();
+  for (uint32_t it = 1;; ++it) {
+    uint32_t seen;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(l.done) : "memory");
+    if (seen + 1 >= l.at) return true;
+    if ((it & 63) == 0 && globaltimer() - t0 > kWaitLimitNs) {
+      set_status(status, KD_DEV_TIMEOUT);
+      return false;
+    }
+  }
+}
+// The launch before this one is complete from here on, which one thread of the
+// grid tells the next launch; that may start when every CTA has come here.
+__device__ __forceinline__ void chain_pass(const TcLink& l, int lane) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blockIdx.x == 0 && lane == 0)
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(l.done), "r"(l.at) : "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ------------------------------------------------------------------ kernel
 template <int EPI, int BN, bool HAS_T, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcParams P) {
@@ -1088,6 +1117,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
   const uint32_t bars = base + C::TILE_BYTES;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(gbase + C::TILE_BYTES + 200);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::TILE_BYTES + 208);
+  int* chain_items = reinterpret_cast<int*>(gbase + C::TILE_BYTES + 212);
+  constexpr bool kChained = EPI == EPI_GEMM || EPI == EPI_TOKG;
 
   Sync S;
   S.full = bars;                              // [STAGES]
@@ -1126,6 +1157,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
         prefetch_map(&P.ma[s]);
         prefetch_map(&P.mb[s]);
       }
+    if (kChained)
+      *chain_items =
+          P.link.chain != TC_CHAIN_NEXT || chain_enter(P.link, S.status) ? P.items : 0;
   }
   if (warp == 1) {
     if (PAIR) {  // one warp of each CTA of the pair allocates collectively
@@ -1141,13 +1175,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
   if (PAIR) cluster_sync();  // the peer's barriers and TMEM exist before any remote use
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  const int items = kChained ? *chain_items : P.items;
 
   if (warp == 0) {
     // ---------------------------------------------------------- TMA producer
     int stage = 0;
     uint32_t phase = 0, issued = 0, par = 0;
     bool ok = true;
-    for (int item = cid; ok && item < P.items; item += ncl) {
+    // what was acquired above was written through the generic proxy
+    if (kChained && P.link.chain) asm volatile("fence.proxy.async.global;" ::: "memory");
+    for (int item = cid; ok && item < items; item += ncl) {
       int m_tile, split, t0, t1, kb0 = 0, kb1 = P.kb[0], part = 0, id = item;
       if (EPI == EPI_GEMM && P.k_splits) k_range(P, id, part, kb0, kb1);
       item_range(P, id, m_tile, split, t0, t1);
@@ -1206,7 +1243,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
     bool ok = true;
     Sync Sc = S;
     Sc.cluster_acquire = PAIR;  // the peer's epilogue arrives on acc_empty remotely
-    for (int item = cid; ok && item < P.items; item += ncl) {
+    for (int item = cid; ok && item < items; item += ncl) {
       int m_tile, split, t0, t1, kb0 = 0, kb1 = P.kb[0], part = 0, id = item;
       if (EPI == EPI_GEMM && P.k_splits) k_range(P, id, part, kb0, kb1);
       item_range(P, id, m_tile, split, t0, t1);
@@ -1275,7 +1312,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
     uint32_t acc_phase = 0;
     bool ok = true;
     const int r_in_pair = (int)rank * BM + r_in_tile;  // row within the (pair) tile
-    for (int item = cid; ok && item < P.items; item += ncl) {
+    for (int item = cid; ok && item < items; item += ncl) {
       int m_tile, split, t0, t1, kb0 = 0, kb1 = 0, part = 0, id = item;
       if (EPI == EPI_GEMM && P.k_splits) k_range(P, id, part, kb0, kb1);
       item_range(P, id, m_tile, split, t0, t1);
@@ -1570,15 +1607,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
       // A chained launch may overlap the tail of the one before it, and has to
       // leave that one complete: behind its first item each CTA waits for it,
       // and then lets the next launch in, which so finds all but this one done.
-      if ((EPI == EPI_GEMM || EPI == EPI_TOKG) && P.chain && warp == 2 && item == cid) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        asm volatile("griddepcontrol.launch_dependents;");
-      }
+      if (kChained && P.link.chain && warp == 2 && item == cid) chain_pass(P.link, lane);
       if constexpr (EPI == EPI_TOK || EPI == EPI_TOP) {
         if (ok) te.end(P);
       }
     }
   }
+  // (a CTA that gave up at its start has not waited yet)
+  if (kChained && P.link.chain && warp == 2 && items == 0) chain_pass(P.link, lane);
   tc_fence_before();
   __syncthreads();
   if (PAIR) cluster_sync();  // no CTA leaves while its peer may still touch it
@@ -1670,7 +1706,7 @@ int launch(const TcParams& P, int num_sms, cudaStream_t s) {
   if (max_clusters <= 0) max_clusters = num_sms / 2;
   const int clusters = P.items < max_clusters ? P.items : max_clusters;
   cfg.gridDim = dim3(2 * clusters);
-  if (P.chain == TC_CHAIN_NEXT) cfg.numAttrs = 2;
+  if (P.link.chain == TC_CHAIN_NEXT) cfg.numAttrs = 2;
   note_launch();
   e = cudaLaunchKernelEx(&cfg, kern, P);
   if (e != cudaSuccess) return (int)e;
@@ -1851,7 +1887,7 @@ int launch_tc_tok_grad(const TcTokGradArgs& a, int num_sms, cudaStream_t s) {
   P.items = P.m_tiles * P.n_tiles;
   P.m_band = band_tiles(P, tc_tile_rows(pair));
   P.tokg = a;
-  P.chain = pair ? a.chain : TC_CHAIN_NONE;
+  if (pair) P.link = a.link;
   return pair ? launch<EPI_TOKG, 256, false, true>(P, num_sms, s)
               : launch<EPI_TOKG, 256, false, false>(P, num_sms, s);
 }
@@ -1904,7 +1940,7 @@ int launch_tc_gemm(const TcGemmArgs& a, int num_sms, cudaStream_t s) {
   // a time lies together (151936 x 4096 from 64 terms: 412 us, 473 us with the row
   // tiles of a column first; filling as much memory takes 307 us)
   P.split_first = P.kb[0] + P.kb[1] <= 8 && !P.k_splits;
-  P.chain = pair ? a.chain : TC_CHAIN_NONE;
+  if (pair) P.link = a.link;
   if (a.terms.src)
     return pair ? launch<EPI_GEMM, 256, true, true>(P, num_sms, s)
                 : launch<EPI_GEMM, 256, true, false>(P, num_sms, s);

@@ -797,3 +797,27 @@ def test_two_streams_at_once():
         for x in ("logprob", "entropy", "topk_idx", "topk_logprob", "stats"):
             assert torch.equal(o[x], ref[x]), x
         assert torch.equal(g["d_h"], grad["d_h"]) and torch.equal(g["d_w"], grad["d_w"])
+
+
+@pytest.mark.parametrize("n,v,d", [(2100, 9000, 64), (700, 30000, 264), (5000, 5003, 136)])
+def test_hidden_backward_by_turns_on_two_sets_of_inputs(n, v, d):
+    """Call after call through one workspace, the inputs changing each time: a
+    value of the chunk or the call before, read in place of this one's, would
+    show.  The same bits as each set's first call."""
+    ws, sides = kd.Workspace(), []
+    for seed in (1, 2):
+        h, w = (x.cuda() for x in _hidden(n, v, d, "bf16", seed))
+        tens = {"h": h, "w": w, "tokens": _tokens(n, v, seed).cuda()}
+        p = kd.LogprobProblem(n_tokens=n, vocab=v, d_model=d, source="hidden")
+        stats = kd.token_logprobs(p, tens)["stats"]
+        up = torch.linspace(-seed, seed, n, device="cuda")
+        ref = kd.token_logprobs_backward(p, tens, stats, d_logprob=up, workspace=ws)
+        sides.append((p, tens, stats, up, ref))
+    got = []
+    for _ in range(8):
+        for p, tens, stats, up, ref in sides:
+            got.append((ref, kd.token_logprobs_backward(p, tens, stats, d_logprob=up, workspace=ws,
+                                                        check=False)))
+    for ref, r in got:
+        assert torch.equal(r["d_h"], ref["d_h"]) and torch.equal(r["d_w"], ref["d_w"])
+        assert int(r["dev_status"].item()) == 0
