@@ -305,7 +305,7 @@ struct TcGemmArgs {
   __nv_bfloat16* c16;      // bf16 output [M, ldc16]
   int64_t ldc16;
   int k_splits;            // > 1: K0 in that many parts (K1 = 0, TC_OUT_F32), part i's sums
-                           // at c32 + i M ldc32
+                           // at c32 + i M ldc32; at most one for each 64 terms of K0
   TcTerms terms;           // added before the result is rounded to bf16
   TcLink link;
   uint32_t* status;

@@ -1407,7 +1407,7 @@ struct LpPlan {
   int64_t R, C;             // backward: chunk of G
   size_t f_z, f_h, f_sums, f_count, f_pub, f_cand, f_bytes;
   int bufs;                 // chunk buffers
-  int ks;                   // parts of K in dH = G W
+  int ks;                   // parts of K in dH = G W, at most
   size_t b_h, b_g, b_dh, b_dw, b_part, b_done, b_rest, b_count, b_list, b_bytes;
 };
 
@@ -1868,6 +1868,9 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
     t.status = dev_status;
     return launch_tc_tok_grad(t, P.nsm, s);
   };
+  // parts of K in dH = G W over a chunk's columns: a narrow last chunk may have
+  // fewer blocks than whole chunks have parts, and a part needs one
+  auto k_parts = [&](const Chunk& k) { return (int)std::min<int64_t>(P.ks, cdiv(k.cc, 64)); };
   // C[m, D] (+)= A B over chunk part i of `parts`
   auto product = [&](const Chunk& k, const __nv_bfloat16* b, int64_t m, int64_t kk, bool a_mn,
                      float* acc, __nv_bfloat16* out, int64_t i, int64_t parts) {
@@ -1888,7 +1891,7 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
     t.link = link();
     const bool last = i + 1 == parts;
     if (!a_mn && P.ks > 1) {  // dH over few rows: K in parts; sum_parts below
-      t.k_splits = P.ks;
+      t.k_splits = k_parts(k);
       t.mode = TC_OUT_F32;
       t.c32 = at<float>(workspace, P.b_part);
       return launch_tc_gemm(t, P.nsm, s);
@@ -1907,7 +1910,7 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
     const bool last = k.ci + 1 == nc;
     note_launch();
     k_sum_parts<<<(unsigned)cdiv(vecs, kRowThreads), kRowThreads, 0, s>>>(
-        at<float4>(workspace, P.b_part), vecs, P.ks, D, terms(k, false, last),
+        at<float4>(workspace, P.b_part), vecs, k_parts(k), D, terms(k, false, last),
         k.ci > 0 ? reinterpret_cast<const float4*>(acc) : nullptr,
         last ? nullptr : reinterpret_cast<float4*>(acc),
         last ? reinterpret_cast<uint2*>(out) : nullptr);

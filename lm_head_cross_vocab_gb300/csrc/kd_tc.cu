@@ -1933,6 +1933,8 @@ int launch_tc_gemm(const TcGemmArgs& a, int num_sms, cudaStream_t s) {
   P.n_tiles = (int)((a.N + bn - 1) / bn);
   P.n_splits = P.n_tiles;
   P.k_splits = a.k_splits > 1 ? a.k_splits : 0;
+  // (a part without terms would leave its sums as the accumulator happens to be)
+  if (P.k_splits > P.kb[0] || (P.k_splits && P.kb[1])) return (int)cudaErrorInvalidValue;
   P.items = P.m_tiles * P.n_tiles * (P.k_splits ? P.k_splits : 1);
   P.m_band = band_tiles(P, tc_tile_rows(pair));
   P.gemm = a;

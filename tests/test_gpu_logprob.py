@@ -821,3 +821,45 @@ def test_hidden_backward_by_turns_on_two_sets_of_inputs(n, v, d):
     for ref, r in got:
         assert torch.equal(r["d_h"], ref["d_h"]) and torch.equal(r["d_w"], ref["d_w"])
         assert int(r["dev_status"].item()) == 0
+
+
+def _hidden_grads_close(n, v, d, want, seed, calls=1):
+    """The bf16 hidden backward against the formula in fp64 (torch, on the same
+    device), with the bound of test_hidden_backward; every call the same bits."""
+    h, w = (x.cuda() for x in _hidden(n, v, d, "bf16", seed))
+    y = _tokens(n, v, seed).cuda()
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, d_model=d, source="hidden")
+    tens = {"h": h, "w": w, "tokens": y}
+    out = kd.token_logprobs(p, tens)
+    g = torch.Generator().manual_seed(v)
+    gl, gh = (torch.randn(n, generator=g).cuda(), torch.randn(n, generator=g).cuda() * 0.3)
+    lp = torch.log_softmax(h.double() @ w.double().t(), dim=1)
+    pr, on = lp.exp(), (y != IGN)[:, None]
+    ent = -(pr * lp).sum(dim=1, keepdim=True)
+    a, b = gl.double()[:, None], gh.double()[:, None]
+    gz = -pr * (a + b * (lp + ent))
+    tol = pr * ((a.abs() + b.abs() * (lp.abs() + math.log(v) + 1)) * 200 * U
+                + b.abs() * _e_s(v) * (math.log(v) + 3))
+    gz[torch.arange(n), y.clamp(min=0)] += a[:, 0]
+    gz, tol = torch.where(on, gz, 0.0), torch.where(on, tol, 0.0)
+    tol = tol + 2.0 ** -8 * (gz.abs() + tol) + 4 * U * a.abs() * on
+    ws = kd.Workspace()
+    kept = [kd.token_logprobs_backward(p, tens, out["stats"], d_logprob=gl, d_entropy=gh,
+                                       want=want, workspace=ws) for _ in range(calls)]
+    for name, x, xt, m in (("d_h", gz, tol, w.double()), ("d_w", gz.t(), tol.t(), h.double())):
+        if name[2:] not in want:
+            continue
+        ref = x @ m
+        off = xt @ m.abs() + 2 * U * x.shape[1] * ((x.abs() + xt) @ m.abs())
+        off = off + 2.0 ** -8 * (ref.abs() + off) + TINY
+        assert ((kept[0][name].double() - ref).abs() <= off).all(), name
+        assert all(torch.equal(kept[0][name], r[name]) for r in kept[1:])
+
+
+# On 152 SMs the products of a whole chunk take 2, 12, 2, 2 and 3 parts of K; the
+# last chunk has 13, 428, 40, 20 and 17 columns, 1, 7, 1, 1 and 1 blocks of 64.
+@pytest.mark.parametrize("n,v,d", [(1813, 5133, 96), (8, 399788, 272), (3439, 5160, 144),
+                                   (2629, 5140, 456), (1287, 7697, 680)])
+@pytest.mark.parametrize("want", [("h", "w"), ("h",)])
+def test_hidden_backward_with_a_narrow_last_chunk(n, v, d, want):
+    _hidden_grads_close(n, v, d, want, n + v, calls=2)
