@@ -373,7 +373,7 @@ kd_status kd_logprob_fwd(const kd_logprob_problem* problem, const kd_logprob_inp
  *   d_logits [N, V] rows of pitch ld_d_logits (logits source; elements
  *            between the rows are left as they are; it may be the logits
  *            themselves when both pitches are equal)
- *   d_h [N, D], d_w [V, D]    (hidden source)
+ *   d_h [N, D], d_w [V, D]    (hidden source; bf16: 16-byte aligned)
  * A bad token contributes no d_logprob term.  bf16 hidden problems round d z
  * to bf16 (at most 2^-8 of each element) before the products with W and H,
  * whose sums are fp32; what that takes from a row's element v = y goes into

@@ -1555,6 +1555,9 @@ kd_status lp_inputs(const LpPlan& P, const kd_logprob_inputs* in) {
   return KD_OK;
 }
 
+// bf16: rows are stored in 16-byte vectors
+bool grad_ok(const LpPlan& P, const void* g) { return !P.bf16 || aligned16(g); }
+
 bool ws_ok(const void* ws, size_t have, size_t need) {
   return need == 0 || (ws && have >= need && reinterpret_cast<uintptr_t>(ws) % kAlign == 0);
 }
@@ -1704,6 +1707,7 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
   if (P.hidden ? d_logits != nullptr : (d_h || d_w)) return KD_ERR_INVALID_ARG;
   if (P.n > 0 && (!stats || !aligned16(stats) || (d_logprob && !in->tokens)))
     return KD_ERR_INVALID_ARG;
+  if (P.n > 0 && (!grad_ok(P, d_h) || !grad_ok(P, d_w))) return KD_ERR_UNSUPPORTED;
   if (!ws_ok(workspace, ws_bytes, P.b_bytes)) return KD_ERR_WORKSPACE;
   st = lp_device();
   if (st != KD_OK) return st;

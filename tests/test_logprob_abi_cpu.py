@@ -165,3 +165,26 @@ def test_binding_refuses_wrong_tensors(kd):
         kd.GradList([])
     with pytest.raises(ValueError):
         kd.GradList([torch.zeros(3)])
+
+
+def test_unaligned_hidden_gradients_are_refused(kd):
+    """bf16 gradients are stored in 16-byte vectors: a buffer at another address,
+    a view behind a tensor of odd length for example, is refused before anything
+    is launched.  fp32 ones take any element's address, and without tokens d_w is
+    only cleared."""
+    lib = kd.load_library()
+    ins = kd.kd_logprob_inputs(h=FAKE, w=FAKE, tokens=FAKE)
+
+    def bwd(p, dh, dw):
+        return lib.kd_logprob_bwd(ctypes.byref(p), ctypes.byref(ins), FAKE, None, None, dh, dw,
+                                  None, None, None, 0, None)
+
+    p = _prob(kd, source="hidden")
+    for off in (2, 4, 8, 14):
+        assert bwd(p, 2 * FAKE + off, None) == kd.KD_ERR_UNSUPPORTED
+        assert bwd(p, None, 3 * FAKE + off) == kd.KD_ERR_UNSUPPORTED
+        assert bwd(p, 2 * FAKE, 3 * FAKE + off) == kd.KD_ERR_UNSUPPORTED
+    assert bwd(p, 2 * FAKE + 16, 3 * FAKE + 32) == kd.KD_ERR_WORKSPACE  # and no further
+    for kw in (dict(dtype="fp32"), dict(n_tokens=0)):
+        p = _prob(kd, source="hidden", **kw)
+        assert bwd(p, 2 * FAKE + 4, 3 * FAKE + 8) == kd.KD_ERR_WORKSPACE
