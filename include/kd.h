@@ -206,7 +206,9 @@ kd_status kd_fwd(const kd_problem* problem, const kd_inputs* inputs, float* ce_s
  *              "Teacher descriptors", tied teachers share the weight)
  *   d_logits_s [N, V]   d loss / d z_s      (logit students)
  * The teacher is detached from every KL variant (orda-kernel README, "KL
- * variants").  Ignored tokens get exactly zero gradient rows. */
+ * variants").  Ignored tokens get exactly zero gradient rows.
+ * bf16 gradients of hidden states and weights, kd_bwd_grads' among them, are
+ * 16-byte aligned (KD_ERR_UNSUPPORTED otherwise). */
 kd_status kd_bwd(const kd_problem* problem, const kd_inputs* inputs, const float* stats,
                  const float* d_loss, float grad_scale, void* d_h_s, void* d_w_s,
                  void* d_logits_s, uint32_t* dev_status, void* workspace, size_t ws_bytes,

@@ -730,6 +730,11 @@ static kd_status bwd_impl(const kd_problem* problem, const kd_inputs* in, const 
   // no tokens (or a teacher CE weight of 0): the weight / teacher gradients
   // are zero, written as such
   const bool no_tce = p->w_teacher_ce == 0.f;
+  // the tensor-core products store their rows in 16-byte vectors
+  if (P.path == PATH_TC && P.n > 0 &&
+      (!aligned16(d_h_s) || !aligned16(d_w_s) ||
+       (!no_tce && (!aligned16(d_h_t) || !aligned16(d_w_t)))))
+    return KD_ERR_UNSUPPORTED;
   if (P.n == 0 || (no_tce && (d_h_t || d_w_t))) {
     st = check_device();
     if (st != KD_OK) return st;

@@ -231,3 +231,25 @@ def test_teacher_grads_argument_rules(kd):
                             None, None, 0, None) == kd.KD_ERR_INVALID_ARG
     # well-formed requests get as far as the workspace / device checks
     assert call(d_h_t=1, d_w_t=1) in (kd.KD_ERR_WORKSPACE, kd.KD_ERR_NO_DEVICE)
+
+
+@pytest.mark.parametrize("name", ["d_h_s", "d_w_s", "d_h_t", "d_w_t"])
+def test_unaligned_hidden_gradients_are_refused(kd, name):
+    """The tensor-core products store bf16 gradients in 16-byte vectors: a buffer
+    at another address is refused before anything is launched.  fp32 ones take
+    any element's address."""
+    lib = kd.load_library()
+    fake = 1 << 20
+    ins = kd.kd_inputs(h_s=fake, w_s=fake, h_t=fake, w_t=fake, labels=fake)
+
+    def call(off, dtype="bf16"):
+        p = _prob(kd, teacher="separate", d_teacher=64, w_teacher_ce=0.5, dtype=dtype)
+        p.teacher_grads = 1
+        grads = kd.kd_grads(**{name: 2 * fake + off})
+        return lib.kd_bwd_grads(ctypes.byref(p), ctypes.byref(ins), fake, None, 1.0,
+                                ctypes.byref(grads), None, None, 0, None)
+
+    for off in (2, 4, 8, 14):
+        assert call(off) == kd.KD_ERR_UNSUPPORTED
+    assert call(16) == kd.KD_ERR_WORKSPACE  # and no further
+    assert call(4, "fp32") == kd.KD_ERR_WORKSPACE
