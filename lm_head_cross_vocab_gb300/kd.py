@@ -656,10 +656,11 @@ def token_logprobs(problem: LogprobProblem, tensors: dict, workspace: Optional[W
             _dense("topk_logprob", out.get("topk_logprob"), (n, k), f32, dev),
             _dense("stats", out.get("stats"), (n, KD_LOGPROB_STATS), f32, dev))
     cp = problem.to_c(ld)
+    ws = workspace or Workspace()  # (one made here is held until the call has returned)
     with _on(dev) as stream:
         wptr, wbytes = None, 0
         if problem.source == "hidden":  # (rows of logits need no workspace)
-            wptr, wbytes = (workspace or Workspace()).get(kd_logprob_workspace_size(cp)[0], dev)
+            wptr, wbytes = ws.get(kd_logprob_workspace_size(cp)[0], dev)
         st = load_library().kd_logprob_fwd(ctypes.byref(cp), ctypes.byref(ins), *ptrs,
                                            out["dev_status"].data_ptr(), wptr, wbytes, stream)
     if st != KD_OK:
@@ -692,10 +693,11 @@ def token_logprobs_backward(problem: LogprobProblem, tensors: dict, stats: torch
         ldg = _rows_pitch("d_logits", out["d_logits"], (n, v), dtype, dev)
         pz = out["d_logits"].data_ptr()
     cp = problem.to_c(ld, ldg)
+    ws = workspace or Workspace()
     with _on(dev) as stream:
         wptr, wbytes = None, 0
         if problem.source == "hidden":
-            wptr, wbytes = (workspace or Workspace()).get(kd_logprob_workspace_size(cp)[1], dev)
+            wptr, wbytes = ws.get(kd_logprob_workspace_size(cp)[1], dev)
         st = load_library().kd_logprob_bwd(
             ctypes.byref(cp), ctypes.byref(ins),
             _dense("stats", stats, (n, KD_LOGPROB_STATS), f32, dev),
@@ -754,8 +756,9 @@ def clip_grad_norm(grads, max_norm: float, *, out=None, workspace: Optional[Work
     gl = grads if isinstance(grads, GradList) else GradList(grads, out)
     dev = gl.device
     norm = torch.empty((), device=dev, dtype=torch.float32)
+    ws = workspace or Workspace()
     with _on(dev) as stream:
-        wptr, wbytes = (workspace or Workspace()).get(gl._bytes, dev)
+        wptr, wbytes = ws.get(gl._bytes, dev)
         st = load_library().kd_clip_grad_norm(gl._grads, gl._outs, gl._numel, len(gl.grads),
                                               gl.dtype, float(max_norm), norm.data_ptr(),
                                               gl.dev_status.data_ptr(), wptr, wbytes, stream)

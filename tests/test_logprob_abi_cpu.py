@@ -188,3 +188,74 @@ def test_unaligned_hidden_gradients_are_refused(kd):
     for kw in (dict(dtype="fp32"), dict(n_tokens=0)):
         p = _prob(kd, source="hidden", **kw)
         assert bwd(p, 2 * FAKE + 4, 3 * FAKE + 8) == kd.KD_ERR_WORKSPACE
+
+
+class _Fake:
+    """Stands in for the library: no kernel runs, what a call is given is kept."""
+
+    def __init__(self, kd, monkeypatch):
+        import contextlib
+        import weakref
+        self.alive, self.status, self.seen = [], 0, []
+        made = []
+
+        class Tracked(kd.Workspace):
+            def __init__(self):
+                super().__init__()
+                made.append(weakref.ref(self))
+
+        def call(*args):
+            self.alive.append(bool(made) and made[-1]() is not None)
+            word = next(a for a in args if isinstance(a, int) and a in self.words)
+            self.seen.append(word)
+            if self.status:
+                ctypes.c_int32.from_address(word).value |= self.status
+            return kd.KD_OK
+
+        self.words = set()
+        zeros = kd.torch.zeros
+
+        def status_word(*a, **kw):
+            t = zeros(*a, **kw)
+            if t.dtype == kd.torch.int32 and t.dim() == 0:
+                self.words.add(t.data_ptr())
+            return t
+
+        monkeypatch.setattr(kd, "Workspace", Tracked)
+        monkeypatch.setattr(kd, "load_library", lambda: self)
+        monkeypatch.setattr(kd, "kd_logprob_workspace_size", lambda p: (1000, 1000))
+        monkeypatch.setattr(kd, "_on", lambda dev: contextlib.nullcontext(0))
+        monkeypatch.setattr(kd.torch, "zeros", status_word)
+        self.kd_logprob_fwd = self.kd_logprob_bwd = self.kd_clip_grad_norm = call
+        self.kd_clip_grad_norm_workspace_size = lambda *a: kd.KD_OK
+        self.kd_status_string = lambda s: b"status"
+
+
+def _as_cuda(t):
+    """A tensor here that says it is on a GPU."""
+    import torch
+
+    class Device(torch.Tensor):
+        is_cuda = True
+
+    return t.as_subclass(Device)
+
+
+def _hidden_call(kd, n=4, v=50, d=8):
+    import torch
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, d_model=d, source="hidden")
+    bf = torch.bfloat16
+    return p, {"h": _as_cuda(torch.zeros(n, d, dtype=bf)), "w": torch.zeros(v, d, dtype=bf),
+               "tokens": torch.zeros(n, dtype=torch.int64)}
+
+
+def test_a_calls_own_workspace_lives_until_it_returns(kd, monkeypatch):
+    """Without a workspace of the caller's: the one made for the call is still
+    held while the library enqueues its kernels."""
+    import torch
+    fake = _Fake(kd, monkeypatch)
+    p, tens = _hidden_call(kd)
+    out = kd.token_logprobs(p, tens)
+    kd.token_logprobs_backward(p, tens, out["stats"])
+    kd.clip_grad_norm([_as_cuda(torch.zeros(5))], 1.0)
+    assert fake.alive == [True, True, True]
