@@ -626,6 +626,16 @@ def _logprob_inputs(problem: LogprobProblem, tensors: dict):
     return ins, dev, ld
 
 
+def _check_and_tell(dev_status: torch.Tensor):
+    """check_status of a word that later calls use again: what is raised is
+    cleared.  (A call that is not checked only adds its bits.)"""
+    try:
+        check_status(dev_status)
+    except KDError:
+        dev_status.zero_()
+        raise
+
+
 def token_logprobs(problem: LogprobProblem, tensors: dict, workspace: Optional[Workspace] = None,
                    check: bool = True, out: Optional[dict] = None, save_stats: bool = True):
     """Run kd_logprob_fwd; returns dict(logprob, entropy, topk_idx, topk_logprob,
@@ -636,7 +646,8 @@ def token_logprobs(problem: LogprobProblem, tensors: dict, workspace: Optional[W
     row takes part and ``logprob`` is None.  ``topk_idx`` / ``topk_logprob``
     are None with topk = 0, ``stats`` with save_stats=False (no backward).
     ``out``: a dict this function returned for the same problem, to be written
-    again.  ``exp(topk_logprob)`` and ``topk_idx`` are a cached top-K teacher of
+    again; its dev_status collects the status bits of its calls until one that
+    checks raises them, or the caller zeroes it.  ``exp(topk_logprob)`` and ``topk_idx`` are a cached top-K teacher of
     ``Problem(teacher="topk")``."""
     ins, dev, ld = _logprob_inputs(problem, tensors)
     n, k, f32 = problem.n_tokens, problem.topk, torch.float32
@@ -666,7 +677,7 @@ def token_logprobs(problem: LogprobProblem, tensors: dict, workspace: Optional[W
     if st != KD_OK:
         raise KDError(st, "kd_logprob_fwd")
     if check:
-        check_status(out["dev_status"])
+        _check_and_tell(out["dev_status"])
     return out
 
 
@@ -679,7 +690,8 @@ def token_logprobs_backward(problem: LogprobProblem, tensors: dict, stats: torch
 
     ``stats`` is token_logprobs' on the same inputs; d_logprob and d_entropy
     are fp32 [N] (None: zero).  ``out`` may bring the gradients' own buffers,
-    for example d_logits over the logits themselves."""
+    for example d_logits over the logits themselves; its dev_status is as
+    token_logprobs'."""
     ins, dev, ld = _logprob_inputs(problem, tensors)
     n, v, d, f32 = problem.n_tokens, problem.vocab, problem.d_model, torch.float32
     dtype = _TORCH_DTYPES[problem.dtype]
@@ -709,7 +721,7 @@ def token_logprobs_backward(problem: LogprobProblem, tensors: dict, stats: torch
     if st != KD_OK:
         raise KDError(st, "kd_logprob_bwd")
     if check:
-        check_status(out["dev_status"])
+        _check_and_tell(out["dev_status"])
     return out
 
 
@@ -765,9 +777,5 @@ def clip_grad_norm(grads, max_norm: float, *, out=None, workspace: Optional[Work
     if st != KD_OK:
         raise KDError(st, "kd_clip_grad_norm")
     if check:
-        try:
-            check_status(gl.dev_status)
-        except KDError:
-            gl.dev_status.zero_()  # told
-            raise
+        _check_and_tell(gl.dev_status)
     return {"norm": norm, "grads": gl.out, "dev_status": gl.dev_status}

@@ -863,3 +863,27 @@ def _hidden_grads_close(n, v, d, want, seed, calls=1):
 @pytest.mark.parametrize("want", [("h", "w"), ("h",)])
 def test_hidden_backward_with_a_narrow_last_chunk(n, v, d, want):
     _hidden_grads_close(n, v, d, want, n + v, calls=2)
+
+
+def test_a_reused_out_after_a_bad_token():
+    """An error that was raised is told: the next call with the same dict of
+    outputs and good tokens passes, in both directions."""
+    n, v = 6, 500
+    z, y = _logits(n, v, "fp32", 2).cuda(), torch.arange(n, device="cuda")
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, dtype="fp32")
+    good, bad = {"logits": z, "tokens": y}, {"logits": z, "tokens": y + v}
+    out = kd.token_logprobs(p, good)
+    up = torch.ones(n, device="cuda")
+    grad = kd.token_logprobs_backward(p, good, out["stats"], d_logprob=up)
+    ref = out["logprob"].clone(), grad["d_logits"].clone()
+    with pytest.raises(kd.KDError):
+        kd.token_logprobs(p, bad, out=out)
+    assert torch.equal(kd.token_logprobs(p, good, out=out)["logprob"], ref[0])
+    with pytest.raises(kd.KDError):
+        kd.token_logprobs_backward(p, bad, out["stats"], d_logprob=up, out=grad)
+    r = kd.token_logprobs_backward(p, good, out["stats"], d_logprob=up, out=grad)
+    assert torch.equal(r["d_logits"], ref[1])
+    # without a check the bits stay for the caller
+    kd.token_logprobs(p, bad, out=out, check=False)
+    assert int(kd.token_logprobs(p, good, out=out, check=False)["dev_status"].item()) \
+        == kd.KD_DEV_BAD_LABEL

@@ -259,3 +259,28 @@ def test_a_calls_own_workspace_lives_until_it_returns(kd, monkeypatch):
     kd.token_logprobs_backward(p, tens, out["stats"])
     kd.clip_grad_norm([_as_cuda(torch.zeros(5))], 1.0)
     assert fake.alive == [True, True, True]
+
+
+def test_an_error_is_told_once(kd, monkeypatch):
+    """A dict of outputs that is used again: the status of a call that raised is
+    told, and the next call without an error passes."""
+    fake = _Fake(kd, monkeypatch)
+    p, tens = _hidden_call(kd)
+    out = kd.token_logprobs(p, tens)
+    grad = kd.token_logprobs_backward(p, tens, out["stats"])
+    for call in (lambda **kw: kd.token_logprobs(p, tens, out=out, **kw),
+                 lambda **kw: kd.token_logprobs_backward(p, tens, out["stats"], out=grad, **kw)):
+        fake.status = kd.KD_DEV_BAD_LABEL
+        with pytest.raises(kd.KDError) as e:
+            call()
+        assert e.value.status == kd.KD_ERR_BAD_LABEL
+        fake.status = 0
+        call()
+        # without a check the bits stay, for the caller to read and to clear
+        fake.status = kd.KD_DEV_BAD_LABEL
+        call(check=False)
+        fake.status = 0
+        assert int(call(check=False)["dev_status"]) == kd.KD_DEV_BAD_LABEL
+        with pytest.raises(kd.KDError):
+            call()
+        call()
