@@ -626,6 +626,17 @@ def _logprob_inputs(problem: LogprobProblem, tensors: dict):
     return ins, dev, ld
 
 
+def _status_word(out: dict, device) -> int:
+    """The status word of a dict of outputs; a new one where it has none."""
+    w = out.get("dev_status")
+    if w is None:
+        w = out["dev_status"] = torch.zeros((), device=device, dtype=torch.int32)
+    if w.numel() != 1 or w.dtype != torch.int32 or w.device != device:
+        raise ValueError(f"dev_status: expected one torch.int32 on {device}, "
+                         f"got {tuple(w.shape)} {w.dtype} on {w.device}")
+    return w.data_ptr()
+
+
 def _check_and_tell(dev_status: torch.Tensor):
     """check_status of a word that later calls use again: what is raised is
     cleared.  (A call that is not checked only adds its bits.)"""
@@ -646,8 +657,10 @@ def token_logprobs(problem: LogprobProblem, tensors: dict, workspace: Optional[W
     row takes part and ``logprob`` is None.  ``topk_idx`` / ``topk_logprob``
     are None with topk = 0, ``stats`` with save_stats=False (no backward).
     ``out``: a dict this function returned for the same problem, to be written
-    again; its dev_status collects the status bits of its calls until one that
-    checks raises them, or the caller zeroes it.  ``exp(topk_logprob)`` and ``topk_idx`` are a cached top-K teacher of
+    again, or one with the caller's own (what it lacks is left out).  Its
+    dev_status (made where there is none) collects the status bits of its calls
+    until one that checks raises them, or the caller zeroes it.
+    ``exp(topk_logprob)`` and ``topk_idx`` are a cached top-K teacher of
     ``Problem(teacher="topk")``."""
     ins, dev, ld = _logprob_inputs(problem, tensors)
     n, k, f32 = problem.n_tokens, problem.topk, torch.float32
@@ -659,21 +672,21 @@ def token_logprobs(problem: LogprobProblem, tensors: dict, workspace: Optional[W
             "topk_logprob": torch.empty(n, k, device=dev, dtype=f32) if k else None,
             "stats": (torch.empty(n, KD_LOGPROB_STATS, device=dev, dtype=f32)
                       if save_stats else None),
-            "dev_status": torch.zeros((), device=dev, dtype=torch.int32),
         }
     ptrs = (_dense("logprob", out.get("logprob"), (n,), f32, dev),
             _dense("entropy", out.get("entropy"), (n,), f32, dev),
             _dense("topk_idx", out.get("topk_idx"), (n, k), torch.int32, dev),
             _dense("topk_logprob", out.get("topk_logprob"), (n, k), f32, dev),
-            _dense("stats", out.get("stats"), (n, KD_LOGPROB_STATS), f32, dev))
+            _dense("stats", out.get("stats"), (n, KD_LOGPROB_STATS), f32, dev),
+            _status_word(out, dev))
     cp = problem.to_c(ld)
     ws = workspace or Workspace()  # (one made here is held until the call has returned)
     with _on(dev) as stream:
         wptr, wbytes = None, 0
         if problem.source == "hidden":  # (rows of logits need no workspace)
             wptr, wbytes = ws.get(kd_logprob_workspace_size(cp)[0], dev)
-        st = load_library().kd_logprob_fwd(ctypes.byref(cp), ctypes.byref(ins), *ptrs,
-                                           out["dev_status"].data_ptr(), wptr, wbytes, stream)
+        st = load_library().kd_logprob_fwd(ctypes.byref(cp), ctypes.byref(ins), *ptrs, wptr,
+                                           wbytes, stream)
     if st != KD_OK:
         raise KDError(st, "kd_logprob_fwd")
     if check:
@@ -696,7 +709,7 @@ def token_logprobs_backward(problem: LogprobProblem, tensors: dict, stats: torch
     n, v, d, f32 = problem.n_tokens, problem.vocab, problem.d_model, torch.float32
     dtype = _TORCH_DTYPES[problem.dtype]
     if out is None:
-        out = {"dev_status": torch.zeros((), device=dev, dtype=torch.int32)}
+        out = {}
         for name in ("h", "w") if problem.source == "hidden" else ("logits",):
             if name in want:
                 out["d_" + name] = torch.empty(tensors[name].shape, device=dev, dtype=dtype)
@@ -717,7 +730,7 @@ def token_logprobs_backward(problem: LogprobProblem, tensors: dict, stats: torch
             _dense("d_entropy", d_entropy, (n,), f32, dev),
             _dense("d_h", out.get("d_h"), (n, d), dtype, dev),
             _dense("d_w", out.get("d_w"), (v, d), dtype, dev), pz,
-            out["dev_status"].data_ptr(), wptr, wbytes, stream)
+            _status_word(out, dev), wptr, wbytes, stream)
     if st != KD_OK:
         raise KDError(st, "kd_logprob_bwd")
     if check:

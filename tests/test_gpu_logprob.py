@@ -887,3 +887,27 @@ def test_a_reused_out_after_a_bad_token():
     kd.token_logprobs(p, bad, out=out, check=False)
     assert int(kd.token_logprobs(p, good, out=out, check=False)["dev_status"].item()) \
         == kd.KD_DEV_BAD_LABEL
+
+
+def test_out_with_the_gradients_alone():
+    """``out`` may bring the gradients and no status word: over the logits, and
+    a head's gradients into a caller's buffers."""
+    n, v, d = 30, 700, 64
+    z, y = _logits(n, v, "bf16", 8).cuda(), _tokens(n, v, 8).cuda()
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, topk=3)
+    out = kd.token_logprobs(p, {"logits": z, "tokens": y})
+    up = torch.linspace(-1, 1, n, device="cuda")
+    ref = kd.token_logprobs_backward(p, {"logits": z, "tokens": y}, out["stats"], d_logprob=up)
+    r = kd.token_logprobs_backward(p, {"logits": z, "tokens": y}, out["stats"], d_logprob=up,
+                                   out={"d_logits": z})
+    assert torch.equal(z, ref["d_logits"]) and int(r["dev_status"].item()) == 0
+    h, w = (x.cuda() for x in _hidden(n, v, d, "bf16", 8))
+    q = kd.LogprobProblem(n_tokens=n, vocab=v, d_model=d, source="hidden")
+    tens = {"h": h, "w": w, "tokens": y}
+    r = kd.token_logprobs(q, tens, out={"logprob": torch.empty(n, device="cuda"),
+                                        "stats": torch.empty(n, 4, device="cuda")})
+    assert int(r["dev_status"].item()) == 0
+    ref = kd.token_logprobs_backward(q, tens, r["stats"], d_logprob=up)
+    g = kd.token_logprobs_backward(q, tens, r["stats"], d_logprob=up,
+                                   out={"d_w": torch.empty_like(w)})
+    assert torch.equal(g["d_w"], ref["d_w"])

@@ -284,3 +284,25 @@ def test_an_error_is_told_once(kd, monkeypatch):
         with pytest.raises(kd.KDError):
             call()
         call()
+
+
+def test_out_needs_no_status_word_and_refuses_a_wrong_one(kd, monkeypatch):
+    """``out`` may bring the gradients alone; a status word that a kernel could
+    not write to is refused before the library is called."""
+    import torch
+    fake = _Fake(kd, monkeypatch)
+    p, tens = _hidden_call(kd)
+    stats = torch.zeros(4, 4)
+    d_w = torch.zeros(50, 8, dtype=torch.bfloat16)
+    r = kd.token_logprobs_backward(p, tens, stats, out={"d_w": d_w})
+    assert r["d_w"] is d_w and int(r["dev_status"]) == 0
+    assert int(kd.token_logprobs(p, tens, out={"logprob": torch.zeros(4)})["dev_status"]) == 0
+    calls = len(fake.seen)
+    assert calls == 2
+    for word in (torch.zeros((), dtype=torch.int64), torch.zeros(2, dtype=torch.int32),
+                 torch.zeros((), dtype=torch.int32, device="meta")):
+        with pytest.raises(ValueError):
+            kd.token_logprobs_backward(p, tens, stats, out={"d_w": d_w, "dev_status": word})
+        with pytest.raises(ValueError):
+            kd.token_logprobs(p, tens, out={"logprob": torch.zeros(4), "dev_status": word})
+    assert len(fake.seen) == calls
