@@ -173,7 +173,16 @@ __global__ void __launch_bounds__(kThreads, 4)
     if (!finite) set_status(status, KD_DEV_NONFINITE);
   }
   const bool clip = finite && norm > (double)max_norm;
-  const float coef = clip ? (float)((double)max_norm / norm) : 1.f;
+  const double ratio = clip ? (double)max_norm / norm : 1.0;
+  float coef = (float)ratio, post = 1.f;
+  // below fp32's normal numbers, where it would lose its bits: in two factors, the
+  // second a power of two; the first is at most 1, and its product with an element
+  // no smaller than the result
+  const bool small = coef < 0x1p-126f;
+  if (small) {
+    post = ratio >= 0x1p-226 ? 0x1p-100f : 0x1p-149f;
+    coef = (float)(ratio * (ratio >= 0x1p-226 ? 0x1p100 : 0x1p149));
+  }
   const uint32_t chunks = tab.first[tab.n];
   for (uint32_t b = blockIdx.x; b < chunks; b += gridDim.x) {
     const uint32_t c = chunks - 1 - b;
@@ -203,6 +212,10 @@ __global__ void __launch_bounds__(kThreads, 4)
             unpack(w[u], v, T());
 #pragma unroll
             for (int e = 0; e < N; ++e) v[e] *= coef;
+            if (small) {
+#pragma unroll
+              for (int e = 0; e < N; ++e) v[e] *= post;
+            }
             w[u] = pack(v, T());
           }
           __stcs(&o[j + u * kThreads], w[u]);
@@ -211,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
     for (int i = i0 + threadIdx.x; i < n; i += kThreads) {
       T v = g[i];
-      if (clip) from_f(to_f(v) * coef, v);
+      if (clip) from_f(to_f(v) * coef * post, v);
       out[i] = v;
     }
   }

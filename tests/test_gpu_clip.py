@@ -149,3 +149,14 @@ def test_norm_alone():
     want, _ = O.clip(cpu, 1.0)
     assert abs(norm.item() - want) <= 40 * U * want
     assert all(torch.equal(g.cpu(), c) for g, c in zip(gpu, cpu))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("scale,max_norm", [(1e30, 1e-8), (1e34, 1e-3), (1e30, 1e-15),
+                                            (1e34, 1e-36), (1e34, 1e34)])
+def test_coefficients_below_the_normal_range(scale, max_norm, dtype):
+    """A large norm over a small bound: max_norm / norm has few bits or none in
+    fp32, the clipped elements have all of theirs."""
+    cpu = _grads([30000, 3], dtype, scale)
+    r = kd.clip_grad_norm([g.cuda() for g in cpu], max_norm)
+    _check(r, cpu, max_norm, dtype, tiny=2.0 ** -126)
