@@ -393,11 +393,14 @@ kd_status kd_logprob_bwd(const kd_logprob_problem* problem, const kd_logprob_inp
  * array of element counts (0 is allowed; its pointers may be NULL), all in
  * `dtype`.  outs[i] may be grads[i] (in place: nothing is written when the
  * norm is within bounds) but may not overlap any tensor otherwise (the same
- * tensor listed twice is refused); outs = NULL only computes the norm.  norm_out: device fp32 scalar or NULL.  Squares are
- * summed in fp32 per thread and in fp64 beyond, in a fixed order; elements up
- * to the largest finite value do not overflow the norm.  If the norm is
- * infinite or NaN, KD_DEV_NONFINITE is set and the gradients are passed on
- * unscaled (so that a training loop can skip the step).
+ * tensor listed twice is refused); outs = NULL only computes the norm.
+ * norm_out: device fp32 scalar or NULL.  Squares are summed in fp32 per thread
+ * and in fp64 beyond, in a fixed order, and elements at either end of the
+ * type's range neither overflow nor vanish in them.  If an element is infinite
+ * or NaN, so is the norm, KD_DEV_NONFINITE is set and the gradients are passed
+ * on unscaled (so that a training loop can skip the step).  A norm of finite
+ * elements beyond fp32 is stored as infinity, but not flagged: the gradients
+ * are clipped by the norm that it is.
  * max_norm >= 0 and finite.  workspace: kd_clip_grad_norm_workspace_size()
  * bytes, 256-byte aligned. */
 kd_status kd_clip_grad_norm_workspace_size(const int64_t* numel, int32_t n_tensors, size_t* bytes);

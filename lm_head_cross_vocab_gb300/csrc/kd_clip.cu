@@ -147,8 +147,9 @@ __global__ void __launch_bounds__(kThreads, 4)
     const int n = (int)min((int64_t)kChunk, tab.t[k].n - at);
     const float s = chunk_squares(g, n, 1.f);
     // squares at the ends of fp32's range: once more, scaled by a power of two
+    // (elements below 2^-49 by 2^96: the least, 2^-149, squares to 2^-106)
     if (!(s <= 3e38f)) sum += (double)chunk_squares(g, n, 0x1p-72f) * 0x1p144;
-    else if (s < 1e-30f) sum += (double)chunk_squares(g, n, 0x1p72f) * 0x1p-144;
+    else if (s < 1e-30f) sum += (double)chunk_squares(g, n, 0x1p96f) * 0x1p-192;
     else sum += (double)s;
   }
   sum = block_sum(sum);

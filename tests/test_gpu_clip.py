@@ -160,3 +160,30 @@ def test_coefficients_below_the_normal_range(scale, max_norm, dtype):
     cpu = _grads([30000, 3], dtype, scale)
     r = kd.clip_grad_norm([g.cuda() for g in cpu], max_norm)
     _check(r, cpu, max_norm, dtype, tiny=2.0 ** -126)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("value,count", [(2.0 ** -133, 50000), (2.0 ** -130, 40000)])
+def test_norm_of_subnormal_gradients(value, count, dtype):
+    """Equal elements far below 2^-126: the norm is value sqrt(count), itself a
+    subnormal number, to half a step of those."""
+    g = [torch.full((count,), value, device="cuda").to(DT[dtype])]
+    norm = kd.clip_grad_norm(g, 1.0)["norm"].item()
+    want = value * math.sqrt(count)
+    assert abs(norm - want) <= 40 * U * want + 2.0 ** -150
+    g = [torch.full((count,), 2.0 ** -133 if dtype == "bf16" else 2.0 ** -149, device="cuda")
+         .to(DT[dtype])]
+    want = float(g[0][0].double()) * math.sqrt(count)
+    assert abs(kd.clip_grad_norm(g, 1.0)["norm"].item() - want) <= 40 * U * want + 2.0 ** -150
+
+
+def test_norm_beyond_fp32():
+    """Finite elements whose norm fp32 cannot hold: stored as infinity, clipped
+    by the norm that it is."""
+    cpu = [torch.full((4,), 3e38), torch.tensor([1e38, -2.0])]
+    r = kd.clip_grad_norm([g.cuda() for g in cpu], 1e30)
+    assert r["norm"].item() == math.inf and int(r["dev_status"].item()) == 0
+    _, ref = O.clip(cpu, 1e30)
+    for got, want in zip(r["grads"], ref):
+        tol = (42 * U + U * (1 + 42 * U)) * np.abs(want) + 2.0 ** -126
+        assert (np.abs(as_f64(got) - want) <= tol).all()
