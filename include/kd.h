@@ -376,6 +376,8 @@ kd_status kd_logprob_fwd(const kd_logprob_problem* problem, const kd_logprob_inp
  *            between the rows are left as they are; it may be the logits
  *            themselves when both pitches are equal)
  *   d_h [N, D], d_w [V, D]    (hidden source; bf16: 16-byte aligned)
+ * A gradient that overlaps the inputs or the other gradient otherwise is
+ * refused (KD_ERR_INVALID_ARG).
  * A bad token contributes no d_logprob term.  bf16 hidden problems round d z
  * to bf16 (at most 2^-8 of each element) before the products with W and H,
  * whose sums are fp32; what that takes from a row's element v = y goes into

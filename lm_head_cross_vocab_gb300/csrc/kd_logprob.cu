@@ -1555,6 +1555,33 @@ kd_status lp_inputs(const LpPlan& P, const kd_logprob_inputs* in) {
   return KD_OK;
 }
 
+bool spans_meet(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+// A gradient that shares memory with what the backward still reads or writes
+// otherwise.  d_logits may be the logits element by element, or lie between
+// their rows.
+bool bwd_overlaps(const LpPlan& P, const kd_logprob_inputs* in, const void* d_h, const void* d_w,
+                  const void* d_logits) {
+  const size_t esz = P.bf16 ? 2 : 4;
+  if (P.hidden) {
+    const size_t nh = (size_t)P.n * P.d * esz, nw = (size_t)P.v * P.d * esz;
+    return spans_meet(d_h, nh, in->h, nh) || spans_meet(d_h, nh, in->w, nw) ||
+           spans_meet(d_w, nw, in->h, nh) || spans_meet(d_w, nw, in->w, nw) ||
+           spans_meet(d_h, nh, d_w, nw);
+  }
+  const size_t row = (size_t)P.v * esz, pz = (size_t)P.ld * esz, pg = (size_t)P.ldg * esz;
+  if (!spans_meet(in->logits, (size_t)(P.n - 1) * pz + row, d_logits,
+                  (size_t)(P.n - 1) * pg + row))
+    return false;
+  if (pz != pg) return true;
+  const uintptr_t z = reinterpret_cast<uintptr_t>(in->logits);
+  const uintptr_t g = reinterpret_cast<uintptr_t>(d_logits);
+  const size_t off = (g > z ? g - z : z - g) % pz;
+  return g != z && (off < row || pz - off < row);
+}
+
 // bf16: rows are stored in 16-byte vectors
 bool grad_ok(const LpPlan& P, const void* g) { return !P.bf16 || aligned16(g); }
 
@@ -1709,6 +1736,7 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
     return KD_ERR_INVALID_ARG;
   if (P.n > 0 && (!grad_ok(P, d_h) || !grad_ok(P, d_w))) return KD_ERR_UNSUPPORTED;
   if (!ws_ok(workspace, ws_bytes, P.b_bytes)) return KD_ERR_WORKSPACE;
+  if (P.n > 0 && bwd_overlaps(P, in, d_h, d_w, d_logits)) return KD_ERR_INVALID_ARG;
   st = lp_device();
   if (st != KD_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1727,7 +1755,6 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
   a.status = dev_status;
   if (!P.hidden) {
     if (!d_logits) return KD_OK;
-    if (d_logits == in->logits && P.ld != P.ldg) return KD_ERR_INVALID_ARG;
     a.z = in->logits;
     a.n = P.n;
     a.cols = P.v;

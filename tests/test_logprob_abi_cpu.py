@@ -306,3 +306,37 @@ def test_out_needs_no_status_word_and_refuses_a_wrong_one(kd, monkeypatch):
         with pytest.raises(ValueError):
             kd.token_logprobs(p, tens, out={"logprob": torch.zeros(4), "dev_status": word})
     assert len(fake.seen) == calls
+
+
+def test_gradients_that_overlap_what_is_read_are_refused(kd):
+    """d_logits may be the logits, or lie between their rows; any other overlap,
+    and any of the hidden gradients', would be read after it was written."""
+    lib = kd.load_library()
+
+    def bwd(p, ins, dh=None, dw=None, dz=None):
+        return lib.kd_logprob_bwd(ctypes.byref(p), ctypes.byref(ins), FAKE, None, None, dh, dw,
+                                  dz, None, FAKE, 1 << 24, None)
+
+    z = 1 << 30
+    ins = kd.kd_logprob_inputs(logits=z, tokens=FAKE)
+    tight, wide = _prob(kd), _prob(kd, ld=250, ldg=250)  # 8 rows of 100
+    for p, off in ((tight, 2), (tight, -2), (tight, 200), (tight, -1598), (wide, 2), (wide, 198),
+                   (wide, -302), (wide, 502), (wide, 302), (_prob(kd, ld=100, ldg=250), 0),
+                   (_prob(kd, ld=250, ldg=100), 1000)):
+        assert bwd(p, ins, dz=z + off) == kd.KD_ERR_INVALID_ARG, off
+    import torch
+    here = not torch.cuda.is_available()  # (well-formed calls would launch)
+    if here:
+        for p, off in ((tight, 0), (tight, 1600), (tight, -1600), (wide, 0), (wide, 200),
+                       (wide, 300), (wide, -200), (wide, 700), (wide, 3700), (wide, -3700)):
+            assert bwd(p, ins, dz=z + off) == kd.KD_ERR_NO_DEVICE, off
+    p, h, w = _prob(kd, source="hidden"), 1 << 30, 1 << 31  # 1024 and 12800 bytes
+    ins = kd.kd_logprob_inputs(h=h, w=w, tokens=FAKE)
+    far = 1 << 32
+    for dh, dw in ((h, None), (None, w), (h + 1008, None), (None, h + 16), (w + 12784, None),
+                   (None, w - 12784), (far, far + 1008), (far + 12784, far)):
+        assert bwd(p, ins, dh, dw) == kd.KD_ERR_INVALID_ARG, (dh, dw)
+    if here:
+        for dh, dw in ((h + 1024, w + 12800), (far, far + 1024), (far + 12800, far),
+                       (h - 1024, None)):
+            assert bwd(p, ins, dh, dw) == kd.KD_ERR_NO_DEVICE, (dh, dw)
