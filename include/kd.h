@@ -316,6 +316,8 @@ kd_status kd_mix_teacher_logits(const void* const* logits, int32_t k, const floa
  * With exp() of the latter as probabilities they are the cached teacher of
  * KD_TEACHER_TOPK (probabilities not renormalised: orda-kernel README,
  * "Teacher descriptors"; Full-Chunked-KL-Loss README, "Methods").
+ * Every array is aligned to its elements (KD_ERR_INVALID_ARG otherwise), some
+ * to 16 bytes, as stated there.
  * A logit of -infinity is an id of probability 0.  A row in which every logit
  * is -infinity has no distribution: logprob -infinity, entropy 0, the ids
  * 0..K-1 with log-probability -infinity, and a zero gradient row.  A row with

@@ -349,6 +349,8 @@ extern "C" kd_status kd_clip_grad_norm(const void* const* grads, void* const* ou
     return KD_ERR_INVALID_ARG;
   if (dtype != KD_BF16 && dtype != KD_FP32) return KD_ERR_INVALID_ARG;
   if (!(std::isfinite(max_norm) && max_norm >= 0.f)) return KD_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(norm_out) | reinterpret_cast<uintptr_t>(dev_status)) % 4)
+    return KD_ERR_INVALID_ARG;
   const size_t esz = dtype == KD_BF16 ? 2 : 4;
   for (int32_t i = 0; i < n_tensors; ++i) {
     if (numel[i] == 0) continue;

@@ -1395,6 +1395,11 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+// Arrays of elements of `size` bytes, each at a multiple of that.
+template <class... P>
+bool aligned_to(uintptr_t size, P... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & (size - 1)) == 0;
+}
 
 struct LpPlan {
   bool hidden, bf16;
@@ -1549,8 +1554,10 @@ kd_status lp_device() {
 kd_status lp_inputs(const LpPlan& P, const kd_logprob_inputs* in) {
   if (!in) return KD_ERR_INVALID_ARG;
   if (P.n == 0) return KD_OK;
-  if (!P.hidden) return in->logits ? KD_OK : KD_ERR_INVALID_ARG;
-  if (!in->h || !in->w) return KD_ERR_INVALID_ARG;
+  if (!aligned_to(8, in->tokens)) return KD_ERR_INVALID_ARG;
+  if (!P.hidden)
+    return in->logits && aligned_to(P.bf16 ? 2 : 4, in->logits) ? KD_OK : KD_ERR_INVALID_ARG;
+  if (!in->h || !in->w || (!P.bf16 && !aligned_to(4, in->h, in->w))) return KD_ERR_INVALID_ARG;
   if (P.bf16 && (!aligned16(in->h) || !aligned16(in->w))) return KD_ERR_UNSUPPORTED;
   return KD_OK;
 }
@@ -1638,6 +1645,8 @@ extern "C" kd_status kd_logprob_fwd(const kd_logprob_problem* p, const kd_logpro
   if (st != KD_OK) return st;
   if (logprob && !in->tokens && P.n > 0) return KD_ERR_INVALID_ARG;
   if (stats && !aligned16(stats)) return KD_ERR_INVALID_ARG;
+  if (!aligned_to(4, logprob, entropy, topk_idx, topk_logprob, dev_status))
+    return KD_ERR_INVALID_ARG;
   if (!ws_ok(workspace, ws_bytes, P.f_bytes)) return KD_ERR_WORKSPACE;
   st = lp_device();
   if (st != KD_OK) return st;
@@ -1733,6 +1742,9 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
   if (st != KD_OK) return st;
   if (P.hidden ? d_logits != nullptr : (d_h || d_w)) return KD_ERR_INVALID_ARG;
   if (P.n > 0 && (!stats || !aligned16(stats) || (d_logprob && !in->tokens)))
+    return KD_ERR_INVALID_ARG;
+  if (!aligned_to(4, d_logprob, d_entropy, dev_status) ||
+      !aligned_to(P.bf16 ? 2 : 4, d_h, d_w, d_logits))
     return KD_ERR_INVALID_ARG;
   if (P.n > 0 && (!grad_ok(P, d_h) || !grad_ok(P, d_w))) return KD_ERR_UNSUPPORTED;
   if (!ws_ok(workspace, ws_bytes, P.b_bytes)) return KD_ERR_WORKSPACE;

@@ -340,3 +340,43 @@ def test_gradients_that_overlap_what_is_read_are_refused(kd):
         for dh, dw in ((h + 1024, w + 12800), (far, far + 1024), (far + 12800, far),
                        (h - 1024, None)):
             assert bwd(p, ins, dh, dw) == kd.KD_ERR_NO_DEVICE, (dh, dw)
+
+
+def test_arrays_off_their_elements_boundaries_are_refused(kd):
+    """An address that is no multiple of its elements' size, by name; the same
+    call with every address in order gets as far as the workspace."""
+    lib = kd.load_library()
+
+    def fwd(p, ins, **o):
+        names = ("logprob", "entropy", "topk_idx", "topk_logprob", "stats", "dev_status")
+        return lib.kd_logprob_fwd(ctypes.byref(p), ctypes.byref(ins),
+                                  *[o.get(x, 3 * FAKE) for x in names], None, 0, None)
+
+    def bwd(p, ins, **o):
+        names = ("d_logprob", "d_entropy", "d_h", "d_w", "d_logits", "dev_status")
+        return lib.kd_logprob_bwd(ctypes.byref(p), ctypes.byref(ins), FAKE,
+                                  *[o.get(x) for x in names], None, 0, None)
+
+    for dtype, size in (("bf16", 2), ("fp32", 4)):
+        p = _prob(kd, source="hidden", dtype=dtype)
+        base = dict(h=FAKE, w=2 * FAKE, tokens=FAKE)
+        ins = kd.kd_logprob_inputs(**base)
+        assert fwd(p, ins) == bwd(p, ins, d_h=FAKE) == kd.KD_ERR_WORKSPACE
+        for name in ("logprob", "entropy", "topk_idx", "topk_logprob", "stats", "dev_status"):
+            assert fwd(p, ins, **{name: 3 * FAKE + 2}) == kd.KD_ERR_INVALID_ARG, name
+        for name in ("d_logprob", "d_entropy", "dev_status"):
+            assert bwd(p, ins, d_h=FAKE, **{name: FAKE + 2}) == kd.KD_ERR_INVALID_ARG, name
+        for name in ("d_h", "d_w"):
+            assert bwd(p, ins, **{name: FAKE + size // 2}) == kd.KD_ERR_INVALID_ARG, name
+        for name, off in (("tokens", 4),) + ((("h", 2), ("w", 2)) if dtype == "fp32" else ()):
+            bad = kd.kd_logprob_inputs(**{**base, name: base[name] + off})
+            assert fwd(p, bad) == bwd(p, bad, d_h=FAKE) == kd.KD_ERR_INVALID_ARG, name
+        p = _prob(kd, dtype=dtype)
+        bad = kd.kd_logprob_inputs(logits=FAKE + size // 2, tokens=FAKE)
+        assert fwd(p, bad) == kd.KD_ERR_INVALID_ARG
+        assert bwd(p, kd.kd_logprob_inputs(logits=FAKE, tokens=FAKE), d_logits=3 * FAKE + size // 2) \
+            == kd.KD_ERR_INVALID_ARG
+    arr, cnt = (ctypes.c_void_p * 1)(FAKE), (ctypes.c_int64 * 1)(10)
+    for norm, status in ((FAKE + 2, None), (None, FAKE + 1)):
+        assert lib.kd_clip_grad_norm(arr, arr, cnt, 1, kd.KD_FP32, 1.0, norm, status, FAKE,
+                                     1 << 20, None) == kd.KD_ERR_INVALID_ARG
