@@ -911,3 +911,47 @@ def test_out_with_the_gradients_alone():
     g = kd.token_logprobs_backward(q, tens, r["stats"], d_logprob=up,
                                    out={"d_w": torch.empty_like(w)})
     assert torch.equal(g["d_w"], ref["d_w"])
+
+
+@pytest.mark.parametrize("tokens", ["uniform", "sampled"])
+@pytest.mark.parametrize("scale", [1, 16])
+@pytest.mark.parametrize("n,v,d", [(500, 2000, 256), (900, 7000, 64), (40, 3001, 128)])
+def test_the_tokens_own_element_keeps_more_than_bf16(n, v, d, scale, tokens):
+    """G is rounded to bf16, and what that takes from a token's own element goes
+    into both products all the same.  Both forms of the products, of G rounded
+    and of G rounded but there, are made in fp64 and rounded to bf16; the
+    library's has to be as near the exact one as the latter, which lies clearly
+    nearer than the former.  (G in fp32 is off by some 1e-6 relative: one element
+    in a thousand rounds the other way, from one side of the exact value to the
+    other about as far, so that the norm of the error, over n d roundings or v d,
+    stays within 2 %.)"""
+    h, w = (x.cuda() for x in _hidden(n, v, d, "bf16", n))
+    h *= scale  # (exact; 16: the likeliest id has 0.6 to 0.8 on average)
+    z = h.double() @ w.double().t()
+    lp = torch.log_softmax(z, dim=1)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    if tokens == "uniform":
+        y = torch.randint(0, v, (n,), generator=g, device="cuda")
+    else:
+        y = torch.multinomial(lp.exp(), 1, generator=g)[:, 0]
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, d_model=d, source="hidden")
+    tens = {"h": h, "w": w, "tokens": y}
+    out = kd.token_logprobs(p, tens)
+    up = torch.randn(n, generator=g, device="cuda")
+    r = kd.token_logprobs_backward(p, tens, out["stats"], d_logprob=up)
+    gz = -lp.exp() * up.double()[:, None]
+    rows = torch.arange(n, device="cuda")
+    gz[rows, y] += up.double()
+    cut = gz.bfloat16().double()
+    own_h = cut.clone()
+    own_h[rows, y] = gz[rows, y]
+    few = torch.bincount(y, minlength=v)[y] <= 4
+    own_w = cut.clone()
+    own_w[rows[few], y[few]] = gz[rows[few], y[few]]
+    for name, exact, plain, own in (
+            ("d_h", gz @ w.double(), cut @ w.double(), own_h @ w.double()),
+            ("d_w", gz.t() @ h.double(), cut.t() @ h.double(), own_w.t() @ h.double())):
+        err = [float((x.bfloat16().double() - exact).norm() / exact.norm()) for x in (plain, own)]
+        got = float((r[name].double() - exact).norm() / exact.norm())
+        assert err[0] > 1.1 * err[1], (name, err)  # else this shows nothing
+        assert got <= 1.02 * err[1], (name, got, err)
