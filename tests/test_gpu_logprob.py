@@ -955,3 +955,43 @@ def test_the_tokens_own_element_keeps_more_than_bf16(n, v, d, scale, tokens):
         got = float((r[name].double() - exact).norm() / exact.norm())
         assert err[0] > 1.1 * err[1], (name, err)  # else this shows nothing
         assert got <= 1.02 * err[1], (name, got, err)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,v,k", [(700, 9000, 1), (1500, 4099, 20), (400, 32003, 64)])
+def test_many_rows_forward_and_backward(n, v, k, dtype):
+    """More rows than the oracle takes: the definitions in fp64 on the same
+    device, with the tolerances above."""
+    t = (1.0, 0.7, 2.0)[(n + v) % 3]
+    z, y = _logits(n, v, dtype, n + v).cuda(), _tokens(n, v, n + v).cuda()
+    on = y != IGN
+    p = kd.LogprobProblem(n_tokens=n, vocab=v, topk=k, dtype=dtype, temperature=t)
+    tens = {"logits": z, "tokens": y}
+    out = kd.token_logprobs(p, tens)
+    zz = z.double()
+    lp = torch.log_softmax(zz / t, dim=1)
+    pr = lp.exp()
+    ent = -(pr * lp).sum(dim=1)
+    x = (zz.amax(dim=1, keepdim=True) - zz) / t
+    es, yy = _e_s(v), y.clamp(min=0)[:, None]
+    off = (out["logprob"].double() - lp.gather(1, yy)[:, 0]).abs()
+    assert (off <= es + (2 * x + 2 * lp.abs() + 4).gather(1, yy)[:, 0] * U)[on].all()
+    assert ((out["entropy"].double() - ent).abs() <= es * (math.log(v) + 3))[on].all()
+    assert (out["logprob"][~on] == 0).all() and (out["entropy"][~on] == 0).all()
+    ids = torch.sort(zz, dim=1, descending=True, stable=True)[1][:, :k]
+    assert torch.equal(out["topk_idx"][on], ids[on].int())
+    off = (out["topk_logprob"].double() - lp.gather(1, ids)).abs()
+    assert (off <= es + (2 * x + 2 * lp.abs() + 4).gather(1, ids) * U)[on].all()
+    g = torch.Generator().manual_seed(v)
+    gl, gh = torch.randn(n, generator=g).cuda(), torch.randn(n, generator=g).cuda() * 0.3
+    r = kd.token_logprobs_backward(p, tens, out["stats"], d_logprob=gl, d_entropy=gh)
+    a, b = gl.double()[:, None], gh.double()[:, None]
+    ref = -pr * (a + b * (lp + ent[:, None]))
+    ref[torch.arange(n), yy[:, 0]] += a[:, 0]
+    ref = torch.where(on[:, None], ref / t, 0.0)
+    bracket = a.abs() + b.abs() * (lp.abs() + math.log(v) + 1)
+    tol = pr * (((4 * x + 16) * U + es) * bracket + b.abs() * es * (math.log(v) + 3)
+                + 8 * U * bracket) / t
+    tol = tol + HALF[dtype] * (ref.abs() + tol) + 4 * U * a.abs() / t + TINY
+    assert ((r["d_logits"].double() - ref).abs() <= tol).all()
+    assert (r["d_logits"][~on] == 0).all()
