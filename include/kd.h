@@ -306,8 +306,8 @@ kd_status kd_mix_teacher_logits(const void* const* logits, int32_t k, const floa
                                 uint32_t* dev_status, void* stream);
 
 /* Token log-probabilities.  For every token row n with logits z (given, or
- * z = H W^T of hidden states and a head weight, which is never stored as a
- * (tokens x vocab) matrix), a = z / temperature and p = softmax(a):
+ * z = H W^T of hidden states and a head weight), a = z / temperature and
+ * p = softmax(a):
  *   logprob[n]  = a[y] - logsumexp(a)          y = tokens[n]
  *   entropy[n]  = - sum_v p_v log p_v
  *   top alternatives: the K ids with the largest logits, best first (equal
@@ -325,7 +325,13 @@ kd_status kd_mix_teacher_logits(const void* const* logits, int32_t k, const floa
  * Rows whose token is ignore_index are not computed, whatever their logits or
  * hidden states hold: logprob 0, entropy 0, statistics 0, the ids 0..K-1 with
  * log-probability -infinity (so such a row is a valid KD_TEACHER_TOPK row of
- * mass 0), a zero gradient row and no share in d_w. */
+ * mass 0), a zero gradient row and no share in d_w.
+ * What of z = H W^T is held: nothing in the forward of bf16 problems with up to
+ * 128 alternatives.  Otherwise the workspace takes fp32 logits of some rows at a
+ * time, at most 128 MiB of them or of 256 rows, and the backward chunks of z's
+ * gradient: the whole of it where that is at most 8 Mi elements (48 Mi in bf16
+ * with at most 256 rows), else chunks that do not grow with tokens times
+ * vocabulary. */
 typedef struct kd_logprob_problem {
   int64_t n_tokens;      /* N >= 0                                            */
   int64_t vocab;         /* V >= 1                                            */

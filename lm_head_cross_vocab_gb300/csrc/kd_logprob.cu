@@ -1788,8 +1788,9 @@ extern "C" kd_status kd_logprob_bwd(const kd_logprob_problem* p, const kd_logpro
   void* hm = at<char>(workspace, P.b_h);
   // What rounding the tokens' elements of G to bf16 took from them (fp32) goes
   // into both products at their end: into d_h[i] with W's row of token i, into
-  // d_w[v] with the hidden states of the tokens v where they are few (the sum
-  // of many averages the roundings out).  Rows without a token in range keep 0.
+  // d_w[v] with the hidden states of the tokens v where they are few (the lists
+  // hold kTermRows; of an id that more tokens share G's rounding stays).  Rows
+  // without a token in range keep 0.
   float* rest = P.bf16 ? at<float>(workspace, P.b_rest) : nullptr;
   int32_t* count = P.bf16 ? at<int32_t>(workspace, P.b_count) : nullptr;
   int32_t* list = P.bf16 ? at<int32_t>(workspace, P.b_list) : nullptr;

@@ -1483,7 +1483,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
           }
         } else if constexpr (EPI == EPI_TOKG) {
           // tensor-bound: 4096 x 32000, D 2048 in 330 us over five chunks (1.6
-          // PFLOP/s); whole backward with its products 970 us (1.66 PFLOP/s)
+          // PFLOP/s); whole backward with its products 1072-1107 us on inputs that
+          // change from call to call (1.5 PFLOP/s), 950-970 us on the same ones
           const TcTokGradArgs& a = P.tokg;
 #pragma unroll 1
           for (int cc = 0; cc < BN / 2; cc += 32) {
@@ -1500,8 +1501,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc(const __grid_constant__ TcPa
               for (int j = 0; j < 32; j += 2) lp_grad_pair(v[j], v[j + 1], tg, a.k2);
               const int64_t jy = tg.y - (a.c0 + lc0);
               if (tg.y >= 0 && jy >= 0 && jy < 32) {
-                // the token's element, nearly always by far the largest of the
-                // row: what rounding takes from it is added to the products
+                // the token's element, by far the largest of the row where the
+                // softmax is flat: what rounding takes from it is added to the
+                // products (the other elements keep theirs)
                 const float g = pick32(v, (int)jy) + tg.cy;
                 a.rest[a.r0 + g_row] = g - __bfloat162float(__float2bfloat16(g));
 #pragma unroll
