@@ -65,10 +65,12 @@ def bytes_per_step(w: I.Workload):
 
 
 # library sources behind each measured family: the projection and the mixing
-# kernels stand alone, and so do the token log-probabilities and the gradient
-# clipping (no counter captured); the loss path is everything else in csrc/
+# kernels stand alone, and so do the token log-probabilities, the gradient
+# clipping and the row operators around the head (no counter captured); the loss
+# path is everything else in csrc/
 SOURCE_GROUPS = {"project": ("kd_project.cu",), "mix": ("kd_mix.cu",),
-                 "logprob": ("kd_logprob.cu",), "clip": ("kd_clip.cu",)}
+                 "logprob": ("kd_logprob.cu",), "clip": ("kd_clip.cu",),
+                 "rows": ("kd_rows.cuh", "kd_norm.cu", "kd_embed.cu", "kd_verify.cu")}
 
 
 def kernel_sources_hash(group: str = "loss") -> str:
@@ -83,6 +85,8 @@ def kernel_sources_hash(group: str = "loss") -> str:
             continue
         if f.endswith(".cu") and (f not in SOURCE_GROUPS[group] if group in SOURCE_GROUPS
                                   else f in own):
+            continue
+        if f in own and f not in SOURCE_GROUPS.get(group, ()):  # another group's header
             continue
         h.update(f.encode())
         with open(os.path.join(csrc, f), "rb") as fh:

@@ -82,7 +82,8 @@ typedef enum kd_status {
                                      * kd_project_teacher_logits + a
                                      * KD_TEACHER_LOGITS teacher instead) */
 #define KD_DEV_NONFINITE 0x20u /* kd_clip_grad_norm: the norm is infinite or NaN;
-                                * the gradients are passed on unscaled */
+                                * the gradients are passed on unscaled.
+                                * kd_verify_drafts: a row without a distribution */
 
 typedef enum kd_dtype { KD_BF16 = 0, KD_FP32 = 1 } kd_dtype;
 
@@ -421,6 +422,124 @@ kd_status kd_clip_grad_norm_workspace_size(const int64_t* numel, int32_t n_tenso
 kd_status kd_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numel,
                             int32_t n_tensors, int32_t dtype, float max_norm, float* norm_out,
                             uint32_t* dev_status, void* workspace, size_t ws_bytes, void* stream);
+
+/* Verification of drafted tokens (speculative decoding): a drafter, for example
+ * the distilled student, has drafted up to K tokens for each of B sequences,
+ * and the target's logits over the same rows say which of them stand.  For
+ * sequence b, with p = softmax(target_logits[b, i] / t_target) and
+ * q = softmax(draft_logits[b, i] / t_draft) (no draft_logits: q is 1 at the
+ * drafted token, as for drafts that were looked up):
+ *   draft i is accepted when uniform[b, i] q(x_i) < p(x_i), the first that is
+ *   not ends the sequence's drafts;
+ *   one more token is drawn behind the accepted ones: the first arrival of a
+ *   race, argmax_v r_v / noise[b, v] (equal: lowest id), which for exponential
+ *   noise is v with probability r_v / sum r.  r = max(p - q, 0) at the first
+ *   rejected row (p itself where p <= q everywhere), r = p at the row behind the
+ *   last draft.  With uniform and exponential random numbers the emitted tokens
+ *   are distributed as the target's own samples.
+ * t_target = 0: greedy.  A draft is accepted when it is the id with the largest
+ * target logit (equal: lowest id), the drawn token is that id, neither
+ * draft_logits nor random numbers are used, and logprob is that at temperature 1.
+ * A logit of -infinity is an id of probability 0.  A target row without a
+ * distribution (a NaN, a +infinity, or nothing but -infinity) rejects its draft
+ * and draws nothing: the token is ignore_index, its logprob NaN.  A draft row
+ * without one rejects its draft, and the token is drawn from p.  Both set
+ * KD_DEV_NONFINITE.  A drafted id outside [0, V) is rejected and sets
+ * KD_DEV_BAD_LABEL.  Rows behind the last draft's successor are not read.
+ * Noise is within [2^-100, 2^100]; an id whose noise is not takes no part.
+ * A drafter over another vocabulary: kd_project_teacher_logits moves its logits
+ * onto the target's ids first (then t_draft = 1). */
+typedef struct kd_verify_problem {
+  int64_t n_seqs;        /* B >= 0                                            */
+  int64_t vocab;         /* V >= 1                                            */
+  int64_t ld_target;     /* pitch of the target's rows in elements; 0 = vocab */
+  int64_t ld_draft;      /* pitch of the drafter's rows; 0 = vocab            */
+  int64_t ignore_index;  /* written behind a sequence's last token            */
+  int32_t n_drafts;      /* K, 0..KD_VERIFY_MAX_DRAFTS                        */
+  int32_t dtype;         /* kd_dtype of the logits                            */
+  float t_target;        /* > 0, or 0: greedy                                 */
+  float t_draft;         /* > 0                                               */
+} kd_verify_problem;
+#define KD_VERIFY_MAX_DRAFTS 32
+
+/* Device pointers; NULL where the problem does not use one. */
+typedef struct kd_verify_inputs {
+  const void* target_logits; /* [B, K + 1] rows of V, of pitch ld_target        */
+  const void* draft_logits;  /* [B, K] rows of V, of pitch ld_draft, or NULL    */
+  const int64_t* drafts;     /* [B, K] drafted ids                              */
+  const int32_t* lengths;    /* [B] drafts of each sequence, 0..K (more counts  */
+                             /* as K and sets KD_DEV_BAD_LABEL), negative: the  */
+                             /* sequence takes no part; NULL: K each            */
+  const float* uniform;      /* [B, K] in [0, 1)                                */
+  const float* noise;        /* [B, V] exponential random numbers               */
+} kd_verify_inputs;
+
+/* Outputs (any may be NULL): tokens int64 [B, K + 1], the accepted drafts, the
+ * drawn token and ignore_index behind it; accepted int32 [B]; logprob fp32
+ * [B, K + 1], log p of each token, 0 behind the last.  A sequence that takes no
+ * part gets ignore_index, 0 and 0.  workspace: kd_verify_workspace_size() bytes,
+ * 256-byte aligned.  Decisions are taken in fp32; results do not depend on
+ * timing. */
+kd_status kd_verify_workspace_size(const kd_verify_problem* problem, size_t* bytes);
+kd_status kd_verify_drafts(const kd_verify_problem* problem, const kd_verify_inputs* inputs,
+                           int64_t* tokens, int32_t* accepted, float* logprob,
+                           uint32_t* dev_status, void* workspace, size_t ws_bytes, void* stream);
+
+/* Embedding lookup in the table W [V, D] (for a tied model the head weight
+ * itself) and its gradient:
+ *   h[n] = scale W[tokens[n]]
+ *   d_w[v] (+)= scale sum over the n with tokens[n] = v of d_h[n]
+ * Rows whose token is ignore_index are zero and take no part in d_w, whatever
+ * d_h holds there; so are those whose token is outside [0, V), which sets
+ * KD_DEV_BAD_LABEL.  The gradient adds each id's rows in fp32 in an order that
+ * depends on the tokens alone (ascending n, cut into runs of fixed length where
+ * there are many) and rounds once; accumulate = 0 writes every row of d_w (zeros
+ * where an id does not occur), accumulate = 1 adds to what d_w holds, for
+ * example kd_bwd's d_w_s of a tied model, and touches only the rows of ids that
+ * occur.  Outputs may not overlap inputs.  workspace: 256-byte aligned. */
+typedef struct kd_embed_problem {
+  int64_t n_tokens;      /* N, 0..2^30                                        */
+  int64_t vocab;         /* V, 1..2^30                                        */
+  int64_t d_model;       /* D >= 1                                            */
+  int64_t ignore_index;
+  int32_t dtype;         /* kd_dtype of W, h and their gradients              */
+  float scale;           /* finite                                            */
+} kd_embed_problem;
+kd_status kd_embed_workspace_size(const kd_embed_problem* problem, size_t* bwd_bytes);
+kd_status kd_embed_fwd(const kd_embed_problem* problem, const int64_t* tokens, const void* w,
+                       void* h, uint32_t* dev_status, void* stream);
+kd_status kd_embed_bwd(const kd_embed_problem* problem, const int64_t* tokens, const void* d_h,
+                       void* d_w, int32_t accumulate, uint32_t* dev_status, void* workspace,
+                       size_t ws_bytes, void* stream);
+
+/* Root-mean-square norm of rows, with the residual's addition: the last norm of
+ * a model, whose output the hidden sources above read and whose backward takes
+ * the d_h they give.
+ *   s = x + residual (x alone where that is NULL)
+ *   h = s r (weight + weight_offset),   r = 1 / sqrt(mean(s^2) + eps)
+ * s is formed, and its norm taken, in fp32; `sum` (may be NULL) gets it rounded
+ * to dtype.  Backward, with s as it was stored (and r of that s), d_sum the
+ * gradient that reaches s from elsewhere (may be NULL) and g = d_h (weight +
+ * weight_offset):
+ *   d_x = r g - s r^3 mean(g s) + d_sum         (also the residual's gradient)
+ *   d_weight = sum over rows of d_h s r         (fp32, in a fixed order)
+ * Either gradient may be NULL to skip it.  h or sum may be x or residual
+ * themselves, and d_x any of s, d_h and d_sum; outputs may not overlap the inputs
+ * or one another otherwise.  workspace: 256-byte aligned. */
+typedef struct kd_rmsnorm_problem {
+  int64_t n_tokens;      /* N, 0..2^31 - 1                                    */
+  int64_t d_model;       /* D, 1..KD_RMSNORM_MAX_D                            */
+  int32_t dtype;         /* kd_dtype of all tensors                           */
+  float eps;             /* >= 0, finite                                      */
+  float weight_offset;   /* finite: 0, or 1 for weights stored around 0       */
+} kd_rmsnorm_problem;
+#define KD_RMSNORM_MAX_D 32768
+kd_status kd_rmsnorm_workspace_size(const kd_rmsnorm_problem* problem, size_t* bwd_bytes);
+kd_status kd_rmsnorm_fwd(const kd_rmsnorm_problem* problem, const void* x, const void* residual,
+                         const void* weight, void* sum, void* h, void* stream);
+kd_status kd_rmsnorm_bwd(const kd_rmsnorm_problem* problem, const void* s, const void* weight,
+                         const void* d_h, const void* d_sum, void* d_x, void* d_weight,
+                         void* workspace, size_t ws_bytes, void* stream);
 
 /* Static description of a status code. */
 const char* kd_status_string(kd_status status);

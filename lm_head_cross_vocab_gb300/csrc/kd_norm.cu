@@ -1,0 +1,387 @@
+// Root-mean-square norm of rows with the residual's addition, and its backward.
+//
+//   s = x + residual,  r = (mean s^2 + eps)^-1/2,  h = s r w
+//   d_x = r g - s r^3 mean(g s) + d_sum,  g = d_h w;   d_w = sum_n d_h s r
+//
+// TPR threads hold a row in registers, so every tensor is read once and the
+// sums of a row (s^2; backward: also g s) are one reduction.  Rows of whole
+// 16-byte vectors move as such; others (an odd width, a view at an odd offset)
+// element by element, neighbouring threads on neighbouring elements.
+// The backward's blocks take rows in turn and keep their share of d_w in
+// registers; a second kernel adds the blocks' shares in a fixed order.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "kd_internal.h"
+#include "kd_rows.cuh"
+
+namespace kd {
+namespace {
+
+struct NormArgs {
+  const void *x, *res, *w, *dh;  // backward: x is s, res is d_sum
+  void *sum, *h;                 // backward: h is d_x
+  float* part;                   // backward: [grid][d] shares of d_w, or NULL
+  int64_t n;
+  int d;
+  float eps, off;
+};
+
+// A thread's elements of a row: VPT vectors, TPR apart, or VPT * N elements,
+// TPR apart.  Zero beyond the row.
+template <class T, int TPR, int VPT, bool VEC>
+struct RowPart {
+  static constexpr int N = RowVec<T>::N, E = VPT * N;
+  uint4 w[VPT];
+
+  __device__ __forceinline__ void load(const T* p, int d, int t) {
+    if constexpr (VEC) {
+      const uint4* q = reinterpret_cast<const uint4*>(p);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        w[i] = i * TPR + t < d / N ? q[i * TPR + t] : make_uint4(0, 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        float v[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const int at = (i * N + e) * TPR + t;
+          v[e] = at < d ? to_f(p[at]) : 0.f;
+        }
+        w[i] = RowVec<T>::put(v);
+      }
+    }
+  }
+  __device__ __forceinline__ void get(int i, float* v) const { RowVec<T>::get(w[i], v); }
+  // the values of vector i
+  static __device__ __forceinline__ void store(T* p, int d, int t, int i, const float* v) {
+    if constexpr (VEC) {
+      if (i * TPR + t < d / N) reinterpret_cast<uint4*>(p)[i * TPR + t] = RowVec<T>::put(v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const int at = (i * N + e) * TPR + t;
+        if (at < d) from_f(v[e], p[at]);
+      }
+    }
+  }
+  // column of element e of vector i
+  static __device__ __forceinline__ int column(int t, int i, int e) {
+    return VEC ? (i * TPR + t) * N + e : (i * N + e) * TPR + t;
+  }
+};
+
+constexpr int norm_block(int tpr) { return tpr < 128 ? 128 : tpr; }
+
+// Sums of a row over its TPR threads, in every one of them.  `red` holds
+// TPR / 32 pairs; a block that calls it again passes the other of two buffers.
+template <int TPR>
+__device__ __forceinline__ float2 row_sums(float2 v, float2* red) {
+#pragma unroll
+  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+  }
+  if constexpr (TPR > 32) {
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = red[threadIdx.x & (TPR / 32 - 1)];
+#pragma unroll
+    for (int o = TPR / 64; o > 0; o >>= 1) {
+      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    }
+  }
+  return v;
+}
+
+template <class T, int TPR, int VPT, bool VEC>
+__global__ void __launch_bounds__(norm_block(TPR)) k_norm_fwd(NormArgs a) {
+  using P = RowPart<T, TPR, VPT, VEC>;
+  constexpr int N = P::N;
+  __shared__ float2 red[32];
+  const int t = threadIdx.x % TPR;
+  const int64_t row = (int64_t)blockIdx.x * (norm_block(TPR) / TPR) + threadIdx.x / TPR;
+  const bool on = row < a.n;
+  const int64_t at = (on ? row : 0) * a.d;
+  P x, r, w;
+  x.load(static_cast<const T*>(a.x) + at, a.d, t);
+  if (a.res) r.load(static_cast<const T*>(a.res) + at, a.d, t);
+  w.load(static_cast<const T*>(a.w), a.d, t);
+  float s[P::E], sq = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    x.get(i, s + i * N);
+    if (a.res) {
+      float v[N];
+      r.get(i, v);
+#pragma unroll
+      for (int e = 0; e < N; ++e) s[i * N + e] += v[e];
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) sq = fmaf(s[i * N + e], s[i * N + e], sq);
+    if (a.sum && on) P::store(static_cast<T*>(a.sum) + at, a.d, t, i, s + i * N);
+  }
+  sq = row_sums<TPR>(make_float2(sq, 0.f), red).x;
+  const float scale = 1.f / sqrtf(sq / (float)a.d + a.eps);
+  if (!on) return;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    float v[N];
+    w.get(i, v);
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = s[i * N + e] * scale * (v[e] + a.off);
+    P::store(static_cast<T*>(a.h) + at, a.d, t, i, v);
+  }
+}
+
+template <class T, int TPR, int VPT, bool VEC>
+__global__ void __launch_bounds__(norm_block(TPR)) k_norm_bwd(NormArgs a) {
+  using P = RowPart<T, TPR, VPT, VEC>;
+  constexpr int N = P::N, ROWS = norm_block(TPR) / TPR;
+  __shared__ float2 red[2][32];
+  chain_next();
+  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  P w;
+  w.load(static_cast<const T*>(a.w), a.d, t);
+  float dw[P::E];
+#pragma unroll
+  for (int e = 0; e < P::E; ++e) dw[e] = 0.f;
+  const float inv_d = 1.f / (float)a.d;
+  int turn = 0;
+  for (int64_t first = (int64_t)blockIdx.x * ROWS; first < a.n; first += (int64_t)gridDim.x * ROWS) {
+    const bool on = first + sub < a.n;
+    const int64_t at = (on ? first + sub : 0) * a.d;
+    P s, g, up;
+    s.load(static_cast<const T*>(a.x) + at, a.d, t);
+    g.load(static_cast<const T*>(a.dh) + at, a.d, t);
+    if (a.res) up.load(static_cast<const T*>(a.res) + at, a.d, t);
+    float2 sums = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      float sv[N], gv[N], wv[N];
+      s.get(i, sv);
+      g.get(i, gv);
+      w.get(i, wv);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        sums.x = fmaf(sv[e], sv[e], sums.x);
+        sums.y = fmaf(gv[e] * (wv[e] + a.off), sv[e], sums.y);
+      }
+    }
+    sums = row_sums<TPR>(sums, red[turn]);
+    turn ^= 1;
+    if (!on) continue;
+    const float r = 1.f / sqrtf(sums.x * inv_d + a.eps);
+    const float c = r * r * r * (sums.y * inv_d);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      float sv[N], gv[N], wv[N];
+      s.get(i, sv);
+      g.get(i, gv);
+      w.get(i, wv);
+      float o[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        o[e] = fmaf(-c, sv[e], r * (gv[e] * (wv[e] + a.off)));
+        dw[i * N + e] = fmaf(gv[e], sv[e] * r, dw[i * N + e]);
+      }
+      if (a.res) {
+        float uv[N];
+        up.get(i, uv);
+#pragma unroll
+        for (int e = 0; e < N; ++e) o[e] += uv[e];
+      }
+      if (a.h) P::store(static_cast<T*>(a.h) + at, a.d, t, i, o);
+    }
+  }
+  if (!a.part) return;
+  // the block's share: its row groups in order
+  if constexpr (ROWS > 1) {
+    __shared__ float share[TPR * P::E];
+    for (int q = 0; q < ROWS; ++q) {
+      if (sub == q) {
+#pragma unroll
+        for (int e = 0; e < P::E; ++e) {
+          if (q) dw[e] += share[e * TPR + t];
+          share[e * TPR + t] = dw[e];
+        }
+      }
+      __syncthreads();
+    }
+    if (sub != ROWS - 1) return;
+  }
+  float* part = a.part + (int64_t)blockIdx.x * a.d;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const int c = P::column(t, i, e);
+      if (c < a.d) part[c] = dw[i * N + e];
+    }
+}
+
+// d_w: 32 columns a block; each warp adds every eighth share, then the warps'
+// sums in order.
+template <class T>
+__global__ void __launch_bounds__(256) k_norm_weight(const float* part, int parts, int d, T* dw) {
+  __shared__ float sum[8][33];
+  chain_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float v = 0.f;
+  if (c < d)
+    for (int p = warp; p < parts; p += 8) v += part[(int64_t)p * d + c];
+  sum[warp][lane] = v;
+  __syncthreads();
+  if (warp == 0 && c < d) {
+    for (int q = 1; q < 8; ++q) v += sum[q][lane];
+    from_f(v, dw[c]);
+  }
+}
+
+int norm_grid(int64_t n, int64_t d, int esz) {
+  const int64_t vecs = rows_div(d * esz, 16);
+  const int rows = vecs <= 32 ? 16 : vecs <= 128 ? 4 : 1;  // rows of a block
+  const int per_sm = vecs <= 512 ? 4 : vecs <= 1024 ? 2 : 1;
+  return (int)std::min<int64_t>(rows_div(n, rows), (int64_t)std::max(1, tc_num_sms()) * per_sm);
+}
+
+template <class T, bool VEC, class F>
+bool norm_shape(int d, F&& run) {
+  const int vecs = (d + RowVec<T>::N - 1) / RowVec<T>::N;
+#define KD_SHAPE(TPR, VPT) \
+  return run(std::integral_constant<int, TPR>(), std::integral_constant<int, VPT>())
+  if (vecs <= 8) KD_SHAPE(8, 1);
+  if (vecs <= 32) KD_SHAPE(8, 4);
+  if (vecs <= 64) KD_SHAPE(32, 2);
+  if (vecs <= 128) KD_SHAPE(32, 4);
+  if (vecs <= 256) KD_SHAPE(128, 2);
+  if (vecs <= 512) KD_SHAPE(128, 4);
+  if (vecs <= 1024) KD_SHAPE(256, 4);
+  if (vecs <= 2048) KD_SHAPE(512, 4);
+  if (vecs <= 4096) KD_SHAPE(1024, 4);
+  KD_SHAPE(1024, 8);
+#undef KD_SHAPE
+}
+
+template <class T, bool VEC>
+bool norm_run(const NormArgs& a, void* d_w, int grid, cudaStream_t s) {
+  return norm_shape<T, VEC>(a.d, [&](auto tpr, auto vpt) {
+    constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value;
+    constexpr int block = norm_block(TPR);
+    if (!a.dh)
+      return rows_launch(k_norm_fwd<T, TPR, VPT, VEC>, rows_div(a.n, block / TPR), block, 0, false,
+                         s, a);
+    if (!rows_launch(k_norm_bwd<T, TPR, VPT, VEC>, grid, block, 0, false, s, a)) return false;
+    return !d_w || rows_launch(k_norm_weight<T>, rows_div(a.d, 32), 256, 0, true, s,
+                               (const float*)a.part, grid, a.d, static_cast<T*>(d_w));
+  });
+}
+
+bool norm_dispatch(const NormArgs& a, bool bf16, bool vec, void* d_w, int grid, cudaStream_t s) {
+  if (bf16)
+    return vec ? norm_run<__nv_bfloat16, true>(a, d_w, grid, s)
+               : norm_run<__nv_bfloat16, false>(a, d_w, grid, s);
+  return vec ? norm_run<float, true>(a, d_w, grid, s) : norm_run<float, false>(a, d_w, grid, s);
+}
+
+kd_status norm_check(const kd_rmsnorm_problem* p) {
+  if (!p || p->n_tokens < 0 || p->n_tokens > INT32_MAX || p->d_model < 1 ||
+      p->d_model > KD_RMSNORM_MAX_D)
+    return KD_ERR_INVALID_ARG;
+  if (p->dtype != KD_BF16 && p->dtype != KD_FP32) return KD_ERR_INVALID_ARG;
+  if (!(std::isfinite(p->eps) && p->eps >= 0.f) || !std::isfinite(p->weight_offset))
+    return KD_ERR_INVALID_ARG;
+  return KD_OK;
+}
+
+}  // namespace
+}  // namespace kd
+
+using namespace kd;
+
+extern "C" kd_status kd_rmsnorm_workspace_size(const kd_rmsnorm_problem* p, size_t* bwd_bytes) {
+  const kd_status st = norm_check(p);
+  if (st != KD_OK) return st;
+  if (bwd_bytes)
+    *bwd_bytes = (size_t)norm_grid(p->n_tokens, p->d_model, p->dtype == KD_BF16 ? 2 : 4) *
+                 (size_t)p->d_model * 4;
+  return KD_OK;
+}
+
+extern "C" kd_status kd_rmsnorm_fwd(const kd_rmsnorm_problem* p, const void* x,
+                                    const void* residual, const void* weight, void* sum, void* h,
+                                    void* stream) {
+  kd_status st = norm_check(p);
+  if (st != KD_OK) return st;
+  const size_t esz = p->dtype == KD_BF16 ? 2 : 4, row = (size_t)p->d_model * esz;
+  const size_t all = (size_t)p->n_tokens * row;
+  if (p->n_tokens > 0 && (!x || !weight || !h)) return KD_ERR_INVALID_ARG;
+  if (!rows_aligned(esz, x, residual, weight, sum, h)) return KD_ERR_INVALID_ARG;
+  if (!rows_over(h, x, all) || !rows_over(h, residual, all) || !rows_over(sum, x, all) ||
+      !rows_over(sum, residual, all) || rows_meet(sum, all, h, all) ||
+      rows_meet(weight, row, h, all) || rows_meet(weight, row, sum, all))
+    return KD_ERR_INVALID_ARG;
+  if ((st = rows_device()) != KD_OK || p->n_tokens == 0) return st;
+  NormArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = x;
+  a.res = residual;
+  a.w = weight;
+  a.sum = sum;
+  a.h = h;
+  a.n = p->n_tokens;
+  a.d = (int)p->d_model;
+  a.eps = p->eps;
+  a.off = p->weight_offset;
+  const bool vec = row % 16 == 0 && rows_aligned(16, x, residual, weight, sum, h);
+  const bool ok = norm_dispatch(a, esz == 2, vec, nullptr, 0, static_cast<cudaStream_t>(stream));
+  return ok && cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA;
+}
+
+extern "C" kd_status kd_rmsnorm_bwd(const kd_rmsnorm_problem* p, const void* sum,
+                                    const void* weight, const void* d_h, const void* d_sum,
+                                    void* d_x, void* d_weight, void* workspace, size_t ws_bytes,
+                                    void* stream) {
+  size_t need = 0;
+  kd_status st = kd_rmsnorm_workspace_size(p, &need);
+  if (st != KD_OK) return st;
+  const size_t esz = p->dtype == KD_BF16 ? 2 : 4, row = (size_t)p->d_model * esz;
+  const size_t all = (size_t)p->n_tokens * row;
+  if (p->n_tokens > 0 && (!sum || !weight || !d_h)) return KD_ERR_INVALID_ARG;
+  if (!rows_aligned(esz, sum, weight, d_h, d_sum, d_x, d_weight)) return KD_ERR_INVALID_ARG;
+  if (!rows_over(d_x, sum, all) || !rows_over(d_x, d_h, all) || !rows_over(d_x, d_sum, all) ||
+      rows_meet(d_x, all, weight, row) || rows_meet(d_weight, row, sum, all) ||
+      rows_meet(d_weight, row, weight, row) || rows_meet(d_weight, row, d_h, all) ||
+      rows_meet(d_weight, row, d_sum, all) || rows_meet(d_weight, row, d_x, all))
+    return KD_ERR_INVALID_ARG;
+  if (d_weight && !rows_ws_ok(workspace, ws_bytes, need)) return KD_ERR_WORKSPACE;
+  if ((st = rows_device()) != KD_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!d_x && !d_weight) return KD_OK;
+  if (p->n_tokens == 0)
+    return d_weight && cudaMemsetAsync(d_weight, 0, row, s) != cudaSuccess ? KD_ERR_CUDA : KD_OK;
+  NormArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = sum;
+  a.res = d_sum;
+  a.w = weight;
+  a.dh = d_h;
+  a.h = d_x;
+  a.part = d_weight ? static_cast<float*>(workspace) : nullptr;
+  a.n = p->n_tokens;
+  a.d = (int)p->d_model;
+  a.eps = p->eps;
+  a.off = p->weight_offset;
+  const bool vec = row % 16 == 0 && rows_aligned(16, sum, weight, d_h, d_sum, d_x);
+  const bool ok = norm_dispatch(a, esz == 2, vec, d_weight,
+                                norm_grid(a.n, a.d, (int)esz), s);
+  return ok && cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA;
+}

@@ -1,0 +1,636 @@
+// Verification of drafted tokens against a target's probabilities.
+//
+//   p = softmax(z_t / T_t), q = softmax(z_d / T_d) per row; draft i stands when
+//   u_i q(x_i) < p(x_i); the token behind the last that stands is
+//   argmax_v r_v / e_v, r = max(p - q, 0) at a rejected row, else p.
+//
+// Two launches.  k_verify_sums reads every row once and keeps its sum of
+// exponentials (greedy: the largest logit's id too), a row in as many parts as
+// give the GPU enough blocks.  k_verify_draw joins the parts, decides which drafts
+// stand (a few values a sequence, so that each of its blocks decides for
+// itself), and runs the race over the one row it ended at, that row in parts
+// again; the block that comes last joins them and writes the sequence's
+// outputs.
+// A race needs one value an id: no running sum across blocks, no order of
+// summation, and the ids' weights need not be normalised, only compared: a
+// beats b when r_a e_b > r_b e_a, without a division.
+// Exponentials are 2^((z - m) k), k = log2(e) / T, m an offset that trails the
+// running maximum; a row's sum S goes with its m, so that p = 2^((z - m) k) / S
+// never takes a difference of two log-sum-exps, and logits of any size keep their
+// accuracy.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "kd_internal.h"
+#include "kd_rows.cuh"
+
+namespace kd {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kUnroll = 4;
+constexpr int kMaxParts = 64;       // of a row
+constexpr int kMostDrafts = KD_VERIFY_MAX_DRAFTS;
+
+// Sum s of one row's (or a part's) exponentials 2^((z - m) k); best: cand_word of
+// the largest logit (greedy).
+struct RowSum {
+  float m, s;
+  uint64_t best;
+};
+// Leader of a race: weight r, noise e, id; nobody: r = 0.
+struct Leader {
+  float r, e;
+  uint32_t id;
+};
+
+struct VerifyArgs {
+  const void *zt, *zd;
+  const int64_t* drafts;
+  const int32_t* lengths;
+  const float *u, *noise;
+  int64_t b, vocab, ldt, ldd, ignore;
+  int k;
+  int greedy;
+  float kt, kd, inv_t;        // log2(e) / T of both, 1 / T of the target
+  int parts, race_parts;
+  RowSum* sums;               // [rows][parts]: B (K + 1) target rows, then B K of the drafter
+  Leader* leaders;            // [B][race_parts]
+  uint32_t* arrived;          // [B]
+  int64_t* tokens;
+  int32_t* accepted;
+  float* logprob;
+  uint32_t* status;
+};
+
+__device__ __forceinline__ int drafts_of(const VerifyArgs& a, int64_t b) {
+  if (!a.lengths) return a.k;
+  const int l = a.lengths[b];
+  return l > a.k ? a.k : l;  // negative: takes no part
+}
+
+// One part of a row of V elements: whole 16-byte vectors, and the loose
+// elements at either end of the row, which the first part takes.
+template <class T>
+struct Part {
+  static constexpr int N = RowVec<T>::N;
+  const T* z;
+  int64_t vocab;
+  int head, tail;             // loose elements
+  int64_t v0, v1;             // vectors
+
+  __device__ __forceinline__ Part(const T* z_, int64_t vocab_, int part, int parts)
+      : z(z_), vocab(vocab_) {
+    const int skew = (int)((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T));
+    const int64_t lead = min((int64_t)(skew ? N - skew : 0), vocab);
+    const int64_t vecs = (vocab - lead) / N;
+    head = (int)lead;
+    tail = (int)(vocab - lead - vecs * N);
+    v0 = vecs * part / parts;
+    v1 = vecs * (part + 1) / parts;
+    if (part) head_in = 0, tail = 0;
+    else head_in = head;
+  }
+  int head_in;
+  __device__ __forceinline__ const uint4* vectors() const {
+    return reinterpret_cast<const uint4*>(z + head);
+  }
+  __device__ __forceinline__ int loose() const { return head_in + tail; }
+  __device__ __forceinline__ int64_t loose_at(int i) const {
+    return i < head_in ? i : vocab - tail + (i - head_in);
+  }
+};
+
+// largest of a vector, a NaN kept
+__device__ __forceinline__ float vec_top(uint4 w, float) {
+  return max_nan(max_nan(__uint_as_float(w.x), __uint_as_float(w.y)),
+                 max_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ float vec_top(uint4 w, __nv_bfloat16) {
+  const uint32_t m = max_nan_bf16x2(max_nan_bf16x2(w.x, w.y), max_nan_bf16x2(w.z, w.w));
+  return max_nan(bf16lo(m), bf16hi(m));
+}
+
+struct Fold {
+  float k, m, up;  // a logit above `up` moves the offset
+  float2 s;
+  __device__ __forceinline__ void init(float k_) {
+    k = k_;
+    m = up = neg_inf();
+    s = make_float2(0.f, 0.f);
+  }
+  __device__ __forceinline__ void expect(float top) {
+    if (top > up) {
+      const float f = ex2((m - top) * k);
+      s = make_float2(s.x * f, s.y * f);
+      m = top;
+      up = top + 8.f / k;
+    }
+  }
+  __device__ __forceinline__ void pair(float z0, float z1) {
+    const float2 x = mul2(sub2(make_float2(z0, z1), make_float2(m, m)), make_float2(k, k));
+    s = add2(s, make_float2(ex2(x.x), ex2(x.y)));
+  }
+  __device__ __forceinline__ void one(float z) {
+    if (z == neg_inf()) return;
+    expect(z);
+    s.x += ex2((z - m) * k);
+  }
+};
+__device__ __forceinline__ void join_sum(float& m, float& s, float m2, float s2, float k) {
+  const float to = fmaxf(m, m2);
+  if (m != to) s *= ex2((m - to) * k);
+  if (m2 != to) s2 *= ex2((m2 - to) * k);
+  s += s2;
+  m = to;
+}
+// all lanes' sums, in every lane
+__device__ __forceinline__ void warp_sum(float& m, float& s, float k) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+    join_sum(m, s, m2, s2, k);
+  }
+}
+__device__ __forceinline__ uint64_t warp_best(uint64_t w) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const uint64_t x = __shfl_xor_sync(0xffffffffu, w, o);
+    w = x > w ? x : w;
+  }
+  return w;
+}
+// a row with a distribution: neither a NaN nor +infinity nor only -infinity
+__device__ __forceinline__ bool sum_ok(const RowSum& r) {
+  return r.s > 0.f && r.s < __int_as_float(0x7f800000) && fabsf(r.m) < __int_as_float(0x7f800000);
+}
+
+template <class T, bool GREEDY>
+__global__ void __launch_bounds__(kThreads) k_verify_sums(VerifyArgs a) {
+  constexpr int N = RowVec<T>::N;
+  __shared__ float wm[kWarps], ws[kWarps];
+  __shared__ uint64_t wb[kWarps];
+  chain_next();
+  const int64_t row = blockIdx.x / a.parts;
+  const int part = (int)(blockIdx.x - row * a.parts);
+  const int64_t targets = a.b * (a.k + 1);
+  const bool draft = row >= targets;
+  const int64_t in = draft ? row - targets : row;
+  const int per = draft ? a.k : a.k + 1;
+  const int64_t b = in / per;
+  const int i = (int)(in - b * per);
+  if (!draft && i == 0 && part == 0 && threadIdx.x == 0) a.arrived[b] = 0;
+  if (i >= drafts_of(a, b) + (draft ? 0 : 1) || drafts_of(a, b) < 0) return;
+  const T* z = static_cast<const T*>(draft ? a.zd : a.zt) + in * (draft ? a.ldd : a.ldt);
+  const Part<T> p(z, a.vocab, part, a.parts);
+  Fold f;
+  f.init(draft ? a.kd : a.kt);
+  float top = neg_inf();
+  int64_t top_at = 0;
+  const uint4* q = p.vectors();
+  const uint4 none = N == 8 ? make_uint4(kNegInfX2, kNegInfX2, kNegInfX2, kNegInfX2)
+                            : make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+  for (int64_t v = p.v0 + threadIdx.x; v < p.v1; v += kUnroll * kThreads) {
+    uint4 w[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      w[u] = v + u * kThreads < p.v1 ? q[v + u * kThreads] : none;
+    float m = vec_top(w[0], T());
+#pragma unroll
+    for (int u = 1; u < kUnroll; ++u) m = max_nan(m, vec_top(w[u], T()));
+    if (m == neg_inf()) continue;
+    f.expect(m);
+    if (GREEDY && m > top) {
+      top = m;
+      bool found = false;
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        float x[N];
+        RowVec<T>::get(w[u], x);
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (!found && x[e] == m) {
+            found = true;
+            top_at = p.head + (v + u * kThreads) * N + e;
+          }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      float x[N];
+      RowVec<T>::get(w[u], x);
+#pragma unroll
+      for (int e = 0; e < N; e += 2) f.pair(x[e], x[e + 1]);
+    }
+  }
+  uint64_t best = top == neg_inf() ? 0 : cand_word(order_key(top), (uint32_t)top_at);
+  if (threadIdx.x < p.loose()) {
+    const int64_t at = p.loose_at(threadIdx.x);
+    const float x = to_f(z[at]);
+    f.one(x);
+    if (GREEDY && x > neg_inf()) {
+      const uint64_t w = cand_word(order_key(x), (uint32_t)at);
+      best = w > best ? w : best;
+    }
+  }
+  float off = f.m, s = f.s.x + f.s.y;
+  warp_sum(off, s, f.k);
+  if (GREEDY) best = warp_best(best);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) {
+    wm[warp] = off;
+    ws[warp] = s;
+    wb[warp] = best;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    off = lane < kWarps ? wm[lane] : neg_inf();
+    s = lane < kWarps ? ws[lane] : 0.f;
+    best = lane < kWarps ? wb[lane] : 0;
+    warp_sum(off, s, f.k);
+    if (GREEDY) best = warp_best(best);
+    if (lane == 0) a.sums[row * a.parts + part] = RowSum{off, s, best};
+  }
+}
+
+// 2^((z - m) k), the roundings of z - m and of the product made up for
+__device__ __forceinline__ float power(float z, float m, float k) {
+  const float d = __fsub_rn(z, m), y = __fsub_rn(z, d);
+  const float lost = __fadd_rn(__fsub_rn(z, __fadd_rn(d, y)), __fsub_rn(y, m));
+  const float x = __fmul_rn(d, k), rest = fmaf(lost, k, fmaf(d, k, -x));
+  const float p = ex2(x) * fmaf(rest, kLn2, 1.f);
+  return x < -150.f ? 0.f : p;  // (z = -inf among others: rest is NaN then)
+}
+
+// a ahead of b
+__device__ __forceinline__ bool ahead(const Leader& a, const Leader& b) {
+  const float x = a.r * b.e, y = b.r * a.e;
+  return x > y || (x == y && a.id < b.id);
+}
+__device__ __forceinline__ Leader warp_leader(Leader l) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const Leader x{__shfl_xor_sync(0xffffffffu, l.r, o), __shfl_xor_sync(0xffffffffu, l.e, o),
+                   __shfl_xor_sync(0xffffffffu, l.id, o)};
+    if (ahead(x, l)) l = x;
+  }
+  return l;
+}
+
+// The race over ids [lo, hi) of one row.
+struct Race {
+  float kt, mt, inv_t;        // of the target's row
+  float kd, md, inv_d;        // of the drafter's (q taken away), inv_d = 0: none
+  int64_t out;                // this id has q = 1, -1: none
+
+  __device__ __forceinline__ void enter(Leader& l, float zt, float zd, float e, int64_t id) const {
+    float r = __fmul_rn(power(zt, mt, kt), inv_t);
+    if (inv_d > 0.f) r = __fsub_rn(r, __fmul_rn(power(zd, md, kd), inv_d));
+    if (id == out) r = 0.f;
+    const Leader n{r, e, (uint32_t)id};
+    if (r > 0.f && e >= 0x1p-100f && e <= 0x1p100f && ahead(n, l)) l = n;
+  }
+};
+template <class T>
+__device__ __forceinline__ Leader race_part(const Race& c, const T* zt, const T* zd,
+                                            const float* noise, int64_t lo, int64_t hi) {
+  constexpr int N = RowVec<T>::N;
+  Leader l{0.f, 1.f, 0xffffffffu};
+  const bool vec = ((reinterpret_cast<uintptr_t>(zt + lo) | reinterpret_cast<uintptr_t>(noise + lo) |
+                     (zd ? reinterpret_cast<uintptr_t>(zd + lo) : 0)) & 15) == 0;
+  int64_t loose = lo;
+  if (vec) {
+    const int64_t vecs = (hi - lo) / N;
+    loose = lo + vecs * N;
+    const uint4* pt = reinterpret_cast<const uint4*>(zt + lo);
+    const uint4* pd = reinterpret_cast<const uint4*>(zd + lo);
+    const float4* pe = reinterpret_cast<const float4*>(noise + lo);
+    for (int64_t v = threadIdx.x; v < vecs; v += kThreads) {
+      const uint4 wt = pt[v], wd = zd ? pd[v] : make_uint4(0, 0, 0, 0);
+      float xt[N], xd[N], e[N];
+#pragma unroll
+      for (int j = 0; j < N / 4; ++j) {
+        const float4 y = __ldcs(&pe[v * (N / 4) + j]);
+        e[4 * j] = y.x, e[4 * j + 1] = y.y, e[4 * j + 2] = y.z, e[4 * j + 3] = y.w;
+      }
+      RowVec<T>::get(wt, xt);
+      RowVec<T>::get(wd, xd);
+#pragma unroll
+      for (int j = 0; j < N; ++j) c.enter(l, xt[j], xd[j], e[j], lo + v * N + j);
+    }
+  }
+  for (int64_t v = loose + threadIdx.x; v < hi; v += kThreads)
+    c.enter(l, to_f(zt[v]), zd ? to_f(zd[v]) : 0.f, noise[v], v);
+  return l;
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads) k_verify_draw(VerifyArgs a) {
+  __shared__ RowSum tgt[kMostDrafts + 1], drf[kMostDrafts];
+  __shared__ Leader lead[kWarps];
+  __shared__ int stands, last;
+  __shared__ uint32_t trouble;
+  const int64_t b = blockIdx.x / a.race_parts;
+  const int part = (int)(blockIdx.x - b * a.race_parts);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = a.k + 1;
+  chain_wait();
+  const int len = drafts_of(a, b);
+  const bool over = a.lengths && a.lengths[b] > a.k;
+  const T* zt = static_cast<const T*>(a.zt) + b * rows * a.ldt;
+  const T* zd = static_cast<const T*>(a.zd) + b * a.k * a.ldd;
+  if (len < 0) {
+    if (part == 0) {
+      for (int i = threadIdx.x; i < rows; i += kThreads) {
+        if (a.tokens) a.tokens[b * rows + i] = a.ignore;
+        if (a.logprob) a.logprob[b * rows + i] = 0.f;
+      }
+      if (a.accepted && threadIdx.x == 0) a.accepted[b] = 0;
+    }
+    return;
+  }
+  // ---- the rows' sums
+  const bool has_q = a.zd != nullptr && !a.greedy;
+  for (int r = warp; r < len + 1 + (has_q ? len : 0); r += kWarps) {
+    const bool draft = r > len;
+    const int i = draft ? r - len - 1 : r;
+    const int64_t row = draft ? a.b * rows + b * a.k + i : b * rows + i;
+    const float k = draft ? a.kd : a.kt;
+    float m = neg_inf(), s = 0.f;
+    uint64_t best = 0;
+    for (int p = lane; p < a.parts; p += 32) {
+      const RowSum x = a.sums[row * a.parts + p];
+      join_sum(m, s, x.m, x.s, k);
+      best = x.best > best ? x.best : best;
+    }
+    warp_sum(m, s, k);
+    best = warp_best(best);
+    if (lane == 0) (draft ? drf[i] : tgt[i]) = RowSum{m, s, best};
+  }
+  __syncthreads();
+  // ---- the drafts that stand: a lane each
+  if (warp == 0) {
+    bool ok = false, bad = false, foreign = false;
+    if (lane < len) {
+      const int64_t x = a.drafts[b * a.k + lane];
+      foreign = x < 0 || x >= a.vocab;
+      const RowSum t = tgt[lane];
+      bad = !sum_ok(t);
+      if (a.greedy) {
+        ok = !foreign && !bad && (int64_t)(uint32_t)~(uint32_t)t.best == x;
+      } else {
+        const bool bad_q = has_q && !sum_ok(drf[lane]);
+        if (!foreign && !bad && !bad_q) {
+          const float p = power(to_f(zt[lane * a.ldt + x]), t.m, a.kt);
+          const float u = a.u[b * a.k + lane];
+          if (has_q) {
+            const RowSum d = drf[lane];
+            const float q = power(to_f(zd[lane * a.ldd + x]), d.m, a.kd);
+            // (products that do not round equal p and q to a rejection at u < 1)
+            ok = (double)u * (double)q * (double)t.s < (double)p * (double)d.s;
+          } else {
+            ok = (double)u * (double)t.s < (double)p;
+          }
+        }
+        bad = bad || bad_q;
+      }
+    }
+    const uint32_t oks = __ballot_sync(0xffffffffu, ok), bads = __ballot_sync(0xffffffffu, bad);
+    const uint32_t foreigns = __ballot_sync(0xffffffffu, foreign);
+    const int n = oks == 0xffffffffu ? 32 : __ffs(~oks) - 1;
+    // what lies behind the first that does not stand is not reported
+    const uint32_t seen = n >= 31 ? 0xffffffffu : (2u << n) - 1;
+    if (lane == 0) {
+      stands = n;
+      trouble = ((bads & seen) || !sum_ok(tgt[n]) ? KD_DEV_NONFINITE : 0) |
+                ((foreigns & seen) || over ? KD_DEV_BAD_LABEL : 0);
+    }
+  }
+  __syncthreads();
+  const int n = stands;
+  const RowSum row = tgt[n];
+  const bool alive = sum_ok(row);
+  // ---- the race
+  Leader l{0.f, 1.f, 0xffffffffu};
+  const float* noise = a.noise + b * a.vocab;
+  zt += n * a.ldt;
+  Race race{a.kt, row.m, 1.f / row.s, a.kd, 0.f, 0.f, -1};
+  const T* q = nullptr;
+  if (!a.greedy && alive) {
+    if (n < len) {
+      if (has_q && sum_ok(drf[n])) {
+        q = zd + n * a.ldd;
+        race.md = drf[n].m;
+        race.inv_d = 1.f / drf[n].s;
+      } else if (!has_q) {
+        race.out = a.drafts[b * a.k + n];
+      }
+    }
+    // parts of whole vectors of 16 logits
+    const int64_t units = (a.vocab + 15) / 16;
+    const int64_t lo = units * part / a.race_parts * 16;
+    const int64_t hi = min(units * (part + 1) / a.race_parts * 16, a.vocab);
+    l = race_part<T>(race, zt, q, noise, lo, hi);
+  }
+  auto block_leader = [&](Leader x) {
+    x = warp_leader(x);
+    __syncthreads();
+    if (lane == 0) lead[warp] = x;
+    __syncthreads();
+    x = lead[lane & (kWarps - 1)];
+    return warp_leader(x);
+  };
+  if (!a.greedy) l = block_leader(l);
+  if (a.race_parts > 1) {
+    if (threadIdx.x == 0) {
+      a.leaders[b * a.race_parts + part] = l;
+      __threadfence();
+      last = atomicAdd(&a.arrived[b], 1) == (uint32_t)a.race_parts - 1;
+      __threadfence();
+    }
+    __syncthreads();
+    if (!last) return;
+    l = Leader{0.f, 1.f, 0xffffffffu};
+    for (int p = threadIdx.x; p < a.race_parts; p += kThreads) {
+      const volatile Leader* o = &a.leaders[b * a.race_parts + p];
+      const Leader x{o->r, o->e, o->id};
+      if (ahead(x, l)) l = x;
+    }
+    l = block_leader(l);
+  }
+  if (!a.greedy && alive && !(l.r > 0.f) && n < len) {
+    // p <= q everywhere: no residual to draw from
+    race.inv_d = 0.f;
+    race.out = -1;
+    l = block_leader(race_part<T>(race, zt, (const T*)nullptr, noise, 0, a.vocab));
+  }
+  // ---- outputs
+  const bool drawn = alive && (a.greedy || l.r > 0.f);
+  const int64_t token = a.greedy ? (int64_t)(uint32_t)~(uint32_t)row.best : (int64_t)l.id;
+  if (threadIdx.x < rows) {
+    const int i = threadIdx.x;
+    const int64_t x = i < n ? a.drafts[b * a.k + i] : i == n && drawn ? token : a.ignore;
+    if (a.tokens) a.tokens[b * rows + i] = x;
+    if (a.logprob) {
+      float lp = 0.f;
+      if (i < n || (i == n && drawn)) {
+        const RowSum t = tgt[i];
+        const float z = to_f(zt[(i - n) * a.ldt + x]);
+        lp = fmaf(z - t.m, a.inv_t, -logf(t.s));
+      } else if (i == n) {
+        lp = __int_as_float(0x7fffffff);
+      }
+      a.logprob[b * rows + i] = lp;
+    }
+  }
+  if (threadIdx.x == 0) {
+    if (a.accepted) a.accepted[b] = n;
+    const uint32_t t = trouble | (drawn ? 0u : KD_DEV_NONFINITE);
+    if (t) set_status(a.status, t);
+  }
+}
+
+// ------------------------------------------------------------------ plan
+struct VerifyPlan {
+  int parts, race_parts;
+  int64_t rows;
+  size_t sums, leaders, arrived, bytes;
+};
+
+kd_status verify_plan(const kd_verify_problem* p, VerifyPlan& P) {
+  if (!p || p->n_seqs < 0 || p->n_seqs > (int64_t)1 << 20 || p->vocab < 1 ||
+      p->vocab > (int64_t)1 << 30 || p->n_drafts < 0 || p->n_drafts > KD_VERIFY_MAX_DRAFTS)
+    return KD_ERR_INVALID_ARG;
+  if (p->dtype != KD_BF16 && p->dtype != KD_FP32) return KD_ERR_INVALID_ARG;
+  if (!(std::isfinite(p->t_target) && p->t_target >= 0.f) ||
+      !(std::isfinite(p->t_draft) && p->t_draft > 0.f) || !std::isfinite(kL2E / p->t_draft) ||
+      (p->t_target > 0.f && !std::isfinite(kL2E / p->t_target)))
+    return KD_ERR_INVALID_ARG;
+  if ((p->ld_target && p->ld_target < p->vocab) || (p->ld_draft && p->ld_draft < p->vocab))
+    return KD_ERR_INVALID_ARG;
+  const int nsm = std::max(1, tc_num_sms());
+  const int64_t bytes = p->vocab * (p->dtype == KD_BF16 ? 2 : 4);
+  P.rows = p->n_seqs * (2 * p->n_drafts + 1);
+  const int64_t r = std::max<int64_t>(P.rows, 1), b = std::max<int64_t>(p->n_seqs, 1);
+  // parts of at least 8 KB, some 16 blocks an SM
+  P.parts = (int)std::max<int64_t>(1, std::min<int64_t>({rows_div((int64_t)nsm * 16, r),
+                                                         bytes / 8192, kMaxParts}));
+  P.race_parts = (int)std::max<int64_t>(1, std::min<int64_t>({rows_div((int64_t)nsm * 4, b),
+                                                              p->vocab / 2048, kMaxParts}));
+  size_t off = 0;
+  P.sums = rows_take(off, (size_t)r * P.parts * sizeof(RowSum));
+  P.leaders = rows_take(off, (size_t)b * P.race_parts * sizeof(Leader));
+  P.arrived = rows_take(off, (size_t)b * 4);
+  P.bytes = off;
+  return KD_OK;
+}
+
+// An output over an input, or over another output.
+bool verify_overlaps(const kd_verify_problem* p, const kd_verify_inputs* in, const int64_t* tokens,
+                     const int32_t* accepted, const float* logprob) {
+  const size_t n = (size_t)p->n_seqs, k = (size_t)p->n_drafts, v = (size_t)p->vocab;
+  const size_t esz = p->dtype == KD_BF16 ? 2 : 4;
+  const size_t lt = p->ld_target ? p->ld_target : v, ld = p->ld_draft ? p->ld_draft : v;
+  struct Span {
+    const void* p;
+    size_t bytes;
+  };
+  const Span outs[] = {{tokens, n * (k + 1) * 8}, {accepted, n * 4}, {logprob, n * (k + 1) * 4}};
+  const Span ins[] = {{in->target_logits, ((n * (k + 1) - 1) * lt + v) * esz},
+                      {k ? in->draft_logits : nullptr, k ? ((n * k - 1) * ld + v) * esz : 0},
+                      {in->drafts, n * k * 8}, {in->lengths, n * 4}, {in->uniform, n * k * 4},
+                      {in->noise, n * v * 4}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Span& x : ins)
+      if (rows_meet(outs[i].p, outs[i].bytes, x.p, x.bytes)) return true;
+    for (int j = 0; j < i; ++j)
+      if (rows_meet(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return true;
+  }
+  return false;
+}
+
+template <class T>
+bool verify_run(const VerifyArgs& a, int64_t rows, cudaStream_t s) {
+  const bool ok = a.greedy
+      ? rows_launch(k_verify_sums<T, true>, rows * a.parts, kThreads, 0, false, s, a)
+      : rows_launch(k_verify_sums<T, false>, rows * a.parts, kThreads, 0, false, s, a);
+  return ok && rows_launch(k_verify_draw<T>, a.b * a.race_parts, kThreads, 0, true, s, a);
+}
+
+}  // namespace
+}  // namespace kd
+
+using namespace kd;
+
+extern "C" kd_status kd_verify_workspace_size(const kd_verify_problem* p, size_t* bytes) {
+  VerifyPlan P;
+  const kd_status st = verify_plan(p, P);
+  if (st != KD_OK) return st;
+  if (bytes) *bytes = P.bytes;
+  return KD_OK;
+}
+
+extern "C" kd_status kd_verify_drafts(const kd_verify_problem* p, const kd_verify_inputs* in,
+                                      int64_t* tokens, int32_t* accepted, float* logprob,
+                                      uint32_t* dev_status, void* workspace, size_t ws_bytes,
+                                      void* stream) {
+  VerifyPlan P;
+  kd_status st = verify_plan(p, P);
+  if (st != KD_OK) return st;
+  if (!in) return KD_ERR_INVALID_ARG;
+  const bool greedy = p->t_target == 0.f;
+  const int64_t n = p->n_seqs, k = p->n_drafts, v = p->vocab;
+  const size_t esz = p->dtype == KD_BF16 ? 2 : 4;
+  if (n > 0 && (!in->target_logits || (k > 0 && !in->drafts) || (!greedy && !in->noise) ||
+                (!greedy && k > 0 && !in->uniform)))
+    return KD_ERR_INVALID_ARG;
+  if (!rows_aligned(esz, in->target_logits, in->draft_logits) ||
+      !rows_aligned(8, in->drafts, tokens) ||
+      !rows_aligned(4, in->lengths, in->uniform, in->noise, accepted, logprob, dev_status))
+    return KD_ERR_INVALID_ARG;
+  if (n > 0 && verify_overlaps(p, in, tokens, accepted, logprob)) return KD_ERR_INVALID_ARG;
+  if (!rows_ws_ok(workspace, ws_bytes, P.bytes)) return KD_ERR_WORKSPACE;
+  if ((st = rows_device()) != KD_OK || n == 0) return st;
+  char* ws = static_cast<char*>(workspace);
+  VerifyArgs a;
+  memset(&a, 0, sizeof(a));
+  a.zt = in->target_logits;
+  a.zd = k > 0 && !greedy ? in->draft_logits : nullptr;
+  a.drafts = in->drafts;
+  a.lengths = in->lengths;
+  a.u = in->uniform;
+  a.noise = in->noise;
+  a.b = n;
+  a.vocab = v;
+  a.ldt = p->ld_target ? p->ld_target : v;
+  a.ldd = p->ld_draft ? p->ld_draft : v;
+  a.ignore = p->ignore_index;
+  a.k = (int)k;
+  a.greedy = greedy;
+  a.kt = greedy ? kL2E : kL2E / p->t_target;
+  a.kd = kL2E / p->t_draft;
+  a.inv_t = greedy ? 1.f : 1.f / p->t_target;
+  a.parts = P.parts;
+  a.race_parts = greedy ? 1 : P.race_parts;
+  a.sums = reinterpret_cast<RowSum*>(ws + P.sums);
+  a.leaders = reinterpret_cast<Leader*>(ws + P.leaders);
+  a.arrived = reinterpret_cast<uint32_t*>(ws + P.arrived);
+  a.tokens = tokens;
+  a.accepted = accepted;
+  a.logprob = logprob;
+  a.status = dev_status;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t rows = a.zd ? P.rows : n * (k + 1);
+  const bool ok = esz == 2 ? verify_run<__nv_bfloat16>(a, rows, s) : verify_run<float>(a, rows, s);
+  return ok && cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA;
+}

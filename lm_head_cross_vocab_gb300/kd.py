@@ -10,7 +10,9 @@ Low-level names mirror the ABI one to one: ``kd_workspace_size``, ``kd_fwd``,
 ``kd_bwd``, ``kd_status_string``, ``kd_device_supported``, ``kd_abi_version``,
 ``kd_diag_gemm_bf16``.  ``forward`` / ``backward`` are conveniences that build
 the structs from keyword arguments and tensors, and so are ``token_logprobs`` /
-``token_logprobs_backward`` (kd_logprob_*) and ``clip_grad_norm``.
+``token_logprobs_backward`` (kd_logprob_*), ``clip_grad_norm``, ``verify_drafts``,
+``embed_tokens`` / ``embed_tokens_backward`` (kd_embed_*) and ``rms_norm`` /
+``rms_norm_backward`` (kd_rmsnorm_*).
 """
 from __future__ import annotations
 
@@ -87,6 +89,34 @@ class kd_logprob_inputs(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in ("logits", "h", "w", "tokens")]
 
 
+class kd_verify_problem(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int64), ("vocab", ctypes.c_int64), ("ld_target", ctypes.c_int64),
+        ("ld_draft", ctypes.c_int64), ("ignore_index", ctypes.c_int64),
+        ("n_drafts", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("t_target", ctypes.c_float), ("t_draft", ctypes.c_float),
+    ]
+
+
+class kd_verify_inputs(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in
+                ("target_logits", "draft_logits", "drafts", "lengths", "uniform", "noise")]
+
+
+class kd_embed_problem(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("d_model", ctypes.c_int64),
+        ("ignore_index", ctypes.c_int64), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+    ]
+
+
+class kd_rmsnorm_problem(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int64), ("d_model", ctypes.c_int64), ("dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+    ]
+
+
 class KDError(RuntimeError):
     def __init__(self, status: int, where: str):
         super().__init__(f"{where}: {kd_status_string(status)} (status {status})")
@@ -136,13 +166,26 @@ def load_library(path: str = LIB_PATH):
     lib.kd_clip_grad_norm_workspace_size.argtypes = [vp, i32, sz]
     lib.kd_clip_grad_norm.argtypes = [vp, vp, vp, i32, i32, ctypes.c_float, vp, vp, vp,
                                       ctypes.c_size_t, vp]
+    V, VI = ctypes.POINTER(kd_verify_problem), ctypes.POINTER(kd_verify_inputs)
+    E, R = ctypes.POINTER(kd_embed_problem), ctypes.POINTER(kd_rmsnorm_problem)
+    lib.kd_verify_workspace_size.argtypes = [V, sz]
+    lib.kd_verify_drafts.argtypes = [V, VI, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.kd_embed_workspace_size.argtypes = [E, sz]
+    lib.kd_embed_fwd.argtypes = [E, vp, vp, vp, vp, vp]
+    lib.kd_embed_bwd.argtypes = [E, vp, vp, vp, i32, vp, vp, ctypes.c_size_t, vp]
+    lib.kd_rmsnorm_workspace_size.argtypes = [R, sz]
+    lib.kd_rmsnorm_fwd.argtypes = [R, vp, vp, vp, vp, vp, vp]
+    lib.kd_rmsnorm_bwd.argtypes = [R, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
     lib.kd_launch_count.restype = ctypes.c_uint64
     for f in ("kd_workspace_size", "kd_fwd", "kd_bwd", "kd_device_supported", "kd_abi_version",
               "kd_diag_gemm_bf16", "kd_set_profile_events", "kd_set_profile_launch_events",
               "kd_fwd_static_scratch", "kd_project_workspace_size", "kd_project_teacher_logits",
               "kd_plan_info", "kd_mix_teacher_logits", "kd_bwd_grads",
               "kd_logprob_workspace_size", "kd_logprob_fwd", "kd_logprob_bwd",
-              "kd_clip_grad_norm_workspace_size", "kd_clip_grad_norm"):
+              "kd_clip_grad_norm_workspace_size", "kd_clip_grad_norm",
+              "kd_verify_workspace_size", "kd_verify_drafts", "kd_embed_workspace_size",
+              "kd_embed_fwd", "kd_embed_bwd", "kd_rmsnorm_workspace_size", "kd_rmsnorm_fwd",
+              "kd_rmsnorm_bwd"):
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -343,7 +386,8 @@ class Workspace:
         return (base + 255) // 256 * 256, nbytes
 
 
-def check_status(dev_status: torch.Tensor, assume_valid: bool = False):
+def check_status(dev_status: torch.Tensor, assume_valid: bool = False,
+                 nonfinite: str = "the gradient norm is infinite or NaN"):
     s = int(dev_status.item())
     if s & KD_DEV_TIMEOUT:
         raise KDError(KD_ERR_TIMEOUT, "device")
@@ -352,7 +396,7 @@ def check_status(dev_status: torch.Tensor, assume_valid: bool = False):
     if s & KD_DEV_BAD_MAP:
         raise KDError(KD_ERR_INVALID_ARG, "token map entry outside [-1, V_student)")
     if s & KD_DEV_NONFINITE:
-        raise KDError(KD_ERR_INVALID_ARG, "the gradient norm is infinite or NaN")
+        raise KDError(KD_ERR_INVALID_ARG, nonfinite)
     if not assume_valid:
         if s & KD_DEV_BAD_LABEL:
             raise KDError(KD_ERR_BAD_LABEL, "device")
@@ -637,11 +681,11 @@ def _status_word(out: dict, device) -> int:
     return w.data_ptr()
 
 
-def _check_and_tell(dev_status: torch.Tensor):
+def _check_and_tell(dev_status: torch.Tensor, **kw):
     """check_status of a word that later calls use again: what is raised is
     cleared.  (A call that is not checked only adds its bits.)"""
     try:
-        check_status(dev_status)
+        check_status(dev_status, **kw)
     except KDError:
         dev_status.zero_()
         raise
@@ -792,3 +836,259 @@ def clip_grad_norm(grads, max_norm: float, *, out=None, workspace: Optional[Work
     if check:
         _check_and_tell(gl.dev_status)
     return {"norm": norm, "grads": gl.out, "dev_status": gl.dev_status}
+
+
+# ---------------------------------------------------------------- drafted tokens
+
+KD_VERIFY_MAX_DRAFTS = 32
+
+
+@dataclasses.dataclass(frozen=True)
+class VerifyProblem:
+    """Keyword form of ``kd_verify_problem`` (row pitches come from the tensors).
+    ``t_target`` = 0 is greedy; ``t_draft`` = None is t_target (1 where that is 0)."""
+
+    n_seqs: int
+    vocab: int
+    n_drafts: int = 0
+    dtype: str = "bf16"
+    t_target: float = 1.0
+    t_draft: Optional[float] = None
+    ignore_index: int = -100
+
+    def to_c(self, ld_target: int = 0, ld_draft: int = 0) -> kd_verify_problem:
+        t_draft = (self.t_target or 1.0) if self.t_draft is None else self.t_draft
+        return kd_verify_problem(self.n_seqs, self.vocab, ld_target, ld_draft, self.ignore_index,
+                                 self.n_drafts, DTYPES[self.dtype], self.t_target, t_draft)
+
+
+def _seq_rows_pitch(name: str, t: torch.Tensor, shape, dtype, device) -> int:
+    """Row pitch of [B, K, V] logits whose rows lie at one pitch (0 when dense)."""
+    _same(name, t, shape, dtype, device)
+    if t.is_contiguous():
+        return 0
+    b, k, v = shape
+    s0, s1, s2 = t.stride()
+    pitch = s1 if k > 1 else s0
+    if (s2 != 1 and v > 1) or pitch < v or (b > 1 and k > 0 and s0 != k * pitch):
+        raise ValueError(f"{name}: rows must be contiguous, at one pitch, and may not overlap")
+    return pitch
+
+
+def kd_verify_workspace_size(problem: kd_verify_problem) -> int:
+    n = ctypes.c_size_t(0)
+    st = load_library().kd_verify_workspace_size(ctypes.byref(problem), ctypes.byref(n))
+    if st != KD_OK:
+        raise KDError(st, "kd_verify_workspace_size")
+    return n.value
+
+
+def verify_drafts(problem: VerifyProblem, tensors: dict, workspace: Optional[Workspace] = None,
+                  check: bool = True, out: Optional[dict] = None):
+    """Run kd_verify_drafts; returns dict(tokens, accepted, logprob, dev_status).
+
+    ``tensors``: ``target_logits`` [B, K + 1, V], ``draft_logits`` [B, K, V] (or
+    none: deterministic drafts), ``drafts`` int64 [B, K], ``lengths`` int32 [B]
+    (or none: K each), ``uniform`` fp32 [B, K] in [0, 1) and ``noise`` fp32
+    [B, V], exponential (``Tensor.exponential_``); greedy (t_target = 0) needs
+    no random numbers and does not read draft_logits.  A drafter over another
+    vocabulary: give ``project_teacher_logits`` of its logits, with t_draft = 1.
+    ``out`` and its dev_status are as token_logprobs'."""
+    b, k, v, f32 = problem.n_seqs, problem.n_drafts, problem.vocab, torch.float32
+    target = tensors.get("target_logits")
+    if target is None or not target.is_cuda:
+        raise ValueError("target_logits must be given as a CUDA tensor")
+    dev, dtype = target.device, _TORCH_DTYPES[problem.dtype]
+    draft = tensors.get("draft_logits")
+    ldt = _seq_rows_pitch("target_logits", target, (b, k + 1, v), dtype, dev)
+    ldd = 0 if draft is None else _seq_rows_pitch("draft_logits", draft, (b, k, v), dtype, dev)
+    ins = kd_verify_inputs(
+        target.data_ptr(), _ptr(draft),
+        _dense("drafts", tensors.get("drafts"), (b, k), torch.int64, dev),
+        _dense("lengths", tensors.get("lengths"), (b,), torch.int32, dev),
+        _dense("uniform", tensors.get("uniform"), (b, k), f32, dev),
+        _dense("noise", tensors.get("noise"), (b, v), f32, dev))
+    if out is None:
+        out = {"tokens": torch.empty(b, k + 1, device=dev, dtype=torch.int64),
+               "accepted": torch.empty(b, device=dev, dtype=torch.int32),
+               "logprob": torch.empty(b, k + 1, device=dev, dtype=f32)}
+    ptrs = (_dense("tokens", out.get("tokens"), (b, k + 1), torch.int64, dev),
+            _dense("accepted", out.get("accepted"), (b,), torch.int32, dev),
+            _dense("logprob", out.get("logprob"), (b, k + 1), f32, dev),
+            _status_word(out, dev))
+    cp = problem.to_c(ldt, ldd)
+    ws = workspace or Workspace()
+    with _on(dev) as stream:
+        wptr, wbytes = ws.get(kd_verify_workspace_size(cp), dev)
+        st = load_library().kd_verify_drafts(ctypes.byref(cp), ctypes.byref(ins), *ptrs, wptr,
+                                             wbytes, stream)
+    if st != KD_OK:
+        raise KDError(st, "kd_verify_drafts")
+    if check:
+        _check_and_tell(out["dev_status"], nonfinite="a row of logits has no distribution")
+    return out
+
+
+# ---------------------------------------------------------------- embedding
+
+@dataclasses.dataclass(frozen=True)
+class EmbedProblem:
+    """Keyword form of ``kd_embed_problem``."""
+
+    n_tokens: int
+    vocab: int
+    d_model: int
+    dtype: str = "bf16"
+    scale: float = 1.0
+    ignore_index: int = -100
+
+    def to_c(self) -> kd_embed_problem:
+        return kd_embed_problem(self.n_tokens, self.vocab, self.d_model, self.ignore_index,
+                                DTYPES[self.dtype], self.scale)
+
+
+def kd_embed_workspace_size(problem: kd_embed_problem) -> int:
+    n = ctypes.c_size_t(0)
+    st = load_library().kd_embed_workspace_size(ctypes.byref(problem), ctypes.byref(n))
+    if st != KD_OK:
+        raise KDError(st, "kd_embed_workspace_size")
+    return n.value
+
+
+def embed_tokens(problem: EmbedProblem, w: torch.Tensor, tokens: torch.Tensor, *,
+                 check: bool = True, out: Optional[dict] = None):
+    """Run kd_embed_fwd; returns dict(h, dev_status): ``h`` [N, D], the rows
+    scale * w[tokens] of the table [V, D], zero where a token is ignore_index.
+    ``out`` and its dev_status are as token_logprobs'."""
+    n, d = problem.n_tokens, problem.d_model
+    if not w.is_cuda:
+        raise ValueError("w must be a CUDA tensor")
+    dev, dtype = w.device, _TORCH_DTYPES[problem.dtype]
+    pw = _dense("w", w, (problem.vocab, d), dtype, dev)
+    pt = _dense("tokens", tokens, (n,), torch.int64, dev)
+    if out is None:
+        out = {"h": torch.empty(n, d, device=dev, dtype=dtype)}
+    ph, status = _dense("h", out["h"], (n, d), dtype, dev), _status_word(out, dev)
+    with _on(dev) as stream:
+        st = load_library().kd_embed_fwd(ctypes.byref(problem.to_c()), pt, pw, ph, status, stream)
+    if st != KD_OK:
+        raise KDError(st, "kd_embed_fwd")
+    if check:
+        _check_and_tell(out["dev_status"])
+    return out
+
+
+def embed_tokens_backward(problem: EmbedProblem, tokens: torch.Tensor, d_h: torch.Tensor, *,
+                          accumulate: bool = False, workspace: Optional[Workspace] = None,
+                          check: bool = True, out: Optional[dict] = None):
+    """Run kd_embed_bwd; returns dict(d_w, dev_status): ``d_w`` [V, D], for each
+    id the sum of scale * d_h over its rows.  ``accumulate`` adds to the ``d_w``
+    that ``out`` brings, for example the head gradient of a tied model."""
+    n, v, d = problem.n_tokens, problem.vocab, problem.d_model
+    if not d_h.is_cuda:
+        raise ValueError("d_h must be a CUDA tensor")
+    dev, dtype = d_h.device, _TORCH_DTYPES[problem.dtype]
+    pt = _dense("tokens", tokens, (n,), torch.int64, dev)
+    pg = _dense("d_h", d_h, (n, d), dtype, dev)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs the d_w to add to, in out")
+        out = {"d_w": torch.empty(v, d, device=dev, dtype=dtype)}
+    pw, status = _dense("d_w", out["d_w"], (v, d), dtype, dev), _status_word(out, dev)
+    cp = problem.to_c()
+    ws = workspace or Workspace()
+    with _on(dev) as stream:
+        wptr, wbytes = ws.get(kd_embed_workspace_size(cp), dev)
+        st = load_library().kd_embed_bwd(ctypes.byref(cp), pt, pg, pw, int(accumulate), status,
+                                         wptr, wbytes, stream)
+    if st != KD_OK:
+        raise KDError(st, "kd_embed_bwd")
+    if check:
+        _check_and_tell(out["dev_status"])
+    return out
+
+
+# ---------------------------------------------------------------- norm
+
+KD_RMSNORM_MAX_D = 32768
+
+
+@dataclasses.dataclass(frozen=True)
+class NormProblem:
+    """Keyword form of ``kd_rmsnorm_problem``."""
+
+    n_tokens: int
+    d_model: int
+    dtype: str = "bf16"
+    eps: float = 1e-6
+    weight_offset: float = 0.0
+
+    def to_c(self) -> kd_rmsnorm_problem:
+        return kd_rmsnorm_problem(self.n_tokens, self.d_model, DTYPES[self.dtype], self.eps,
+                                  self.weight_offset)
+
+
+def kd_rmsnorm_workspace_size(problem: kd_rmsnorm_problem) -> int:
+    n = ctypes.c_size_t(0)
+    st = load_library().kd_rmsnorm_workspace_size(ctypes.byref(problem), ctypes.byref(n))
+    if st != KD_OK:
+        raise KDError(st, "kd_rmsnorm_workspace_size")
+    return n.value
+
+
+def rms_norm(problem: NormProblem, x: torch.Tensor, weight: torch.Tensor, *,
+             residual: Optional[torch.Tensor] = None, out: Optional[dict] = None):
+    """Run kd_rmsnorm_fwd; returns dict(h, sum): the normalised rows of
+    x + residual, and that sum (None without a residual, unless ``out`` brings a
+    buffer for it; the backward takes it, or x itself).  ``out`` may bring x or
+    residual as h or sum."""
+    n, d = problem.n_tokens, problem.d_model
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    dev, dtype = x.device, _TORCH_DTYPES[problem.dtype]
+    if out is None:
+        out = {"h": torch.empty(n, d, device=dev, dtype=dtype),
+               "sum": torch.empty(n, d, device=dev, dtype=dtype) if residual is not None else None}
+    rows = (n, d)
+    args = (_dense("x", x, rows, dtype, dev), _dense("residual", residual, rows, dtype, dev),
+            _dense("weight", weight, (d,), dtype, dev),
+            _dense("sum", out.get("sum"), rows, dtype, dev),
+            _dense("h", out["h"], rows, dtype, dev))
+    with _on(dev) as stream:
+        st = load_library().kd_rmsnorm_fwd(ctypes.byref(problem.to_c()), *args, stream)
+    if st != KD_OK:
+        raise KDError(st, "kd_rmsnorm_fwd")
+    return out
+
+
+def rms_norm_backward(problem: NormProblem, s: torch.Tensor, weight: torch.Tensor,
+                      d_h: torch.Tensor, *, d_sum: Optional[torch.Tensor] = None,
+                      want=("x", "weight"), workspace: Optional[Workspace] = None,
+                      out: Optional[dict] = None):
+    """Run kd_rmsnorm_bwd; returns dict of the requested gradients: ``d_x`` [N, D]
+    (of x and of the residual alike) and ``d_weight`` [D].  ``s`` is rms_norm's
+    sum, or its x where there was no residual; ``d_sum`` the gradient that
+    reaches that sum from elsewhere.  ``out`` may bring the gradients' own
+    buffers, d_x among s, d_h and d_sum."""
+    n, d = problem.n_tokens, problem.d_model
+    if not s.is_cuda:
+        raise ValueError("s must be a CUDA tensor")
+    dev, dtype, rows = s.device, _TORCH_DTYPES[problem.dtype], (n, d)
+    if out is None:
+        out = {}
+        if "x" in want:
+            out["d_x"] = torch.empty(n, d, device=dev, dtype=dtype)
+        if "weight" in want:
+            out["d_weight"] = torch.empty(d, device=dev, dtype=dtype)
+    args = (_dense("s", s, rows, dtype, dev), _dense("weight", weight, (d,), dtype, dev),
+            _dense("d_h", d_h, rows, dtype, dev), _dense("d_sum", d_sum, rows, dtype, dev),
+            _dense("d_x", out.get("d_x"), rows, dtype, dev),
+            _dense("d_weight", out.get("d_weight"), (d,), dtype, dev))
+    cp = problem.to_c()
+    ws = workspace or Workspace()
+    with _on(dev) as stream:
+        wptr, wbytes = ws.get(kd_rmsnorm_workspace_size(cp), dev)
+        st = load_library().kd_rmsnorm_bwd(ctypes.byref(cp), *args, wptr, wbytes, stream)
+    if st != KD_OK:
+        raise KDError(st, "kd_rmsnorm_bwd")
+    return out
