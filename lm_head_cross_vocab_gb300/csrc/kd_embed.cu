@@ -2,19 +2,18 @@
 //
 //   h[n] = scale W[tokens[n]],   d_w[v] (+)= scale sum_{n : tokens[n] = v} d_h[n]
 //
-// The gradient is a segmented sum over the tokens sorted by id, in three
-// launches:
-//   k_embed_sort    a block owns a range of ids and reads all tokens twice: it
-//                   counts its ids (and the tokens below them, which is where its
-//                   part of the sorted list starts: no block waits for another),
-//                   then writes its tokens' places.  A warp has its own run of
-//                   the tokens and its own counters, so the list is stable: by id,
-//                   and by n within an id.
-//   k_embed_reduce  a block has kRun places of the sorted list and some columns,
+// The gradient is a segmented sum over the tokens sorted into groups of one id,
+// in three launches:
+//   k_embed_sort    a block owns every G-th id and reads all tokens: it keeps and
+//                   counts its own (and counts the tokens of the blocks before it,
+//                   which is where its part of the list starts: no block waits for
+//                   another), then writes its tokens' places, an id's rows in their
+//                   order.  Every G-th id, since text's frequent ids are neighbours.
+//   k_embed_reduce  a team of threads has a run of the list and some columns,
 //                   and adds up the pieces that start there.  An id with fewer than
 //                   2 kPiece tokens is one piece and is written at once; more are
 //                   cut into pieces of kPiece rows (the last one longer), so that
-//                   a frequent token is not one block's work; their fp32 sums go
+//                   a frequent token is not one team's work; their fp32 sums go
 //                   to the workspace.
 //   k_embed_join    adds the pieces of each such id in order.
 // Each sum's order depends on the tokens alone.
@@ -93,24 +92,30 @@ __global__ void __launch_bounds__(kLookupThreads) k_embed_rows(LookupArgs a) {
 
 // ------------------------------------------------------------------ sort
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
-constexpr int kMaxIds = 1024;  // ids of a block
+constexpr int kMaxIds = 1536;  // ids of a block
 constexpr int kAhead = 8;      // tokens a lane has in flight
+constexpr int kKept = 256;     // tokens a warp keeps
 
-// Places of one id in the sorted list.
+// Places of one id in the list.
 struct Segment {
   int32_t first, count;
+};
+struct Place {
+  int32_t row, id;
 };
 
 struct SortArgs {
   const int64_t* tokens;
   int64_t n, vocab, ignore;
-  int ids;            // of a block
+  int lg, ids;        // 2^lg blocks, ids of a block
   Segment* seg;       // [vocab]
-  int32_t *pos, *id;  // sorted: row, id
+  Place* place;       // [n]
+  int32_t* live;      // places in all
   uint32_t* status;
 };
 
-__device__ __forceinline__ int block_scan_1024(int v, int* warp_sum, int& total) {
+// Sum over the threads before this one; `total` over all.
+__device__ __forceinline__ int block_scan(int v, int* warp_sum, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
 #pragma unroll
@@ -128,79 +133,155 @@ __device__ __forceinline__ int block_scan_1024(int v, int* warp_sum, int& total)
   }
   total = __shfl_sync(0xffffffffu, w, 31);
   const int before = warp ? __shfl_sync(0xffffffffu, w, warp - 1) : 0;
-  return before + x - v;  // exclusive
+  return before + x - v;
+}
+
+// Dynamic shared memory: either [ids] counters and two lists of the tokens kept,
+// or (too many for a list) [kSortWarps][ids] counters.
+constexpr int kListBytes = kSortWarps * kKept * (int)sizeof(Place);
+__host__ __device__ constexpr int sort_smem(int ids) {
+  const int few = (ids * 4 + 15) / 16 * 16 + 2 * kListBytes, many = kSortWarps * ids * 4;
+  return few > many ? few : many;
 }
 
 __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a) {
-  extern __shared__ int counter[];  // [kSortWarps][ids]
-  __shared__ int warp_sum[32], below_sum;
+  extern __shared__ __align__(16) int counter[];
+  __shared__ int warp_sum[32], kept[32], below_sum, crowded;
   chain_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t lo = (int64_t)blockIdx.x * a.ids;
-  for (int i = threadIdx.x; i < kSortWarps * a.ids; i += kSortThreads) counter[i] = 0;
-  if (threadIdx.x == 0) below_sum = 0;
-  __syncthreads();
+  const uint32_t block = blockIdx.x, mask = (1u << a.lg) - 1, before = (1u << lane) - 1;
+  Place* list = reinterpret_cast<Place*>(counter + (a.ids + 3) / 4 * 4);
+  Place* all = list + kSortWarps * kKept;
+  for (int i = threadIdx.x; i < a.ids; i += kSortThreads) counter[i] = 0;
+  if (threadIdx.x == 0) below_sum = crowded = 0;
   // this warp's run of the tokens, whole groups of 32
   const int64_t groups = (a.n + 31) / 32, each = (groups + kSortWarps - 1) / kSortWarps;
   const int64_t begin = warp * each * 32, end = min((warp + 1) * each * 32, a.n);
-  int* mine = counter + warp * a.ids;
-  auto fetch = [&](int64_t at) {  // an id, or -1
-    if (at >= end) return (int64_t)-1;
-    const int64_t t = a.tokens[at];
-    if (t == a.ignore) return (int64_t)-1;
-    if (t < 0 || t >= a.vocab) {
-      if (blockIdx.x == 0) set_status(a.status, KD_DEV_BAD_LABEL);
-      return (int64_t)-1;
-    }
-    return t;
-  };
+  // the block's own number of a token's id, or -1; `below` counts the tokens of the
+  // blocks before it
   int below = 0;
-  // (each warp reads its run twice, and nobody writes it: no copy is kept)
+  auto own = [&](int64_t at) {
+    const int64_t t = at < end ? a.tokens[at] : a.ignore;
+    if (t == a.ignore) return -1;
+    if ((uint64_t)t >= (uint64_t)a.vocab) {
+      if (block == 0) set_status(a.status, KD_DEV_BAD_LABEL);
+      return -1;
+    }
+    const uint32_t of = (uint32_t)t & mask;
+    below += of < block;
+    return of == block ? (int)((uint32_t)t >> a.lg) : -1;
+  };
+  auto put = [&](int p, int64_t row, int k) {
+    a.place[p] = Place{(int32_t)row, (int32_t)(((uint32_t)k << a.lg) + block)};
+  };
+  __syncthreads();
+  int mine = 0;  // tokens of this warp's run that the block owns
   for (int64_t at = begin + lane; at - lane < end; at += 32 * kAhead) {
-    int64_t t[kAhead];
+    int k[kAhead];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) t[u] = fetch(at + u * 32);
+    for (int u = 0; u < kAhead; ++u) k[u] = own(at + u * 32);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      if (t[u] >= 0 && t[u] < lo) ++below;
-      else if (t[u] >= lo && t[u] < lo + a.ids) atomicAdd(&mine[t[u] - lo], 1);
+      const uint32_t in = __ballot_sync(0xffffffffu, k[u] >= 0);
+      if (!in) continue;
+      const int i = mine + __popc(in & before);
+      if (k[u] >= 0) {
+        atomicAdd(&counter[k[u]], 1);
+        if (i < kKept) list[warp * kKept + i] = Place{(int32_t)(at + u * 32), k[u]};
+      }
+      mine += __popc(in);
     }
   }
   below = __reduce_add_sync(0xffffffffu, below);
-  if (lane == 0 && below) atomicAdd(&below_sum, below);
+  if (lane == 0) {
+    if (below) atomicAdd(&below_sum, below);
+    kept[warp] = mine;
+    if (mine > kKept) crowded = 1;
+  }
   __syncthreads();
-  // counts to places: by id, then by warp
-  int count = 0, total;
-  const int own = threadIdx.x;
-  if (own < a.ids)
-    for (int w = 0; w < kSortWarps; ++w) count += counter[w * a.ids + own];
-  int place = below_sum + block_scan_1024(count, warp_sum, total);
-  if (own < a.ids) {
-    if (lo + own < a.vocab) a.seg[lo + own] = Segment{place, count};
+  // counts to places
+  int first = below_sum;
+  const int total = __reduce_add_sync(0xffffffffu, kept[lane]);
+  const bool few = !crowded;
+  if (block == mask && threadIdx.x == 0) *a.live = below_sum + total;
+  for (int i0 = 0; i0 < a.ids; i0 += kSortThreads) {
+    const int id = i0 + threadIdx.x, count = id < a.ids ? counter[id] : 0;
+    int sum;
+    const int place = first + block_scan(count, warp_sum, sum);
+    if (id < a.ids) {
+      const int64_t v = ((int64_t)id << a.lg) + block;
+      if (v < a.vocab) a.seg[v] = Segment{place, count};
+      counter[id] = place;
+    }
+    first += sum;
+    __syncthreads();
+  }
+  if (few) {
+    // one list, which a warp goes through in order
+    const int c = kept[lane];
+    int x = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const int to = __shfl_sync(0xffffffffu, x - c, warp);
+    for (int i = lane; i < mine; i += 32) all[to + i] = list[warp * kKept + i];
+    __syncthreads();
+    if (warp) return;
+    for (int i0 = 0; i0 < total; i0 += 32) {
+      const Place x = i0 + lane < total ? all[i0 + lane] : Place{0, -1};
+      const uint32_t same = __match_any_sync(0xffffffffu, x.id);
+      const int p = x.id >= 0 ? counter[x.id] + __popc(same & before) : 0;
+      __syncwarp();
+      if (x.id >= 0) {
+        if (lane == __ffs(same) - 1) counter[x.id] += __popc(same);
+        put(p, x.row, x.id);
+      }
+      __syncwarp();
+    }
+    return;
+  }
+  // an id that is a large part of all tokens: each warp counts its run again, apart,
+  // and walks through it once its places are known
+  int next[(kMaxIds + kSortThreads - 1) / kSortThreads];
+#pragma unroll
+  for (int j = 0; j * kSortThreads < kMaxIds; ++j)
+    if (j * kSortThreads + threadIdx.x < a.ids) next[j] = counter[j * kSortThreads + threadIdx.x];
+  __syncthreads();
+  for (int i = threadIdx.x; i < kSortWarps * a.ids; i += kSortThreads) counter[i] = 0;
+  __syncthreads();
+  int* run = counter + warp * a.ids;
+  for (int64_t at = begin + lane; at - lane < end; at += 32) {
+    const int k = own(at);
+    if (k >= 0) atomicAdd(&run[k], 1);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j * kSortThreads < kMaxIds; ++j) {
+    const int id = j * kSortThreads + threadIdx.x;
+    if (id >= a.ids) break;
+    int place = next[j];
     for (int w = 0; w < kSortWarps; ++w) {
-      const int c = counter[w * a.ids + own];
-      counter[w * a.ids + own] = place;
+      const int c = counter[w * a.ids + id];
+      counter[w * a.ids + id] = place;
       place += c;
     }
   }
-  if (!total) return;  // (the whole block)
   __syncthreads();
   for (int64_t at = begin + lane; at - lane < end; at += 32 * kAhead) {
-    int64_t t[kAhead];
+    int k[kAhead];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) t[u] = fetch(at + u * 32);
+    for (int u = 0; u < kAhead; ++u) k[u] = own(at + u * 32);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int k = t[u] >= lo && t[u] < lo + a.ids ? (int)(t[u] - lo) : -1;
-      if (!__any_sync(0xffffffffu, k >= 0)) continue;
-      const uint32_t same = __match_any_sync(0xffffffffu, k);
-      int p = 0;
-      if (k >= 0) p = mine[k] + __popc(same & ((1u << lane) - 1));
+      if (!__any_sync(0xffffffffu, k[u] >= 0)) continue;
+      const uint32_t same = __match_any_sync(0xffffffffu, k[u]);
+      const int p = k[u] >= 0 ? run[k[u]] + __popc(same & before) : 0;
       __syncwarp();
-      if (k >= 0) {
-        if (lane == __ffs(same) - 1) mine[k] += __popc(same);
-        a.pos[p] = (int32_t)(at + u * 32);
-        a.id[p] = (int32_t)t[u];
+      if (k[u] >= 0) {
+        if (lane == __ffs(same) - 1) run[k[u]] += __popc(same);
+        put(p, at + u * 32, k[u]);
       }
       __syncwarp();
     }
@@ -208,184 +289,288 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a) {
 }
 
 // ------------------------------------------------------------------ reduce
-constexpr int kRun = 32;     // places of the sorted list a block starts pieces in
-constexpr int kPiece = 32;   // rows of a piece of a frequent id
+constexpr int kPiece = 16;   // rows of a piece of a frequent id
+constexpr int kMinRun = 4, kMostRun = kPiece;  // a run starts one piece of a frequent id at most
 constexpr int kReduceThreads = 128;
+constexpr int kReduceWarps = kReduceThreads / 32;
 constexpr int kRowsAhead = 8;
+constexpr int kMostRows = 2 * kMostRun + 2 * kPiece;  // rows a team reads, those added to among them
+constexpr int kZeroBytes = 65536;  // of d_w that a block fills with zeros, about
 
 struct ReduceGradArgs {
   const void* dh;
   void* dw;
   const Segment* seg;
-  const int32_t *pos, *id;
-  float* part;        // [n / kPiece + 1][d] sums of frequent ids' pieces
+  const Place* place;
+  const int32_t* live;
+  int32_t* head;      // [runs]: the frequent id whose places begin in this run, or -1
+  float* part;        // [runs][d] sums of frequent ids' pieces, by the run they start in
   int64_t n, vocab, d;
+  int run;            // places of the list a team starts pieces in, a power of two
   int slices;         // of the columns
+  int64_t teams;      // blocks that add; the others write the rows of zeros
+  int zeros;          // ids of each of those
   int accumulate;
   float scale;
 };
 
-// A thread's columns of one row: a vector, or N elements kReduceThreads apart.
-template <class T, bool VEC>
+// A thread's columns of one row: a vector, or N elements TEAM apart (held as they
+// came, so that nothing waits for them before they are added).
+template <class T, int TEAM, bool VEC>
 struct Columns {
   static constexpr int N = RowVec<T>::N;
-  static constexpr int64_t kSlice = (int64_t)kReduceThreads * N;
-  static __device__ __forceinline__ void load(const T* row, int64_t c0, int64_t d, float* v) {
+  static constexpr int64_t kSlice = (int64_t)TEAM * N;
+  uint4 w;
+  T x[N];
+  __device__ __forceinline__ void load(const T* row, int64_t c0, int64_t d, int t) {
     if constexpr (VEC) {
-      const int64_t c = c0 + threadIdx.x * N;
-      RowVec<T>::get(c < d ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0), v);
+      const int64_t c = c0 + t * N;
+      w = c < d ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
     } else {
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const int64_t c = c0 + e * kReduceThreads + threadIdx.x;
-        v[e] = c < d ? to_f(row[c]) : 0.f;
+        const int64_t c = c0 + e * TEAM + t;
+        if (c < d) x[e] = row[c];
+        else from_f(0.f, x[e]);
       }
     }
   }
-  static __device__ __forceinline__ void store(T* row, int64_t c0, int64_t d, const float* v) {
+  __device__ __forceinline__ void get(float* v) const {
     if constexpr (VEC) {
-      const int64_t c = c0 + threadIdx.x * N;
+      RowVec<T>::get(w, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] = to_f(x[e]);
+    }
+  }
+  static __device__ __forceinline__ void store(T* row, int64_t c0, int64_t d, int t,
+                                               const float* v) {
+    if constexpr (VEC) {
+      const int64_t c = c0 + t * N;
       if (c < d) __stcs(reinterpret_cast<uint4*>(row + c), RowVec<T>::put(v));
     } else {
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const int64_t c = c0 + e * kReduceThreads + threadIdx.x;
+        const int64_t c = c0 + e * TEAM + t;
         if (c < d) from_f(v[e], row[c]);
       }
     }
   }
-  static __device__ __forceinline__ void store_part(float* row, int64_t c0, int64_t d,
+  static __device__ __forceinline__ void store_part(float* row, int64_t c0, int64_t d, int t,
                                                     const float* v) {
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      const int64_t c = VEC ? c0 + threadIdx.x * N + e : c0 + e * kReduceThreads + threadIdx.x;
+      const int64_t c = VEC ? c0 + t * N + e : c0 + e * TEAM + t;
       if (c < d) row[c] = v[e];
     }
   }
 };
 
-template <class T, bool VEC>
+// A block's share of the ids: zeros where an id does not occur, a warp a row.
+template <class T>
+__device__ __forceinline__ void zero_rows(const ReduceGradArgs& a, int64_t share) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t lo = share * a.zeros, hi = min(lo + a.zeros, a.vocab);
+  for (int64_t v0 = lo + warp; v0 < hi; v0 += 32 * kReduceWarps) {
+    const int64_t mine = v0 + lane * kReduceWarps;
+    uint32_t none = __ballot_sync(0xffffffffu, mine < hi && a.seg[mine].count == 0);
+    for (; none; none &= none - 1) {
+      T* row = static_cast<T*>(a.dw) + (v0 + (__ffs(none) - 1) * kReduceWarps) * a.d;
+      const int64_t lead = min((int64_t)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) /
+                                   (int64_t)sizeof(T), a.d);
+      const int64_t vecs = (a.d - lead) / RowVec<T>::N, tail = lead + vecs * RowVec<T>::N;
+      if (lane < lead) from_f(0.f, row[lane]);
+      uint4* p = reinterpret_cast<uint4*>(row + lead);
+      for (int64_t i = lane; i < vecs; i += 32) __stcs(&p[i], make_uint4(0, 0, 0, 0));
+      if (tail + lane < a.d) from_f(0.f, row[tail + lane]);
+    }
+  }
+}
+
+// A team adds up the pieces that start in its run of places, over its columns.
+// The rows it reads (the pieces', and behind each the row of d_w that the sum is
+// added to) are one list, so that kRowsAhead of them are always on their way,
+// wherever the pieces end: most ids occur once or twice.
+template <class T, int TEAM, bool VEC>
 __global__ void __launch_bounds__(kReduceThreads) k_embed_reduce(ReduceGradArgs a) {
-  using C = Columns<T, VEC>;
-  constexpr int N = C::N;
-  // pieces that start here: first place, rows, id, and whether the sum goes to `part`
-  __shared__ int p_first[kRun], p_rows[kRun], p_id[kRun], p_part[kRun], pieces;
-  __shared__ int rows[kRun + 2 * kPiece];
+  using C = Columns<T, TEAM, VEC>;
+  constexpr int N = C::N, kTeams = kReduceThreads / TEAM;
+  __shared__ int src_[kTeams][kMostRows], out_[kTeams][kMostRows], rows_[kTeams];
+  constexpr int kAheadHere = VEC ? kRowsAhead : kRowsAhead / 2;
   chain_wait();
   chain_next();
-  const int64_t run = blockIdx.x / a.slices;
-  const int64_t c0 = (blockIdx.x - run * a.slices) * C::kSlice;
-  const int64_t at = run * kRun;
-  const int live = a.seg[a.vocab - 1].first + a.seg[a.vocab - 1].count;  // places in all
+  if (blockIdx.x >= a.teams) {
+    zero_rows<T>(a, blockIdx.x - a.teams);
+    return;
+  }
+  const int team = threadIdx.x / TEAM, t = threadIdx.x % TEAM;
+  const int64_t item = (int64_t)blockIdx.x * kTeams + team;
+  const int64_t run = item / a.slices, at = run * a.run;
+  const int64_t c0 = (item - run * a.slices) * C::kSlice;
   T* dw = static_cast<T*>(a.dw);
   const T* dh = static_cast<const T*>(a.dh);
-  if (threadIdx.x < 32) {
-    int len = 0, v = 0, part = 0;
-    const int64_t p = at + threadIdx.x;
-    if (p < live) {
-      v = a.id[p];
-      const Segment s = a.seg[v];
-      const int off = (int)(p - s.first);
+  // src: a row of d_h, or ~id of a row of d_w that is added to.  out: none (-1), the
+  // row of d_w that ends here, or -2: part[run]
+  int *src = src_[team], *out = out_[team];
+  if (t < 32) {  // two places a lane: the run's, and as far as its last piece goes
+    static_assert(kMostRun - 1 + 2 * kPiece - 1 < 64, "places of the last piece");
+    const Place none{0, 0};
+    const Place x0 = at + t < a.n ? a.place[at + t] : none;
+    const Place x1 = at + t + 32 < a.n ? a.place[at + t + 32] : none;
+    const int64_t live = *a.live;
+    int len = 0, ends = -1, heads = -1;
+    if (t < a.run && at + t < live) {
+      const Segment s = a.seg[x0.id];
+      const int off = (int)(at + t - s.first);
       if (s.count < 2 * kPiece) {
         len = off == 0 ? s.count : 0;
+        ends = x0.id;
       } else {
         const int q = s.count / kPiece, j = off / kPiece;
-        part = 1;
         if (off % kPiece == 0 && j < q) len = j < q - 1 ? kPiece : s.count - j * kPiece;
+        ends = -2;
+        if (off == 0) heads = x0.id;
       }
     }
+    heads = __reduce_max_sync(0xffffffffu, heads);
+    if (t == 0 && c0 == 0 && at < a.n) a.head[run] = heads;
+    // the pieces lie one behind the other: a place's row is its distance from the
+    // first one's start, and the rows added to that come before it
     const uint32_t starts = __ballot_sync(0xffffffffu, len > 0);
-    if (len > 0) {
-      const int k = __popc(starts & ((1u << threadIdx.x) - 1));
-      p_first[k] = threadIdx.x;
-      p_rows[k] = len;
-      p_id[k] = v;
-      p_part[k] = part;
-    }
-    if (threadIdx.x == 0) pieces = __popc(starts);
+    const uint32_t added = __ballot_sync(0xffffffffu, len > 0 && ends >= 0 && a.accumulate);
+    const int begin = __ffs(starts) - 1;
+    auto list = [&](int i, int row) {
+      const uint32_t upto = i < 31 ? (2u << i) - 1 : 0xffffffffu;
+      const int from = max(31 - __clz(starts & upto), 0);  // its piece's start
+      const int n = __shfl_sync(0xffffffffu, len, from), o = __shfl_sync(0xffffffffu, ends, from);
+      if (!starts || i < begin || i >= from + n) return;
+      const int to = i - begin + __popc(added & ((1u << from) - 1));
+      const bool last = i == from + n - 1, old = (added >> from) & 1;
+      src[to] = row;
+      out[to] = last && !old ? o : -1;
+      if (last && old) {
+        src[to + 1] = ~o;
+        out[to + 1] = o;
+      }
+    };
+    list(t, x0.row);
+    list(t + 32, x1.row);
+    const int final = starts ? 31 - __clz(starts) : 0;
+    const int n = __shfl_sync(0xffffffffu, len, final);
+    if (t == 0) rows_[team] = starts ? final + n - begin + __popc(added) : 0;
   }
-  static_assert(kRun == 32, "a lane a place");
-  for (int i = threadIdx.x; i < kRun + 2 * kPiece; i += kReduceThreads)
-    rows[i] = at + i < live ? a.pos[at + i] : 0;
-  // rows of ids that do not occur, dealt out to all runs
-  if (!a.accumulate) {
-    const int64_t runs = gridDim.x / a.slices;
-    float zero[N];
+  if (TEAM > 32) __syncthreads();  // (of the block's teams)
+  else __syncwarp();
+  const int rows = rows_[team];
+  float sum[N];
 #pragma unroll
-    for (int e = 0; e < N; ++e) zero[e] = 0.f;
-    for (int64_t v = run; v < a.vocab; v += runs)
-      if (a.seg[v].count == 0) C::store(dw + v * a.d, c0, a.d, zero);
-  }
-  __syncthreads();
-  for (int k = 0; k < pieces; ++k) {
-    const int first = p_first[k], len = p_rows[k];
-    float sum[N];
+  for (int e = 0; e < N; ++e) sum[e] = 0.f;
+  for (int r = 0; r < rows; r += kAheadHere) {
+    C w[kAheadHere];
 #pragma unroll
-    for (int e = 0; e < N; ++e) sum[e] = 0.f;
-    for (int r = 0; r < len; r += kRowsAhead) {
-      float v[kRowsAhead][N];
-#pragma unroll
-      for (int u = 0; u < kRowsAhead; ++u)
-        if (r + u < len) C::load(dh + (int64_t)rows[first + r + u] * a.d, c0, a.d, v[u]);
-#pragma unroll
-      for (int u = 0; u < kRowsAhead; ++u)
-        if (r + u < len) {
-#pragma unroll
-          for (int e = 0; e < N; ++e) sum[e] += v[u][e];
-        }
+    for (int u = 0; u < kAheadHere; ++u) {
+      if (r + u >= rows) break;
+      const int i = src[r + u];
+      w[u].load(i >= 0 ? dh + (int64_t)i * a.d : dw + (int64_t)~i * a.d, c0, a.d, t);
     }
-    if (p_part[k]) {
-      C::store_part(a.part + (at + first) / kPiece * a.d, c0, a.d, sum);
-    } else {
-      T* row = dw + (int64_t)p_id[k] * a.d;
-      float old[N];
-      if (a.accumulate) C::load(row, c0, a.d, old);
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        sum[e] = a.accumulate ? fmaf(a.scale, sum[e], old[e]) : a.scale * sum[e];
-      C::store(row, c0, a.d, sum);
+    for (int u = 0; u < kAheadHere; ++u) {
+      if (r + u >= rows) break;
+      const int i = src[r + u], o = out[r + u];
+      float v[N];
+      w[u].get(v);
+      if (i >= 0) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) sum[e] += v[e];
+        if (o == -1) continue;
+      }
+      if (o >= 0) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = i >= 0 ? a.scale * sum[e] : fmaf(a.scale, sum[e], v[e]);
+        C::store(dw + (int64_t)o * a.d, c0, a.d, t, v);
+      } else {
+        C::store_part(a.part + run * a.d, c0, a.d, t, sum);
+      }
+#pragma unroll
+      for (int e = 0; e < N; ++e) sum[e] = 0.f;
     }
   }
 }
 
 // ------------------------------------------------------------------ join
-constexpr int kJoinThreads = 256, kJoinCols = 32;
-constexpr int kJoinPlaces = 8192;  // places a block looks for frequent ids in
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinPlaces = 1024;  // places whose runs a block looks for frequent ids in
+constexpr int kJoinCols = 128;   // columns of a block, four a lane
+constexpr int kWarpParts = 64;   // pieces of an id that are one warp's work
+
+struct Four {
+  float v[4];
+};
+
+// The sum of pieces first, first + step, ... of q, kRowsAhead of them on their way.
+__device__ __forceinline__ Four join_parts(const float* part, int64_t apart, int64_t d, int64_t c,
+                                           int first, int step, int q) {
+  Four s{{0.f, 0.f, 0.f, 0.f}};
+  for (int j = first; j < q; j += step * kRowsAhead) {
+    float v[kRowsAhead][4];
+#pragma unroll
+    for (int u = 0; u < kRowsAhead; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[u][e] = j + u * step < q && c + 32 * e < d ? part[(j + u * step) * apart + c + 32 * e]
+                                                     : 0.f;
+#pragma unroll
+    for (int u = 0; u < kRowsAhead; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s.v[e] += v[u][e];
+  }
+  return s;
+}
 
 template <class T>
 __global__ void __launch_bounds__(kJoinThreads) k_embed_join(ReduceGradArgs a, int cols) {
-  constexpr int kWarps = kJoinThreads / 32;
   __shared__ int heads[kJoinPlaces / (2 * kPiece) + 1], count;
-  __shared__ float sums[kWarps][33];
+  __shared__ Four sums[kJoinWarps][32];
   if (threadIdx.x == 0) count = 0;
   chain_wait();
   __syncthreads();
   const int64_t chunk = blockIdx.x / cols;
-  const int64_t c = (blockIdx.x - chunk * cols) * kJoinCols + (threadIdx.x & 31);
-  const int warp = threadIdx.x >> 5;
-  const int64_t at = chunk * kJoinPlaces;
-  const int live = a.seg[a.vocab - 1].first + a.seg[a.vocab - 1].count;
-  for (int64_t p = at + threadIdx.x; p < at + kJoinPlaces && p < live; p += kJoinThreads) {
-    const int v = a.id[p];
-    const Segment s = a.seg[v];
-    if (p == s.first && s.count >= 2 * kPiece) heads[atomicAdd(&count, 1)] = v;  // any order
-  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = (blockIdx.x - chunk * cols) * kJoinCols + lane;
+  const int here = kJoinPlaces / a.run;  // runs, a thread each
+  const int64_t run = chunk * here + threadIdx.x, runs = (a.n + a.run - 1) / a.run;
+  const int v = threadIdx.x < here && run < runs ? a.head[run] : -1;
+  if (v >= 0) heads[atomicAdd(&count, 1)] = v;  // (in any order: each is summed by itself)
   __syncthreads();
   const int n = count;
-  for (int k = 0; k < n; ++k) {
-    const int v = heads[k];
-    const Segment s = a.seg[v];
+  auto finish = [&](int v, const Four& s) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + 32 * e < a.d) {
+        T& o = static_cast<T*>(a.dw)[(int64_t)v * a.d + c + 32 * e];
+        from_f(a.accumulate ? fmaf(a.scale, s.v[e], to_f(o)) : a.scale * s.v[e], o);
+      }
+  };
+  // piece j begins kPiece j places behind the first: kPiece / run runs
+  const int64_t apart = a.d * (kPiece / a.run);
+  auto parts = [&](const Segment& s) { return a.part + (int64_t)(s.first / a.run) * a.d; };
+  for (int k = warp; k < n; k += kJoinWarps) {
+    const Segment s = a.seg[heads[k]];
     const int q = s.count / kPiece;
-    const float* part = a.part + (int64_t)(s.first / kPiece) * a.d + c;
-    float x = 0.f;
-    if (c < a.d)
-      for (int j = warp; j < q; j += kWarps) x += part[(int64_t)j * a.d];
-    sums[warp][threadIdx.x & 31] = x;
+    if (q <= kWarpParts) finish(heads[k], join_parts(parts(s), apart, a.d, c, 0, 1, q));
+  }
+  for (int k = 0; k < n; ++k) {  // more pieces: all warps, their sums in order
+    const Segment s = a.seg[heads[k]];
+    const int q = s.count / kPiece;
+    if (q <= kWarpParts) continue;
+    sums[warp][lane] = join_parts(parts(s), apart, a.d, c, warp, kJoinWarps, q);
     __syncthreads();
-    if (warp == 0 && c < a.d) {
-      for (int w = 1; w < kWarps; ++w) x += sums[w][threadIdx.x];
-      T& o = static_cast<T*>(a.dw)[(int64_t)v * a.d + c];
-      from_f(a.accumulate ? fmaf(a.scale, x, to_f(o)) : a.scale * x, o);
+    if (warp == 0) {
+      Four x = sums[0][lane];
+      for (int w = 1; w < kJoinWarps; ++w)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x.v[e] += sums[w][lane].v[e];
+      finish(heads[k], x);
     }
     __syncthreads();
   }
@@ -393,8 +578,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_embed_join(ReduceGradArgs a, i
 
 // ------------------------------------------------------------------ plan
 struct EmbedPlan {
-  int ids;             // of a sorting block
-  size_t seg, pos, id, part, bytes;
+  int lg, ids;         // sorting blocks and the ids of each
+  int run;             // places a team starts pieces in
+  size_t seg, place, live, head, part, bytes;
 };
 
 kd_status embed_plan(const kd_embed_problem* p, EmbedPlan& P) {
@@ -403,15 +589,23 @@ kd_status embed_plan(const kd_embed_problem* p, EmbedPlan& P) {
     return KD_ERR_INVALID_ARG;
   if (p->dtype != KD_BF16 && p->dtype != KD_FP32) return KD_ERR_INVALID_ARG;
   if (!std::isfinite(p->scale)) return KD_ERR_INVALID_ARG;
-  const int nsm = std::max(1, tc_num_sms());
-  P.ids = 64;
-  while (P.ids < kMaxIds && p->vocab > (int64_t)nsm * P.ids) P.ids *= 2;
+  P.lg = 7;  // 128 blocks, or as many as have kMaxIds ids at most
+  while (rows_div(p->vocab, (int64_t)1 << P.lg) > kMaxIds) ++P.lg;
+  P.ids = (int)rows_div(p->vocab, (int64_t)1 << P.lg);
+  const int esz = p->dtype == KD_BF16 ? 2 : 4;
+  // runs as short as leaves 16 teams an SM or, beyond that, kMostRun places: the
+  // rows of a short run are one batch of loads
+  const int64_t slices = rows_div(p->d_model * esz, 128 * 16);
+  const int64_t teams = (int64_t)std::max(1, tc_num_sms()) * 16;
+  P.run = kMinRun;
+  while (P.run < kMostRun && p->n_tokens * slices > teams * P.run) P.run *= 2;
+  const int64_t runs = rows_div(p->n_tokens, P.run);
   size_t off = 0;
   P.seg = rows_take(off, (size_t)p->vocab * sizeof(Segment));
-  P.pos = rows_take(off, (size_t)p->n_tokens * 4);
-  P.id = rows_take(off, (size_t)p->n_tokens * 4);
-  P.part = rows_take(off, p->n_tokens >= 2 * kPiece
-                              ? (size_t)(p->n_tokens / kPiece + 1) * p->d_model * 4 : 0);
+  P.place = rows_take(off, (size_t)p->n_tokens * sizeof(Place));
+  P.live = rows_take(off, 4);
+  P.head = rows_take(off, (size_t)runs * 4);
+  P.part = rows_take(off, p->n_tokens >= 2 * kPiece ? (size_t)runs * p->d_model * 4 : 0);
   P.bytes = off;
   return KD_OK;
 }
@@ -426,18 +620,32 @@ bool lookup_run(LookupArgs a, bool vec, cudaStream_t s) {
              : rows_launch(k_embed_rows<T, false>, grid, kLookupThreads, 0, false, s, a);
 }
 
+// A team of as many warps as a row has vectors for, up to a block.
+template <class T, int TEAM, bool VEC>
+bool reduce_team(ReduceGradArgs a, cudaStream_t s) {
+  a.slices = (int)rows_div(a.d, Columns<T, TEAM, VEC>::kSlice);
+  a.teams = rows_div(rows_div(a.n, a.run) * a.slices, kReduceThreads / TEAM);
+  // Many small blocks, behind the ones that add: they fill the table from front to
+  // back, which memory takes at 7.4 TB/s, and at 6.5 TB/s from everywhere at once.
+  a.zeros = (int)std::min<int64_t>(128, std::max<int64_t>(1, kZeroBytes / (a.d * (int64_t)sizeof(T))));
+  const int64_t grid = a.teams + (a.accumulate ? 0 : rows_div(a.vocab, a.zeros));
+  return grid <= INT32_MAX &&
+         rows_launch(k_embed_reduce<T, TEAM, VEC>, grid, kReduceThreads, 0, true, s, a);
+}
 template <class T>
-bool reduce_run(ReduceGradArgs a, bool vec, cudaStream_t s) {
-  a.slices = (int)rows_div(a.d, Columns<T, true>::kSlice);
-  // at least some blocks for the zero rows
-  const int64_t runs = std::max<int64_t>(rows_div(a.n, kRun), a.accumulate ? 1 : 256);
-  const int64_t grid = runs * a.slices;
-  const int64_t cols = rows_div(a.d, kJoinCols), join = rows_div(a.n, kJoinPlaces) * cols;
-  if (grid > INT32_MAX || join > INT32_MAX) return false;
-  const bool ok = vec ? rows_launch(k_embed_reduce<T, true>, grid, kReduceThreads, 0, true, s, a)
-                      : rows_launch(k_embed_reduce<T, false>, grid, kReduceThreads, 0, true, s, a);
+bool reduce_run(const ReduceGradArgs& a, bool vec, cudaStream_t s) {
+  auto team = [&](auto size) {
+    constexpr int TEAM = decltype(size)::value;
+    return vec ? reduce_team<T, TEAM, true>(a, s) : reduce_team<T, TEAM, false>(a, s);
+  };
+  const int64_t vecs = rows_div(a.d, RowVec<T>::N);
+  const bool ok = vecs <= 32   ? team(std::integral_constant<int, 32>())
+                  : vecs <= 64 ? team(std::integral_constant<int, 64>())
+                               : team(std::integral_constant<int, 128>());
   if (!ok || a.n < 2 * kPiece) return ok;
-  return rows_launch(k_embed_join<T>, join, kJoinThreads, 0, true, s, a, (int)cols);
+  const int64_t cols = rows_div(a.d, kJoinCols), join = rows_div(a.n, kJoinPlaces) * cols;
+  return join <= INT32_MAX &&
+         rows_launch(k_embed_join<T>, join, kJoinThreads, 0, true, s, a, (int)cols);
 }
 
 }  // namespace
@@ -466,7 +674,7 @@ extern "C" kd_status kd_embed_fwd(const kd_embed_problem* p, const int64_t* toke
   if (rows_meet(h, all, w, (size_t)p->vocab * row) ||
       rows_meet(h, all, tokens, (size_t)p->n_tokens * 8))
     return KD_ERR_INVALID_ARG;
-  // (a launch has at most 2^31 - 1 blocks of 2048 16-byte vectors or 1024 elements)
+  // (a launch has at most 2^31 - 1 blocks)
   if ((p->n_tokens * rows_div(p->d_model, 32 * kSpan)) / 8 >= INT32_MAX) return KD_ERR_UNSUPPORTED;
   if ((st = rows_device()) != KD_OK || p->n_tokens == 0) return st;
   LookupArgs a;
@@ -502,7 +710,7 @@ extern "C" kd_status kd_embed_bwd(const kd_embed_problem* p, const int64_t* toke
   if (rows_meet(d_w, table, d_h, (size_t)p->n_tokens * row) ||
       rows_meet(d_w, table, tokens, (size_t)p->n_tokens * 8))
     return KD_ERR_INVALID_ARG;
-  if (rows_div(std::max<int64_t>(p->n_tokens, 8192), kRun) * rows_div(p->d_model, 512) >= INT32_MAX)
+  if (rows_div(p->n_tokens, kMostRun) * rows_div(p->d_model, 32) + p->vocab >= INT32_MAX)
     return KD_ERR_UNSUPPORTED;
   if (!rows_ws_ok(workspace, ws_bytes, P.bytes)) return KD_ERR_WORKSPACE;
   if ((st = rows_device()) != KD_OK) return st;
@@ -516,28 +724,31 @@ extern "C" kd_status kd_embed_bwd(const kd_embed_problem* p, const int64_t* toke
   t.n = p->n_tokens;
   t.vocab = p->vocab;
   t.ignore = p->ignore_index;
+  t.lg = P.lg;
   t.ids = P.ids;
   t.seg = reinterpret_cast<Segment*>(ws + P.seg);
-  t.pos = reinterpret_cast<int32_t*>(ws + P.pos);
-  t.id = reinterpret_cast<int32_t*>(ws + P.id);
+  t.place = reinterpret_cast<Place*>(ws + P.place);
+  t.live = reinterpret_cast<int32_t*>(ws + P.live);
   t.status = dev_status;
-  const int smem = kSortWarps * P.ids * 4;
+  const int smem = sort_smem(P.ids);
   if (smem > 40000 && cudaFuncSetAttribute(k_embed_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            smem) != cudaSuccess)
     return KD_ERR_CUDA;
-  if (!rows_launch(k_embed_sort, rows_div(p->vocab, P.ids), kSortThreads, (size_t)smem, false, s, t))
+  if (!rows_launch(k_embed_sort, (int64_t)1 << P.lg, kSortThreads, (size_t)smem, false, s, t))
     return KD_ERR_CUDA;
   ReduceGradArgs a;
   memset(&a, 0, sizeof(a));
   a.dh = d_h;
   a.dw = d_w;
   a.seg = t.seg;
-  a.pos = t.pos;
-  a.id = t.id;
+  a.place = t.place;
+  a.live = t.live;
+  a.head = reinterpret_cast<int32_t*>(ws + P.head);
   a.part = reinterpret_cast<float*>(ws + P.part);
   a.n = p->n_tokens;
   a.vocab = p->vocab;
   a.d = p->d_model;
+  a.run = P.run;
   a.accumulate = accumulate;
   a.scale = p->scale;
   const bool vec = row % 16 == 0 && rows_aligned(16, d_h, d_w);
