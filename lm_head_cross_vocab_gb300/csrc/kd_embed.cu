@@ -157,40 +157,55 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a) {
   // this warp's run of the tokens, whole groups of 32
   const int64_t groups = (a.n + 31) / 32, each = (groups + kSortWarps - 1) / kSortWarps;
   const int64_t begin = warp * each * 32, end = min((warp + 1) * each * 32, a.n);
-  // the block's own number of a token's id, or -1; `below` counts the tokens of the
-  // blocks before it
-  int below = 0;
+  // a token's id modulo the blocks, ~0 where it has none
+  const uint32_t vocab = (uint32_t)a.vocab;
+  const bool inside = (uint64_t)a.ignore < (uint64_t)a.vocab;
+  auto owner = [&](int64_t t) {
+    const uint32_t id = (uint32_t)t;
+    bool in = (uint32_t)((uint64_t)t >> 32) == 0 && id < vocab;
+    if (!in && t != a.ignore && block == 0) set_status(a.status, KD_DEV_BAD_LABEL);
+    if (inside) in = in && t != a.ignore;
+    return in ? id & mask : 0xffffffffu;
+  };
+  // the block's own number of a token's id, or -1
   auto own = [&](int64_t at) {
     const int64_t t = at < end ? a.tokens[at] : a.ignore;
-    if (t == a.ignore) return -1;
-    if ((uint64_t)t >= (uint64_t)a.vocab) {
-      if (block == 0) set_status(a.status, KD_DEV_BAD_LABEL);
-      return -1;
-    }
-    const uint32_t of = (uint32_t)t & mask;
-    below += of < block;
-    return of == block ? (int)((uint32_t)t >> a.lg) : -1;
+    return owner(t) == block ? (int)((uint32_t)t >> a.lg) : -1;
   };
   auto put = [&](int p, int64_t row, int k) {
     a.place[p] = Place{(int32_t)row, (int32_t)(((uint32_t)k << a.lg) + block)};
   };
   __syncthreads();
-  int mine = 0;  // tokens of this warp's run that the block owns
-  for (int64_t at = begin + lane; at - lane < end; at += 32 * kAhead) {
-    int k[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) k[u] = own(at + u * 32);
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const uint32_t in = __ballot_sync(0xffffffffu, k[u] >= 0);
-      if (!in) continue;
-      const int i = mine + __popc(in & before);
-      if (k[u] >= 0) {
-        atomicAdd(&counter[k[u]], 1);
-        if (i < kKept) list[warp * kKept + i] = Place{(int32_t)(at + u * 32), k[u]};
-      }
-      mine += __popc(in);
+  // tokens of this warp's run that the block owns, and of the blocks before it
+  int mine = 0, below = 0;
+  auto take = [&](int64_t at, int64_t t) {
+    const uint32_t of = owner(t);
+    below += of < block;
+    const uint32_t in = __ballot_sync(0xffffffffu, of == block);
+    if (!in) return;
+    const int i = mine + __popc(in & before);
+    if (of == block) {
+      const int k = (int)((uint32_t)t >> a.lg);
+      atomicAdd(&counter[k], 1);
+      if (i < kKept) list[warp * kKept + i] = Place{(int32_t)at, k};
     }
+    mine += __popc(in);
+  };
+  int64_t at = begin + lane;
+  for (; at - lane + 32 * kAhead <= end; at += 32 * kAhead) {
+    int64_t t[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) t[u] = a.tokens[at + u * 32];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) take(at + u * 32, t[u]);
+  }
+  if (at - lane < end) {
+    int64_t t[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) t[u] = at + u * 32 < end ? a.tokens[at + u * 32] : a.ignore;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (at - lane + u * 32 < end) take(at + u * 32, t[u]);
   }
   below = __reduce_add_sync(0xffffffffu, below);
   if (lane == 0) {

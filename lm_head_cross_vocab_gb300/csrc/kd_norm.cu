@@ -78,6 +78,8 @@ struct RowPart {
 };
 
 constexpr int norm_block(int tpr) { return tpr < 128 ? 128 : tpr; }
+// Blocks of the backward on an SM: 512 threads, whose registers hold d_w's share.
+constexpr int norm_per_sm(int tpr) { return tpr <= 128 ? 4 : tpr <= 256 ? 2 : 1; }
 
 // Sums of a row over its TPR threads, in every one of them.  `red` holds
 // TPR / 32 pairs; a block that calls it again passes the other of two buffers.
@@ -141,27 +143,74 @@ __global__ void __launch_bounds__(norm_block(TPR)) k_norm_fwd(NormArgs a) {
   }
 }
 
+// Backward.  With whole vectors (and rows that leave room for it) a thread's own
+// vectors of the rows to come are on their way into shared memory, stages - 1 rows
+// ahead: 16 warps an SM hold too few loads in their registers to keep memory
+// busy.  Each thread reads only what it copied itself, so the ring needs no barrier.
+template <int TPR, int VPT, bool VEC>
+constexpr bool norm_ring() {
+  return VEC && TPR * VPT <= 2048;
+}
 template <class T, int TPR, int VPT, bool VEC>
-__global__ void __launch_bounds__(norm_block(TPR)) k_norm_bwd(NormArgs a) {
+__global__ void __launch_bounds__(norm_block(TPR), norm_per_sm(TPR)) k_norm_bwd(NormArgs a, int stages) {
   using P = RowPart<T, TPR, VPT, VEC>;
-  constexpr int N = P::N, ROWS = norm_block(TPR) / TPR;
+  constexpr int N = P::N, BLOCK = norm_block(TPR), ROWS = BLOCK / TPR;
+  constexpr bool RING = norm_ring<TPR, VPT, VEC>();
+  extern __shared__ uint4 ring[];  // [stages][2 or 3 tensors][VPT][BLOCK]
   __shared__ float2 red[2][32];
   chain_next();
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const int64_t step = (int64_t)gridDim.x * ROWS, begin = (int64_t)blockIdx.x * ROWS;
+  auto copy = [&](int slot, const void* tensor, int64_t row) {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(tensor) + row * a.d);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (i * TPR + t < a.d / N) {
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(&ring[(slot * VPT + i) * BLOCK + threadIdx.x]);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src + i * TPR + t)
+                     : "memory");
+      }
+  };
+  const int tensors = a.res ? 3 : 2;
+  auto ask = [&](int stage, int64_t first) {
+    if (first + sub < a.n) {
+      copy(stage * tensors, a.x, first + sub);
+      copy(stage * tensors + 1, a.dh, first + sub);
+      if (a.res) copy(stage * tensors + 2, a.res, first + sub);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto take = [&](int slot, P& p) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      p.w[i] = i * TPR + t < a.d / N ? ring[(slot * VPT + i) * BLOCK + threadIdx.x]
+                                     : make_uint4(0, 0, 0, 0);
+  };
+  if constexpr (RING)
+    for (int q = 0; q < stages; ++q) ask(q, begin + q * step);
   P w;
   w.load(static_cast<const T*>(a.w), a.d, t);
   float dw[P::E];
 #pragma unroll
   for (int e = 0; e < P::E; ++e) dw[e] = 0.f;
   const float inv_d = 1.f / (float)a.d;
-  int turn = 0;
-  for (int64_t first = (int64_t)blockIdx.x * ROWS; first < a.n; first += (int64_t)gridDim.x * ROWS) {
+  int turn = 0, stage = 0;
+  for (int64_t first = begin; first < a.n; first += step) {
     const bool on = first + sub < a.n;
     const int64_t at = (on ? first + sub : 0) * a.d;
     P s, g, up;
-    s.load(static_cast<const T*>(a.x) + at, a.d, t);
-    g.load(static_cast<const T*>(a.dh) + at, a.d, t);
-    if (a.res) up.load(static_cast<const T*>(a.res) + at, a.d, t);
+    if constexpr (RING) {
+      if (stages == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+      else if (stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+      else asm volatile("cp.async.wait_group 1;" ::: "memory");
+      take(stage * tensors, s);
+      take(stage * tensors + 1, g);
+      if (a.res) take(stage * tensors + 2, up);
+    } else {
+      s.load(static_cast<const T*>(a.x) + at, a.d, t);
+      g.load(static_cast<const T*>(a.dh) + at, a.d, t);
+      if (a.res) up.load(static_cast<const T*>(a.res) + at, a.d, t);
+    }
     float2 sums = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -177,28 +226,33 @@ __global__ void __launch_bounds__(norm_block(TPR)) k_norm_bwd(NormArgs a) {
     }
     sums = row_sums<TPR>(sums, red[turn]);
     turn ^= 1;
-    if (!on) continue;
-    const float r = 1.f / sqrtf(sums.x * inv_d + a.eps);
-    const float c = r * r * r * (sums.y * inv_d);
+    if (on) {
+      const float r = 1.f / sqrtf(sums.x * inv_d + a.eps);
+      const float c = r * r * r * (sums.y * inv_d);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      float sv[N], gv[N], wv[N];
-      s.get(i, sv);
-      g.get(i, gv);
-      w.get(i, wv);
-      float o[N];
+      for (int i = 0; i < VPT; ++i) {
+        float sv[N], gv[N], wv[N];
+        s.get(i, sv);
+        g.get(i, gv);
+        w.get(i, wv);
+        float o[N];
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        o[e] = fmaf(-c, sv[e], r * (gv[e] * (wv[e] + a.off)));
-        dw[i * N + e] = fmaf(gv[e], sv[e] * r, dw[i * N + e]);
+        for (int e = 0; e < N; ++e) {
+          o[e] = fmaf(-c, sv[e], r * (gv[e] * (wv[e] + a.off)));
+          dw[i * N + e] = fmaf(gv[e], sv[e] * r, dw[i * N + e]);
+        }
+        if (a.res) {
+          float uv[N];
+          up.get(i, uv);
+#pragma unroll
+          for (int e = 0; e < N; ++e) o[e] += uv[e];
+        }
+        if (a.h) P::store(static_cast<T*>(a.h) + at, a.d, t, i, o);
       }
-      if (a.res) {
-        float uv[N];
-        up.get(i, uv);
-#pragma unroll
-        for (int e = 0; e < N; ++e) o[e] += uv[e];
-      }
-      if (a.h) P::store(static_cast<T*>(a.h) + at, a.d, t, i, o);
+    }
+    if constexpr (RING) {  // (the slot's values have all been used)
+      ask(stage, first + stages * step);
+      stage = stage + 1 == stages ? 0 : stage + 1;
     }
   }
   if (!a.part) return;
@@ -227,60 +281,100 @@ __global__ void __launch_bounds__(norm_block(TPR)) k_norm_bwd(NormArgs a) {
     }
 }
 
-// d_w: 32 columns a block; each warp adds every eighth share, then the warps'
-// sums in order.
+// d_w: 32 columns a block; a warp adds every 32nd share, then the warps' sums in
+// order.
+constexpr int kWeightThreads = 1024, kWeightAhead = 10;
 template <class T>
-__global__ void __launch_bounds__(256) k_norm_weight(const float* part, int parts, int d, T* dw) {
-  __shared__ float sum[8][33];
+__global__ void __launch_bounds__(kWeightThreads) k_norm_weight(const float* part, int parts, int d, T* dw) {
+  constexpr int kWarps = kWeightThreads / 32;
+  __shared__ float sum[kWarps][33];
   chain_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
-  if (c < d)
-    for (int p = warp; p < parts; p += 8) v += part[(int64_t)p * d + c];
+  for (int p = warp; p < parts; p += kWarps * kWeightAhead) {
+    float x[kWeightAhead];
+#pragma unroll
+    for (int u = 0; u < kWeightAhead; ++u)
+      x[u] = c < d && p + u * kWarps < parts ? part[(int64_t)(p + u * kWarps) * d + c] : 0.f;
+#pragma unroll
+    for (int u = 0; u < kWeightAhead; ++u) v += x[u];
+  }
   sum[warp][lane] = v;
   __syncthreads();
   if (warp == 0 && c < d) {
-    for (int q = 1; q < 8; ++q) v += sum[q][lane];
+#pragma unroll
+    for (int q = 1; q < kWarps; ++q) v += sum[q][lane];
     from_f(v, dw[c]);
   }
 }
 
-int norm_grid(int64_t n, int64_t d, int esz) {
-  const int64_t vecs = rows_div(d * esz, 16);
-  const int rows = vecs <= 32 ? 16 : vecs <= 128 ? 4 : 1;  // rows of a block
-  const int per_sm = vecs <= 512 ? 4 : vecs <= 1024 ? 2 : 1;
-  return (int)std::min<int64_t>(rows_div(n, rows), (int64_t)std::max(1, tc_num_sms()) * per_sm);
-}
-
-template <class T, bool VEC, class F>
-bool norm_shape(int d, F&& run) {
-  const int vecs = (d + RowVec<T>::N - 1) / RowVec<T>::N;
+// Threads of a row and vectors of a thread.  The backward holds at most 16
+// elements a thread, whose shares of d_w stay in registers.
+template <class T, bool BACKWARD, class F>
+auto norm_shape(int64_t d, F&& run) {
+  const int64_t vecs = rows_div(d, RowVec<T>::N);
 #define KD_SHAPE(TPR, VPT) \
   return run(std::integral_constant<int, TPR>(), std::integral_constant<int, VPT>())
   if (vecs <= 8) KD_SHAPE(8, 1);
-  if (vecs <= 32) KD_SHAPE(8, 4);
-  if (vecs <= 64) KD_SHAPE(32, 2);
-  if (vecs <= 128) KD_SHAPE(32, 4);
-  if (vecs <= 256) KD_SHAPE(128, 2);
-  if (vecs <= 512) KD_SHAPE(128, 4);
-  if (vecs <= 1024) KD_SHAPE(256, 4);
-  if (vecs <= 2048) KD_SHAPE(512, 4);
-  if (vecs <= 4096) KD_SHAPE(1024, 4);
-  KD_SHAPE(1024, 8);
+  if constexpr (BACKWARD && RowVec<T>::N == 8) {
+    if (vecs <= 16) KD_SHAPE(8, 2);
+    if (vecs <= 64) KD_SHAPE(32, 2);
+    if (vecs <= 256) KD_SHAPE(128, 2);
+    if (vecs <= 512) KD_SHAPE(256, 2);
+    if (vecs <= 1024) KD_SHAPE(512, 2);
+    if (vecs <= 2048) KD_SHAPE(1024, 2);
+    KD_SHAPE(1024, 4);
+  } else {
+    if (vecs <= 32) KD_SHAPE(8, 4);
+    if (vecs <= 64) KD_SHAPE(32, 2);
+    if (vecs <= 128) KD_SHAPE(32, 4);
+    if (vecs <= 256) KD_SHAPE(128, 2);
+    if (vecs <= 512) KD_SHAPE(128, 4);
+    if (vecs <= 1024) KD_SHAPE(256, 4);
+    if (vecs <= 2048) KD_SHAPE(512, 4);
+    if (vecs <= 4096) KD_SHAPE(1024, 4);
+    KD_SHAPE(1024, 8);
+  }
 #undef KD_SHAPE
+}
+
+// Blocks of the backward: each writes a share of d_w, so that few rows take few
+// blocks.
+int norm_grid(int64_t n, int64_t d, bool bf16) {
+  auto grid = [&](auto tpr, auto) {
+    constexpr int TPR = decltype(tpr)::value;
+    return (int)std::min<int64_t>(rows_div(n, 4 * (norm_block(TPR) / TPR)),
+                                  (int64_t)std::max(1, tc_num_sms()) * norm_per_sm(TPR));
+  };
+  return bf16 ? norm_shape<__nv_bfloat16, true>(d, grid) : norm_shape<float, true>(d, grid);
 }
 
 template <class T, bool VEC>
 bool norm_run(const NormArgs& a, void* d_w, int grid, cudaStream_t s) {
-  return norm_shape<T, VEC>(a.d, [&](auto tpr, auto vpt) {
-    constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value;
-    constexpr int block = norm_block(TPR);
-    if (!a.dh)
+  if (!a.dh)
+    return norm_shape<T, false>(a.d, [&](auto tpr, auto vpt) {
+      constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value;
+      constexpr int block = norm_block(TPR);
       return rows_launch(k_norm_fwd<T, TPR, VPT, VEC>, rows_div(a.n, block / TPR), block, 0, false,
                          s, a);
-    if (!rows_launch(k_norm_bwd<T, TPR, VPT, VEC>, grid, block, 0, false, s, a)) return false;
-    return !d_w || rows_launch(k_norm_weight<T>, rows_div(a.d, 32), 256, 0, true, s,
+    });
+  return norm_shape<T, true>(a.d, [&](auto tpr, auto vpt) {
+    constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value;
+    constexpr int block = norm_block(TPR);
+    size_t smem = 0;
+    int stages = 0;
+    auto kern = k_norm_bwd<T, TPR, VPT, VEC>;
+    if constexpr (norm_ring<TPR, VPT, VEC>()) {  // 220 KB for an SM's blocks: 2 stages at least
+      const size_t row = (size_t)(a.res ? 3 : 2) * VPT * block * 16;
+      stages = (int)std::min<size_t>(4, (size_t)220 * 1024 / norm_per_sm(TPR) / row);
+      smem = stages * row;
+      if (smem > 40000 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)smem) != cudaSuccess)
+        return false;
+    }
+    if (!rows_launch(kern, grid, block, smem, false, s, a, stages)) return false;
+    return !d_w || rows_launch(k_norm_weight<T>, rows_div(a.d, 32), kWeightThreads, 0, true, s,
                                (const float*)a.part, grid, a.d, static_cast<T*>(d_w));
   });
 }
@@ -311,7 +405,7 @@ extern "C" kd_status kd_rmsnorm_workspace_size(const kd_rmsnorm_problem* p, size
   const kd_status st = norm_check(p);
   if (st != KD_OK) return st;
   if (bwd_bytes)
-    *bwd_bytes = (size_t)norm_grid(p->n_tokens, p->d_model, p->dtype == KD_BF16 ? 2 : 4) *
+    *bwd_bytes = (size_t)norm_grid(p->n_tokens, p->d_model, p->dtype == KD_BF16) *
                  (size_t)p->d_model * 4;
   return KD_OK;
 }
@@ -381,7 +475,6 @@ extern "C" kd_status kd_rmsnorm_bwd(const kd_rmsnorm_problem* p, const void* sum
   a.eps = p->eps;
   a.off = p->weight_offset;
   const bool vec = row % 16 == 0 && rows_aligned(16, sum, weight, d_h, d_sum, d_x);
-  const bool ok = norm_dispatch(a, esz == 2, vec, d_weight,
-                                norm_grid(a.n, a.d, (int)esz), s);
+  const bool ok = norm_dispatch(a, esz == 2, vec, d_weight, norm_grid(a.n, a.d, esz == 2), s);
   return ok && cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA;
 }
