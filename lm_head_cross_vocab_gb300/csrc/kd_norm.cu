@@ -79,7 +79,9 @@ struct RowPart {
 
 constexpr int norm_block(int tpr) { return tpr < 128 ? 128 : tpr; }
 // Blocks of the backward on an SM: 512 threads, whose registers hold d_w's share.
-constexpr int norm_per_sm(int tpr) { return tpr <= 128 ? 4 : tpr <= 256 ? 2 : 1; }
+constexpr int norm_per_sm(int tpr, int vpt) {
+  return tpr <= 128 ? (vpt == 5 ? 3 : 4) : tpr <= 256 ? 2 : 1;
+}
 
 // Sums of a row over its TPR threads, in every one of them.  `red` holds
 // TPR / 32 pairs; a block that calls it again passes the other of two buffers.
@@ -93,7 +95,7 @@ __device__ __forceinline__ float2 row_sums(float2 v, float2* red) {
   if constexpr (TPR > 32) {
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = red[threadIdx.x & (TPR / 32 - 1)];
+    v = red[threadIdx.x / TPR * (TPR / 32) + (threadIdx.x & (TPR / 32 - 1))];
 #pragma unroll
     for (int o = TPR / 64; o > 0; o >>= 1) {
       v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
@@ -152,7 +154,7 @@ constexpr bool norm_ring() {
   return VEC && TPR * VPT <= 2048;
 }
 template <class T, int TPR, int VPT, bool VEC>
-__global__ void __launch_bounds__(norm_block(TPR), norm_per_sm(TPR)) k_norm_bwd(NormArgs a, int stages) {
+__global__ void __launch_bounds__(norm_block(TPR), norm_per_sm(TPR, VPT)) k_norm_bwd(NormArgs a, int stages) {
   using P = RowPart<T, TPR, VPT, VEC>;
   constexpr int N = P::N, BLOCK = norm_block(TPR), ROWS = BLOCK / TPR;
   constexpr bool RING = norm_ring<TPR, VPT, VEC>();
@@ -202,7 +204,8 @@ __global__ void __launch_bounds__(norm_block(TPR), norm_per_sm(TPR)) k_norm_bwd(
     if constexpr (RING) {
       if (stages == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
       else if (stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
-      else asm volatile("cp.async.wait_group 1;" ::: "memory");
+      else if (stages == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+      else asm volatile("cp.async.wait_group 0;" ::: "memory");
       take(stage * tensors, s);
       take(stage * tensors + 1, g);
       if (a.res) take(stage * tensors + 2, up);
@@ -320,8 +323,12 @@ auto norm_shape(int64_t d, F&& run) {
   if constexpr (BACKWARD && RowVec<T>::N == 8) {
     if (vecs <= 16) KD_SHAPE(8, 2);
     if (vecs <= 64) KD_SHAPE(32, 2);
+    if (vecs <= 96) KD_SHAPE(32, 3);
+    if (vecs <= 128) KD_SHAPE(64, 2);
     if (vecs <= 256) KD_SHAPE(128, 2);
+    if (vecs <= 384) KD_SHAPE(128, 3);
     if (vecs <= 512) KD_SHAPE(256, 2);
+    if (vecs <= 768) KD_SHAPE(256, 3);
     if (vecs <= 1024) KD_SHAPE(512, 2);
     if (vecs <= 2048) KD_SHAPE(1024, 2);
     KD_SHAPE(1024, 4);
@@ -329,8 +336,10 @@ auto norm_shape(int64_t d, F&& run) {
     if (vecs <= 32) KD_SHAPE(8, 4);
     if (vecs <= 64) KD_SHAPE(32, 2);
     if (vecs <= 128) KD_SHAPE(32, 4);
+    if (vecs <= 160) KD_SHAPE(32, 5);
     if (vecs <= 256) KD_SHAPE(128, 2);
     if (vecs <= 512) KD_SHAPE(128, 4);
+    if (vecs <= 640) KD_SHAPE(128, 5);
     if (vecs <= 1024) KD_SHAPE(256, 4);
     if (vecs <= 2048) KD_SHAPE(512, 4);
     if (vecs <= 4096) KD_SHAPE(1024, 4);
@@ -342,10 +351,10 @@ auto norm_shape(int64_t d, F&& run) {
 // Blocks of the backward: each writes a share of d_w, so that few rows take few
 // blocks.
 int norm_grid(int64_t n, int64_t d, bool bf16) {
-  auto grid = [&](auto tpr, auto) {
-    constexpr int TPR = decltype(tpr)::value;
+  auto grid = [&](auto tpr, auto vpt) {
+    constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value;
     return (int)std::min<int64_t>(rows_div(n, 4 * (norm_block(TPR) / TPR)),
-                                  (int64_t)std::max(1, tc_num_sms()) * norm_per_sm(TPR));
+                                  (int64_t)std::max(1, tc_num_sms()) * norm_per_sm(TPR, VPT));
   };
   return bf16 ? norm_shape<__nv_bfloat16, true>(d, grid) : norm_shape<float, true>(d, grid);
 }
@@ -365,9 +374,9 @@ bool norm_run(const NormArgs& a, void* d_w, int grid, cudaStream_t s) {
     size_t smem = 0;
     int stages = 0;
     auto kern = k_norm_bwd<T, TPR, VPT, VEC>;
-    if constexpr (norm_ring<TPR, VPT, VEC>()) {  // 220 KB for an SM's blocks: 2 stages at least
+    if constexpr (norm_ring<TPR, VPT, VEC>()) {  // 220 KB for an SM's blocks: 2 stages or more
       const size_t row = (size_t)(a.res ? 3 : 2) * VPT * block * 16;
-      stages = (int)std::min<size_t>(4, (size_t)220 * 1024 / norm_per_sm(TPR) / row);
+      stages = (int)std::min<size_t>(4, (size_t)220 * 1024 / norm_per_sm(TPR, VPT) / row);
       smem = stages * row;
       if (smem > 40000 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)smem) != cudaSuccess)

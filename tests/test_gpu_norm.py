@@ -56,7 +56,7 @@ def _check_bwd(r, s, c, dtype, d_sum, n, **kw):
 
 SHAPES = [(1, 1), (3, 7), (5, 64), (17, 72), (33, 256), (9, 264), (700, 520), (50, 1000),
           (40, 1001), (1300, 1024), (7, 2048), (300, 4096), (48, 4104), (5, 8192), (6, 12288),
-          (3, 16384), (2, 16389), (2, 32768)]
+          (3, 16384), (2, 16389), (2, 32768), (11, 32767), (100, 129), (70, 513), (2000, 61)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -123,24 +123,31 @@ def test_in_place(d, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-def test_views_at_odd_elements(dtype):
-    """Contiguous views whose first element is not at 16 bytes."""
-    n, d = 21, 512
+@pytest.mark.parametrize("d", [512, 517])
+@pytest.mark.parametrize("shifts", [(1, 2, 3, 4, 5, 3), (3, 3, 3, 3, 3, 3), (0, 0, 0, 0, 1, 0)])
+def test_views_at_odd_elements(shifts, d, dtype):
+    """Contiguous views whose first element is not at 16 bytes: all alike, or not."""
+    n = 21
     c = _data(n, d, dtype, seed=2)
-    t = {}
-    for i, (k, v) in enumerate(c.items()):
-        store = torch.full((v.numel() + 16,), 7.0, dtype=v.dtype, device="cuda")
-        t[k] = store[i + 1:i + 1 + v.numel()].view(v.shape)
-        t[k].copy_(v)
+
+    def view(shift, like, value=None):
+        store = torch.full((like.numel() + 16,), 3.0, dtype=like.dtype, device="cuda")
+        v = store[shift:shift + like.numel()].view(like.shape)
+        if value is not None:
+            v.copy_(value)
+        return v, store
+
+    t = {k: view(s, v, v)[0] for s, (k, v) in zip(shifts, c.items())}
     p = kd.NormProblem(n_tokens=n, d_model=d, dtype=dtype)
-    store = torch.full((n * d + 16,), 3.0, dtype=DT[dtype], device="cuda")
-    out = {"h": store[3:3 + n * d].view(n, d), "sum": torch.empty(n, d, dtype=DT[dtype],
-                                                                    device="cuda")}
+    stores = [view(shifts[5], c["x"]) for _ in range(3)]
+    out = {"h": stores[0][0], "sum": stores[1][0]}
     r = kd.rms_norm(p, t["x"], t["weight"], residual=t["residual"], out=out)
     _check_fwd(r, c, dtype, True)
-    assert (store[:3] == 3.0).all() and (store[3 + n * d:] == 3.0).all()
-    g = kd.rms_norm_backward(p, r["sum"], t["weight"], t["d_h"], d_sum=t["d_sum"])
+    g = kd.rms_norm_backward(p, r["sum"], t["weight"], t["d_h"], d_sum=t["d_sum"], out={
+        "d_x": stores[2][0], "d_weight": torch.empty_like(t["weight"])})
     _check_bwd(g, r["sum"], c, dtype, True, n)
+    for _, store in stores:  # nothing beside the rows
+        assert (store[:shifts[5]] == 3.0).all() and (store[shifts[5] + n * d:] == 3.0).all()
 
 
 def test_special_rows():
