@@ -9,11 +9,11 @@
 // give the GPU enough blocks.  k_verify_draw joins the parts, decides which drafts
 // stand (a few values a sequence, so that each of its blocks decides for
 // itself), and runs the race over the one row it ended at, that row in parts
-// again; the block that comes last joins them and writes the sequence's
-// outputs.
-// A race needs one value an id: no running sum across blocks, no order of
-// summation, and the ids' weights need not be normalised, only compared: a
-// beats b when r_a e_b > r_b e_a, without a division.
+// again; the block that comes last writes the sequence's outputs.
+// A race needs one value an id: no running sum across blocks, and no order of
+// summation.  r <= p, so that once a block has some id's score r / e, all others
+// are held against it by their p alone, which costs an exponential and a compare;
+// only the few that pass have their q read and their score formed.
 // Exponentials are 2^((z - m) k), k = log2(e) / T, m an offset that trails the
 // running maximum; a row's sum S goes with its m, so that p = 2^((z - m) k) / S
 // never takes a difference of two log-sum-exps, and logits of any size keep their
@@ -43,11 +43,6 @@ struct RowSum {
   float m, s;
   uint64_t best;
 };
-// Leader of a race: weight r, noise e, id; nobody: r = 0.
-struct Leader {
-  float r, e;
-  uint32_t id;
-};
 
 struct VerifyArgs {
   const void *zt, *zd;
@@ -60,7 +55,7 @@ struct VerifyArgs {
   float kt, kd, inv_t;        // log2(e) / T of both, 1 / T of the target
   int parts, race_parts;
   RowSum* sums;               // [rows][parts]: B (K + 1) target rows, then B K of the drafter
-  Leader* leaders;            // [B][race_parts]
+  uint64_t* leader;           // [B]: the largest score, and the complement of its id
   uint32_t* arrived;          // [B]
   int64_t* tokens;
   int32_t* accepted;
@@ -189,7 +184,10 @@ __global__ void __launch_bounds__(kThreads) k_verify_sums(VerifyArgs a) {
   const int per = draft ? a.k : a.k + 1;
   const int64_t b = in / per;
   const int i = (int)(in - b * per);
-  if (!draft && i == 0 && part == 0 && threadIdx.x == 0) a.arrived[b] = 0;
+  if (!draft && i == 0 && part == 0 && threadIdx.x == 0) {
+    a.arrived[b] = 0;
+    a.leader[b] = 0;
+  }
   if (i >= drafts_of(a, b) + (draft ? 0 : 1) || drafts_of(a, b) < 0) return;
   const T* z = static_cast<const T*>(draft ? a.zd : a.zt) + in * (draft ? a.ldd : a.ldt);
   const Part<T> p(z, a.vocab, part, a.parts);
@@ -198,23 +196,18 @@ __global__ void __launch_bounds__(kThreads) k_verify_sums(VerifyArgs a) {
   float top = neg_inf();
   int64_t top_at = 0;
   const uint4* q = p.vectors();
-  const uint4 none = N == 8 ? make_uint4(kNegInfX2, kNegInfX2, kNegInfX2, kNegInfX2)
-                            : make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
-  for (int64_t v = p.v0 + threadIdx.x; v < p.v1; v += kUnroll * kThreads) {
-    uint4 w[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      w[u] = v + u * kThreads < p.v1 ? q[v + u * kThreads] : none;
+  auto take = [&](const uint4* w, int64_t v, auto count) {
+    constexpr int C = decltype(count)::value;
     float m = vec_top(w[0], T());
 #pragma unroll
-    for (int u = 1; u < kUnroll; ++u) m = max_nan(m, vec_top(w[u], T()));
-    if (m == neg_inf()) continue;
+    for (int u = 1; u < C; ++u) m = max_nan(m, vec_top(w[u], T()));
+    if (m == neg_inf()) return;
     f.expect(m);
     if (GREEDY && m > top) {
       top = m;
       bool found = false;
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
+      for (int u = 0; u < C; ++u) {
         float x[N];
         RowVec<T>::get(w[u], x);
 #pragma unroll
@@ -226,12 +219,23 @@ __global__ void __launch_bounds__(kThreads) k_verify_sums(VerifyArgs a) {
       }
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < C; ++u) {
       float x[N];
       RowVec<T>::get(w[u], x);
 #pragma unroll
       for (int e = 0; e < N; e += 2) f.pair(x[e], x[e + 1]);
     }
+  };
+  int64_t v = p.v0 + threadIdx.x;
+  for (; v + (kUnroll - 1) * kThreads < p.v1; v += kUnroll * kThreads) {
+    uint4 w[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) w[u] = q[v + u * kThreads];
+    take(w, v, std::integral_constant<int, kUnroll>());
+  }
+  for (; v < p.v1; v += kThreads) {
+    const uint4 w = q[v];
+    take(&w, v, std::integral_constant<int, 1>());
   }
   uint64_t best = top == neg_inf() ? 0 : cand_word(order_key(top), (uint32_t)top_at);
   if (threadIdx.x < p.loose()) {
@@ -272,72 +276,130 @@ __device__ __forceinline__ float power(float z, float m, float k) {
   return x < -150.f ? 0.f : p;  // (z = -inf among others: rest is NaN then)
 }
 
-// a ahead of b
-__device__ __forceinline__ bool ahead(const Leader& a, const Leader& b) {
-  const float x = a.r * b.e, y = b.r * a.e;
-  return x > y || (x == y && a.id < b.id);
-}
-__device__ __forceinline__ Leader warp_leader(Leader l) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Leader x{__shfl_xor_sync(0xffffffffu, l.r, o), __shfl_xor_sync(0xffffffffu, l.e, o),
-                   __shfl_xor_sync(0xffffffffu, l.id, o)};
-    if (ahead(x, l)) l = x;
-  }
-  return l;
-}
-
-// The race over ids [lo, hi) of one row.
+// The race over ids of one row.  A score's word: its bits above, the complement of
+// the id below, so that a larger word is ahead and equal scores go to the lowest
+// id; 0: nobody.  All blocks' words are compared as integers: no order matters.
 struct Race {
   float kt, mt, inv_t;        // of the target's row
   float kd, md, inv_d;        // of the drafter's (q taken away), inv_d = 0: none
   int64_t out;                // this id has q = 1, -1: none
 
-  __device__ __forceinline__ void enter(Leader& l, float zt, float zd, float e, int64_t id) const {
+  __device__ __forceinline__ uint64_t score(float zt, float zd, float e, int64_t id) const {
     float r = __fmul_rn(power(zt, mt, kt), inv_t);
     if (inv_d > 0.f) r = __fsub_rn(r, __fmul_rn(power(zd, md, kd), inv_d));
-    if (id == out) r = 0.f;
-    const Leader n{r, e, (uint32_t)id};
-    if (r > 0.f && e >= 0x1p-100f && e <= 0x1p100f && ahead(n, l)) l = n;
+    if (!(r > 0.f && e >= 0x1p-60f && e <= 0x1p60f) || id == out) return 0;
+    const float s = __fdiv_rn(r, e);
+    return s > 0.f ? (uint64_t)__float_as_uint(s) << 32 | (uint32_t)~(uint32_t)id : 0;
   }
 };
+constexpr int kList = 1024;  // ids that a block takes a closer look at
+struct RaceShared {
+  uint64_t best;
+  int count;
+  int list[kList];
+};
+// The block's leader of ids [lo, hi), in every thread.
 template <class T>
-__device__ __forceinline__ Leader race_part(const Race& c, const T* zt, const T* zd,
-                                            const float* noise, int64_t lo, int64_t hi) {
-  constexpr int N = RowVec<T>::N;
-  Leader l{0.f, 1.f, 0xffffffffu};
-  const bool vec = ((reinterpret_cast<uintptr_t>(zt + lo) | reinterpret_cast<uintptr_t>(noise + lo) |
-                     (zd ? reinterpret_cast<uintptr_t>(zd + lo) : 0)) & 15) == 0;
-  int64_t loose = lo;
-  if (vec) {
-    const int64_t vecs = (hi - lo) / N;
-    loose = lo + vecs * N;
-    const uint4* pt = reinterpret_cast<const uint4*>(zt + lo);
-    const uint4* pd = reinterpret_cast<const uint4*>(zd + lo);
-    const float4* pe = reinterpret_cast<const float4*>(noise + lo);
-    for (int64_t v = threadIdx.x; v < vecs; v += kThreads) {
-      const uint4 wt = pt[v], wd = zd ? pd[v] : make_uint4(0, 0, 0, 0);
-      float xt[N], xd[N], e[N];
-#pragma unroll
-      for (int j = 0; j < N / 4; ++j) {
-        const float4 y = __ldcs(&pe[v * (N / 4) + j]);
-        e[4 * j] = y.x, e[4 * j + 1] = y.y, e[4 * j + 2] = y.z, e[4 * j + 3] = y.w;
+__device__ __forceinline__ uint64_t race_part(const Race& c, const T* zt, const T* zd,
+                                              const float* noise, int64_t lo, int64_t hi,
+                                              RaceShared& sh) {
+  constexpr int N = 8;  // ids a thread takes at a time
+  if (threadIdx.x == 0) {
+    sh.best = 0;
+    sh.count = 0;
+  }
+  __syncthreads();
+  const bool vec = ((reinterpret_cast<uintptr_t>(zt + lo) | reinterpret_cast<uintptr_t>(noise + lo)) & 15) == 0;
+  const int n = (int)(hi - lo), step = kThreads * N;
+  zt += lo;
+  noise += lo;
+  // element j of a thread's ids from `at` on: neighbours, or kThreads apart
+  auto id_of = [&](int at, int j) { return vec ? at + (int)threadIdx.x * N + j : at + j * kThreads + (int)threadIdx.x; };
+  auto load = [&](int at, float* z, float* e) {
+    const int first = at + (int)threadIdx.x * N;
+    if (vec && first + N <= n) {
+      if constexpr (RowVec<T>::N == 8) {
+        RowVec<T>::get(*reinterpret_cast<const uint4*>(zt + first), z);
+      } else {
+        RowVec<T>::get(*reinterpret_cast<const uint4*>(zt + first), z);
+        RowVec<T>::get(*reinterpret_cast<const uint4*>(zt + first + 4), z + 4);
       }
-      RowVec<T>::get(wt, xt);
-      RowVec<T>::get(wd, xd);
+      const float4 a = *reinterpret_cast<const float4*>(noise + first);
+      const float4 b = *reinterpret_cast<const float4*>(noise + first + 4);
+      e[0] = a.x, e[1] = a.y, e[2] = a.z, e[3] = a.w;
+      e[4] = b.x, e[5] = b.y, e[6] = b.z, e[7] = b.w;
+    } else {
 #pragma unroll
-      for (int j = 0; j < N; ++j) c.enter(l, xt[j], xd[j], e[j], lo + v * N + j);
+      for (int j = 0; j < N; ++j) {
+        const int i = id_of(at, j);
+        z[j] = i < n ? to_f(zt[i]) : neg_inf();
+        e[j] = i < n ? noise[i] : 1.f;
+      }
+    }
+  };
+  auto exact = [&](int i) {
+    return c.score(to_f(zt[i]), zd ? to_f(zd[lo + i]) : 0.f, noise[i], lo + i);
+  };
+  auto offer = [&](uint64_t w) {
+    if (w) atomicMax((unsigned long long*)&sh.best, (unsigned long long)w);
+  };
+  float z[N], e[N];
+  // some scores: of each thread's first ids the one that p makes the likeliest
+  load(0, z, e);
+  {
+    float most = 0.f;
+    int at = -1;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const float x = __fdividef(ex2((z[j] - c.mt) * c.kt), e[j]);
+      if (x > most) {
+        most = x;
+        at = j;
+      }
+    }
+    uint64_t w = at >= 0 ? exact(id_of(0, at)) : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const uint64_t x = __shfl_xor_sync(0xffffffffu, w, o);
+      w = x > w ? x : w;
+    }
+    if ((threadIdx.x & 31) == 0) offer(w);
+  }
+  __syncthreads();
+  // p = 2^x / S, x = (z - m) k: an id may be ahead if 2^x > score S e.  The factor
+  // covers the roundings of this test: of x (|x| 2^-23, 2^x being 0 below x = -126),
+  // of the power (2^-22) and of the products
+  const float held = __uint_as_float((uint32_t)(sh.best >> 32)) / c.inv_t * (1.f - 0x1p-14f);
+  const float2 k2 = make_float2(c.kt, c.kt), m2 = make_float2(c.mt, c.mt), h2 = make_float2(held, held);
+  __syncthreads();
+  for (int at = 0; at < n; at += step) {
+    if (at) load(at, z, e);
+    uint32_t pass = 0;
+#pragma unroll
+    for (int j = 0; j < N; j += 2) {
+      const float2 x = mul2(sub2(make_float2(z[j], z[j + 1]), m2), k2);
+      const float2 y = mul2(make_float2(e[j], e[j + 1]), h2);
+      if (ex2(x.x) > y.x) pass |= 1u << j;
+      if (ex2(x.y) > y.y) pass |= 2u << j;
+    }
+    for (; pass; pass &= pass - 1) {
+      const int i = id_of(at, __ffs(pass) - 1);
+      const int k = atomicAdd(&sh.count, 1);
+      if (k < kList) sh.list[k] = i;
+      else offer(exact(i));
     }
   }
-  for (int64_t v = loose + threadIdx.x; v < hi; v += kThreads)
-    c.enter(l, to_f(zt[v]), zd ? to_f(zd[v]) : 0.f, noise[v], v);
-  return l;
+  __syncthreads();
+  const int count = min(sh.count, kList);
+  for (int k = threadIdx.x; k < count; k += kThreads) offer(exact(sh.list[k]));
+  __syncthreads();
+  return sh.best;
 }
 
 template <class T>
 __global__ void __launch_bounds__(kThreads) k_verify_draw(VerifyArgs a) {
   __shared__ RowSum tgt[kMostDrafts + 1], drf[kMostDrafts];
-  __shared__ Leader lead[kWarps];
+  __shared__ RaceShared race_shared;
   __shared__ int stands, last;
   __shared__ uint32_t trouble;
   const int64_t b = blockIdx.x / a.race_parts;
@@ -359,8 +421,19 @@ __global__ void __launch_bounds__(kThreads) k_verify_draw(VerifyArgs a) {
     }
     return;
   }
-  // ---- the rows' sums
+  // ---- what the decisions need of each draft, on its way while the sums are joined
   const bool has_q = a.zd != nullptr && !a.greedy;
+  int64_t x = -1;
+  float zx = 0.f, qx = 0.f, u = 0.f;
+  if (warp == 0 && lane < len) {
+    x = a.drafts[b * a.k + lane];
+    if (!a.greedy) u = a.u[b * a.k + lane];
+    if (x >= 0 && x < a.vocab) {
+      zx = to_f(zt[lane * a.ldt + x]);
+      if (has_q) qx = to_f(zd[lane * a.ldd + x]);
+    }
+  }
+  // ---- the rows' sums
   for (int r = warp; r < len + 1 + (has_q ? len : 0); r += kWarps) {
     const bool draft = r > len;
     const int i = draft ? r - len - 1 : r;
@@ -374,7 +447,7 @@ __global__ void __launch_bounds__(kThreads) k_verify_draw(VerifyArgs a) {
       best = x.best > best ? x.best : best;
     }
     warp_sum(m, s, k);
-    best = warp_best(best);
+    if (a.greedy) best = warp_best(best);
     if (lane == 0) (draft ? drf[i] : tgt[i]) = RowSum{m, s, best};
   }
   __syncthreads();
@@ -382,7 +455,6 @@ __global__ void __launch_bounds__(kThreads) k_verify_draw(VerifyArgs a) {
   if (warp == 0) {
     bool ok = false, bad = false, foreign = false;
     if (lane < len) {
-      const int64_t x = a.drafts[b * a.k + lane];
       foreign = x < 0 || x >= a.vocab;
       const RowSum t = tgt[lane];
       bad = !sum_ok(t);
@@ -391,11 +463,10 @@ __global__ void __launch_bounds__(kThreads) k_verify_draw(VerifyArgs a) {
       } else {
         const bool bad_q = has_q && !sum_ok(drf[lane]);
         if (!foreign && !bad && !bad_q) {
-          const float p = power(to_f(zt[lane * a.ldt + x]), t.m, a.kt);
-          const float u = a.u[b * a.k + lane];
+          const float p = power(zx, t.m, a.kt);
           if (has_q) {
             const RowSum d = drf[lane];
-            const float q = power(to_f(zd[lane * a.ldd + x]), d.m, a.kd);
+            const float q = power(qx, d.m, a.kd);
             // (products that do not round equal p and q to a rejection at u < 1)
             ok = (double)u * (double)q * (double)t.s < (double)p * (double)d.s;
           } else {
@@ -421,12 +492,12 @@ __global__ void __launch_bounds__(kThreads) k_verify_draw(VerifyArgs a) {
   const RowSum row = tgt[n];
   const bool alive = sum_ok(row);
   // ---- the race
-  Leader l{0.f, 1.f, 0xffffffffu};
+  uint64_t leader = 0;
   const float* noise = a.noise + b * a.vocab;
   zt += n * a.ldt;
-  Race race{a.kt, row.m, 1.f / row.s, a.kd, 0.f, 0.f, -1};
-  const T* q = nullptr;
-  if (!a.greedy && alive) {
+  if (!a.greedy) {
+    Race race{a.kt, row.m, 1.f / row.s, a.kd, 0.f, 0.f, -1};
+    const T* q = nullptr;
     if (n < len) {
       if (has_q && sum_ok(drf[n])) {
         q = zd + n * a.ldd;
@@ -440,43 +511,30 @@ __global__ void __launch_bounds__(kThreads) k_verify_draw(VerifyArgs a) {
     const int64_t units = (a.vocab + 15) / 16;
     const int64_t lo = units * part / a.race_parts * 16;
     const int64_t hi = min(units * (part + 1) / a.race_parts * 16, a.vocab);
-    l = race_part<T>(race, zt, q, noise, lo, hi);
-  }
-  auto block_leader = [&](Leader x) {
-    x = warp_leader(x);
-    __syncthreads();
-    if (lane == 0) lead[warp] = x;
-    __syncthreads();
-    x = lead[lane & (kWarps - 1)];
-    return warp_leader(x);
-  };
-  if (!a.greedy) l = block_leader(l);
-  if (a.race_parts > 1) {
-    if (threadIdx.x == 0) {
-      a.leaders[b * a.race_parts + part] = l;
-      __threadfence();
-      last = atomicAdd(&a.arrived[b], 1) == (uint32_t)a.race_parts - 1;
-      __threadfence();
+    if (alive) leader = race_part<T>(race, zt, q, noise, lo, hi, race_shared);
+    if (a.race_parts > 1) {
+      if (threadIdx.x == 0) {
+        if (leader) atomicMax((unsigned long long*)&a.leader[b], (unsigned long long)leader);
+        __threadfence();
+        last = atomicAdd(&a.arrived[b], 1) == (uint32_t)a.race_parts - 1;
+        __threadfence();
+        race_shared.best = *(volatile uint64_t*)&a.leader[b];
+      }
+      __syncthreads();
+      if (!last) return;
+      leader = race_shared.best;
+      __syncthreads();
     }
-    __syncthreads();
-    if (!last) return;
-    l = Leader{0.f, 1.f, 0xffffffffu};
-    for (int p = threadIdx.x; p < a.race_parts; p += kThreads) {
-      const volatile Leader* o = &a.leaders[b * a.race_parts + p];
-      const Leader x{o->r, o->e, o->id};
-      if (ahead(x, l)) l = x;
+    if (alive && !leader && n < len) {
+      // p <= q everywhere: no residual to draw from
+      race.inv_d = 0.f;
+      race.out = -1;
+      leader = race_part<T>(race, zt, (const T*)nullptr, noise, 0, a.vocab, race_shared);
     }
-    l = block_leader(l);
-  }
-  if (!a.greedy && alive && !(l.r > 0.f) && n < len) {
-    // p <= q everywhere: no residual to draw from
-    race.inv_d = 0.f;
-    race.out = -1;
-    l = block_leader(race_part<T>(race, zt, (const T*)nullptr, noise, 0, a.vocab));
   }
   // ---- outputs
-  const bool drawn = alive && (a.greedy || l.r > 0.f);
-  const int64_t token = a.greedy ? (int64_t)(uint32_t)~(uint32_t)row.best : (int64_t)l.id;
+  const bool drawn = alive && (a.greedy || leader);
+  const int64_t token = (int64_t)(uint32_t)~(uint32_t)(a.greedy ? row.best : leader);
   if (threadIdx.x < rows) {
     const int i = threadIdx.x;
     const int64_t x = i < n ? a.drafts[b * a.k + i] : i == n && drawn ? token : a.ignore;
@@ -504,7 +562,7 @@ __global__ void __launch_bounds__(kThreads) k_verify_draw(VerifyArgs a) {
 struct VerifyPlan {
   int parts, race_parts;
   int64_t rows;
-  size_t sums, leaders, arrived, bytes;
+  size_t sums, leader, arrived, bytes;
 };
 
 kd_status verify_plan(const kd_verify_problem* p, VerifyPlan& P) {
@@ -529,7 +587,7 @@ kd_status verify_plan(const kd_verify_problem* p, VerifyPlan& P) {
                                                               p->vocab / 2048, kMaxParts}));
   size_t off = 0;
   P.sums = rows_take(off, (size_t)r * P.parts * sizeof(RowSum));
-  P.leaders = rows_take(off, (size_t)b * P.race_parts * sizeof(Leader));
+  P.leader = rows_take(off, (size_t)b * 8);
   P.arrived = rows_take(off, (size_t)b * 4);
   P.bytes = off;
   return KD_OK;
@@ -623,7 +681,7 @@ extern "C" kd_status kd_verify_drafts(const kd_verify_problem* p, const kd_verif
   a.parts = P.parts;
   a.race_parts = greedy ? 1 : P.race_parts;
   a.sums = reinterpret_cast<RowSum*>(ws + P.sums);
-  a.leaders = reinterpret_cast<Leader*>(ws + P.leaders);
+  a.leader = reinterpret_cast<uint64_t*>(ws + P.leader);
   a.arrived = reinterpret_cast<uint32_t*>(ws + P.arrived);
   a.tokens = tokens;
   a.accepted = accepted;

@@ -23,7 +23,7 @@ def _softmax(z, t):
 
 def race(weight, noise):
     """(first arrival, how far ahead of the second it is: the ratio of their times)."""
-    w = np.where((noise >= 2.0 ** -100) & (noise <= 2.0 ** 100), weight, 0.0)
+    w = np.where((noise >= 2.0 ** -60) & (noise <= 2.0 ** 60), weight, 0.0)
     with np.errstate(divide="ignore"):
         time = np.where(w > 0, noise / w, np.inf)
     first = int(np.argmin(time))
