@@ -517,8 +517,8 @@ kd_status kd_embed_bwd(const kd_embed_problem* problem, const int64_t* tokens, c
  * the d_h they give.
  *   s = x + residual (x alone where that is NULL)
  *   h = s r (weight + weight_offset),   r = 1 / sqrt(mean(s^2) + eps)
- * s is formed, and its norm taken, in fp32; `sum` (may be NULL) gets it rounded
- * to dtype.  Backward, with s as it was stored (and r of that s), d_sum the
+ * s is formed, and its norm taken, in fp32 (elements from 2^63 on have squares
+ * beyond it); `sum` (may be NULL) gets it rounded to dtype.  Backward, with s as it was stored (and r of that s), d_sum the
  * gradient that reaches s from elsewhere (may be NULL) and g = d_h (weight +
  * weight_offset):
  *   d_x = r g - s r^3 mean(g s) + d_sum         (also the residual's gradient)

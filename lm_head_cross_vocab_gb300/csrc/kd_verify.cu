@@ -298,72 +298,86 @@ struct RaceShared {
   int count;
   int list[kList];
 };
+constexpr int kIds = 8;    // ids a thread takes at a time
+constexpr int kAhead = 2;  // times that, on their way
+// kIds neighbouring ids' logits and noise, as they come.
+template <class T>
+struct IdVec {
+  static constexpr int Z = kIds / RowVec<T>::N;
+  uint4 z[Z];
+  float4 e[kIds / 4];
+  __device__ __forceinline__ void load(const T* zt, const float* noise, int first) {
+#pragma unroll
+    for (int i = 0; i < Z; ++i) z[i] = reinterpret_cast<const uint4*>(zt + first)[i];
+#pragma unroll
+    for (int i = 0; i < kIds / 4; ++i) e[i] = __ldcs(&reinterpret_cast<const float4*>(noise + first)[i]);
+  }
+  __device__ __forceinline__ void get(float* x, float* y) const {
+#pragma unroll
+    for (int i = 0; i < Z; ++i) RowVec<T>::get(z[i], x + i * RowVec<T>::N);
+#pragma unroll
+    for (int i = 0; i < kIds / 4; ++i)
+      y[4 * i] = e[i].x, y[4 * i + 1] = e[i].y, y[4 * i + 2] = e[i].z, y[4 * i + 3] = e[i].w;
+  }
+};
 // The block's leader of ids [lo, hi), in every thread.
 template <class T>
 __device__ __forceinline__ uint64_t race_part(const Race& c, const T* zt, const T* zd,
                                               const float* noise, int64_t lo, int64_t hi,
                                               RaceShared& sh) {
-  constexpr int N = 8;  // ids a thread takes at a time
-  if (threadIdx.x == 0) {
+  const int tid = threadIdx.x;
+  if (tid == 0) {
     sh.best = 0;
     sh.count = 0;
   }
   __syncthreads();
-  const bool vec = ((reinterpret_cast<uintptr_t>(zt + lo) | reinterpret_cast<uintptr_t>(noise + lo)) & 15) == 0;
-  const int n = (int)(hi - lo), step = kThreads * N;
-  zt += lo;
-  noise += lo;
-  // element j of a thread's ids from `at` on: neighbours, or kThreads apart
-  auto id_of = [&](int at, int j) { return vec ? at + (int)threadIdx.x * N + j : at + j * kThreads + (int)threadIdx.x; };
-  auto load = [&](int at, float* z, float* e) {
-    const int first = at + (int)threadIdx.x * N;
-    if (vec && first + N <= n) {
-      if constexpr (RowVec<T>::N == 8) {
-        RowVec<T>::get(*reinterpret_cast<const uint4*>(zt + first), z);
-      } else {
-        RowVec<T>::get(*reinterpret_cast<const uint4*>(zt + first), z);
-        RowVec<T>::get(*reinterpret_cast<const uint4*>(zt + first + 4), z + 4);
-      }
-      const float4 a = *reinterpret_cast<const float4*>(noise + first);
-      const float4 b = *reinterpret_cast<const float4*>(noise + first + 4);
-      e[0] = a.x, e[1] = a.y, e[2] = a.z, e[3] = a.w;
-      e[4] = b.x, e[5] = b.y, e[6] = b.z, e[7] = b.w;
-    } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const int i = id_of(at, j);
-        z[j] = i < n ? to_f(zt[i]) : neg_inf();
-        e[j] = i < n ? noise[i] : 1.f;
-      }
-    }
-  };
+  const T* z0 = zt + lo;
+  const float* e0 = noise + lo;
+  const bool vec = ((reinterpret_cast<uintptr_t>(z0) | reinterpret_cast<uintptr_t>(e0)) & 15) == 0;
+  const int n = (int)(hi - lo), whole = vec ? n / kIds * kIds : 0;
+  constexpr int kStep = kThreads * kIds;
   auto exact = [&](int i) {
-    return c.score(to_f(zt[i]), zd ? to_f(zd[lo + i]) : 0.f, noise[i], lo + i);
+    return c.score(to_f(z0[i]), zd ? to_f(zd[lo + i]) : 0.f, e0[i], lo + i);
   };
   auto offer = [&](uint64_t w) {
     if (w) atomicMax((unsigned long long*)&sh.best, (unsigned long long)w);
   };
-  float z[N], e[N];
+  // ids that are not in a vector: kIds of them kThreads apart, or nothing
+  auto singles = [&](int at, float* z, float* e) {
+#pragma unroll
+    for (int j = 0; j < kIds; ++j) {
+      const int i = at + j * kThreads + tid;
+      z[j] = i < n ? to_f(z0[i]) : neg_inf();
+      e[j] = i < n ? e0[i] : 1.f;
+    }
+  };
+  float z[kIds], e[kIds];
   // some scores: of each thread's first ids the one that p makes the likeliest
-  load(0, z, e);
+  if (tid * kIds < whole) {
+    IdVec<T> w;
+    w.load(z0, e0, tid * kIds);
+    w.get(z, e);
+  } else {
+    singles(whole, z, e);
+  }
   {
     float most = 0.f;
     int at = -1;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
+    for (int j = 0; j < kIds; ++j) {
       const float x = __fdividef(ex2((z[j] - c.mt) * c.kt), e[j]);
       if (x > most) {
         most = x;
-        at = j;
+        at = tid * kIds < whole ? tid * kIds + j : whole + j * kThreads + tid;
       }
     }
-    uint64_t w = at >= 0 ? exact(id_of(0, at)) : 0;
+    uint64_t w = at >= 0 ? exact(at) : 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const uint64_t x = __shfl_xor_sync(0xffffffffu, w, o);
       w = x > w ? x : w;
     }
-    if ((threadIdx.x & 31) == 0) offer(w);
+    if ((tid & 31) == 0) offer(w);
   }
   __syncthreads();
   // p = 2^x / S, x = (z - m) k: an id may be ahead if 2^x > score S e.  The factor
@@ -372,32 +386,47 @@ __device__ __forceinline__ uint64_t race_part(const Race& c, const T* zt, const 
   const float held = __uint_as_float((uint32_t)(sh.best >> 32)) / c.inv_t * (1.f - 0x1p-14f);
   const float2 k2 = make_float2(c.kt, c.kt), m2 = make_float2(c.mt, c.mt), h2 = make_float2(held, held);
   __syncthreads();
-  for (int at = 0; at < n; at += step) {
-    if (at) load(at, z, e);
+  auto sift = [&](const float* z, const float* e, int first, int apart) {
     uint32_t pass = 0;
 #pragma unroll
-    for (int j = 0; j < N; j += 2) {
+    for (int j = 0; j < kIds; j += 2) {
       const float2 x = mul2(sub2(make_float2(z[j], z[j + 1]), m2), k2);
       const float2 y = mul2(make_float2(e[j], e[j + 1]), h2);
       if (ex2(x.x) > y.x) pass |= 1u << j;
       if (ex2(x.y) > y.y) pass |= 2u << j;
     }
     for (; pass; pass &= pass - 1) {
-      const int i = id_of(at, __ffs(pass) - 1);
+      const int i = first + (__ffs(pass) - 1) * apart;
       const int k = atomicAdd(&sh.count, 1);
       if (k < kList) sh.list[k] = i;
       else offer(exact(i));
     }
+  };
+  for (int at = tid * kIds; at < whole; at += kAhead * kStep) {
+    IdVec<T> w[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (at + u * kStep < whole) w[u].load(z0, e0, at + u * kStep);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (at + u * kStep < whole) {
+        w[u].get(z, e);
+        sift(z, e, at + u * kStep, 1);
+      }
+  }
+  for (int at = whole; at < n; at += kStep) {
+    singles(at, z, e);
+    sift(z, e, at + tid, kThreads);
   }
   __syncthreads();
   const int count = min(sh.count, kList);
-  for (int k = threadIdx.x; k < count; k += kThreads) offer(exact(sh.list[k]));
+  for (int k = tid; k < count; k += kThreads) offer(exact(sh.list[k]));
   __syncthreads();
   return sh.best;
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads) k_verify_draw(VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) k_verify_draw(VerifyArgs a) {
   __shared__ RowSum tgt[kMostDrafts + 1], drf[kMostDrafts];
   __shared__ RaceShared race_shared;
   __shared__ int stands, last;
@@ -580,11 +609,20 @@ kd_status verify_plan(const kd_verify_problem* p, VerifyPlan& P) {
   const int64_t bytes = p->vocab * (p->dtype == KD_BF16 ? 2 : 4);
   P.rows = p->n_seqs * (2 * p->n_drafts + 1);
   const int64_t r = std::max<int64_t>(P.rows, 1), b = std::max<int64_t>(p->n_seqs, 1);
-  // parts of at least 8 KB, some 16 blocks an SM
-  P.parts = (int)std::max<int64_t>(1, std::min<int64_t>({rows_div((int64_t)nsm * 16, r),
-                                                         bytes / 8192, kMaxParts}));
-  P.race_parts = (int)std::max<int64_t>(1, std::min<int64_t>({rows_div((int64_t)nsm * 4, b),
-                                                              p->vocab / 2048, kMaxParts}));
+  // Parts of a row in the first launch: three blocks an SM where rows are few, else
+  // some 96 KB each (72 rows of 304 KB: 15.6 us with 6 parts, 20.5 with 1, 22.4 with
+  // 34; 3840 rows: 233.6 us with 3, 237.3 with 1, 249.9 with 8), 16 KB at least.
+  P.parts = (int)std::max<int64_t>(1, std::min<int64_t>({std::max(rows_div((int64_t)nsm * 3, r),
+                                                                  (bytes + 49152) / 98304),
+                                                         bytes / 16384, kMaxParts}));
+  // and of the row that is drawn from: as many blocks as the SMs hold, four each, or
+  // where that is one or two a row, four (48 rows of 128256: 31.7 us with 12 parts, 37.7
+  // with 16; 256 rows of 151936: 227.8 us with 4, 247.3 with 2, 237 with 3)
+  const int64_t most = (int64_t)nsm * 4 / b;
+  P.race_parts = (int)std::max<int64_t>(1, std::min<int64_t>({most >= 3 ? most : 4,
+                                                              p->vocab / 4096, kMaxParts}));
+  // (a launch has at most 2^31 - 1 blocks; there are at most 2^27 rows)
+  P.parts = (int)std::min<int64_t>(P.parts, INT32_MAX / r);
   size_t off = 0;
   P.sums = rows_take(off, (size_t)r * P.parts * sizeof(RowSum));
   P.leader = rows_take(off, (size_t)b * 8);

@@ -644,7 +644,8 @@ def _same(name: str, t: torch.Tensor, shape, dtype, device):
 def _dense(name: str, t: Optional[torch.Tensor], shape, dtype, device):
     if t is None:
         return None
-    _same(name, t, shape, dtype, device)
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        _same(name, t, shape, dtype, device)  # (raises)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
@@ -838,6 +839,17 @@ def clip_grad_norm(grads, max_norm: float, *, out=None, workspace: Optional[Work
     return {"norm": norm, "grads": gl.out, "dev_status": gl.dev_status}
 
 
+def _kept(problem, key, make):
+    """make(), kept with a frozen problem: its C struct, its workspace on a device."""
+    kept = problem.__dict__.get("_kept")
+    if kept is None:
+        object.__setattr__(problem, "_kept", kept := {})
+    value = kept.get(key)
+    if value is None:
+        value = kept[key] = make()
+    return value
+
+
 # ---------------------------------------------------------------- drafted tokens
 
 KD_VERIFY_MAX_DRAFTS = 32
@@ -916,10 +928,11 @@ def verify_drafts(problem: VerifyProblem, tensors: dict, workspace: Optional[Wor
             _dense("accepted", out.get("accepted"), (b,), torch.int32, dev),
             _dense("logprob", out.get("logprob"), (b, k + 1), f32, dev),
             _status_word(out, dev))
-    cp = problem.to_c(ldt, ldd)
+    cp = problem.to_c(ldt, ldd) if ldt or ldd else _kept(problem, "c", problem.to_c)
     ws = workspace or Workspace()
     with _on(dev) as stream:
-        wptr, wbytes = ws.get(kd_verify_workspace_size(cp), dev)
+        need = _kept(problem, dev, lambda: kd_verify_workspace_size(cp))
+        wptr, wbytes = ws.get(need, dev)
         st = load_library().kd_verify_drafts(ctypes.byref(cp), ctypes.byref(ins), *ptrs, wptr,
                                              wbytes, stream)
     if st != KD_OK:
@@ -968,9 +981,10 @@ def embed_tokens(problem: EmbedProblem, w: torch.Tensor, tokens: torch.Tensor, *
     pt = _dense("tokens", tokens, (n,), torch.int64, dev)
     if out is None:
         out = {"h": torch.empty(n, d, device=dev, dtype=dtype)}
-    ph, status = _dense("h", out["h"], (n, d), dtype, dev), _status_word(out, dev)
+    ph, status = _dense("h", out.get("h"), (n, d), dtype, dev), _status_word(out, dev)
     with _on(dev) as stream:
-        st = load_library().kd_embed_fwd(ctypes.byref(problem.to_c()), pt, pw, ph, status, stream)
+        cp = _kept(problem, "c", problem.to_c)
+        st = load_library().kd_embed_fwd(ctypes.byref(cp), pt, pw, ph, status, stream)
     if st != KD_OK:
         raise KDError(st, "kd_embed_fwd")
     if check:
@@ -994,11 +1008,11 @@ def embed_tokens_backward(problem: EmbedProblem, tokens: torch.Tensor, d_h: torc
         if accumulate:
             raise ValueError("accumulate needs the d_w to add to, in out")
         out = {"d_w": torch.empty(v, d, device=dev, dtype=dtype)}
-    pw, status = _dense("d_w", out["d_w"], (v, d), dtype, dev), _status_word(out, dev)
-    cp = problem.to_c()
+    pw, status = _dense("d_w", out.get("d_w"), (v, d), dtype, dev), _status_word(out, dev)
+    cp = _kept(problem, "c", problem.to_c)
     ws = workspace or Workspace()
     with _on(dev) as stream:
-        wptr, wbytes = ws.get(kd_embed_workspace_size(cp), dev)
+        wptr, wbytes = ws.get(_kept(problem, dev, lambda: kd_embed_workspace_size(cp)), dev)
         st = load_library().kd_embed_bwd(ctypes.byref(cp), pt, pg, pw, int(accumulate), status,
                                          wptr, wbytes, stream)
     if st != KD_OK:
@@ -1053,9 +1067,10 @@ def rms_norm(problem: NormProblem, x: torch.Tensor, weight: torch.Tensor, *,
     args = (_dense("x", x, rows, dtype, dev), _dense("residual", residual, rows, dtype, dev),
             _dense("weight", weight, (d,), dtype, dev),
             _dense("sum", out.get("sum"), rows, dtype, dev),
-            _dense("h", out["h"], rows, dtype, dev))
+            _dense("h", out.get("h"), rows, dtype, dev))
     with _on(dev) as stream:
-        st = load_library().kd_rmsnorm_fwd(ctypes.byref(problem.to_c()), *args, stream)
+        cp = _kept(problem, "c", problem.to_c)
+        st = load_library().kd_rmsnorm_fwd(ctypes.byref(cp), *args, stream)
     if st != KD_OK:
         raise KDError(st, "kd_rmsnorm_fwd")
     return out
@@ -1084,10 +1099,10 @@ def rms_norm_backward(problem: NormProblem, s: torch.Tensor, weight: torch.Tenso
             _dense("d_h", d_h, rows, dtype, dev), _dense("d_sum", d_sum, rows, dtype, dev),
             _dense("d_x", out.get("d_x"), rows, dtype, dev),
             _dense("d_weight", out.get("d_weight"), (d,), dtype, dev))
-    cp = problem.to_c()
+    cp = _kept(problem, "c", problem.to_c)
     ws = workspace or Workspace()
     with _on(dev) as stream:
-        wptr, wbytes = ws.get(kd_rmsnorm_workspace_size(cp), dev)
+        wptr, wbytes = ws.get(_kept(problem, dev, lambda: kd_rmsnorm_workspace_size(cp)), dev)
         st = load_library().kd_rmsnorm_bwd(ctypes.byref(cp), *args, wptr, wbytes, stream)
     if st != KD_OK:
         raise KDError(st, "kd_rmsnorm_bwd")

@@ -168,6 +168,25 @@ def test_special_rows():
         assert torch.isfinite(h[i]).all() and torch.isfinite(d_x[i]).all()
 
 
+def test_rows_beyond_32_bit_offsets():
+    """The last rows begin past 2^31 elements."""
+    n, d = 530000, 4096
+    free, _ = torch.cuda.mem_get_info()
+    if free < 24e9:
+        pytest.skip("needs 24 GB")
+    c = _data(64, d, "bf16", seed=8)
+    x, d_h = (torch.zeros(n, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    x[-64:], d_h[-64:] = c["x"].cuda(), c["d_h"].cuda()
+    w = c["weight"].cuda()
+    p = kd.NormProblem(n_tokens=n, d_model=d)
+    r = kd.rms_norm(p, x, w)
+    _check_fwd({"h": r["h"][-64:]}, c, "bf16", False)
+    assert int(torch.count_nonzero(r["h"][:-64])) == 0
+    g = kd.rms_norm_backward(p, x, w, d_h)
+    _check_bwd({"d_x": g["d_x"][-64:], "d_weight": g["d_weight"]}, c["x"], c, "bf16", False, 64)
+    assert int(torch.count_nonzero(g["d_x"][:-64])) == 0
+
+
 def test_no_rows():
     p = kd.NormProblem(n_tokens=0, d_model=64)
     x, w = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(64).bfloat16().cuda()
