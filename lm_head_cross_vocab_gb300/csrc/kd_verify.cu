@@ -149,13 +149,15 @@ __device__ __forceinline__ void join_sum(float& m, float& s, float m2, float s2,
   s += s2;
   m = to;
 }
-// all lanes' sums, in every lane
+// all lanes' sums, in every lane: the largest offset first, then one rescale each
 __device__ __forceinline__ void warp_sum(float& m, float& s, float k) {
+  float to = m;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-    join_sum(m, s, m2, s2, k);
-  }
+  for (int o = 16; o > 0; o >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
+  if (m != to) s *= ex2((m - to) * k);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  m = to;
 }
 __device__ __forceinline__ uint64_t warp_best(uint64_t w) {
 #pragma unroll
@@ -276,6 +278,16 @@ __device__ __forceinline__ float power(float z, float m, float k) {
   return x < -150.f ? 0.f : p;  // (z = -inf among others: rest is NaN then)
 }
 
+// u a b < c d, to some 2^-46: with the products' own roundings a u just below 1
+// would count as 1 where a b = c d.  (In fp64, a unit that this GPU has little of,
+// the decisions of a block took 1.5 to 3 us.)
+__device__ __forceinline__ bool below(float u, float a, float b, float c, float d) {
+  const float x = __fmul_rn(a, b), xr = __fmaf_rn(a, b, -x);
+  const float y = __fmul_rn(c, d), yr = __fmaf_rn(c, d, -y);
+  const float z = __fmul_rn(u, x), zr = __fmaf_rn(u, x, -z);
+  return __fadd_rn(__fsub_rn(z, y), __fsub_rn(__fmaf_rn(u, xr, zr), yr)) < 0.f;
+}
+
 // The race over ids of one row.  A score's word: its bits above, the complement of
 // the id below, so that a larger word is ahead and equal scores go to the lowest
 // id; 0: nobody.  All blocks' words are compared as integers: no order matters.
@@ -352,26 +364,46 @@ __device__ __forceinline__ uint64_t race_part(const Race& c, const T* zt, const 
     }
   };
   float z[kIds], e[kIds];
-  // some scores: of each thread's first ids the one that p makes the likeliest
-  if (tid * kIds < whole) {
-    IdVec<T> w;
-    w.load(z0, e0, tid * kIds);
-    w.get(z, e);
-  } else {
-    singles(whole, z, e);
-  }
+  // some scores: of each thread's first ids the one that seems ahead
   {
-    float most = 0.f;
+    float d[kIds];
+    const T* d0 = zd ? zd + lo : nullptr;
+    const bool both = zd && (reinterpret_cast<uintptr_t>(d0) & 15) == 0;
+    const int first = tid * kIds < whole ? tid * kIds : whole + tid;
+    const int apart = tid * kIds < whole ? 1 : kThreads;
+    if (tid * kIds < whole) {
+      IdVec<T> w;
+      w.load(z0, e0, first);
+      if (both) {
+        uint4 y[IdVec<T>::Z];
+#pragma unroll
+        for (int i = 0; i < IdVec<T>::Z; ++i) y[i] = reinterpret_cast<const uint4*>(d0 + first)[i];
+#pragma unroll
+        for (int i = 0; i < IdVec<T>::Z; ++i) RowVec<T>::get(y[i], d + i * RowVec<T>::N);
+      }
+      w.get(z, e);
+    } else {
+      singles(whole, z, e);
+    }
+    if (!both || apart > 1) {
+#pragma unroll
+      for (int j = 0; j < kIds; ++j)
+        d[j] = zd && first + j * apart < n ? to_f(d0[first + j * apart]) : 0.f;
+    }
+    float most = 0.f, zb = 0.f, db = 0.f, eb = 1.f;
     int at = -1;
 #pragma unroll
     for (int j = 0; j < kIds; ++j) {
-      const float x = __fdividef(ex2((z[j] - c.mt) * c.kt), e[j]);
+      const float p = ex2((z[j] - c.mt) * c.kt) * c.inv_t;
+      const float q = ex2((d[j] - c.md) * c.kd) * c.inv_d;  // (inv_d = 0 without a drafter)
+      const float x = __fdividef(p - q, e[j]);
       if (x > most) {
         most = x;
-        at = tid * kIds < whole ? tid * kIds + j : whole + j * kThreads + tid;
+        at = first + j * apart;
+        zb = z[j], db = d[j], eb = e[j];
       }
     }
-    uint64_t w = at >= 0 ? exact(at) : 0;
+    uint64_t w = at >= 0 ? c.score(zb, db, eb, lo + at) : 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const uint64_t x = __shfl_xor_sync(0xffffffffu, w, o);
@@ -436,6 +468,14 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify_draw(VerifyArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = a.k + 1;
   chain_wait();
+  // what the decisions need of each draft, a lane of the first warp each, on its
+  // way while the sums are joined
+  int64_t x = -1;
+  float u = 0.f;
+  if (warp == 0 && lane < a.k) {
+    x = a.drafts[b * a.k + lane];
+    if (!a.greedy) u = a.u[b * a.k + lane];
+  }
   const int len = drafts_of(a, b);
   const bool over = a.lengths && a.lengths[b] > a.k;
   const T* zt = static_cast<const T*>(a.zt) + b * rows * a.ldt;
@@ -450,34 +490,39 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify_draw(VerifyArgs a) {
     }
     return;
   }
-  // ---- what the decisions need of each draft, on its way while the sums are joined
   const bool has_q = a.zd != nullptr && !a.greedy;
-  int64_t x = -1;
-  float zx = 0.f, qx = 0.f, u = 0.f;
-  if (warp == 0 && lane < len) {
-    x = a.drafts[b * a.k + lane];
-    if (!a.greedy) u = a.u[b * a.k + lane];
-    if (x >= 0 && x < a.vocab) {
-      zx = to_f(zt[lane * a.ldt + x]);
-      if (has_q) qx = to_f(zd[lane * a.ldd + x]);
-    }
+  float zx = 0.f, qx = 0.f;
+  if (warp == 0 && lane < len && x >= 0 && x < a.vocab) {
+    zx = to_f(zt[lane * a.ldt + x]);
+    if (has_q) qx = to_f(zd[lane * a.ldd + x]);
   }
-  // ---- the rows' sums
-  for (int r = warp; r < len + 1 + (has_q ? len : 0); r += kWarps) {
-    const bool draft = r > len;
-    const int i = draft ? r - len - 1 : r;
-    const int64_t row = draft ? a.b * rows + b * a.k + i : b * rows + i;
-    const float k = draft ? a.kd : a.kt;
-    float m = neg_inf(), s = 0.f;
-    uint64_t best = 0;
-    for (int p = lane; p < a.parts; p += 32) {
-      const RowSum x = a.sums[row * a.parts + p];
-      join_sum(m, s, x.m, x.s, k);
-      best = x.best > best ? x.best : best;
+  // ---- the rows' sums: two rows of a warp at a time, their parts a lane each
+  const int sums = len + 1 + (has_q ? len : 0);
+  for (int r0 = warp; r0 < sums; r0 += 2 * kWarps) {
+    RowSum v[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = r0 + h * kWarps;
+      v[h] = RowSum{neg_inf(), 0.f, 0};
+      if (r >= sums) continue;
+      const int64_t row = r > len ? a.b * rows + b * a.k + (r - len - 1) : b * rows + r;
+      const float k = r > len ? a.kd : a.kt;
+      if (lane < a.parts) v[h] = a.sums[row * a.parts + lane];
+      if (lane + 32 < a.parts) {
+        const RowSum o = a.sums[row * a.parts + lane + 32];
+        join_sum(v[h].m, v[h].s, o.m, o.s, k);
+        v[h].best = o.best > v[h].best ? o.best : v[h].best;
+      }
     }
-    warp_sum(m, s, k);
-    if (a.greedy) best = warp_best(best);
-    if (lane == 0) (draft ? drf[i] : tgt[i]) = RowSum{m, s, best};
+    static_assert(kMaxParts <= 64, "two parts a lane");
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = r0 + h * kWarps;
+      if (r >= sums) continue;
+      warp_sum(v[h].m, v[h].s, r > len ? a.kd : a.kt);
+      if (a.greedy) v[h].best = warp_best(v[h].best);
+      if (lane == 0) (r > len ? drf[r - len - 1] : tgt[r]) = v[h];
+    }
   }
   __syncthreads();
   // ---- the drafts that stand: a lane each
@@ -496,10 +541,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify_draw(VerifyArgs a) {
           if (has_q) {
             const RowSum d = drf[lane];
             const float q = power(qx, d.m, a.kd);
-            // (products that do not round equal p and q to a rejection at u < 1)
-            ok = (double)u * (double)q * (double)t.s < (double)p * (double)d.s;
+            ok = below(u, q, t.s, p, d.s);
           } else {
-            ok = (double)u * (double)t.s < (double)p;
+            ok = below(u, 1.f, t.s, p, 1.f);
           }
         }
         bad = bad || bad_q;
@@ -543,11 +587,15 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify_draw(VerifyArgs a) {
     if (alive) leader = race_part<T>(race, zt, q, noise, lo, hi, race_shared);
     if (a.race_parts > 1) {
       if (threadIdx.x == 0) {
+        // (release: the leader comes before the arrival; acquire: all of theirs)
         if (leader) atomicMax((unsigned long long*)&a.leader[b], (unsigned long long)leader);
-        __threadfence();
-        last = atomicAdd(&a.arrived[b], 1) == (uint32_t)a.race_parts - 1;
-        __threadfence();
-        race_shared.best = *(volatile uint64_t*)&a.leader[b];
+        uint32_t before;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
+                     : "=r"(before)
+                     : "l"(&a.arrived[b])
+                     : "memory");
+        last = before == (uint32_t)a.race_parts - 1;
+        if (last) race_shared.best = *(volatile uint64_t*)&a.leader[b];
       }
       __syncthreads();
       if (!last) return;
@@ -564,21 +612,19 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify_draw(VerifyArgs a) {
   // ---- outputs
   const bool drawn = alive && (a.greedy || leader);
   const int64_t token = (int64_t)(uint32_t)~(uint32_t)(a.greedy ? row.best : leader);
-  if (threadIdx.x < rows) {
-    const int i = threadIdx.x;
-    const int64_t x = i < n ? a.drafts[b * a.k + i] : i == n && drawn ? token : a.ignore;
-    if (a.tokens) a.tokens[b * rows + i] = x;
-    if (a.logprob) {
-      float lp = 0.f;
-      if (i < n || (i == n && drawn)) {
-        const RowSum t = tgt[i];
-        const float z = to_f(zt[(i - n) * a.ldt + x]);
-        lp = fmaf(z - t.m, a.inv_t, -logf(t.s));
-      } else if (i == n) {
-        lp = __int_as_float(0x7fffffff);
+  if (warp == 0) {
+    auto put = [&](int i, int64_t x, float z) {  // place i: an accepted draft, the drawn one, none
+      const bool there = i < n || (i == n && drawn);
+      if (a.tokens) a.tokens[b * rows + i] = there ? x : a.ignore;
+      if (a.logprob) {
+        const RowSum t = tgt[min(i, n)];
+        a.logprob[b * rows + i] = there ? fmaf(z - t.m, a.inv_t, -logf(t.s))
+                                        : i == n ? __int_as_float(0x7fffffff) : 0.f;
       }
-      a.logprob[b * rows + i] = lp;
-    }
+    };
+    const float z = drawn ? to_f(zt[token]) : 0.f;
+    if (lane < rows) put(lane, lane < n ? x : token, lane < n ? zx : z);
+    if (lane == 0 && rows > 32) put(32, token, z);
   }
   if (threadIdx.x == 0) {
     if (a.accepted) a.accepted[b] = n;
