@@ -33,11 +33,13 @@ struct NormArgs {
 };
 
 // A thread's elements of a row: VPT vectors, TPR apart, or VPT * N elements,
-// TPR apart.  Zero beyond the row.
+// TPR apart (held as they came: packed, each load would be waited for before the
+// next).  Zero beyond the row.
 template <class T, int TPR, int VPT, bool VEC>
 struct RowPart {
   static constexpr int N = RowVec<T>::N, E = VPT * N;
-  uint4 w[VPT];
+  uint4 w[VEC ? VPT : 1];
+  T x[VEC ? 1 : E];
 
   __device__ __forceinline__ void load(const T* p, int d, int t) {
     if constexpr (VEC) {
@@ -47,18 +49,20 @@ struct RowPart {
         w[i] = i * TPR + t < d / N ? q[i * TPR + t] : make_uint4(0, 0, 0, 0);
     } else {
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        float v[N];
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const int at = (i * N + e) * TPR + t;
-          v[e] = at < d ? to_f(p[at]) : 0.f;
-        }
-        w[i] = RowVec<T>::put(v);
+      for (int e = 0; e < E; ++e) {
+        if (e * TPR + t < d) x[e] = p[e * TPR + t];
+        else from_f(0.f, x[e]);
       }
     }
   }
-  __device__ __forceinline__ void get(int i, float* v) const { RowVec<T>::get(w[i], v); }
+  __device__ __forceinline__ void get(int i, float* v) const {
+    if constexpr (VEC) {
+      RowVec<T>::get(w[i], v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] = to_f(x[i * N + e]);
+    }
+  }
   // the values of vector i
   static __device__ __forceinline__ void store(T* p, int d, int t, int i, const float* v) {
     if constexpr (VEC) {
