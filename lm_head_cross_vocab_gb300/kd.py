@@ -850,6 +850,26 @@ def _kept(problem, key, make):
     return value
 
 
+def _need(problem, cp, size, device) -> int:
+    """Bytes of workspace of a problem on a device."""
+    def ask():
+        with _on(device):
+            return size(cp)
+    return _kept(problem, device, ask)
+
+
+def _enqueue(name: str, device: torch.device, *args):
+    """One library call on the device's current stream; raises what it refuses."""
+    i, fn = device.index, getattr(load_library(), name)
+    if torch._C._cuda_getDevice() == i:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    if st != KD_OK:
+        raise KDError(st, name)
+
+
 # ---------------------------------------------------------------- drafted tokens
 
 KD_VERIFY_MAX_DRAFTS = 32
@@ -876,7 +896,8 @@ class VerifyProblem:
 
 def _seq_rows_pitch(name: str, t: torch.Tensor, shape, dtype, device) -> int:
     """Row pitch of [B, K, V] logits whose rows lie at one pitch (0 when dense)."""
-    _same(name, t, shape, dtype, device)
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        _same(name, t, shape, dtype, device)  # (raises)
     if t.is_contiguous():
         return 0
     b, k, v = shape
@@ -930,13 +951,8 @@ def verify_drafts(problem: VerifyProblem, tensors: dict, workspace: Optional[Wor
             _status_word(out, dev))
     cp = problem.to_c(ldt, ldd) if ldt or ldd else _kept(problem, "c", problem.to_c)
     ws = workspace or Workspace()
-    with _on(dev) as stream:
-        need = _kept(problem, dev, lambda: kd_verify_workspace_size(cp))
-        wptr, wbytes = ws.get(need, dev)
-        st = load_library().kd_verify_drafts(ctypes.byref(cp), ctypes.byref(ins), *ptrs, wptr,
-                                             wbytes, stream)
-    if st != KD_OK:
-        raise KDError(st, "kd_verify_drafts")
+    wptr, wbytes = ws.get(_need(problem, cp, kd_verify_workspace_size, dev), dev)
+    _enqueue("kd_verify_drafts", dev, ctypes.byref(cp), ctypes.byref(ins), *ptrs, wptr, wbytes)
     if check:
         _check_and_tell(out["dev_status"], nonfinite="a row of logits has no distribution")
     return out
@@ -982,11 +998,8 @@ def embed_tokens(problem: EmbedProblem, w: torch.Tensor, tokens: torch.Tensor, *
     if out is None:
         out = {"h": torch.empty(n, d, device=dev, dtype=dtype)}
     ph, status = _dense("h", out.get("h"), (n, d), dtype, dev), _status_word(out, dev)
-    with _on(dev) as stream:
-        cp = _kept(problem, "c", problem.to_c)
-        st = load_library().kd_embed_fwd(ctypes.byref(cp), pt, pw, ph, status, stream)
-    if st != KD_OK:
-        raise KDError(st, "kd_embed_fwd")
+    cp = _kept(problem, "c", problem.to_c)
+    _enqueue("kd_embed_fwd", dev, ctypes.byref(cp), pt, pw, ph, status)
     if check:
         _check_and_tell(out["dev_status"])
     return out
@@ -1011,12 +1024,9 @@ def embed_tokens_backward(problem: EmbedProblem, tokens: torch.Tensor, d_h: torc
     pw, status = _dense("d_w", out.get("d_w"), (v, d), dtype, dev), _status_word(out, dev)
     cp = _kept(problem, "c", problem.to_c)
     ws = workspace or Workspace()
-    with _on(dev) as stream:
-        wptr, wbytes = ws.get(_kept(problem, dev, lambda: kd_embed_workspace_size(cp)), dev)
-        st = load_library().kd_embed_bwd(ctypes.byref(cp), pt, pg, pw, int(accumulate), status,
-                                         wptr, wbytes, stream)
-    if st != KD_OK:
-        raise KDError(st, "kd_embed_bwd")
+    wptr, wbytes = ws.get(_need(problem, cp, kd_embed_workspace_size, dev), dev)
+    _enqueue("kd_embed_bwd", dev, ctypes.byref(cp), pt, pg, pw, int(accumulate), status, wptr,
+             wbytes)
     if check:
         _check_and_tell(out["dev_status"])
     return out
@@ -1068,11 +1078,8 @@ def rms_norm(problem: NormProblem, x: torch.Tensor, weight: torch.Tensor, *,
             _dense("weight", weight, (d,), dtype, dev),
             _dense("sum", out.get("sum"), rows, dtype, dev),
             _dense("h", out.get("h"), rows, dtype, dev))
-    with _on(dev) as stream:
-        cp = _kept(problem, "c", problem.to_c)
-        st = load_library().kd_rmsnorm_fwd(ctypes.byref(cp), *args, stream)
-    if st != KD_OK:
-        raise KDError(st, "kd_rmsnorm_fwd")
+    cp = _kept(problem, "c", problem.to_c)
+    _enqueue("kd_rmsnorm_fwd", dev, ctypes.byref(cp), *args)
     return out
 
 
@@ -1101,9 +1108,6 @@ def rms_norm_backward(problem: NormProblem, s: torch.Tensor, weight: torch.Tenso
             _dense("d_weight", out.get("d_weight"), (d,), dtype, dev))
     cp = _kept(problem, "c", problem.to_c)
     ws = workspace or Workspace()
-    with _on(dev) as stream:
-        wptr, wbytes = ws.get(_kept(problem, dev, lambda: kd_rmsnorm_workspace_size(cp)), dev)
-        st = load_library().kd_rmsnorm_bwd(ctypes.byref(cp), *args, wptr, wbytes, stream)
-    if st != KD_OK:
-        raise KDError(st, "kd_rmsnorm_bwd")
+    wptr, wbytes = ws.get(_need(problem, cp, kd_rmsnorm_workspace_size, dev), dev)
+    _enqueue("kd_rmsnorm_bwd", dev, ctypes.byref(cp), *args, wptr, wbytes)
     return out
