@@ -663,10 +663,13 @@ kd_status verify_plan(const kd_verify_problem* p, VerifyPlan& P) {
                                                          bytes / 16384, kMaxParts}));
   // and of the row that is drawn from: as many blocks as the SMs hold, four each, or
   // where that is one or two a row, four (48 rows of 128256: 31.7 us with 12 parts, 37.7
-  // with 16; 256 rows of 151936: 227.8 us with 4, 247.3 with 2, 237 with 3)
+  // with 16; 256 rows of 151936: 227.8 us with 4, 247.3 with 2, 237 with 3); parts
+  // below 8192 ids only up to two blocks an SM (16 rows of 151936: 12.5 us with 16,
+  // 13.5 with 37), and of 2048 at least
   const int64_t most = (int64_t)nsm * 4 / b;
-  P.race_parts = (int)std::max<int64_t>(1, std::min<int64_t>({most >= 3 ? most : 4,
-                                                              p->vocab / 4096, kMaxParts}));
+  P.race_parts = (int)std::max<int64_t>(
+      1, std::min<int64_t>({most >= 3 ? most : 4, std::max(p->vocab / 8192, (int64_t)nsm * 2 / b),
+                            p->vocab / 2048, kMaxParts}));
   // (a launch has at most 2^31 - 1 blocks; there are at most 2^27 rows)
   P.parts = (int)std::min<int64_t>(P.parts, INT32_MAX / r);
   size_t off = 0;
