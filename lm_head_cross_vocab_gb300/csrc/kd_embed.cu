@@ -20,7 +20,7 @@
 // The lookup is bound by its writes (16384 x 4096 bf16 32 us, 4.2 TB/s written and each
 // id's row read once), the gradient of a whole table by the table's (16384 tokens of 4096
 // into 151936 rows 203 us, a fill alone 164-170 us), that of few ids by the latency of
-// three launches (4096 tokens of 2048 added to 32000 rows 18 us: sort 5, reduce 8, join 5).
+// three launches (4096 tokens of 2048 added to 32000 rows 16 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -153,6 +153,11 @@ struct Segment {
 };
 struct Place {
   int32_t row, id;
+};
+// A frequent id (id -1: none) whose places begin in a run.
+struct Head {
+  int32_t id;
+  Segment seg;
 };
 
 struct SortArgs {
@@ -369,7 +374,7 @@ struct ReduceGradArgs {
   const Segment* seg;
   const Place* place;
   const int32_t* live;
-  int32_t* head;      // [runs]: the frequent id whose places begin in this run, or -1
+  Head* head;         // [runs]
   float* part;        // [runs][d] sums of frequent ids' pieces, by the run they start in
   int64_t n, vocab, d;
   int run;            // places of the list a team starts pieces in, a power of two
@@ -484,7 +489,8 @@ __global__ void __launch_bounds__(kReduceThreads) k_embed_reduce(ReduceGradArgs 
     const Place x0 = at + t < a.n ? a.place[at + t] : none;
     const Place x1 = at + t + 32 < a.n ? a.place[at + t + 32] : none;
     const int64_t live = *a.live;
-    int len = 0, ends = -1, heads = -1;
+    int len = 0, ends = -1;
+    Head head{-1, Segment{0, 0}};
     if (t < a.run && at + t < live) {
       const Segment s = a.seg[x0.id];
       const int off = (int)(at + t - s.first);
@@ -495,11 +501,11 @@ __global__ void __launch_bounds__(kReduceThreads) k_embed_reduce(ReduceGradArgs 
         const int q = s.count / kPiece, j = off / kPiece;
         if (off % kPiece == 0 && j < q) len = j < q - 1 ? kPiece : s.count - j * kPiece;
         ends = -2;
-        if (off == 0) heads = x0.id;
+        if (off == 0) head = Head{x0.id, s};
       }
     }
-    heads = __reduce_max_sync(0xffffffffu, heads);
-    if (t == 0 && c0 == 0 && at < a.n) a.head[run] = heads;
+    const uint32_t heads = __ballot_sync(0xffffffffu, head.id >= 0);
+    if (t == (heads ? __ffs(heads) - 1 : 0) && c0 == 0 && at < a.n) a.head[run] = head;
     // the pieces lie one behind the other: a place's row is its distance from the
     // first one's start, and the rows added to that come before it
     const uint32_t starts = __ballot_sync(0xffffffffu, len > 0);
@@ -595,7 +601,8 @@ __device__ __forceinline__ Four join_parts(const float* part, int64_t apart, int
 
 template <class T>
 __global__ void __launch_bounds__(kJoinThreads) k_embed_join(ReduceGradArgs a, int cols) {
-  __shared__ int heads[kJoinPlaces / (2 * kPiece) + 1], count;
+  __shared__ Head heads[kJoinPlaces / (2 * kPiece) + 1];
+  __shared__ int count;
   __shared__ Four sums[kJoinWarps][32];
   if (threadIdx.x == 0) count = 0;
   chain_wait();
@@ -605,38 +612,49 @@ __global__ void __launch_bounds__(kJoinThreads) k_embed_join(ReduceGradArgs a, i
   const int64_t c = (blockIdx.x - chunk * cols) * kJoinCols + lane;
   const int here = kJoinPlaces / a.run;  // runs, a thread each
   const int64_t run = chunk * here + threadIdx.x, runs = (a.n + a.run - 1) / a.run;
-  const int v = threadIdx.x < here && run < runs ? a.head[run] : -1;
-  if (v >= 0) heads[atomicAdd(&count, 1)] = v;  // (in any order: each is summed by itself)
+  if (threadIdx.x < here && run < runs) {
+    const Head h = a.head[run];
+    if (h.id >= 0) heads[atomicAdd(&count, 1)] = h;  // (in any order: each is summed by itself)
+  }
   __syncthreads();
   const int n = count;
-  auto finish = [&](int v, const Four& s) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (c + 32 * e < a.d) {
-        T& o = static_cast<T*>(a.dw)[(int64_t)v * a.d + c + 32 * e];
-        from_f(a.accumulate ? fmaf(a.scale, s.v[e], to_f(o)) : a.scale * s.v[e], o);
-      }
-  };
   // piece j begins kPiece j places behind the first: kPiece / run runs
   const int64_t apart = a.d * (kPiece / a.run);
-  auto parts = [&](const Segment& s) { return a.part + (int64_t)(s.first / a.run) * a.d; };
+  auto parts = [&](const Head& h) { return a.part + (int64_t)(h.seg.first / a.run) * a.d; };
+  auto row = [&](const Head& h) { return static_cast<T*>(a.dw) + (int64_t)h.id * a.d + c; };
+  auto old = [&](const Head& h) {  // what is added to
+    Four o{{0.f, 0.f, 0.f, 0.f}};
+    if (a.accumulate)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + 32 * e < a.d) o.v[e] = to_f(row(h)[32 * e]);
+    return o;
+  };
+  auto finish = [&](const Head& h, const Four& s, const Four& o) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + 32 * e < a.d)
+        from_f(a.accumulate ? fmaf(a.scale, s.v[e], o.v[e]) : a.scale * s.v[e], row(h)[32 * e]);
+  };
   for (int k = warp; k < n; k += kJoinWarps) {
-    const Segment s = a.seg[heads[k]];
-    const int q = s.count / kPiece;
-    if (q <= kWarpParts) finish(heads[k], join_parts(parts(s), apart, a.d, c, 0, 1, q));
+    const Head h = heads[k];
+    const int q = h.seg.count / kPiece;
+    if (q > kWarpParts) continue;
+    const Four o = old(h);
+    finish(h, join_parts(parts(h), apart, a.d, c, 0, 1, q), o);
   }
   for (int k = 0; k < n; ++k) {  // more pieces: all warps, their sums in order
-    const Segment s = a.seg[heads[k]];
-    const int q = s.count / kPiece;
+    const Head h = heads[k];
+    const int q = h.seg.count / kPiece;
     if (q <= kWarpParts) continue;
-    sums[warp][lane] = join_parts(parts(s), apart, a.d, c, warp, kJoinWarps, q);
+    sums[warp][lane] = join_parts(parts(h), apart, a.d, c, warp, kJoinWarps, q);
     __syncthreads();
     if (warp == 0) {
       Four x = sums[0][lane];
       for (int w = 1; w < kJoinWarps; ++w)
 #pragma unroll
         for (int e = 0; e < 4; ++e) x.v[e] += sums[w][lane].v[e];
-      finish(heads[k], x);
+      finish(h, x, old(h));
     }
     __syncthreads();
   }
@@ -670,7 +688,7 @@ kd_status embed_plan(const kd_embed_problem* p, EmbedPlan& P) {
   P.seg = rows_take(off, (size_t)p->vocab * sizeof(Segment));
   P.place = rows_take(off, (size_t)p->n_tokens * sizeof(Place));
   P.live = rows_take(off, 4);
-  P.head = rows_take(off, (size_t)runs * 4);
+  P.head = rows_take(off, (size_t)runs * sizeof(Head));
   P.part = rows_take(off, p->n_tokens >= 2 * kPiece ? (size_t)runs * p->d_model * 4 : 0);
   P.bytes = off;
   return KD_OK;
@@ -815,7 +833,7 @@ extern "C" kd_status kd_embed_bwd(const kd_embed_problem* p, const int64_t* toke
   a.seg = t.seg;
   a.place = t.place;
   a.live = t.live;
-  a.head = reinterpret_cast<int32_t*>(ws + P.head);
+  a.head = reinterpret_cast<Head*>(ws + P.head);
   a.part = reinterpret_cast<float*>(ws + P.part);
   a.n = p->n_tokens;
   a.vocab = p->vocab;

@@ -211,11 +211,11 @@ def test_repeats_exactly_and_in_graphs_that_share_a_workspace():
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             kd.embed_tokens_backward(p, tokens, d_h, workspace=ws, out=out, check=False)
-        jobs.append((graph, out["d_w"], ref))
-    for _, o, _ in jobs:
-        o.zero_()
+        jobs.append((graph, out["d_w"], ref, tokens, d_h))  # (a graph reads its inputs' memory)
+    for job in jobs:
+        job[1].zero_()
     for _ in range(3):
-        for graph, _, _ in jobs:
-            graph.replay()
+        for job in jobs:
+            job[0].replay()
     torch.cuda.synchronize()
-    assert all(torch.equal(o, ref) for _, o, ref in jobs)
+    assert all(torch.equal(o, ref) for _, o, ref, _, _ in jobs)

@@ -144,3 +144,46 @@ def test_a_drafter_over_another_vocabulary():
     sure = ref["margin"] > 1e-3
     assert sure.sum() >= b - 2
     assert (r["tokens"].cpu().numpy() == ref["tokens"])[sure].all()
+
+
+def test_calls_on_two_streams_at_once():
+    """Each with its own workspace and outputs, their inputs shared, over and over."""
+    g = torch.Generator().manual_seed(25)
+    n, v, d, b, k = 3000, 9000, 520, 6, 3
+    w = torch.randn(v, d, generator=g).bfloat16().cuda()
+    tokens = (torch.rand(n, generator=g) ** 4 * v).long().cuda()
+    d_h = torch.randn(n, d, generator=g).bfloat16().cuda()
+    gain = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    target = torch.randn(b, k + 1, v, generator=g).bfloat16().cuda()
+    drafts = torch.randint(0, v, (b, k), generator=g).cuda()
+    u, e = torch.rand(b, k, generator=g).cuda(), torch.rand(b, v, generator=g).cuda() + 0.01
+    ep = kd.EmbedProblem(n_tokens=n, vocab=v, d_model=d)
+    np_ = kd.NormProblem(n_tokens=n, d_model=d)
+    vp = kd.VerifyProblem(n_seqs=b, n_drafts=k, vocab=v)
+    ins = {"target_logits": target, "draft_logits": target[:, 1:].contiguous(), "drafts": drafts,
+           "uniform": u, "noise": e}
+
+    def step(ws, out):
+        out["x"] = kd.embed_tokens(ep, w, tokens, check=False, out=out.get("x"))
+        out["h"] = kd.rms_norm(np_, out["x"]["h"], gain, out=out.get("h"))
+        out["n"] = kd.rms_norm_backward(np_, out["x"]["h"], gain, d_h, workspace=ws[0],
+                                        out=out.get("n"))
+        out["t"] = kd.embed_tokens_backward(ep, tokens, out["n"]["d_x"], workspace=ws[1],
+                                            check=False, out=out.get("t"))
+        out["v"] = kd.verify_drafts(vp, ins, workspace=ws[2], check=False, out=out.get("v"))
+        return out
+
+    ref = step([kd.Workspace() for _ in range(3)], {})
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    held = [([kd.Workspace() for _ in range(3)], {}) for _ in streams]
+    for _ in range(8):
+        for s, (ws, out) in zip(streams, held):
+            with torch.cuda.stream(s):
+                step(ws, out)
+    torch.cuda.synchronize()
+    for _, out in held:
+        for op, r in ref.items():
+            for name, t in r.items():
+                if t is not None:
+                    assert torch.equal(out[op][name], t), (op, name)
