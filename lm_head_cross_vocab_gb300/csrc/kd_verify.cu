@@ -198,8 +198,11 @@ __global__ void __launch_bounds__(kThreads) k_verify_sums(VerifyArgs a) {
   const Part<T> p(z, a.vocab, part, a.parts);
   Fold f;
   f.init(draft ? a.kd : a.kt);
+  // greedy: the largest logit and the step it came in; who has the block's largest
+  // looks that step's vectors through once more
   float top = neg_inf();
-  int64_t top_at = 0;
+  int64_t top_v = 0;
+  int top_n = 0;
   const uint4* q = p.vectors();
   auto take = [&](const uint4* w, int64_t v, auto count) {
     constexpr int C = decltype(count)::value;
@@ -210,18 +213,8 @@ __global__ void __launch_bounds__(kThreads) k_verify_sums(VerifyArgs a) {
     f.expect(m);
     if (GREEDY && m > top) {
       top = m;
-      bool found = false;
-#pragma unroll
-      for (int u = 0; u < C; ++u) {
-        float x[N];
-        RowVec<T>::get(w[u], x);
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-          if (!found && x[e] == m) {
-            found = true;
-            top_at = p.head + (v + u * kThreads) * N + e;
-          }
-      }
+      top_v = v;
+      top_n = C;
     }
 #pragma unroll
     for (int u = 0; u < C; ++u) {
@@ -242,20 +235,42 @@ __global__ void __launch_bounds__(kThreads) k_verify_sums(VerifyArgs a) {
     const uint4 w = q[v];
     take(&w, v, std::integral_constant<int, 1>());
   }
-  uint64_t best = top == neg_inf() ? 0 : cand_word(order_key(top), (uint32_t)top_at);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint64_t best = 0;
+  float loose = neg_inf();
+  int64_t loose_at = 0;
   if (threadIdx.x < p.loose()) {
-    const int64_t at = p.loose_at(threadIdx.x);
-    const float x = to_f(z[at]);
-    f.one(x);
-    if (GREEDY && x > neg_inf()) {
-      const uint64_t w = cand_word(order_key(x), (uint32_t)at);
-      best = w > best ? w : best;
+    loose_at = p.loose_at(threadIdx.x);
+    loose = to_f(z[loose_at]);
+    f.one(loose);
+  }
+  if (GREEDY) {
+    float most = fmaxf(top, loose);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (lane == 0) wm[warp] = most;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) most = fmaxf(most, wm[w]);
+    __syncthreads();
+    if (most > neg_inf()) {
+      if (loose == most) best = cand_word(order_key(most), (uint32_t)loose_at);
+      if (top == most) {
+        int64_t at = -1;
+        for (int u = 0; u < top_n && at < 0; ++u) {
+          float x[N];
+          RowVec<T>::get(q[top_v + u * kThreads], x);
+#pragma unroll
+          for (int e = N - 1; e >= 0; --e)
+            if (x[e] == most) at = p.head + (top_v + u * kThreads) * N + e;
+        }
+        const uint64_t w = cand_word(order_key(most), (uint32_t)at);
+        best = w > best ? w : best;
+      }
     }
   }
   float off = f.m, s = f.s.x + f.s.y;
   warp_sum(off, s, f.k);
   if (GREEDY) best = warp_best(best);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (lane == 0) {
     wm[warp] = off;
     ws[warp] = s;
