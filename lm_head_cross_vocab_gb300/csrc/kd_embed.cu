@@ -143,9 +143,11 @@ __global__ void __launch_bounds__(kLookupThreads) k_embed_short(LookupArgs a) {
 
 // ------------------------------------------------------------------ sort
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
-constexpr int kMaxIds = 1536;  // ids of a block
+constexpr int kMaxIds = 1216;  // ids of a block
 constexpr int kAhead = 8;      // tokens a lane has in flight
-constexpr int kKept = 256;     // tokens a warp keeps
+constexpr int kKept = 128;     // tokens a warp keeps, each as its place in the warp's
+constexpr int kPlaceBits = 21; // run below and its id's number above
+constexpr int kOneWarp = 512;  // tokens of a block that one warp puts in order
 
 // Places of one id in the list.
 struct Segment {
@@ -192,13 +194,15 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sum, int& total) {
   return before + x - v;
 }
 
-// Dynamic shared memory: either [ids] counters and two lists of the tokens kept,
-// or (too many for a list) [kSortWarps][ids] counters.
-constexpr int kListBytes = kSortWarps * kKept * (int)sizeof(Place);
+// Dynamic shared memory: [ids] counters, the warps' lists of the tokens kept, and
+// one list of them all or [kSortWarps][ids] counters.
+constexpr int kListBytes = kSortWarps * kKept * 4;
 __host__ __device__ constexpr int sort_smem(int ids) {
-  const int few = (ids * 4 + 15) / 16 * 16 + 2 * kListBytes, many = kSortWarps * ids * 4;
-  return few > many ? few : many;
+  const int many = kSortWarps * ids * 4, one = kOneWarp * (int)sizeof(Place);
+  return (ids + 3) / 4 * 16 + kListBytes + (many > one ? many : one);
 }
+static_assert(sort_smem(kMaxIds) <= 226 * 1024, "shared memory of a block");
+static_assert(kMaxIds <= 1 << (32 - kPlaceBits), "a token in 32 bits");
 
 __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a) {
   extern __shared__ __align__(16) int counter[];
@@ -206,8 +210,9 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a) {
   chain_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t block = blockIdx.x, mask = (1u << a.lg) - 1, before = (1u << lane) - 1;
-  Place* list = reinterpret_cast<Place*>(counter + (a.ids + 3) / 4 * 4);
-  Place* all = list + kSortWarps * kKept;
+  uint32_t* list = reinterpret_cast<uint32_t*>(counter + (a.ids + 3) / 4 * 4) + warp * kKept;
+  int* more = counter + (a.ids + 3) / 4 * 4 + kSortWarps * kKept;
+  int* run = more + warp * a.ids;  // this warp's own counters
   for (int i = threadIdx.x; i < a.ids; i += kSortThreads) counter[i] = 0;
   if (threadIdx.x == 0) below_sum = crowded = 0;
   // this warp's run of the tokens, whole groups of 32
@@ -223,29 +228,43 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a) {
     if (inside) in = in && t != a.ignore;
     return in ? id & mask : 0xffffffffu;
   };
-  // the block's own number of a token's id, or -1
-  auto own = [&](int64_t at) {
-    const int64_t t = at < end ? a.tokens[at] : a.ignore;
-    return owner(t) == block ? (int)((uint32_t)t >> a.lg) : -1;
-  };
-  auto put = [&](int p, int64_t row, int k) {
-    a.place[p] = Place{(int32_t)row, (int32_t)(((uint32_t)k << a.lg) + block)};
+  auto row_of = [&](uint32_t x) { return (int)(begin + (x & ((1u << kPlaceBits) - 1))); };
+  auto id_of = [&](uint32_t x) { return (int)(x >> kPlaceBits); };
+  // the lanes' tokens (k -1: none) to their places, the next of each id in `next`
+  auto rank = [&](int* next, int row, int k) {
+    const uint32_t same = __match_any_sync(0xffffffffu, k);
+    const int p = k >= 0 ? next[k] + __popc(same & before) : 0;
+    __syncwarp();
+    if (k >= 0) {
+      if (lane == __ffs(same) - 1) next[k] += __popc(same);
+      a.place[p] = Place{row, (int32_t)(((uint32_t)k << a.lg) + block)};
+    }
+    __syncwarp();
   };
   __syncthreads();
-  // tokens of this warp's run that the block owns, and of the blocks before it
-  int mine = 0, below = 0;
+  // tokens of this warp's run that the block owns, in the list, and from `full` on
+  // only counted; and tokens of the blocks before it
+  int mine = 0, owned = 0, below = 0;
+  int64_t full = -1;
+  const bool may_fill = each * 32 > kKept;
+  if (may_fill)
+    for (int i = lane; i < a.ids; i += 32) run[i] = 0;
+  __syncwarp();
   auto take = [&](int64_t at, int64_t t) {
     const uint32_t of = owner(t);
     below += of < block;
     const uint32_t in = __ballot_sync(0xffffffffu, of == block);
     if (!in) return;
-    const int i = mine + __popc(in & before);
+    const int k = (int)((uint32_t)t >> a.lg), more = __popc(in);
+    if (full < 0 && (mine + more > kKept || at - lane - begin >= (1 << kPlaceBits) - 32))
+      full = at - lane;
     if (of == block) {
-      const int k = (int)((uint32_t)t >> a.lg);
       atomicAdd(&counter[k], 1);
-      if (i < kKept) list[warp * kKept + i] = Place{(int32_t)at, k};
+      if (full < 0) list[mine + __popc(in & before)] = (uint32_t)k << kPlaceBits | (uint32_t)(at - begin);
+      else atomicAdd(&run[k], 1);
     }
-    mine += __popc(in);
+    owned += more;
+    if (full < 0) mine += more;
   };
   int64_t at = begin + lane;
   for (; at - lane + 32 * kAhead <= end; at += 32 * kAhead) {
@@ -266,14 +285,13 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a) {
   below = __reduce_add_sync(0xffffffffu, below);
   if (lane == 0) {
     if (below) atomicAdd(&below_sum, below);
-    kept[warp] = mine;
-    if (mine > kKept) crowded = 1;
+    kept[warp] = owned;
+    if (full >= 0) crowded = 1;
   }
   __syncthreads();
   // counts to places
   int first = below_sum;
   const int total = __reduce_add_sync(0xffffffffu, kept[lane]);
-  const bool few = !crowded;
   if (block == mask && threadIdx.x == 0) *a.live = below_sum + total;
   for (int i0 = 0; i0 < a.ids; i0 += kSortThreads) {
     const int id = i0 + threadIdx.x, count = id < a.ids ? counter[id] : 0;
@@ -287,7 +305,7 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a) {
     first += sum;
     __syncthreads();
   }
-  if (few) {
+  if (total <= kOneWarp && !crowded) {
     // one list, which a warp goes through in order
     const int c = kept[lane];
     int x = c;
@@ -297,64 +315,49 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a) {
       if (lane >= o) x += y;
     }
     const int to = __shfl_sync(0xffffffffu, x - c, warp);
-    for (int i = lane; i < mine; i += 32) all[to + i] = list[warp * kKept + i];
+    Place* all = reinterpret_cast<Place*>(more);
+    for (int i = lane; i < mine; i += 32) all[to + i] = Place{row_of(list[i]), id_of(list[i])};
     __syncthreads();
     if (warp) return;
     for (int i0 = 0; i0 < total; i0 += 32) {
       const Place x = i0 + lane < total ? all[i0 + lane] : Place{0, -1};
-      const uint32_t same = __match_any_sync(0xffffffffu, x.id);
-      const int p = x.id >= 0 ? counter[x.id] + __popc(same & before) : 0;
-      __syncwarp();
-      if (x.id >= 0) {
-        if (lane == __ffs(same) - 1) counter[x.id] += __popc(same);
-        put(p, x.row, x.id);
-      }
-      __syncwarp();
+      rank(counter, x.row, x.id);
     }
     return;
   }
-  // an id that is a large part of all tokens: each warp counts its run again, apart,
-  // and walks through it once its places are known
-  int next[(kMaxIds + kSortThreads - 1) / kSortThreads];
-#pragma unroll
-  for (int j = 0; j * kSortThreads < kMaxIds; ++j)
-    if (j * kSortThreads + threadIdx.x < a.ids) next[j] = counter[j * kSortThreads + threadIdx.x];
+  // many tokens: each warp counts its own apart, and places them once it knows where
+  // (16384 tokens, two in five the same: 9.8 us, by one warp 27).  Those that it has
+  // not kept it reads again.
+  if (!may_fill)
+    for (int i = lane; i < a.ids; i += 32) run[i] = 0;
+  __syncwarp();
+  for (int i = lane; i < mine; i += 32) atomicAdd(&run[id_of(list[i])], 1);
   __syncthreads();
-  for (int i = threadIdx.x; i < kSortWarps * a.ids; i += kSortThreads) counter[i] = 0;
-  __syncthreads();
-  int* run = counter + warp * a.ids;
-  for (int64_t at = begin + lane; at - lane < end; at += 32) {
-    const int k = own(at);
-    if (k >= 0) atomicAdd(&run[k], 1);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j * kSortThreads < kMaxIds; ++j) {
-    const int id = j * kSortThreads + threadIdx.x;
-    if (id >= a.ids) break;
-    int place = next[j];
+  for (int id = threadIdx.x; id < a.ids; id += kSortThreads) {
+    int place = counter[id];
     for (int w = 0; w < kSortWarps; ++w) {
-      const int c = counter[w * a.ids + id];
-      counter[w * a.ids + id] = place;
-      place += c;
+      int& c = more[w * a.ids + id];
+      const int n = c;
+      c = place;
+      place += n;
     }
   }
   __syncthreads();
-  for (int64_t at = begin + lane; at - lane < end; at += 32 * kAhead) {
-    int k[kAhead];
+  for (int i0 = 0; i0 < mine; i0 += 32) {
+    const bool on = i0 + lane < mine;
+    const uint32_t x = on ? list[i0 + lane] : 0;
+    rank(run, row_of(x), on ? id_of(x) : -1);
+  }
+  if (full < 0) return;
+  for (int64_t at = full + lane; at - lane < end; at += 32 * kAhead) {
+    int64_t t[kAhead];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) k[u] = own(at + u * 32);
+    for (int u = 0; u < kAhead; ++u) t[u] = at + u * 32 < end ? a.tokens[at + u * 32] : a.ignore;
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      if (!__any_sync(0xffffffffu, k[u] >= 0)) continue;
-      const uint32_t same = __match_any_sync(0xffffffffu, k[u]);
-      const int p = k[u] >= 0 ? run[k[u]] + __popc(same & before) : 0;
-      __syncwarp();
-      if (k[u] >= 0) {
-        if (lane == __ffs(same) - 1) run[k[u]] += __popc(same);
-        put(p, at + u * 32, k[u]);
-      }
-      __syncwarp();
+      const bool in = owner(t[u]) == block;
+      if (__any_sync(0xffffffffu, in))
+        rank(run, (int)(at + u * 32), in ? (int)((uint32_t)t[u] >> a.lg) : -1);
     }
   }
 }
@@ -570,13 +573,12 @@ __global__ void __launch_bounds__(kReduceThreads) k_embed_reduce(ReduceGradArgs 
 }
 
 // ------------------------------------------------------------------ join
-constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinPlaces = 1024;  // places whose runs a block looks for frequent ids in
-constexpr int kJoinCols = 128;   // columns of a block, four a lane
+constexpr int kJoinCols = 4;     // columns of a lane, 32 apart
 constexpr int kWarpParts = 64;   // pieces of an id that are one warp's work
 
 struct Four {
-  float v[4];
+  float v[kJoinCols];
 };
 
 // The sum of pieces first, first + step, ... of q, kRowsAhead of them on their way.
@@ -584,32 +586,33 @@ __device__ __forceinline__ Four join_parts(const float* part, int64_t apart, int
                                            int first, int step, int q) {
   Four s{{0.f, 0.f, 0.f, 0.f}};
   for (int j = first; j < q; j += step * kRowsAhead) {
-    float v[kRowsAhead][4];
+    float v[kRowsAhead][kJoinCols];
 #pragma unroll
     for (int u = 0; u < kRowsAhead; ++u)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+      for (int e = 0; e < kJoinCols; ++e)
         v[u][e] = j + u * step < q && c + 32 * e < d ? part[(j + u * step) * apart + c + 32 * e]
                                                      : 0.f;
 #pragma unroll
     for (int u = 0; u < kRowsAhead; ++u)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s.v[e] += v[u][e];
+      for (int e = 0; e < kJoinCols; ++e) s.v[e] += v[u][e];
   }
   return s;
 }
 
-template <class T>
-__global__ void __launch_bounds__(kJoinThreads) k_embed_join(ReduceGradArgs a, int cols) {
+template <class T, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_embed_join(ReduceGradArgs a, int cols) {
+  constexpr int kWarps = THREADS / 32;
   __shared__ Head heads[kJoinPlaces / (2 * kPiece) + 1];
   __shared__ int count;
-  __shared__ Four sums[kJoinWarps][32];
+  __shared__ Four sums[kWarps][32];
   if (threadIdx.x == 0) count = 0;
   chain_wait();
   __syncthreads();
   const int64_t chunk = blockIdx.x / cols;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t c = (blockIdx.x - chunk * cols) * kJoinCols + lane;
+  const int64_t c = (blockIdx.x - chunk * cols) * (32 * kJoinCols) + lane;
   const int here = kJoinPlaces / a.run;  // runs, a thread each
   const int64_t run = chunk * here + threadIdx.x, runs = (a.n + a.run - 1) / a.run;
   if (threadIdx.x < here && run < runs) {
@@ -623,20 +626,18 @@ __global__ void __launch_bounds__(kJoinThreads) k_embed_join(ReduceGradArgs a, i
   auto parts = [&](const Head& h) { return a.part + (int64_t)(h.seg.first / a.run) * a.d; };
   auto row = [&](const Head& h) { return static_cast<T*>(a.dw) + (int64_t)h.id * a.d + c; };
   auto old = [&](const Head& h) {  // what is added to
-    Four o{{0.f, 0.f, 0.f, 0.f}};
-    if (a.accumulate)
+    Four o;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (c + 32 * e < a.d) o.v[e] = to_f(row(h)[32 * e]);
+    for (int e = 0; e < kJoinCols; ++e) o.v[e] = a.accumulate && c + 32 * e < a.d ? to_f(row(h)[32 * e]) : 0.f;
     return o;
   };
   auto finish = [&](const Head& h, const Four& s, const Four& o) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < kJoinCols; ++e)
       if (c + 32 * e < a.d)
         from_f(a.accumulate ? fmaf(a.scale, s.v[e], o.v[e]) : a.scale * s.v[e], row(h)[32 * e]);
   };
-  for (int k = warp; k < n; k += kJoinWarps) {
+  for (int k = warp; k < n; k += kWarps) {
     const Head h = heads[k];
     const int q = h.seg.count / kPiece;
     if (q > kWarpParts) continue;
@@ -647,13 +648,13 @@ __global__ void __launch_bounds__(kJoinThreads) k_embed_join(ReduceGradArgs a, i
     const Head h = heads[k];
     const int q = h.seg.count / kPiece;
     if (q <= kWarpParts) continue;
-    sums[warp][lane] = join_parts(parts(h), apart, a.d, c, warp, kJoinWarps, q);
+    sums[warp][lane] = join_parts(parts(h), apart, a.d, c, warp, kWarps, q);
     __syncthreads();
     if (warp == 0) {
       Four x = sums[0][lane];
-      for (int w = 1; w < kJoinWarps; ++w)
+      for (int w = 1; w < kWarps; ++w)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x.v[e] += sums[w][lane].v[e];
+        for (int e = 0; e < kJoinCols; ++e) x.v[e] += sums[w][lane].v[e];
       finish(h, x, old(h));
     }
     __syncthreads();
@@ -733,9 +734,12 @@ bool reduce_run(const ReduceGradArgs& a, bool vec, cudaStream_t s) {
                   : vecs <= 64 ? team(std::integral_constant<int, 64>())
                                : team(std::integral_constant<int, 128>());
   if (!ok || a.n < 2 * kPiece) return ok;
-  const int64_t cols = rows_div(a.d, kJoinCols), join = rows_div(a.n, kJoinPlaces) * cols;
-  return join <= INT32_MAX &&
-         rows_launch(k_embed_join<T>, join, kJoinThreads, 0, true, s, a, (int)cols);
+  // few columns: larger blocks, for an id of many pieces (65536 tokens of 512, all the
+  // same: 70 us with 1024 threads, 89 with 256; 16384 of 4096: 209 and 213 us the other way)
+  const int64_t cols = rows_div(a.d, 32 * kJoinCols), join = rows_div(a.n, kJoinPlaces) * cols;
+  if (join > INT32_MAX) return false;
+  return cols < 16 ? rows_launch(k_embed_join<T, 1024>, join, 1024, 0, true, s, a, (int)cols)
+                   : rows_launch(k_embed_join<T, 256>, join, 256, 0, true, s, a, (int)cols);
 }
 
 }  // namespace

@@ -120,6 +120,21 @@ def test_many_places_of_many_frequent_ids():
     _check_grad(r["d_w"], None, d_h, tokens, v, 1.0, "fp32", False)
 
 
+@pytest.mark.parametrize("share", [0.02, 0.1, 0.4, 1.0])
+@pytest.mark.parametrize("n,v", [(700, 900), (9000, 300), (20000, 151936), (50000, 40000)])
+def test_a_padding_id_that_is_not_ignored(n, v, share):
+    """One id is a large part of all tokens: more than a warp, or a block, keeps."""
+    d = 8
+    g = torch.Generator().manual_seed(n)
+    tokens = _tokens("text", n, v, g)
+    tokens[torch.rand(n, generator=g) < share] = 5
+    tokens[::97] = -100
+    d_h = torch.randn(n, d, generator=g)
+    p = kd.EmbedProblem(n_tokens=n, vocab=v, d_model=d, dtype="fp32")
+    r = kd.embed_tokens_backward(p, tokens.cuda(), d_h.cuda())
+    _check_grad(r["d_w"], None, d_h, tokens, v, 1.0, "fp32", False)
+
+
 def test_bad_tokens_are_told_and_take_no_part():
     n, v, d = 50, 20, 24
     g = torch.Generator().manual_seed(9)
