@@ -220,6 +220,41 @@ def test_equal_rows_always_stand():
     assert (r["tokens"][:, 0].cpu() == first[:, 0])[sure].all() and sure.sum() > 40
 
 
+@pytest.mark.parametrize("v", [900, 20011, 60000])
+@pytest.mark.parametrize("near", [0.05, 0.5])
+def test_rejected_drafts_of_a_near_drafter(near, v):
+    """The id that the drafter overrates most, rejected: what is left to draw from is
+    small beside p, and many ids' p pass what the residual's scores hold.  A weight
+    p - q is off by some 2^-21 p; the smallest share that wins is above 2^-7 here."""
+    b, k = 12, 1
+    c = _data(b, k, v, "fp32", seed=v + 17, std=1.0, near=near)
+    p = torch.softmax(c["target_logits"][:, :1].double(), -1)
+    q = torch.softmax(c["draft_logits"].double(), -1)
+    c["drafts"] = (q - p).argmax(-1)
+    c["uniform"][:] = 1.0 - 2.0 ** -24
+    ref = _apart(c, 1.0, 1.0)
+    c["uniform"][:] = 1.0 - 2.0 ** -24  # (q is above p by far more than FAR)
+    ref = _oracle(c)
+    assert (ref["accepted"] == 0).all() and (ref["margin"] >= FAR).all()
+    y = torch.from_numpy(ref["tokens"][:, :1])
+    won = 1 - q[:, 0].gather(1, y) / p[:, 0].gather(1, y)
+    assert won.min() > 2.0 ** -7
+    _check(_run(c, "fp32"), ref, v, 1.0)
+
+
+def test_equal_rows_that_are_rejected_draw_from_p():
+    """u = 1, outside the range: no residual, and more ids than are looked at closely."""
+    b, k, v = 9, 2, 30001
+    c = _data(b, k, v, "bf16", seed=19, near=0.0)
+    c["uniform"][:] = 1.0
+    time = c["noise"].double() / torch.softmax(c["target_logits"][:, 0].double(), 1)
+    first = time.topk(2, dim=1, largest=False)
+    sure = first.values[:, 1] / first.values[:, 0] > 1 + FAR
+    r = _run(c, "bf16")
+    assert (r["accepted"] == 0).all() and sure.sum() >= b - 1
+    assert (r["tokens"][:, 0].cpu() == first.indices[:, 0])[sure].all()
+
+
 def test_bad_drafts_and_lengths():
     b, k, v = 5, 3, 600
     c = _data(b, k, v, "bf16", seed=10)
