@@ -297,7 +297,7 @@ __device__ __forceinline__ float power(float z, float m, float k) {
 }
 
 // u a b < c d, to some 2^-46: with the products' own roundings a u just below 1
-// would count as 1 where a b = c d.  (In fp64, a unit that this GPU has little of,
+// would count as 1 where a b = c d, as in equal rows whose sums are equal.  (In fp64, a unit that this GPU has little of,
 // the decisions of a block took 1.5 to 3 us.)
 __device__ __forceinline__ bool below(float u, float a, float b, float c, float d) {
   const float x = __fmul_rn(a, b), xr = __fmaf_rn(a, b, -x);

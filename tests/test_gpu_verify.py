@@ -243,8 +243,11 @@ def test_rejected_drafts_of_a_near_drafter(near, v):
 
 
 def test_equal_rows_that_are_rejected_draw_from_p():
-    """u = 1, outside the range: no residual, and more ids than are looked at closely."""
-    b, k, v = 9, 2, 30001
+    """u = 1, outside the range: no residual, and more ids than are looked at closely.
+    The rows are whole 16-byte vectors, so that both sums are formed in the same
+    order and are the same; of rows that begin elsewhere in their vectors they may
+    differ in their last bit, and u q < p may hold at u = 1."""
+    b, k, v = 9, 2, 30000
     c = _data(b, k, v, "bf16", seed=19, near=0.0)
     c["uniform"][:] = 1.0
     time = c["noise"].double() / torch.softmax(c["target_logits"][:, 0].double(), 1)
