@@ -155,6 +155,26 @@ def test_bad_tokens_are_told_and_take_no_part():
     _check_grad(r["d_w"], None, d_h, tokens, v, 1.0, "fp32", False)
 
 
+@pytest.mark.parametrize("d", [24, 1000, 1001])
+@pytest.mark.parametrize("ignore", [0, 7, 41, 2 ** 40])
+def test_an_ignored_id_of_the_vocabulary(ignore, d):
+    """Padding by an id that the table has, or by one far outside it."""
+    n, v = 300, 42
+    g = torch.Generator().manual_seed(13)
+    tokens = torch.randint(0, v, (n,), generator=g)
+    tokens[::5] = ignore
+    w, d_h = torch.randn(v, d, generator=g), torch.randn(n, d, generator=g)
+    p = kd.EmbedProblem(n_tokens=n, vocab=v, d_model=d, dtype="fp32", ignore_index=ignore)
+    h = kd.embed_tokens(p, w.cuda(), tokens.cuda())["h"]
+    assert (as_f64(h) == R.embed(w, tokens.tolist(), ignore_index=ignore)).all()
+    assert (h[::5] == 0).all()
+    r = kd.embed_tokens_backward(p, tokens.cuda(), d_h.cuda())
+    plain = torch.where(tokens == ignore, -100, tokens)
+    _check_grad(r["d_w"], None, d_h, plain, v, 1.0, "fp32", False)
+    if ignore < v:
+        assert (r["d_w"][ignore] == 0).all()
+
+
 def test_no_tokens():
     p = kd.EmbedProblem(n_tokens=0, vocab=5, d_model=8)
     t = torch.empty(0, dtype=torch.int64, device="cuda")
