@@ -383,7 +383,7 @@ struct ReduceGradArgs {
   int run;            // places of the list a team starts pieces in, a power of two
   int slices;         // of the columns
   int64_t teams;      // blocks that add; the others write the rows of zeros
-  int zeros;          // ids of each of those
+  int zeros;          // ids of each of those, a warp's up to 32
   int accumulate;
   float scale;
 };
@@ -440,24 +440,32 @@ struct Columns {
   }
 };
 
-// A block's share of the ids: zeros where an id does not occur, a warp a row.
-template <class T>
+// A block's share of the ids: zeros where an id does not occur.  A warp has a
+// quarter of them, one behind the other.
+template <class T, bool VEC>
 __device__ __forceinline__ void zero_rows(const ReduceGradArgs& a, int64_t share) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t lo = share * a.zeros, hi = min(lo + a.zeros, a.vocab);
-  for (int64_t v0 = lo + warp; v0 < hi; v0 += 32 * kReduceWarps) {
-    const int64_t mine = v0 + lane * kReduceWarps;
-    uint32_t none = __ballot_sync(0xffffffffu, mine < hi && a.seg[mine].count == 0);
-    for (; none; none &= none - 1) {
-      T* row = static_cast<T*>(a.dw) + (v0 + (__ffs(none) - 1) * kReduceWarps) * a.d;
-      const int64_t lead = min((int64_t)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) /
-                                   (int64_t)sizeof(T), a.d);
-      const int64_t vecs = (a.d - lead) / RowVec<T>::N, tail = lead + vecs * RowVec<T>::N;
-      if (lane < lead) from_f(0.f, row[lane]);
-      uint4* p = reinterpret_cast<uint4*>(row + lead);
-      for (int64_t i = lane; i < vecs; i += 32) __stcs(&p[i], make_uint4(0, 0, 0, 0));
-      if (tail + lane < a.d) from_f(0.f, row[tail + lane]);
-    }
+  const int lane = threadIdx.x & 31, each = a.zeros / kReduceWarps;
+  const int64_t v0 = share * a.zeros + (threadIdx.x >> 5) * each;
+  uint32_t none = __ballot_sync(0xffffffffu, lane < each && v0 + lane < a.vocab &&
+                                                 a.seg[v0 + lane].count == 0);
+  T* rows = static_cast<T*>(a.dw) + v0 * a.d;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const int64_t row_vecs = a.d / RowVec<T>::N;
+  if (VEC && row_vecs < 32) {  // all its rows' vectors in one run
+    const int vecs = (int)row_vecs;
+    for (int i = lane; i < each * vecs; i += 32)
+      if ((none >> (i / vecs)) & 1) __stcs(&reinterpret_cast<uint4*>(rows)[i], zero);
+    return;
+  }
+  for (; none; none &= none - 1) {
+    T* row = rows + (__ffs(none) - 1) * a.d;
+    const int64_t lead = min((int64_t)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) /
+                                 (int64_t)sizeof(T), a.d);
+    const int64_t vecs = (a.d - lead) / RowVec<T>::N, tail = lead + vecs * RowVec<T>::N;
+    if (lane < lead) from_f(0.f, row[lane]);
+    uint4* p = reinterpret_cast<uint4*>(row + lead);
+    for (int64_t i = lane; i < vecs; i += 32) __stcs(&p[i], zero);
+    if (tail + lane < a.d) from_f(0.f, row[tail + lane]);
   }
 }
 
@@ -474,7 +482,7 @@ __global__ void __launch_bounds__(kReduceThreads) k_embed_reduce(ReduceGradArgs 
   chain_wait();
   chain_next();
   if (blockIdx.x >= a.teams) {
-    zero_rows<T>(a, blockIdx.x - a.teams);
+    zero_rows<T, VEC>(a, blockIdx.x - a.teams);
     return;
   }
   const int team = threadIdx.x / TEAM, t = threadIdx.x % TEAM;
@@ -718,7 +726,8 @@ bool reduce_team(ReduceGradArgs a, cudaStream_t s) {
   a.teams = rows_div(rows_div(a.n, a.run) * a.slices, kReduceThreads / TEAM);
   // Many small blocks, behind the ones that add: they fill the table from front to
   // back, which memory takes at 7.4 TB/s, and at 6.5 TB/s from everywhere at once.
-  a.zeros = (int)std::min<int64_t>(128, std::max<int64_t>(1, kZeroBytes / (a.d * (int64_t)sizeof(T))));
+  a.zeros = kReduceWarps * (int)std::min<int64_t>(
+      32, std::max<int64_t>(1, kZeroBytes / kReduceWarps / (a.d * (int64_t)sizeof(T))));
   const int64_t grid = a.teams + (a.accumulate ? 0 : rows_div(a.vocab, a.zeros));
   return grid <= INT32_MAX &&
          rows_launch(k_embed_reduce<T, TEAM, VEC>, grid, kReduceThreads, 0, true, s, a);
