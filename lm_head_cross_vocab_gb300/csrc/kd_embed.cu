@@ -19,8 +19,8 @@
 // Each sum's order depends on the tokens alone.
 // The lookup is bound by its writes (16384 x 4096 bf16 32 us, 4.2 TB/s written and each
 // id's row read once), the gradient of a whole table by the table's (16384 tokens of 4096
-// into 151936 rows 203 us, a fill alone 164-170 us), that of few ids by the latency of
-// three launches (4096 tokens of 2048 added to 32000 rows 16 us).
+// into 151936 rows 206 us, a fill alone 164-170 us), that of few ids by the latency of
+// three launches (4096 tokens of 2048 added to 32000 rows 17 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -834,8 +834,9 @@ extern "C" kd_status kd_embed_bwd(const kd_embed_problem* p, const int64_t* toke
   t.live = reinterpret_cast<int32_t*>(ws + P.live);
   t.status = dev_status;
   const int smem = sort_smem(P.ids);
+  // (always the same limit: another thread may be about to launch with more)
   if (smem > 40000 && cudaFuncSetAttribute(k_embed_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           smem) != cudaSuccess)
+                                           sort_smem(kMaxIds)) != cudaSuccess)
     return KD_ERR_CUDA;
   if (!rows_launch(k_embed_sort, (int64_t)1 << P.lg, kSortThreads, (size_t)smem, false, s, t))
     return KD_ERR_CUDA;

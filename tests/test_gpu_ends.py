@@ -8,6 +8,11 @@ looked up again.  All in fp32 against fp64 compositions of the oracles: each
 step's tolerance is that of its own test, and the compositions are compared at
 1e-4 of the largest element, some hundred times the sum of their errors
 (sums of up to 1500 terms of fp32, 1500 u = 1e-4 at the very worst)."""
+import ctypes
+import functools
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -187,3 +192,78 @@ def test_calls_on_two_streams_at_once():
             for name, t in r.items():
                 if t is not None:
                     assert torch.equal(out[op][name], t), (op, name)
+
+
+@pytest.mark.parametrize("op", ["norm", "embed"])
+def test_calls_from_two_threads_at_once(op):
+    """Two threads whose calls need different amounts of a kernel's shared memory
+    (the norm's backward with and without d_sum, tables of 32000 and 151936 ids),
+    each on its own stream, through the C ABI, where they do run at once: neither's
+    call is refused, and the results are those of one thread."""
+    g, lib = torch.Generator().manual_seed(26), kd.load_library()
+    n, d = 8, 4096
+    s, d_h, up = (torch.randn(n, d, generator=g).bfloat16().cuda() for _ in range(3))
+    gain = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    rows = torch.randn(n, 8, generator=g).bfloat16().cuda()
+    held = [s, d_h, up, gain, rows]
+
+    def prepared(which, stream):
+        """(call, its outputs)"""
+        if op == "norm":
+            cp = kd.NormProblem(n_tokens=n, d_model=d).to_c()
+            size = kd.kd_rmsnorm_workspace_size(cp)
+            outs = [torch.zeros_like(s), torch.zeros_like(gain)]
+        else:
+            vocab = (32000, 151936)[which]
+            cp = kd.EmbedProblem(n_tokens=n, vocab=vocab, d_model=8).to_c()
+            size = kd.kd_embed_workspace_size(cp)
+            outs = [torch.zeros(vocab, 8, dtype=torch.bfloat16, device="cuda")]
+        # (memory of the allocator is 512-byte aligned)
+        ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+        tokens = torch.arange(n, device="cuda") * 797
+        held.extend([cp, ws, tokens, *outs])
+        if op == "norm":
+            args = (ctypes.byref(cp), s.data_ptr(), gain.data_ptr(), d_h.data_ptr(),
+                    up.data_ptr() if which else None, outs[0].data_ptr(), outs[1].data_ptr(),
+                    ws.data_ptr(), size, stream.cuda_stream)
+            return functools.partial(lib.kd_rmsnorm_bwd, *args), outs
+        args = (ctypes.byref(cp), tokens.data_ptr(), rows.data_ptr(), outs[0].data_ptr(), 1, None,
+                ws.data_ptr(), size, stream.cuda_stream)
+        return functools.partial(lib.kd_embed_bwd, *args), outs
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    jobs = [prepared(i, stream) for i, stream in enumerate(streams)]
+    torch.cuda.synchronize()
+    want = []
+    for call, outs in jobs:
+        assert call() == kd.KD_OK
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in outs])
+    told = [[], []]
+
+    def work(i):
+        call = jobs[i][0]
+        for _ in range(100):
+            told[i].extend(call() for _ in range(100))
+            streams[i].synchronize()
+
+    interval = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    try:
+        threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(interval)
+    assert [len(t) for t in told] == [10000, 10000]
+    assert set(told[0] + told[1]) == {kd.KD_OK}
+    for (call, outs), ref in zip(jobs, want):
+        for t in outs:
+            t.zero_()
+        torch.cuda.synchronize()
+        assert call() == kd.KD_OK
+        torch.cuda.synchronize()
+        for got, t in zip(outs, ref):
+            assert torch.equal(got, t)
