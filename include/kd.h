@@ -446,7 +446,9 @@ kd_status kd_clip_grad_norm(const void* const* grads, void* const* outs, const i
  * without one rejects its draft, and the token is drawn from p.  Both set
  * KD_DEV_NONFINITE.  A drafted id outside [0, V) is rejected and sets
  * KD_DEV_BAD_LABEL.  Rows behind the last draft's successor are not read.
- * Noise is within [2^-60, 2^60]; an id whose noise is not takes no part.
+ * Noise is within [2^-60, 2^60]; an id whose noise is not takes no part.  Where
+ * no id with r > 0 takes part nothing is drawn either: ignore_index, NaN and
+ * KD_DEV_NONFINITE.
  * A drafter over another vocabulary: kd_project_teacher_logits moves its logits
  * onto the target's ids first (then t_draft = 1). */
 typedef struct kd_verify_problem {

@@ -314,10 +314,13 @@ struct Race {
   float kd, md, inv_d;        // of the drafter's (q taken away), inv_d = 0: none
   int64_t out;                // this id has q = 1, -1: none
 
-  __device__ __forceinline__ uint64_t score(float zt, float zd, float e, int64_t id) const {
+  __device__ __forceinline__ float weight(float zt, float zd, int64_t id) const {
     float r = __fmul_rn(power(zt, mt, kt), inv_t);
     if (inv_d > 0.f) r = __fsub_rn(r, __fmul_rn(power(zd, md, kd), inv_d));
-    if (!(r > 0.f && e >= 0x1p-60f && e <= 0x1p60f) || id == out) return 0;
+    return id == out ? 0.f : r;
+  }
+  static __device__ __forceinline__ uint64_t score(float r, float e, int64_t id) {
+    if (!(r > 0.f && e >= 0x1p-60f && e <= 0x1p60f)) return 0;
     const float s = __fdiv_rn(r, e);
     return s > 0.f ? (uint64_t)__float_as_uint(s) << 32 | (uint32_t)~(uint32_t)id : 0;
   }
@@ -326,6 +329,7 @@ constexpr int kList = 1024;  // ids that a block takes a closer look at
 struct RaceShared {
   uint64_t best;
   int count;
+  int rest;  // while best is 0: whether some id has a weight, whatever its noise
   int list[kList];
 };
 constexpr int kIds = 8;    // ids a thread takes at a time
@@ -359,6 +363,7 @@ __device__ __forceinline__ uint64_t race_part(const Race& c, const T* zt, const 
   if (tid == 0) {
     sh.best = 0;
     sh.count = 0;
+    sh.rest = 0;
   }
   __syncthreads();
   const T* z0 = zt + lo;
@@ -367,7 +372,9 @@ __device__ __forceinline__ uint64_t race_part(const Race& c, const T* zt, const 
   const int n = (int)(hi - lo), whole = vec ? n / kIds * kIds : 0;
   constexpr int kStep = kThreads * kIds;
   auto exact = [&](int i) {
-    return c.score(to_f(z0[i]), zd ? to_f(zd[lo + i]) : 0.f, e0[i], lo + i);
+    const float r = c.weight(to_f(z0[i]), zd ? to_f(zd[lo + i]) : 0.f, lo + i);
+    if (r > 0.f) sh.rest = 1;
+    return c.score(r, e0[i], lo + i);
   };
   auto offer = [&](uint64_t w) {
     if (w) atomicMax((unsigned long long*)&sh.best, (unsigned long long)w);
@@ -421,7 +428,7 @@ __device__ __forceinline__ uint64_t race_part(const Race& c, const T* zt, const 
         zb = z[j], db = d[j], eb = e[j];
       }
     }
-    uint64_t w = at >= 0 ? c.score(zb, db, eb, lo + at) : 0;
+    uint64_t w = at >= 0 ? c.score(c.weight(zb, db, lo + at), eb, lo + at) : 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const uint64_t x = __shfl_xor_sync(0xffffffffu, w, o);
@@ -432,7 +439,9 @@ __device__ __forceinline__ uint64_t race_part(const Race& c, const T* zt, const 
   __syncthreads();
   // p = 2^x / S, x = (z - m) k: an id may be ahead if 2^x > score S e.  The factor
   // covers the roundings of this test: of x (|x| 2^-23, 2^x being 0 below x = -126),
-  // of the power (2^-22) and of the products
+  // of the power (2^-22) and of the products.  Without a score yet every id of some
+  // p passes, that of infinite or NaN noise too (where 0 e is NaN), so that `rest`
+  // is known where nobody arrives
   const float held = __uint_as_float((uint32_t)(sh.best >> 32)) / c.inv_t * (1.f - 0x1p-14f);
   const float2 k2 = make_float2(c.kt, c.kt), m2 = make_float2(c.mt, c.mt), h2 = make_float2(held, held);
   __syncthreads();
@@ -442,8 +451,8 @@ __device__ __forceinline__ uint64_t race_part(const Race& c, const T* zt, const 
     for (int j = 0; j < kIds; j += 2) {
       const float2 x = mul2(sub2(make_float2(z[j], z[j + 1]), m2), k2);
       const float2 y = mul2(make_float2(e[j], e[j + 1]), h2);
-      if (ex2(x.x) > y.x) pass |= 1u << j;
-      if (ex2(x.y) > y.y) pass |= 2u << j;
+      if (!(ex2(x.x) <= y.x)) pass |= 1u << j;
+      if (!(ex2(x.y) <= y.y)) pass |= 2u << j;
     }
     for (; pass; pass &= pass - 1) {
       const int i = first + (__ffs(pass) - 1) * apart;
@@ -593,6 +602,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify_draw(VerifyArgs a) {
   const bool alive = sum_ok(row);
   // ---- the race
   uint64_t leader = 0;
+  bool rest = false;  // nobody has arrived, but some id of this row might have with other noise
   const float* noise = a.noise + b * a.vocab;
   zt += n * a.ldt;
   if (!a.greedy) {
@@ -611,26 +621,37 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify_draw(VerifyArgs a) {
     const int64_t units = (a.vocab + 15) / 16;
     const int64_t lo = units * part / a.race_parts * 16;
     const int64_t hi = min(units * (part + 1) / a.race_parts * 16, a.vocab);
-    if (alive) leader = race_part<T>(race, zt, q, noise, lo, hi, race_shared);
+    if (alive) {
+      leader = race_part<T>(race, zt, q, noise, lo, hi, race_shared);
+      rest = race_shared.rest;
+    }
     if (a.race_parts > 1) {
       if (threadIdx.x == 0) {
         // (release: the leader comes before the arrival; acquire: all of theirs)
         if (leader) atomicMax((unsigned long long*)&a.leader[b], (unsigned long long)leader);
+        // the blocks that arrived, and above them those that found a weight
+        const uint32_t here = 1u | (uint32_t)rest << 16;
         uint32_t before;
-        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;"
                      : "=r"(before)
-                     : "l"(&a.arrived[b])
+                     : "l"(&a.arrived[b]), "r"(here)
                      : "memory");
-        last = before == (uint32_t)a.race_parts - 1;
-        if (last) race_shared.best = *(volatile uint64_t*)&a.leader[b];
+        last = (before & 0xffff) == (uint32_t)a.race_parts - 1;
+        if (last) {
+          race_shared.best = *(volatile uint64_t*)&a.leader[b];
+          race_shared.rest = (before + here) >> 16;
+        }
       }
+      static_assert(kMaxParts < 1 << 16, "arrivals in 16 bits");
       __syncthreads();
       if (!last) return;
       leader = race_shared.best;
+      rest = race_shared.rest;
       __syncthreads();
     }
-    if (alive && !leader && n < len) {
-      // p <= q everywhere: no residual to draw from
+    if (alive && !leader && !rest && n < len) {
+      // p <= q everywhere: no residual to draw from.  (Where there is one whose ids all
+      // have noise that takes no part, nothing is drawn.)
       race.inv_d = 0.f;
       race.out = -1;
       leader = race_part<T>(race, zt, (const T*)nullptr, noise, 0, a.vocab, race_shared);
