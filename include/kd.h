@@ -440,7 +440,8 @@ kd_status kd_clip_grad_norm(const void* const* grads, void* const* outs, const i
  * t_target = 0: greedy.  A draft is accepted when it is the id with the largest
  * target logit (equal: lowest id), the drawn token is that id, neither
  * draft_logits nor random numbers are used, and logprob is that at temperature 1.
- * A logit of -infinity is an id of probability 0.  A target row without a
+ * A logit of -infinity is an id of probability 0, and one whose probability is
+ * below 2^-126 of the row's largest may count as such.  A target row without a
  * distribution (a NaN, a +infinity, or nothing but -infinity) rejects its draft
  * and draws nothing: the token is ignore_index, its logprob NaN.  A draft row
  * without one rejects its draft, and the token is drawn from p.  Both set

@@ -306,7 +306,9 @@ __device__ __forceinline__ bool below(float u, float a, float b, float c, float 
   return __fadd_rn(__fsub_rn(z, y), __fsub_rn(__fmaf_rn(u, xr, zr), yr)) < 0.f;
 }
 
-// The race over ids of one row.  A score's word: its bits above, the complement of
+// The race over ids of one row.  A score is 2^64 r / e: within fp32 for every r <= 1
+// and every noise that takes part (r = 2^-100 behind noise of 2^60 is lost without the
+// factor).  Its word: its bits above, the complement of
 // the id below, so that a larger word is ahead and equal scores go to the lowest
 // id; 0: nobody.  All blocks' words are compared as integers: no order matters.
 struct Race {
@@ -321,7 +323,7 @@ struct Race {
   }
   static __device__ __forceinline__ uint64_t score(float r, float e, int64_t id) {
     if (!(r > 0.f && e >= 0x1p-60f && e <= 0x1p60f)) return 0;
-    const float s = __fdiv_rn(r, e);
+    const float s = __fdiv_rn(__fmul_rn(r, 0x1p64f), e);
     return s > 0.f ? (uint64_t)__float_as_uint(s) << 32 | (uint32_t)~(uint32_t)id : 0;
   }
 };
@@ -442,7 +444,9 @@ __device__ __forceinline__ uint64_t race_part(const Race& c, const T* zt, const 
   // of the power (2^-22) and of the products.  Without a score yet every id of some
   // p passes, that of infinite or NaN noise too (where 0 e is NaN), so that `rest`
   // is known where nobody arrives
-  const float held = __uint_as_float((uint32_t)(sh.best >> 32)) / c.inv_t * (1.f - 0x1p-14f);
+  // (a ratio near fp32's lower end has lost bits: everything passes)
+  const float ratio = __uint_as_float((uint32_t)(sh.best >> 32)) * 0x1p-64f;
+  const float held = ratio < 0x1p-100f ? 0.f : ratio / c.inv_t * (1.f - 0x1p-14f);
   const float2 k2 = make_float2(c.kt, c.kt), m2 = make_float2(c.mt, c.mt), h2 = make_float2(held, held);
   __syncthreads();
   auto sift = [&](const float* z, const float* e, int first, int apart) {

@@ -1,5 +1,6 @@
 """Draft verification behind a rejected draft, where no id with p > q has usable
-noise, against the fp64 oracle.
+noise, and weights and noise at the ends of their ranges, against the
+fp64 oracle.
 
 Whole numbers are equal: decisions are kept 1e-4 off their borders, the kernels'
 are off by less than 1e-5.  log p, u = 2^-24: a thread adds the exponentials of its
@@ -112,4 +113,23 @@ def test_without_a_rest_the_target_itself_is_drawn_from(v, dtype):
     r, ref = _both(c, dtype)
     assert (ref["accepted"] == 0).all() and ref["tokens"][3, 0] == -100
     assert all(ref["tokens"][s, 0] % 2 == 1 for s in (0, 1, 2, 4))
+    _check(r, ref, v)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("v", [40, 9000, 60001])
+@pytest.mark.parametrize("size", [2.0 ** 60, 2.0 ** -59, 1.0])
+def test_weights_and_noise_at_the_ends_of_their_ranges(size, v, dtype):
+    """Only ids of p = 2^-94 and less have noise that takes part, 2^60 or 2^-60 among it."""
+    z = torch.full((3, 1, v), -65.0)
+    z[:, :, 0], z[:, :, 11] = 0.0, -80.0
+    c = {"target_logits": z.to(DT[dtype]), "drafts": torch.zeros(3, 0, dtype=torch.int64),
+         "uniform": torch.zeros(3, 0), "noise": torch.full((3, v), size)}
+    c["noise"][:, 0] = 0.0
+    c["noise"][0, 5] *= 0.5
+    c["noise"][1, v // 2] *= 0.5
+    c["noise"][2] = -1.0
+    c["noise"][2, 11] = size  # the least likely one alone is left
+    r, ref = _both(c, dtype)
+    assert ref["tokens"][:, 0].tolist() == [5, v // 2, 11]
     _check(r, ref, v)
