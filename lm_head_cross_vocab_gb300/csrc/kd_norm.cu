@@ -1,8 +1,10 @@
 // Root-mean-square norm of rows with the residual's addition, and its backward.
 //
 //   s = x + residual,  r = (mean s^2 + eps)^-1/2,  h = s r w
-//   d_x = r g - s r^3 mean(g s) + d_sum,  g = d_h w;   d_w = sum_n d_h s r
+//   d_x = r g - (s r) r m + d_sum,  g = d_h w,  m = r mean(g s);   d_w = sum_n d_h s r
 //
+// (s r is of size 1 and m of g's, whatever the row's; an r^3 would leave fp32's range
+// from rows of 2^42 on.)
 // TPR threads hold a row in registers, so every tensor is read once and the
 // sums of a row (s^2; backward: also g s) are one reduction.  Rows of whole
 // 16-byte vectors move as such; others (an odd width, a view at an odd offset)
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(norm_block(TPR), norm_per_sm(TPR, VPT)) k_norm
     turn ^= 1;
     if (on) {
       const float r = 1.f / sqrtf(sums.x * inv_d + a.eps);
-      const float c = r * r * r * (sums.y * inv_d);
+      const float rm = r * (r * (sums.y * inv_d));
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         float sv[N], gv[N], wv[N];
@@ -253,8 +255,9 @@ __global__ void __launch_bounds__(norm_block(TPR), norm_per_sm(TPR, VPT)) k_norm
         float o[N];
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-          o[e] = fmaf(-c, sv[e], r * (gv[e] * (wv[e] + a.off)));
-          dw[i * N + e] = fmaf(gv[e], sv[e] * r, dw[i * N + e]);
+          const float y = sv[e] * r;
+          o[e] = fmaf(-y, rm, r * (gv[e] * (wv[e] + a.off)));
+          dw[i * N + e] = fmaf(gv[e], y, dw[i * N + e]);
         }
         if (a.res) {
           float uv[N];
