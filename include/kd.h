@@ -520,12 +520,16 @@ kd_status kd_embed_bwd(const kd_embed_problem* problem, const int64_t* tokens, c
  * the d_h they give.
  *   s = x + residual (x alone where that is NULL)
  *   h = s r (weight + weight_offset),   r = 1 / sqrt(mean(s^2) + eps)
- * s is formed, and its norm taken, in fp32 (elements from 2^63 on have squares
- * beyond it); `sum` (may be NULL) gets it rounded to dtype.  Backward, with s as it was stored (and r of that s), d_sum the
- * gradient that reaches s from elsewhere (may be NULL) and g = d_h (weight +
- * weight_offset):
+ * s is formed, and its norm taken, in fp32; `sum` (may be NULL) gets it rounded to
+ * dtype.  Backward, with s as it was stored (and r of that s), d_sum the gradient
+ * that reaches s from elsewhere (may be NULL) and g = d_h (weight + weight_offset):
  *   d_x = r g - s r^3 mean(g s) + d_sum         (also the residual's gradient)
  *   d_weight = sum over rows of d_h s r         (fp32, in a fixed order)
+ * Range: a row's sum of squares has to lie below 2^128 (elements of 2^56.5 in a row
+ * of 32768, of 2^61.5 in one of 32; beyond, r is 0 and so is the row), and with an
+ * eps below 2^-126 its mean square not below 2^-126; a row of zeros needs eps > 0
+ * (NaN without).  Backward: so has the sum of |g s| to lie below 2^128, and products
+ * g s count down to 2^-126.
  * Either gradient may be NULL to skip it.  h or sum may be x or residual
  * themselves, and d_x any of s, d_h and d_sum; outputs may not overlap the inputs
  * or one another otherwise.  workspace: 256-byte aligned. */

@@ -1,5 +1,5 @@
-"""The norm and its backward over rows of large and of tiny magnitude, against the
-fp64 oracle.
+"""The norm and its backward over rows of large and of tiny magnitude, up to the
+limits that the header states, against the fp64 oracle.
 
 Tolerances as tests/test_gpu_norm.py derives them (E = 64 elements a thread at most,
 u = 2^-24): r within (E / 2 + 10) u; the sum of g s within (E + 14) u of the sum of
@@ -59,3 +59,39 @@ def test_rows_of_large_and_tiny_magnitude(power, d, dtype):
         ref = R.rms_norm_grad(r["sum"], w, d_h, up, eps=eps)
         assert _near(b["d_x"], ref["d_x"], 4 * E * U * ref["x_size"], dtype)
         assert _near(b["d_weight"], ref["d_weight"], (n + E) * U * ref["w_size"], dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [32, 32767, 32768])
+def test_rows_just_inside_the_stated_limits(d, dtype):
+    """Sums of squares of 2^127 at most, and of a mean square of 2^-126 at least."""
+    up = int((127 - np.log2(d)) // 2)
+    n = 4
+    g = torch.Generator().manual_seed(d + 1)
+    sign = torch.where(torch.rand(n, d, generator=g) < 0.5, -1.0, 1.0)
+    size = torch.tensor([2.0 ** up, 2.0 ** (up - 1), 2.0 ** -62, 2.0 ** -63])[:, None]
+    x = (sign * size).to(DT[dtype])
+    w = (1 + 0.2 * torch.randn(d, generator=g)).to(DT[dtype])
+    d_h = (0.5 * torch.randn(n, d, generator=g) + 0.5 * sign).to(DT[dtype])
+    p = kd.NormProblem(n_tokens=n, d_model=d, dtype=dtype, eps=0.0)
+    h, _ = R.rms_norm(x, w, eps=0.0)
+    assert _near(kd.rms_norm(p, x.cuda(), w.cuda())["h"], h, (E / 2 + 14) * U * np.abs(h), dtype)
+    b = kd.rms_norm_backward(p, x.cuda(), w.cuda(), d_h.cuda())
+    ref = R.rms_norm_grad(x, w, d_h, eps=0.0)
+    assert _near(b["d_x"], ref["d_x"], 4 * E * U * ref["x_size"], dtype)
+    assert _near(b["d_weight"], ref["d_weight"], (n + E) * U * ref["w_size"], dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_rows_beyond_the_stated_limits(dtype):
+    """As stated: a sum of squares beyond fp32 makes a row of zeros, and a row of zeros
+    has no norm without eps; other rows are not touched by either."""
+    x = torch.ones(3, 32768, dtype=DT[dtype])
+    x[0], x[2] = 2.0 ** 57, 0.0
+    w = torch.ones(32768, dtype=DT[dtype]).cuda()
+    h = kd.rms_norm(kd.NormProblem(n_tokens=3, d_model=32768, dtype=dtype, eps=0.0), x.cuda(),
+                    w)["h"]
+    assert (h[0] == 0).all() and (h[1] == 1).all() and torch.isnan(h[2]).all()
+    h = kd.rms_norm(kd.NormProblem(n_tokens=3, d_model=32768, dtype=dtype, eps=1e-30), x.cuda(),
+                    w)["h"]
+    assert (h[0] == 0).all() and (h[1] == 1).all() and (h[2] == 0).all()
