@@ -1155,13 +1155,14 @@ int launch_join(void (*kern)(LpJoin), int64_t grid, int threads, const LpJoin& j
   return (int)cudaLaunchKernelEx(&cfg, kern, j);
 }
 
+constexpr int kRowBlocks = 8;  // of a cluster at most
 // Blocks of a cluster for each row: enough of them to give every SM work, as
 // long as a slice keeps 16 KiB and no SM gets more than four blocks (with up to
 // twice as many blocks 80 rows of 151936 bf16 with 20 alternatives took 24 us for
 // 18 us, 333 fp32 rows of 32003 25 us for 16 us).
 int row_blocks(int64_t n, int64_t row_bytes, int nsm) {
   int c = 1;
-  while (c < 8 && n * c * 2 <= 4 * nsm && row_bytes / (2 * c) >= 16384) c *= 2;
+  while (c < kRowBlocks && n * c * 2 <= 4 * nsm && row_bytes / (2 * c) >= 16384) c *= 2;
   return c;
 }
 
@@ -1169,8 +1170,11 @@ template <class T, int NT, bool TOPK, bool CL = false>
 int launch_rows_nt(const LpArgs& a, int blocks, cudaStream_t s) {
   auto kern = k_logprob_rows<T, NT, TOPK, CL>;
   const int smem = row_smem<NT>(a.topk, blocks);
+  // (always the same limit: another thread may be about to launch with more)
+  constexpr int most = row_smem<NT>(NT == 128 ? kFewK : kMaxTopk, CL ? kRowBlocks : 1);
+  static_assert(most <= 200 * 1024, "shared memory of a block");
   if (smem > 40000 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           smem) != cudaSuccess)
+                                           most) != cudaSuccess)
     return 1;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
