@@ -699,8 +699,9 @@ int launch_mix_cluster(MixParams P, int c, int64_t sc, cudaStream_t s, bool* lau
   const int nsm = tc_num_sms() > 0 ? tc_num_sms() : 1;
   const size_t smem = (size_t)sc * sizeof(TI) * (size_t)P.k;
   auto kern = k_mix_cluster<TI, TO, GEO, WIDE, KT>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-      cudaSuccess)
+  // (always the same limit: another thread may be about to launch with more)
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)(WIDE ? kMixBufWide : kMixBuf)) != cudaSuccess)
     return 1;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));

@@ -36,8 +36,21 @@ def _logprob(which, stream, held):
                              *[t.data_ptr() for t in outs], None, 0, stream.cuda_stream), outs
 
 
+def _mix(which, stream, held):
+    v = (400, 20000)[which]
+    g = torch.Generator().manual_seed(2)
+    z = [torch.randn(1, v, generator=g).bfloat16().cuda() for _ in range(2)]
+    ptrs = (ctypes.c_void_p * 2)(*[t.data_ptr() for t in z])
+    outs = [torch.zeros(1, v, device="cuda"), torch.zeros((), dtype=torch.int32, device="cuda")]
+    held += [*z, ptrs]
+    return functools.partial(kd.load_library().kd_mix_teacher_logits, ptrs, 2, None, 1, v,
+                             kd.KD_BF16, kd.KD_MIX_ARITHMETIC, outs[0].data_ptr(), kd.KD_FP32,
+                             outs[1].data_ptr(), stream.cuda_stream), outs
+
+
 JOBS = {
     "logprob": _logprob,
+    "mix": _mix,
 }
 
 
