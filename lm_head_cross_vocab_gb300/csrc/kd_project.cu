@@ -1509,7 +1509,9 @@ bool x_plan_shape(int64_t vt, int64_t vs, const XShape& sh, XPlan* P) {
   if (P->recv_cap < 8) return false;
   P->smem = (size_t)(P->sc + P->send_cap + P->recv_cap) * (size_t)elem;
   auto kern = k_project_exchange<TI, TO, XT>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)P->smem) !=
+  // (always the same limit: another thread may be about to launch with more, or to ask
+  // how many clusters of its shape fit)
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem) !=
       cudaSuccess) {
     (void)cudaGetLastError();
     return false;
@@ -1580,8 +1582,9 @@ int launch_project(const void* zt, int64_t n, int64_t vt, int64_t vs, float inv_
                    void* out, uint32_t* status, const XLayout* X, cudaStream_t s) {
   const size_t smem = 2 * (size_t)sc * sizeof(TI);
   auto kern = k_project_slices<TI, TO>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-      cudaSuccess)
+  // (always the same limit, as the exchange's)
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)(2 * kSliceMax)) != cudaSuccess)
     return 1;
   const int nsm = tc_num_sms() > 0 ? tc_num_sms() : 1;
   const int grid = (int)std::min<int64_t>(n * nsl, (int64_t)nsm);
@@ -1727,7 +1730,8 @@ bool pl_plan(int64_t vt, int64_t vs, XPlan* P, int* steps) {
 template <typename TI, int MODE, bool SKEW, int STEPS>
 int launch_pl(const XPlan& xp, const PLParams& P, cudaStream_t s) {
   auto kern = k_proj_loss<TI, MODE, SKEW, STEPS>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)xp.smem) !=
+  // (always the same limit, as the exchange's)
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPLSmem) !=
       cudaSuccess)
     return 1;
   cudaLaunchConfig_t cfg;

@@ -20,6 +20,12 @@ def _lib():
     assert kd.kd_device_supported(0), "tests need an sm_103 GPU"
 
 
+def _space(nbytes, held):
+    ws = kd.Workspace()
+    held.append(ws)
+    return ws.get(nbytes, torch.device("cuda:0"))
+
+
 def _logprob(which, stream, held):
     """Alternatives of one long row, 128 or 1024 of them: a cluster of eight blocks."""
     k, v = (128, 1024)[which], 151936
@@ -48,10 +54,51 @@ def _mix(which, stream, held):
                              outs[1].data_ptr(), stream.cuda_stream), outs
 
 
+def _project(sizes, which, stream, held):
+    vt, vs = sizes[which]
+    g = torch.Generator().manual_seed(3)
+    z = torch.randn(1, vt, generator=g).bfloat16().cuda()
+    tmap = torch.randint(0, vs, (vt,), generator=g, dtype=torch.int32).cuda()
+    nbytes, lib = ctypes.c_size_t(0), kd.load_library()
+    assert lib.kd_project_workspace_size(vt, vs, ctypes.byref(nbytes)) == kd.KD_OK
+    outs = [torch.zeros(1, vs, device="cuda"), torch.zeros((), dtype=torch.int32, device="cuda")]
+    held += [z, tmap]
+    return functools.partial(lib.kd_project_teacher_logits, tmap.data_ptr(), vt, vs, z.data_ptr(),
+                             1, kd.KD_BF16, 1.0, outs[0].data_ptr(), kd.KD_FP32,
+                             outs[1].data_ptr(), *_space(nbytes.value, held),
+                             stream.cuda_stream), outs
+
+
+def _projected_loss(which, stream, held):
+    n, vt, vs = 2, (200, 50000)[which], 700
+    g = torch.Generator().manual_seed(4)
+    t = {"logits_s": torch.randn(n, vs, generator=g).bfloat16().cuda(),
+         "logits_t": torch.randn(n, vt, generator=g).bfloat16().cuda(),
+         "labels": torch.zeros(n, dtype=torch.int64, device="cuda"),
+         "token_map": torch.randint(0, vs, (vt,), generator=g, dtype=torch.int32).cuda()}
+    cp = kd.Problem(n_tokens=n, vocab=vs, dtype="bf16", student="logits", teacher="projected",
+                    variant="forward", t_student=1.0, t_teacher=1.0, w_student_ce=0.5,
+                    w_teacher_ce=0.0, w_kl=1.0, ignore_index=-100, vocab_teacher=vt).to_c()
+    ins = kd.make_inputs(t)
+    outs = [*(torch.zeros(n, device="cuda") for _ in range(3)),
+            torch.zeros(n, kd.KD_STATS_PER_TOKEN, device="cuda"), torch.zeros((), device="cuda"),
+            torch.zeros((), dtype=torch.int32, device="cuda")]
+    held += [t, cp, ins]
+    return functools.partial(kd.load_library().kd_fwd, ctypes.byref(cp), ctypes.byref(ins),
+                             *[o.data_ptr() for o in outs],
+                             *_space(kd.kd_workspace_size(cp)[0], held), stream.cuda_stream), outs
+
+
 JOBS = {
     "logprob": _logprob,
     "mix": _mix,
+    # the staged slices of short and long teacher rows (and an exchange of two blocks an SM)
+    "project": functools.partial(_project, ((1000, 500), (38000, 500))),
+    # an exchange of one block an SM, by the student ids it serves
+    "project_wide": functools.partial(_project, ((8, 20000), (15000, 20000))),
+    "projected_loss": _projected_loss,
 }
+CALLS = {"project": 12000, "projected_loss": 12000}  # (a limit and its launch are a small part)
 
 
 @pytest.mark.parametrize("op", list(JOBS))
@@ -64,7 +111,7 @@ def test_two_threads_at_once(op):
         assert call() == kd.KD_OK
         torch.cuda.synchronize()
         want.append([t.clone() for t in outs])
-    told, times = [[], []], 3000
+    told, times = [[], []], CALLS.get(op, 3000)
 
     def work(i):
         call = jobs[i][0]
