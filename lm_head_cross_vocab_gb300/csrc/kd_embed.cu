@@ -143,7 +143,6 @@ __global__ void __launch_bounds__(kLookupThreads) k_embed_short(LookupArgs a) {
 
 // ------------------------------------------------------------------ sort
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
-constexpr int kMaxIds = 1216;  // ids of a block
 constexpr int kAhead = 8;      // tokens a lane has in flight
 constexpr int kKept = 128;     // tokens a warp keeps, each as its place in the warp's
 constexpr int kPlaceBits = 21; // run below and its id's number above
@@ -201,6 +200,11 @@ __host__ __device__ constexpr int sort_smem(int ids) {
   const int many = kSortWarps * ids * 4, one = kOneWarp * (int)sizeof(Place);
   return (ids + 3) / 4 * 16 + kListBytes + (many > one ? many : one);
 }
+// Ids of a block: as many as shared memory holds (227 KB, 1 KB of it for the kernel's
+// own).  Every block reads all tokens, and at this size an SM holds one: 128 blocks
+// are one wave, 256 two (200019 ids, 60000 tokens of 256 44.4 us with 128 blocks, 50.3
+// with 256; 4096 of 2048 20.0 and 21.5, 16384 of 2048 39.4 and 38.0).
+constexpr int kMaxIds = (226 * 1024 - kListBytes) / ((1 + kSortWarps) * 4) / 4 * 4;
 static_assert(sort_smem(kMaxIds) <= 226 * 1024, "shared memory of a block");
 static_assert(kMaxIds <= 1 << (32 - kPlaceBits), "a token in 32 bits");
 
