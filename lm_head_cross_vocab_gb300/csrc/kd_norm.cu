@@ -327,8 +327,12 @@ __global__ void __launch_bounds__(kWeightThreads) k_norm_weight(const float* par
   }
 }
 
-// Threads of a row and vectors of a thread.  The backward holds at most 16
-// elements a thread, whose shares of d_w stay in registers.
+// Threads of a row and vectors of a thread, for rows of up to KD_RMSNORM_MAX_D
+// elements.  The backward's shares of d_w stay in registers: 16 elements a thread, 20
+// and 24 where a row lies between the powers of two.  Beyond 8192 elements a row takes
+// 1024 threads of 64 registers each, and what those do not hold is spilled (bf16, 4096 x
+// 8192 42 us, 4096 x 12288 125, 4096 x 16384 141, 2048 x 32768 433, for floors of 30,
+// 45, 59 and 59 us).
 template <class T, bool BACKWARD, class F>
 auto norm_shape(int64_t d, F&& run) {
   const int64_t vecs = rows_div(d, RowVec<T>::N);
@@ -357,8 +361,12 @@ auto norm_shape(int64_t d, F&& run) {
     if (vecs <= 640) KD_SHAPE(128, 5);
     if (vecs <= 1024) KD_SHAPE(256, 4);
     if (vecs <= 2048) KD_SHAPE(512, 4);
-    if (vecs <= 4096) KD_SHAPE(1024, 4);
-    KD_SHAPE(1024, 8);
+    if constexpr (RowVec<T>::N == 8) {
+      KD_SHAPE(1024, 4);
+    } else {
+      if (vecs <= 4096) KD_SHAPE(1024, 4);
+      KD_SHAPE(1024, 8);
+    }
   }
 #undef KD_SHAPE
 }
