@@ -687,8 +687,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify_draw(VerifyArgs a) {
 
 // ------------------------------------------------------------------ plan
 struct VerifyPlan {
-  int parts, race_parts;
-  int64_t rows;
+  int parts[2], race_parts;   // parts, rows: of the target alone, and with the drafter's
+  int64_t rows[2];
   size_t sums, leader, arrived, bytes;
 };
 
@@ -705,14 +705,22 @@ kd_status verify_plan(const kd_verify_problem* p, VerifyPlan& P) {
     return KD_ERR_INVALID_ARG;
   const int nsm = std::max(1, tc_num_sms());
   const int64_t bytes = p->vocab * (p->dtype == KD_BF16 ? 2 : 4);
-  P.rows = p->n_seqs * (2 * p->n_drafts + 1);
-  const int64_t r = std::max<int64_t>(P.rows, 1), b = std::max<int64_t>(p->n_seqs, 1);
+  const int64_t b = std::max<int64_t>(p->n_seqs, 1);
   // Parts of a row in the first launch: three blocks an SM where rows are few, else
   // some 96 KB each (72 rows of 304 KB: 15.6 us with 6 parts, 20.5 with 1, 22.4 with
-  // 34; 3840 rows: 233.6 us with 3, 237.3 with 1, 249.9 with 8), 16 KB at least.
-  P.parts = (int)std::max<int64_t>(1, std::min<int64_t>({std::max(rows_div((int64_t)nsm * 3, r),
-                                                                  (bytes + 49152) / 98304),
-                                                         bytes / 16384, kMaxParts}));
+  // 34; 3840 rows: 233.6 us with 3, 237.3 with 1, 249.9 with 8), 16 KB at least.  The
+  // drafter's rows count where they are read.
+  size_t off = 0, sums = 0;
+  for (int i = 0; i < 2; ++i) {
+    P.rows[i] = p->n_seqs * ((i ? 2 : 1) * (int64_t)p->n_drafts + 1);
+    const int64_t r = std::max<int64_t>(P.rows[i], 1);
+    const int64_t parts = std::max<int64_t>(
+        1, std::min<int64_t>({std::max(rows_div((int64_t)nsm * 3, r), (bytes + 49152) / 98304),
+                              bytes / 16384, kMaxParts}));
+    // (a launch has at most 2^31 - 1 blocks; there are at most 2^27 rows)
+    P.parts[i] = (int)std::min<int64_t>(parts, INT32_MAX / r);
+    sums = std::max(sums, (size_t)r * P.parts[i] * sizeof(RowSum));
+  }
   // and of the row that is drawn from: as many blocks as the SMs hold, four each, or
   // where that is one or two a row, four (48 rows of 128256: 31.7 us with 12 parts, 37.7
   // with 16; 256 rows of 151936: 227.8 us with 4, 247.3 with 2, 237 with 3); parts
@@ -722,10 +730,7 @@ kd_status verify_plan(const kd_verify_problem* p, VerifyPlan& P) {
   P.race_parts = (int)std::max<int64_t>(
       1, std::min<int64_t>({most >= 3 ? most : 4, std::max(p->vocab / 8192, (int64_t)nsm * 2 / b),
                             p->vocab / 2048, kMaxParts}));
-  // (a launch has at most 2^31 - 1 blocks; there are at most 2^27 rows)
-  P.parts = (int)std::min<int64_t>(P.parts, INT32_MAX / r);
-  size_t off = 0;
-  P.sums = rows_take(off, (size_t)r * P.parts * sizeof(RowSum));
+  P.sums = rows_take(off, sums);
   P.leader = rows_take(off, (size_t)b * 8);
   P.arrived = rows_take(off, (size_t)b * 4);
   P.bytes = off;
@@ -825,7 +830,7 @@ extern "C" kd_status kd_verify_drafts(const kd_verify_problem* p, const kd_verif
   a.kt = greedy ? kL2E : kL2E / p->t_target;
   a.kd = kL2E / p->t_draft;
   a.inv_t = greedy ? 1.f : 1.f / p->t_target;
-  a.parts = P.parts;
+  a.parts = P.parts[a.zd != nullptr];
   a.race_parts = greedy ? 1 : P.race_parts;
   a.sums = reinterpret_cast<RowSum*>(ws + P.sums);
   a.leader = reinterpret_cast<uint64_t*>(ws + P.leader);
@@ -835,7 +840,7 @@ extern "C" kd_status kd_verify_drafts(const kd_verify_problem* p, const kd_verif
   a.logprob = logprob;
   a.status = dev_status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int64_t rows = a.zd ? P.rows : n * (k + 1);
+  const int64_t rows = P.rows[a.zd != nullptr];
   const bool ok = esz == 2 ? verify_run<__nv_bfloat16>(a, rows, s) : verify_run<float>(a, rows, s);
   return ok && cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA;
 }

@@ -133,3 +133,38 @@ def test_weights_and_noise_at_the_ends_of_their_ranges(size, v, dtype):
     r, ref = _both(c, dtype)
     assert ref["tokens"][:, 0].tolist() == [5, v // 2, 11]
     _check(r, ref, v)
+
+
+@pytest.mark.parametrize("b,k,v", [(19, 12, 32000), (8, 5, 40000), (16, 4, 33000), (3, 32, 20000),
+                                   (1, 1, 151936), (50, 1, 900)])
+@pytest.mark.parametrize("form", ["greedy", "without", "logits"])
+def test_the_workspace_is_what_was_asked_for(form, b, k, v):
+    """Rows are read in parts by how many there are, the drafter's among them or not:
+    every form of the call keeps to one problem's workspace."""
+    g = torch.Generator(device="cuda").manual_seed(b)
+    target = torch.randn(b, k + 1, v, generator=g, device="cuda").bfloat16()
+    t = {"target_logits": target, "drafts": target[:, :k].float().argmax(-1),
+         "uniform": torch.zeros(b, k, device="cuda"),
+         "noise": torch.rand(b, v, generator=g, device="cuda") + 0.5}
+    t["drafts"][:, -1] = 3  # (mostly not the largest: greedy ends there)
+    if form == "logits":
+        t["draft_logits"] = target[:, :k].contiguous()
+    p = kd.VerifyProblem(n_seqs=b, n_drafts=k, vocab=v, t_target=0.0 if form == "greedy" else 1.0)
+    size = kd.kd_verify_workspace_size(p.to_c())
+    buf = torch.full((size + 4096,), 77, dtype=torch.uint8, device="cuda")
+    assert buf.data_ptr() % 256 == 0
+
+    class Exact:
+        def get(self, nbytes, device):
+            assert nbytes == size
+            return buf.data_ptr(), nbytes
+
+    r = kd.verify_drafts(p, t, workspace=Exact())
+    assert (buf[size:] == 77).all()
+    if form == "greedy":
+        best = target.float().argmax(-1)
+        stood = (best[:, :k] == t["drafts"]).long().cumprod(1).sum(1)
+        assert torch.equal(r["accepted"].long(), stood)
+        assert torch.equal(r["tokens"].gather(1, stood[:, None]), best.gather(1, stood[:, None]))
+    else:
+        assert (r["accepted"] == k).all()
