@@ -373,7 +373,10 @@ def _device_of(t: dict):
 
 
 class Workspace:
-    """Reusable device workspace (PyTorch allocation, 256-byte aligned)."""
+    """Reusable device workspace (PyTorch allocation, 256-byte aligned) of the calls of
+    one stream.  A call that needs more than it holds lets its buffer go for a larger
+    one: where captured graphs share it, the call that needs most comes before the first
+    capture (or each graph has its own), and it lives as long as they are replayed."""
 
     def __init__(self):
         self.buf = None
