@@ -202,11 +202,16 @@ __host__ __device__ constexpr int sort_smem(int ids) {
 }
 // Ids of a block: as many as shared memory holds (227 KB, 1 KB of it for the kernel's
 // own).  Every block reads all tokens, and at this size an SM holds one: 128 blocks
-// are one wave, 256 two (200019 ids, 60000 tokens of 256 44.4 us with 128 blocks, 50.3
-// with 256; 4096 of 2048 20.0 and 21.5, 16384 of 2048 39.4 and 38.0).
+// are one wave, 256 two (200019 ids, 60000 tokens of 256 47.5 us with 128 blocks, 53.7
+// with 256; 4096 of 2048 23.3 and 24.0, 16384 of 2048 43.5 and 44.0).
 constexpr int kMaxIds = (226 * 1024 - kListBytes) / ((1 + kSortWarps) * 4) / 4 * 4;
 static_assert(sort_smem(kMaxIds) <= 226 * 1024, "shared memory of a block");
 static_assert(kMaxIds <= 1 << (32 - kPlaceBits), "a token in 32 bits");
+// The reduction may start while the sort ends, unless the sort's shared memory takes an
+// SM's largest setting, 228 KB: the reduction's blocks that come to such an SM meanwhile
+// have 28 KB of L1 to read through (16384 tokens of 2048, 200019 ids: 43.5 us, started
+// early 47.2; 151936 ids, which need 196 KB: 42.6 and, early, 42.1).
+constexpr int kChainedSmem = 194 * 1024;
 
 __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a) {
   extern __shared__ __align__(16) int counter[];
@@ -725,7 +730,7 @@ bool lookup_run(LookupArgs a, bool vec, cudaStream_t s) {
 
 // A team of as many warps as a row has vectors for, up to a block.
 template <class T, int TEAM, bool VEC>
-bool reduce_team(ReduceGradArgs a, cudaStream_t s) {
+bool reduce_team(ReduceGradArgs a, bool chained, cudaStream_t s) {
   a.slices = (int)rows_div(a.d, Columns<T, TEAM, VEC>::kSlice);
   a.teams = rows_div(rows_div(a.n, a.run) * a.slices, kReduceThreads / TEAM);
   // Many small blocks, behind the ones that add: they fill the table from front to
@@ -734,13 +739,14 @@ bool reduce_team(ReduceGradArgs a, cudaStream_t s) {
       32, std::max<int64_t>(1, kZeroBytes / kReduceWarps / (a.d * (int64_t)sizeof(T))));
   const int64_t grid = a.teams + (a.accumulate ? 0 : rows_div(a.vocab, a.zeros));
   return grid <= INT32_MAX &&
-         rows_launch(k_embed_reduce<T, TEAM, VEC>, grid, kReduceThreads, 0, true, s, a);
+         rows_launch(k_embed_reduce<T, TEAM, VEC>, grid, kReduceThreads, 0, chained, s, a);
 }
 template <class T>
-bool reduce_run(const ReduceGradArgs& a, bool vec, cudaStream_t s) {
+bool reduce_run(const ReduceGradArgs& a, bool vec, bool chained, cudaStream_t s) {
   auto team = [&](auto size) {
     constexpr int TEAM = decltype(size)::value;
-    return vec ? reduce_team<T, TEAM, true>(a, s) : reduce_team<T, TEAM, false>(a, s);
+    return vec ? reduce_team<T, TEAM, true>(a, chained, s)
+               : reduce_team<T, TEAM, false>(a, chained, s);
   };
   const int64_t vecs = rows_div(a.d, RowVec<T>::N);
   const bool ok = vecs <= 32   ? team(std::integral_constant<int, 32>())
@@ -860,6 +866,8 @@ extern "C" kd_status kd_embed_bwd(const kd_embed_problem* p, const int64_t* toke
   a.accumulate = accumulate;
   a.scale = p->scale;
   const bool vec = row % 16 == 0 && rows_aligned(16, d_h, d_w);
-  const bool ok = esz == 2 ? reduce_run<__nv_bfloat16>(a, vec, s) : reduce_run<float>(a, vec, s);
+  const bool chained = smem <= kChainedSmem;
+  const bool ok = esz == 2 ? reduce_run<__nv_bfloat16>(a, vec, chained, s)
+                           : reduce_run<float>(a, vec, chained, s);
   return ok && cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA;
 }
