@@ -528,8 +528,8 @@ kd_status kd_embed_bwd(const kd_embed_problem* problem, const int64_t* tokens, c
  * Range: a row's sum of squares has to lie below 2^128 (elements of 2^56.5 in a row
  * of 32768, of 2^61.5 in one of 32; beyond, r is 0 and so is the row), and with an
  * eps below 2^-126 its mean square not below 2^-126; a row of zeros needs eps > 0
- * (NaN without).  Backward: so has the sum of |g s| to lie below 2^128, and products
- * g s count down to 2^-126.
+ * (NaN without).  Backward: so has the sum of |g s| to lie below 2^128, and the
+ * products g s and r d_h count down to 2^-126.
  * Either gradient may be NULL to skip it.  h or sum may be x or residual
  * themselves, and d_x any of s, d_h and d_sum; outputs may not overlap the inputs
  * or one another otherwise.  workspace: 256-byte aligned. */

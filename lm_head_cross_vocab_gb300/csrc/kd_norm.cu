@@ -256,9 +256,18 @@ __global__ void __launch_bounds__(norm_block(TPR), norm_per_sm(TPR, VPT)) k_norm
         float o[N];
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-          const float y = sv[e] * r;
-          o[e] = fmaf(-y, rm, r * (gv[e] * (wv[e] + a.off)));
-          dw[i * N + e] = fmaf(gv[e], y, dw[i * N + e]);
+          // (s r is in both gradients, or r g is: with 64 registers the latter spills
+          // less, 2048 x 32768 bf16 223 us and 434; else the former is no slower, 8000 x
+          // 5120 51.5 us and 54.0)
+          if constexpr (TPR < 1024) {
+            const float y = sv[e] * r;
+            o[e] = fmaf(-y, rm, r * (gv[e] * (wv[e] + a.off)));
+            dw[i * N + e] = fmaf(gv[e], y, dw[i * N + e]);
+          } else {
+            const float y = gv[e] * r;
+            o[e] = fmaf(-(sv[e] * r), rm, y * (wv[e] + a.off));
+            dw[i * N + e] = fmaf(y, sv[e], dw[i * N + e]);
+          }
         }
         if (a.res) {
           float uv[N];
@@ -332,7 +341,7 @@ __global__ void __launch_bounds__(kWeightThreads) k_norm_weight(const float* par
 // elements.  The backward's shares of d_w stay in registers: 16 elements a thread, 20
 // and 24 where a row lies between the powers of two.  Beyond 8192 elements a row takes
 // 1024 threads of 64 registers each, and what those do not hold is spilled (bf16, 4096 x
-// 8192 42 us, 4096 x 12288 125, 4096 x 16384 141, 2048 x 32768 433, for floors of 30,
+// 8192 42 us, 4096 x 12288 118, 4096 x 16384 135, 2048 x 32768 223, for floors of 30,
 // 45, 59 and 59 us).
 template <class T, bool BACKWARD, class F>
 auto norm_shape(int64_t d, F&& run) {
