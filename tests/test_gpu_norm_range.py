@@ -3,7 +3,7 @@ limits that the header states, against the fp64 oracle.
 
 Tolerances as tests/test_gpu_norm.py derives them (E = 64 elements a thread at most,
 u = 2^-24): r within (E / 2 + 10) u; the sum of g s within (E + 14) u of the sum of
-absolute values.  d_x = r (g - (s r) m), m = r mean(g s): each term holds r up to
+absolute values.  d_x = r g - (s r) (r m), m = r mean(g s): each term holds r up to
 three times, so that it is off by at most 4 E u of its absolute value.  All factors
 are normal fp32 numbers within the stated range: nothing is lost below it."""
 import numpy as np
